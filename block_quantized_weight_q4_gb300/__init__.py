@@ -9,4 +9,5 @@ from .binding import (  # noqa: F401
     QmvError, library_path, load_library, weight_bytes, scale_offset,
     matvec, matvec_grouped, matvec_grouped_noalloc, matvec_glu, FLAG_OVERLAP, FLAG_BF16_WEIGHTS, MAX_GROUP, NOALLOC_MAX_BATCH, dequant,
     validate, quantize, quantize_q4_fit, quantize_x, matvec_qx, matvec_qx_grouped, gguf_bytes, gguf_to_mlb, Step, matrix_wtype, strerror, last_error,
+    rmsnorm, KvCache, KvBatch, kv_write, kv_read, attend, logprobs, OUT_Q8, NORM_MAX_COLS, MAX_TOP, MAX_GIVEN,
 )

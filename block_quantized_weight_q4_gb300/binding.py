@@ -98,6 +98,17 @@ def load_library():
     lib.qmv_matvec_qx_grouped.argtypes = [i32, i32, i32, i32, vp, i32, ctypes.c_uint, vp]
     lib.qmv_matvec_qx.restype = i32
     lib.qmv_matvec_qx.argtypes = [i32, i32, i64, i64, vp, vp, vp, i32, vp]
+    f32 = ctypes.c_float
+    lib.qmv_rmsnorm.restype = i32
+    lib.qmv_rmsnorm.argtypes = [i32, i64, i64, vp, vp, vp, vp, f32, i32, vp, vp]
+    lib.qmv_kv_write.restype = i32
+    lib.qmv_kv_write.argtypes = [vp, vp, i32, vp, i64, vp, i64, vp]
+    lib.qmv_kv_read.restype = i32
+    lib.qmv_kv_read.argtypes = [vp, vp, i32, vp, vp, vp]
+    lib.qmv_attend.restype = i32
+    lib.qmv_attend.argtypes = [vp, vp, i32, i32, vp, i64, f32, i32, i32, vp, i64, vp]
+    lib.qmv_logprobs.restype = i32
+    lib.qmv_logprobs.argtypes = [i64, i64, vp, i64, vp, i32, vp, vp, i32, vp, vp, vp]
     lib.qmv_check_device.restype = i32
     lib.qmv_check_device.argtypes = []
     lib.qmv_strerror.restype = ctypes.c_char_p
@@ -482,6 +493,224 @@ def quantize_q4_fit(scale_dtype: int, src, W=None, stream=None):
                                             _stream(stream))
     _check(st, "qmv_quantize_q4_fit")
     return W, int(first.item())
+
+
+OUT_Q8 = 16
+NORM_MAX_COLS = 32768
+MAX_TOP = 32
+MAX_GIVEN = 64
+
+
+def _raw_stream(stream, device_index):
+    """The stream's handle as an integer; the device's current stream by default."""
+    if device_index < 0:
+        raise ValueError("CUDA tensors are needed")
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def rmsnorm(x, weight, eps: float = 1e-5, residual=None, residual_out=None, out="q8", y=None, stream=None):
+    """Root-mean-square norm with the residual's addition (qmv_rmsnorm): with s = x + residual,
+    y = s * weight / sqrt(mean(s^2) + eps).  x: (rows, cols) or (cols,) float32/bfloat16 CUDA tensor;
+    residual: float32 of x's shape or None; residual_out: where s is stored (residual itself for an
+    update in place), or None.  out: "q8" (the uint8 Q8_0 / f32-scale image that matvec_qx reads),
+    "bf16" or "f32".  Returns y."""
+    import torch
+    cols = x.shape[-1]
+    rows = x.shape[0] if x.dim() == 2 else 1
+    if x.dim() not in (1, 2) or not x.is_contiguous():
+        raise ValueError("x must be a contiguous (rows, cols) tensor")
+    if weight.dtype != torch.float32 or weight.numel() != cols or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 (cols,) tensor")
+    for t in (residual, residual_out):
+        if t is not None and (t.dtype != torch.float32 or t.shape != x.shape or not t.is_contiguous()):
+            raise ValueError("residual and residual_out must be contiguous float32 tensors of x's shape")
+    if out == "q8":
+        code = OUT_Q8
+        if y is None:
+            y = torch.empty(weight_bytes(Q8_0, SCALE_F32, rows, cols), dtype=torch.uint8, device=x.device)
+        elif y.dtype != torch.uint8 or y.numel() < weight_bytes(Q8_0, SCALE_F32, rows, cols) or not y.is_contiguous():
+            raise ValueError("y must be a contiguous uint8 tensor of the image's bytes")
+    elif out in ("bf16", "f32"):
+        code, dtype = (X_BF16, torch.bfloat16) if out == "bf16" else (X_F32, torch.float32)
+        if y is None:
+            y = torch.empty(x.shape, dtype=dtype, device=x.device)
+        elif y.dtype != dtype or y.shape != x.shape or not y.is_contiguous():
+            raise ValueError("y must be a contiguous tensor of x's shape and the output's type")
+    else:
+        raise ValueError("out must be 'q8', 'bf16' or 'f32'")
+    st = load_library().qmv_rmsnorm(_x_dtype(x), rows, cols, x.data_ptr(),
+                                    None if residual is None else residual.data_ptr(),
+                                    None if residual_out is None else residual_out.data_ptr(), weight.data_ptr(), eps,
+                                    code, y.data_ptr(), _raw_stream(stream, x.get_device()))
+    _check(st, "qmv_rmsnorm")
+    return y
+
+
+class _KvCacheC(ctypes.Structure):
+    """qmv_kv_cache of include/qmv.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_tokens", ctypes.c_int)]
+
+
+class _KvBatchC(ctypes.Structure):
+    """qmv_kv_batch of include/qmv.h."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int), ("kv_len", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("n_seq", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("max_rows", ctypes.c_int), ("max_len", ctypes.c_int)]
+
+
+class KvCache:
+    """One layer's paged cache of keys and values in 8 bits (qmv_kv_cache): k and v are int8 CUDA
+    tensors (pages, kv_heads, page_tokens, head_dim), k_scale and v_scale float32 (pages, kv_heads).
+    KvCache.empty() makes them."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4 or v.shape != k.shape or k.dtype != torch.int8 or v.dtype != torch.int8:
+            raise ValueError("k and v must be int8 (pages, kv_heads, page_tokens, head_dim) tensors")
+        for t in (k_scale, v_scale):
+            if t.dtype != torch.float32 or t.shape != k.shape[:2] or not t.is_contiguous():
+                raise ValueError("k_scale and v_scale must be contiguous float32 (pages, kv_heads) tensors")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.n_pages,
+                            self.kv_heads, self.head_dim, self.page_tokens)
+        self._p = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
+        """A cache of zero levels and scales."""
+        import torch
+        shape = (n_pages, kv_heads, page_tokens, head_dim)
+        return cls(torch.zeros(shape, dtype=torch.int8, device=device), torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], device=device), torch.zeros(shape[:2], device=device))
+
+
+class KvBatch:
+    """The rows of calls over a cache (qmv_kv_batch): page_table (sequences, pages) int32, kv_len
+    (sequences,) int32, starts (sequences + 1,) int32 or None for one row a sequence: CUDA tensors whose
+    contents are read when a call runs on the device, so a decode loop updates them in place.  rows: the
+    call's rows in all; max_rows, max_len: upper bounds of a sequence's rows and of kv_len (by
+    default rows, and what the table would hold in pages of 128).
+    A close max_len lets the calls choose better."""
+
+    def __init__(self, page_table, kv_len, starts=None, rows=None, max_rows=None, max_len=None):
+        import torch
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 0 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be an int32 (sequences, pages) tensor with contiguous rows")
+        n = page_table.shape[0]
+        if kv_len.dtype != torch.int32 or tuple(kv_len.shape) != (n,) or not kv_len.is_contiguous():
+            raise ValueError("kv_len must be a contiguous int32 (sequences,) tensor")
+        if starts is None:
+            rows, max_rows = n, 1
+        else:
+            if starts.dtype != torch.int32 or tuple(starts.shape) != (n + 1,) or not starts.is_contiguous():
+                raise ValueError("starts must be a contiguous int32 (sequences + 1,) tensor")
+            if rows is None:
+                raise ValueError("rows is needed with starts")
+            max_rows = rows if max_rows is None else max_rows
+        self.page_table, self.kv_len, self.starts = page_table, kv_len, starts
+        self.n_seq, self.rows, self.max_rows = n, rows, max_rows
+        self.max_len = 128 * page_table.shape[1] if max_len is None else max_len
+        stride = page_table.stride(0) if n > 1 else page_table.shape[1]
+        self._c = _KvBatchC(page_table.data_ptr(), stride, page_table.shape[1], kv_len.data_ptr(), None if starts is None else starts.data_ptr(),
+                            n, rows, max_rows, self.max_len)
+        self._p = ctypes.addressof(self._c)
+
+
+def _head_rows(t, heads, dim, rows, what):
+    """The row stride of a (rows, heads, dim) tensor whose rows are contiguous."""
+    if tuple(t.shape) != (rows, heads, dim) or (rows > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
+        raise ValueError(f"{what} must be a ({rows}, {heads}, {dim}) tensor with contiguous rows")
+    return t.stride(0) if rows > 1 else heads * dim
+
+
+def kv_write(cache: KvCache, batch: KvBatch, k, v, stream=None):
+    """Writes the call's rows into the cache (qmv_kv_write): k and v (rows, kv_heads, head_dim) CUDA
+    tensors of one type, float32 or bfloat16; rows may be strided (a slice of a wider row)."""
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have one type")
+    ks = _head_rows(k, cache.kv_heads, cache.head_dim, batch.rows, "k")
+    vs = _head_rows(v, cache.kv_heads, cache.head_dim, batch.rows, "v")
+    st = load_library().qmv_kv_write(cache._p, batch._p, _x_dtype(k), k.data_ptr(), ks, v.data_ptr(), vs,
+                                     _raw_stream(stream, k.get_device()))
+    _check(st, "qmv_kv_write")
+
+
+def kv_read(cache: KvCache, batch: KvBatch, dtype=None, k=None, v=None, stream=None):
+    """Reads the call's rows back (qmv_kv_read) as (rows, kv_heads, head_dim) tensors of dtype
+    (torch.bfloat16 by default, or torch.float32).  Returns k, v."""
+    import torch
+    if dtype is None:
+        dtype = torch.bfloat16 if k is None else k.dtype
+    shape = (batch.rows, cache.kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    for t in (k, v):
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError("k and v must be contiguous (rows, kv_heads, head_dim) tensors of the asked type")
+    st = load_library().qmv_kv_read(cache._p, batch._p, _x_dtype(k), k.data_ptr(), v.data_ptr(),
+                                    _raw_stream(stream, k.get_device()))
+    _check(st, "qmv_kv_read")
+    return k, v
+
+
+def attend(cache: KvCache, batch: KvBatch, q, out=None, scale=None, causal: bool = True, window: int = 0, stream=None):
+    """Softmax attention of the call's rows over the cache (qmv_attend): q (rows, heads, head_dim)
+    float32/bfloat16 CUDA tensor, rows may be strided; scale defaults to 1 / sqrt(head_dim).  Returns
+    out, (rows, heads, head_dim) of q's type."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be a (rows, heads, head_dim) tensor")
+    heads = q.shape[1]
+    qs = _head_rows(q, heads, cache.head_dim, batch.rows, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype:
+        raise ValueError("out must have q's type")
+    os_ = _head_rows(out, heads, cache.head_dim, batch.rows, "out")
+    st = load_library().qmv_attend(cache._p, batch._p, heads, _x_dtype(q), q.data_ptr(), qs,
+                                   cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                                   out.data_ptr(), os_, _raw_stream(stream, q.get_device()))
+    _check(st, "qmv_attend")
+    return out
+
+
+def logprobs(logits, given=None, top: int = 0, entropy: bool = True, stream=None):
+    """Log probabilities from logits (rows, vocab), float32, rows may be strided (qmv_logprobs): of
+    the given ids (rows, n) int64, the entropy, and the `top` largest with their ids.  Returns
+    (given_logprob, entropy, top_ids, top_logprob); what was not asked for is None."""
+    import torch
+    if logits.dim() != 2 or logits.dtype != torch.float32 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a float32 (rows, vocab) tensor with contiguous rows")
+    rows, vocab = logits.shape
+    dev = logits.device
+    n = 0
+    glp = ent = ids = tlp = None
+    if given is not None:
+        if given.dtype != torch.int64 or given.dim() != 2 or given.shape[0] != rows or not given.is_contiguous():
+            raise ValueError("given must be a contiguous int64 (rows, n) tensor")
+        n = given.shape[1]
+        glp = torch.empty((rows, n), dtype=torch.float32, device=dev)
+    if entropy:
+        ent = torch.empty((rows,), dtype=torch.float32, device=dev)
+    if top > 0:
+        ids = torch.empty((rows, top), dtype=torch.int32, device=dev)
+        tlp = torch.empty((rows, top), dtype=torch.float32, device=dev)
+    st = load_library().qmv_logprobs(rows, vocab, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
+                                     None if n == 0 else given.data_ptr(), n, None if n == 0 else glp.data_ptr(),
+                                     None if ent is None else ent.data_ptr(), top, None if ids is None else ids.data_ptr(),
+                                     None if tlp is None else tlp.data_ptr(), _raw_stream(stream, logits.get_device()))
+    _check(st, "qmv_logprobs")
+    return glp, ent, ids, tlp
 
 
 def last_error() -> int:

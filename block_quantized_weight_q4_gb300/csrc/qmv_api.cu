@@ -4,6 +4,7 @@
 // Layout (Krafla ".mlb model format v1", "Body"): q array, zero padding to a multiple of 64
 // bytes, d array.  Checks follow the loader's classes ("Validation done by the loader"):
 // unknown enum -> format error; zero dimension, cols not a multiple of 32, overflow -> shape.
+#include <cmath>
 #include <mutex>
 
 #include "qmv_common.cuh"
@@ -68,6 +69,56 @@ int make_ref(int wtype, int scale_dtype, int64_t rows, int64_t cols, const void*
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// A paged cache and a call's rows, checked; `status` is left to the caller.
+int make_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, KvRef* c) {
+  if (cache == nullptr || batch == nullptr) return QMV_E_ARG;
+  if (batch->n_seq < 0 || batch->rows < 0 || batch->max_rows < 0 || batch->max_len < 0 || batch->table_pages < 0)
+    return QMV_E_ARG;
+  if (cache->page_tokens != 16 && cache->page_tokens != 32 && cache->page_tokens != 64 && cache->page_tokens != 128)
+    return QMV_E_SHAPE;
+  if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) return QMV_E_SHAPE;
+  if (cache->kv_heads < 1 || cache->kv_heads > 1024) return QMV_E_SHAPE;
+  if (cache->n_pages < 0 || cache->n_pages > INT32_MAX || batch->n_seq > 65535 || batch->rows > INT32_MAX ||
+      batch->table_stride < batch->table_pages || batch->table_stride > INT32_MAX || batch->max_len > INT32_MAX - 1024)
+    return QMV_E_SHAPE;
+  if (batch->starts == nullptr && batch->rows != batch->n_seq) return QMV_E_SHAPE;
+  c->k = cache->k;
+  c->v = cache->v;
+  c->k_scale = cache->k_scale;
+  c->v_scale = cache->v_scale;
+  c->page_table = batch->page_table;
+  c->kv_len = batch->kv_len;
+  c->starts = batch->starts;
+  c->status = nullptr;
+  c->n_pages = cache->n_pages;
+  c->table_stride = batch->table_stride;
+  c->table_pages = batch->table_pages;
+  c->rows = batch->rows;
+  c->kv_heads = cache->kv_heads;
+  c->head_dim = cache->head_dim;
+  c->page_tokens = cache->page_tokens;
+  c->n_seq = batch->n_seq;
+  c->max_rows = batch->starts == nullptr && batch->max_rows > 1 ? 1 : batch->max_rows;
+  c->max_len = batch->max_len;
+  if (batch->rows == 0 || c->max_rows == 0) return QMV_OK;  // nothing to launch
+  if (c->n_seq == 0) return QMV_E_ARG;
+  if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
+      c->page_table == nullptr || c->kv_len == nullptr)
+    return QMV_E_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(c->page_table, 4) || !aligned(c->kv_len, 4) || !aligned(c->starts, 4))
+    return QMV_E_ALIGN;
+  return QMV_OK;
+}
+
+// Rows of heads x head_dim values, `stride` elements apart.
+int row_stride_status(const void* p, int64_t stride, int heads, int head_dim, int x_dtype, int64_t rows) {
+  const int size = x_dtype == QMV_X_BF16 ? 2 : 4;
+  if (stride < (int64_t)heads * head_dim || stride > INT64_MAX / 4 / (rows > 0 ? rows : 1)) return QMV_E_SHAPE;
+  if (!aligned(p, 16) || stride * size % 16 != 0) return QMV_E_ALIGN;
+  return QMV_OK;
+}
 
 }  // namespace
 
@@ -600,6 +651,126 @@ int qmv_quantize_q4_fit(int scale_dtype, int64_t rows, int64_t cols, const float
                          L.q_bytes, first_bad, dev, stream) == cudaSuccess
              ? QMV_OK
              : QMV_E_CUDA;
+}
+
+int qmv_rmsnorm(int x_dtype, int64_t rows, int64_t cols, const void* x, const float* residual, float* residual_out,
+                const float* weight, float eps, int out_dtype, void* out, cudaStream_t stream) {
+  if (x_dtype != QMV_X_F32 && x_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16 && out_dtype != QMV_OUT_Q8) return QMV_E_FORMAT;
+  if (rows < 0 || !(eps >= 0.f) || std::isinf(eps)) return QMV_E_ARG;
+  if (cols <= 0 || cols % 32 != 0 || cols > QMV_NORM_MAX_COLS) return QMV_E_SHAPE;
+  if (rows == 0) return QMV_OK;
+  Layout L;
+  const int st = make_layout(QMV_Q8_0, QMV_SCALE_F32, rows, cols, &L);
+  if (st != QMV_OK) return st;
+  if (rows > INT32_MAX) return QMV_E_SHAPE;
+  if (x == nullptr || weight == nullptr || out == nullptr) return QMV_E_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(weight, 16) ||
+      !aligned(out, 16))
+    return QMV_E_ALIGN;
+  return launch_rmsnorm(x_dtype == QMV_X_BF16, rows, cols, x, residual, residual_out, weight, eps, out_dtype, out,
+                        L.d_off, stream) == cudaSuccess
+             ? QMV_OK
+             : QMV_E_CUDA;
+}
+
+int qmv_kv_write(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int x_dtype, const void* k, int64_t k_stride,
+                 const void* v, int64_t v_stride, cudaStream_t stream) {
+  if (x_dtype != QMV_X_F32 && x_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  KvRef c;
+  const int st = make_kv(cache, batch, &c);
+  if (st != QMV_OK) return st;
+  if (c.rows == 0 || c.max_rows == 0) return QMV_OK;
+  if (k == nullptr || v == nullptr) return QMV_E_ARG;
+  const int ks = row_stride_status(k, k_stride, c.kv_heads, c.head_dim, x_dtype, c.rows);
+  if (ks != QMV_OK) return ks;
+  const int vs = row_stride_status(v, v_stride, c.kv_heads, c.head_dim, x_dtype, c.rows);
+  if (vs != QMV_OK) return vs;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
+  c.status = dev.status;
+  return launch_kv_write(c, x_dtype == QMV_X_BF16, k, k_stride, v, v_stride, stream) == cudaSuccess ? QMV_OK
+                                                                                                    : QMV_E_CUDA;
+}
+
+int qmv_kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int out_dtype, void* k, void* v,
+                cudaStream_t stream) {
+  if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  KvRef c;
+  const int st = make_kv(cache, batch, &c);
+  if (st != QMV_OK) return st;
+  if (c.rows == 0 || c.max_rows == 0) return QMV_OK;
+  if (k == nullptr || v == nullptr) return QMV_E_ARG;
+  const int64_t stride = (int64_t)c.kv_heads * c.head_dim;
+  const int ks = row_stride_status(k, stride, c.kv_heads, c.head_dim, out_dtype, c.rows);
+  if (ks != QMV_OK) return ks;
+  const int vs = row_stride_status(v, stride, c.kv_heads, c.head_dim, out_dtype, c.rows);
+  if (vs != QMV_OK) return vs;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
+  c.status = dev.status;
+  return launch_kv_read(c, out_dtype == QMV_X_BF16, k, v, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
+}
+
+int qmv_attend(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int heads, int x_dtype, const void* q,
+               int64_t q_stride, float scale, int causal, int window, void* out, int64_t out_stride,
+               cudaStream_t stream) {
+  if (x_dtype != QMV_X_F32 && x_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (window < 0 || !std::isfinite(scale)) return QMV_E_ARG;
+  KvRef c;
+  const int st = make_kv(cache, batch, &c);
+  if (st != QMV_OK) return st;
+  if (heads <= 0 || heads % c.kv_heads != 0 || heads > 65535) return QMV_E_SHAPE;
+  if (c.rows == 0 || c.max_rows == 0) return QMV_OK;
+  if (q == nullptr || out == nullptr) return QMV_E_ARG;
+  const int qs = row_stride_status(q, q_stride, heads, c.head_dim, x_dtype, c.rows);
+  if (qs != QMV_OK) return qs;
+  const int os = row_stride_status(out, out_stride, heads, c.head_dim, x_dtype, c.rows);
+  if (os != QMV_OK) return os;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
+  c.status = dev.status;
+  AttendArgs a;
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.scale = scale;
+  a.heads = heads;
+  a.causal = causal != 0;
+  a.window = window;
+  return launch_attend(c, a, x_dtype == QMV_X_BF16, dev, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
+}
+
+int qmv_logprobs(int64_t rows, int64_t vocab, const float* logits, int64_t stride, const int64_t* given, int n_given,
+                 float* given_logprob, float* entropy, int n_top, int32_t* top_ids, float* top_logprob,
+                 cudaStream_t stream) {
+  if (rows < 0 || n_given < 0 || n_top < 0) return QMV_E_ARG;
+  if (vocab <= 0 || vocab >= INT32_MAX - 4096 || stride < vocab || n_top > QMV_MAX_TOP || n_top > vocab ||
+      n_given > QMV_MAX_GIVEN)
+    return QMV_E_SHAPE;
+  if (rows > INT32_MAX || (rows > 0 && stride > INT64_MAX / 4 / rows)) return QMV_E_SHAPE;
+  if (rows == 0) return QMV_OK;
+  if (logits == nullptr || (n_given > 0 && (given == nullptr || given_logprob == nullptr)) ||
+      (n_top > 0 && (top_ids == nullptr || top_logprob == nullptr)))
+    return QMV_E_ARG;
+  if (!aligned(logits, 4) || !aligned(given, 8) || !aligned(given_logprob, 4) || !aligned(entropy, 4) ||
+      !aligned(top_ids, 4) || !aligned(top_logprob, 4))
+    return QMV_E_ALIGN;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
+  LogprobArgs a;
+  a.logits = logits;
+  a.given = given;
+  a.given_logprob = given_logprob;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprob = top_logprob;
+  a.stride = stride;
+  a.vocab = vocab;
+  a.n_given = n_given;
+  a.n_top = n_top;
+  return launch_logprobs(a, rows, dev, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
 }
 
 int qmv_check_device(void) {

@@ -190,4 +190,63 @@ cudaError_t launch_decode_tc_f32(const MatrixRef* ms, const void* const* xs, flo
                                  bool pdl, const DeviceInfo& dev, const Workspace& ws, cudaStream_t stream,
                                  int act = -1, long long up_batch = 0);
 
+// ---------------------------------------------------------------- between the products
+// Root-mean-square norm (norm.cu): out_dtype QMV_X_F32, QMV_X_BF16, or QMV_OUT_Q8 with the scales at
+// out + out_d_off.
+cudaError_t launch_rmsnorm(bool x_bf16, int64_t rows, int64_t cols, const void* x, const float* residual,
+                           float* residual_out, const float* weight, float eps, int out_dtype, void* out,
+                           int64_t out_d_off, cudaStream_t stream);
+
+// A paged 8-bit cache and the rows of a call over it (validated qmv_kv_cache and qmv_kv_batch).
+struct KvRef {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  const int32_t* kv_len;
+  const int32_t* starts;  // null: row s belongs to sequence s
+  int* status;
+  long long n_pages;
+  long long table_stride;
+  long long rows;
+  int kv_heads;
+  int head_dim;
+  int page_tokens;
+  int n_seq;
+  int max_rows;
+  int max_len;
+  int table_pages;
+};
+cudaError_t launch_kv_write(const KvRef& c, bool x_bf16, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, cudaStream_t stream);
+
+struct AttendArgs {
+  const void* q;
+  void* out;
+  long long q_stride;
+  long long out_stride;
+  float scale;
+  int heads;
+  int causal;
+  int window;
+};
+cudaError_t launch_attend(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev,
+                          cudaStream_t stream);
+
+struct LogprobArgs {
+  const float* logits;
+  const int64_t* given;
+  float* given_logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprob;
+  long long stride;
+  long long vocab;
+  int n_given;
+  int n_top;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace qmv

@@ -497,6 +497,155 @@ int qmv_step_open_wait(qmv_step *step, qmv_step *next, cudaStream_t stream, long
  * QMV_OK or QMV_E_CUDA. */
 int qmv_step_destroy(qmv_step *step);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators between the products of a decode or prompt step: the norm that makes a product's
+ * activations, the cache of keys and values in 8 bits, the attention over it, and what is read
+ * from the logits.  The Krafla page has no counterpart for the paged cache and the log
+ * probabilities (properties of a runtime, not of the format); the norm's 8-bit output is the
+ * runtime's activation image ("Quantization rule", Q8_0 with a float32 scale).
+ * The conventions above hold: asynchronous, caller-owned memory, arguments checked on the host
+ * before anything is launched. */
+
+/* out_dtype of qmv_rmsnorm beside QMV_X_F32 and QMV_X_BF16: the Q8_0 / f32-scale image that
+ * qmv_matvec_qx reads (qmv_weight_bytes(QMV_Q8_0, QMV_SCALE_F32, rows, cols) bytes). */
+#define QMV_OUT_Q8 16
+
+#define QMV_NORM_MAX_COLS 32768
+
+/* Root-mean-square norm with the residual's addition.  For each of `rows` rows of `cols` values:
+ *   s = x + residual            (float32; s = x when residual is NULL)
+ *   r = 1 / sqrt(mean(s^2) + eps)
+ *   y = s * weight * r
+ *   x            : device, rows x cols, x_dtype QMV_X_F32 or QMV_X_BF16, row-major, 16-byte aligned.
+ *   residual     : device, rows x cols float32, or NULL.  residual_out: where s is stored (float32), or
+ *                  NULL; it may be residual itself.  weight: device, cols float32.  16-byte aligned.
+ *   out          : device, 16-byte aligned, fully written: rows x cols float32 or bfloat16 (y rounded
+ *                  once), or for QMV_OUT_Q8 the image: with t = s * weight and amax = max |t| of a block
+ *                  of 32, q = trunc(t * (127 * (1 / amax)) + copysign(0.5, t)) clamped to +-127 and
+ *                  d = amax * RN(1 / 127) * r (the zero block where amax < 1e-30), each step one
+ *                  float32 operation rounded to nearest: qmv_quantize_x's rule with its divisions as
+ *                  products.  r is common to a row, so the levels do not depend on it.  The
+ *                  padding between the image's arrays is written as zeros.
+ *   out and residual_out must not overlap x, weight or each other.
+ * The sum of squares is float32, added in a fixed order.  rows 0 launches nothing.
+ * Returns QMV_OK, QMV_E_FORMAT (x_dtype, out_dtype), QMV_E_ARG (rows < 0, null pointer, eps negative
+ * or not finite), QMV_E_SHAPE (cols not a positive multiple of 32 or above QMV_NORM_MAX_COLS, a size that
+ * overflows), QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_rmsnorm(int x_dtype, int64_t rows, int64_t cols, const void *x, const float *residual,
+                float *residual_out, const float *weight, float eps, int out_dtype, void *out,
+                cudaStream_t stream);
+
+/* A paged cache of keys and values in 8 bits (one layer's): n_pages pages of page_tokens tokens.  A
+ * page holds, for each of kv_heads heads, page_tokens x head_dim int8 levels, and one float32
+ * scale: the value is level * scale.
+ *   k, v             : device, n_pages x kv_heads x page_tokens x head_dim int8, 16-byte aligned.
+ *   k_scale, v_scale : device, n_pages x kv_heads float32, 4-byte aligned.
+ *   page_tokens is 16, 32, 64 or 128; head_dim 64, 128 or 256; kv_heads 1..1024; n_pages below 2^31. */
+typedef struct qmv_kv_cache {
+  int8_t *k;
+  int8_t *v;
+  float *k_scale;
+  float *v_scale;
+  int64_t n_pages;
+  int kv_heads;
+  int head_dim;
+  int page_tokens;
+} qmv_kv_cache;
+
+/* The rows of a call.  Sequence s holds kv_len[s] tokens, token i in page
+ * page_table[s * table_stride + i / page_tokens] at place i % page_tokens; a row of the table has
+ * table_pages entries.  The call's rows
+ * starts[s] .. starts[s + 1] - 1 (one row a sequence, row s, when starts is NULL) are the sequence's
+ * LAST tokens: with n of them, row starts[s] + i is the token at position kv_len[s] - n + i.  So
+ * kv_len counts the tokens that the call itself writes or asks for.
+ *   page_table, kv_len, starts : device int32 (n_seq rows of table_pages entries, n_seq, n_seq + 1).
+ *   rows     : the call's rows in all (starts[n_seq]; n_seq when starts is NULL).
+ *   max_rows : no sequence has more rows in this call; max_len: no kv_len is larger.
+ * These lengths are read on the device.  A sequence that contradicts the call (a length
+ * below 0, above max_len or above what its page table holds, rows outside 0..rows, more of them
+ * than max_rows or than kv_len), and a page id outside the cache among the pages it uses, are not
+ * followed: nothing out of range is read or written, QMV_E_ARG is recorded in the status word
+ * (qmv_check_device) and what the call gives for that sequence is not specified.  Page ids past
+ * a sequence's tokens are not looked at. */
+typedef struct qmv_kv_batch {
+  const int32_t *page_table;
+  int64_t table_stride;
+  int table_pages;
+  const int32_t *kv_len;
+  const int32_t *starts;
+  int n_seq;
+  int64_t rows;
+  int max_rows;
+  int max_len;
+} qmv_kv_batch;
+
+/* Writes the call's rows into the cache.  k and v: device, row r of head h at element
+ * r * stride + h * head_dim (k_stride, v_stride in elements, at least kv_heads * head_dim), x_dtype
+ * QMV_X_F32 or QMV_X_BF16, each row 16-byte aligned.  For each page that receives rows, each head,
+ * and K and V apart (float32 operations rounded to nearest):
+ *   want = max |x| over the call's rows in the page * RN(1 / 127)   (0 where that maximum is below 1e-30)
+ *   had  = the page's scale if it holds tokens from before the call's rows, else 0
+ *   d    = max(want, had), stored;  where d > had, the levels of those earlier tokens become
+ *          trunc(level * (had / d) + copysign(0.5, level))
+ *   level = trunc(x * (1 / d) + copysign(0.5, x)) clamped to +-127, 0 where d is 0.
+ * A page is written by one sequence only: sequences may share pages that no row of the call falls
+ * into.  Each raise of a page's scale moves its earlier levels by at most half a step of the new
+ * scale.  x is meant to be finite.  Places of the page after the last row are left as they are.
+ * Returns QMV_OK, QMV_E_FORMAT (x_dtype), QMV_E_ARG (null pointer, negative count), QMV_E_SHAPE (the cache's
+ * or the rows' numbers, strides), QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_kv_write(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int x_dtype, const void *k,
+                 int64_t k_stride, const void *v, int64_t v_stride, cudaStream_t stream);
+
+/* Reads the call's rows back: k and v (device, rows x kv_heads x head_dim, contiguous, 16-byte
+ * aligned, out_dtype QMV_X_F32 or QMV_X_BF16) receive level * scale, one float32 product (rounded once
+ * more to bfloat16).  Returns as qmv_kv_write. */
+int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dtype, void *k, void *v,
+                cudaStream_t stream);
+
+/* Softmax attention of the call's rows over the cache.  q: row r of head h at element
+ * r * q_stride + h * head_dim; heads a multiple of kv_heads, head h reads key/value head
+ * h / (heads / kv_heads); q and out share x_dtype (QMV_X_F32 or QMV_X_BF16); out likewise with
+ * out_stride, rows 16-byte aligned; out must not overlap q.
+ *   z_j = scale * q . K_j,  p = softmax of z over the keys that the mask leaves,  out = sum_j p_j V_j
+ * with K_j = level * scale of the cache.  The row at position p sees the keys j <= p (causal != 0)
+ * or every key of its sequence (causal = 0), and with window > 0 only those with
+ * j > p - window.  A row that sees no key gives zeros.  What the pages hold beyond a
+ * sequence's tokens, and the pages that a window hides whole, do not enter.
+ * Scores, softmax and sums are float32.  The levels enter the tensor core as exact halves; q
+ * as halves after a power-of-two scale of its row (exact for bfloat16, a pair hi + lo of 22 bits for
+ * float32); the weights p rounded to half (a pair hi + lo for float32), scaled so that the
+ * largest p * V scale is near 1.  Results do not depend on timing.
+ * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream,
+ * allocated on the stream's first such call and kept; while a stream without one is being
+ * captured, the call does not split.
+ * Returns QMV_OK, QMV_E_FORMAT (x_dtype), QMV_E_ARG (null pointer, negative count, window < 0, scale not
+ * finite), QMV_E_SHAPE (the cache's or rows' numbers, heads, strides), QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_attend(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int heads, int x_dtype, const void *q,
+               int64_t q_stride, float scale, int causal, int window, void *out, int64_t out_stride,
+               cudaStream_t stream);
+
+#define QMV_MAX_TOP 32
+#define QMV_MAX_GIVEN 64
+
+/* Log probabilities from rows of logits (float32, as the products leave them).
+ *   logits  : device, row r at element r * stride (stride >= vocab), 4-byte aligned (16-byte aligned
+ *             rows are read faster).
+ *   given   : device, rows x n_given int64 token ids, or NULL with n_given 0.  given_logprob: device,
+ *             rows x n_given float32: logit - log sum_j e^logit_j; NaN for an id outside 0..vocab-1.
+ *   entropy : device, rows float32, or NULL: -sum_j p_j log p_j.
+ *   top_ids, top_logprob : device, rows x n_top int32 / float32: the n_top largest logits in
+ *             descending order, equal ones by the lower id first (+0 and -0 are equal), or NULL with n_top 0.
+ * A logit of -infinity is a masked id: probability 0, nothing to the entropy.  In a row where every logit
+ * is -infinity the log probabilities are -infinity and the entropy 0.  A row that holds NaN or
+ * +infinity gives NaN log probabilities and entropy (its top_ids by value, NaN taken as the largest).
+ * Sums are float32, the maximum subtracted; results do not depend on timing.
+ * n_top <= QMV_MAX_TOP, n_top <= vocab, n_given <= QMV_MAX_GIVEN; vocab below 2^31 - 4096.
+ * Uses a workspace of the calling stream as qmv_attend does.
+ * Returns QMV_OK, QMV_E_ARG (null pointer, negative count), QMV_E_SHAPE, QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t stride, const int64_t *given,
+                 int n_given, float *given_logprob, float *entropy, int n_top, int32_t *top_ids,
+                 float *top_logprob, cudaStream_t stream);
+
 /* Synchronizes the current device, then returns and clears the status word that the
  * kernels set when a bounded wait runs out (QMV_E_TIMEOUT); QMV_OK when none was set,
  * QMV_E_CUDA when the device reports a CUDA error.  When the word was set it also zeroes the

@@ -1,0 +1,169 @@
+"""qmv_attend against softmax attention in 64 bits over the cache's own values."""
+import numpy as np
+import pytest
+
+import ops_ref
+from helpers import dev_x
+from test_gpu_kv import batch_of, ints, make
+
+pytestmark = pytest.mark.gpu
+F = np.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def qmv():
+    import torch
+    from block_quantized_weight_q4_gb300.build import build
+    import block_quantized_weight_q4_gb300 as q
+    assert torch.cuda.is_available()
+    build()
+    q.load_library()
+    yield q
+    assert q.last_error() == 0
+
+
+def filled(qmv, lens, heads, dim, page, seed):
+    """A cache whose pages hold random levels and scales over a wide range; what lies past a
+    sequence's tokens is loud, and unused pages' scales are NaN."""
+    import torch
+    cache, twin, table, td = make(qmv, lens, heads, dim, page, seed)
+    rng = np.random.default_rng(seed)
+    for i in range(2):
+        twin.lev[i][:] = rng.integers(-127, 128, twin.lev[i].shape, dtype=np.int8)
+        twin.scale[i][:] = (2.0 ** rng.uniform(-9, -5, twin.scale[i].shape)).astype(F)
+    used = {int(p) for s, n in enumerate(lens) for p in table[s, :-(-n // page)]}
+    for i in range(2):
+        twin.scale[i][[p for p in range(cache.n_pages) if p not in used]] = np.nan
+    for t, a in ((cache.k, twin.lev[0]), (cache.v, twin.lev[1]), (cache.k_scale, twin.scale[0]), (cache.v_scale, twin.scale[1])):
+        t.copy_(torch.from_numpy(a))
+    return cache, twin, table, td
+
+
+def queries(rng, rows, heads, dim, bf16, amp=1.0):
+    x = (amp * rng.standard_normal((rows, heads, dim))).astype(F)
+    if not bf16:
+        return x, dev_x(x)
+    code = (x.view(np.uint32) >> 16).astype(np.uint16)
+    return ops_ref.f32_of_bf16(code), dev_x(code)
+
+
+def check(twin, table, lens, counts, qf, got, scale, causal, window, bf16, what=""):
+    got = got.float().cpu().numpy().astype(np.float64)
+    row = 0
+    for s, n in enumerate(counts):
+        if n == 0:
+            continue
+        k, v = twin.values(0, table[s], lens[s]), twin.values(1, table[s], lens[s])
+        ref, mag, amp = ops_ref.attend(qf[row:row + n], k, v, lens[s] - n, scale, causal, window)
+        bound = ops_ref.attend_bound(mag, amp, ref, k.shape[2], lens[s], bf16)
+        err = np.abs(got[row:row + n] - ref)
+        bad = ~(err <= bound)
+        assert not bad.any(), (what, s, lens[s], n, int(bad.sum()), np.argwhere(bad)[0], float((err / bound).max()))
+        row += n
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("heads,kvh,dim,page", [(32, 8, 128, 64), (4, 4, 64, 16), (14, 2, 64, 32), (8, 1, 128, 128),
+                                                (2, 2, 256, 64), (16, 1, 128, 16), (24, 1, 64, 64), (12, 2, 256, 32)])
+def test_single_tokens(qmv, heads, kvh, dim, page, bf16):
+    """Lengths around pages and tiles, from one key on."""
+    rng = np.random.default_rng(dim + heads)
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 700, 1531]
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=page)
+    qf, qd = queries(rng, len(lens), heads, dim, bf16)
+    b = qmv.KvBatch(td, ints(lens), max_len=max(lens))
+    got = qmv.attend(cache, b, qd)
+    check(twin, table, lens, [1] * len(lens), qf, got, dim ** -0.5, True, 0, bf16)
+    again = qmv.attend(cache, b, qd)
+    assert bool((got == again).all())  # no order of arrival in the result
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 5), (True, 100), (False, 0), (False, 33)])
+@pytest.mark.parametrize("heads,kvh,dim,page", [(8, 2, 128, 64), (6, 6, 64, 16), (4, 1, 256, 32)])
+def test_runs_of_tokens(qmv, heads, kvh, dim, page, causal, window, bf16):
+    """Short and long runs of rows over cached tokens, ragged, one sequence without rows."""
+    rng = np.random.default_rng(heads + window)
+    lens = [5, 200, 64, 0, 333, 130]
+    counts = [5, 3, 64, 0, 150, 129]
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=window)
+    qf, qd = queries(rng, sum(counts), heads, dim, bf16)
+    got = qmv.attend(cache, batch_of(qmv, td, lens, counts), qd, causal=causal, window=window)
+    check(twin, table, lens, counts, qf, got, dim ** -0.5, causal, window, bf16)
+
+
+@pytest.mark.parametrize("n,length", [(1, 20011), (4, 9000), (700, 2500), (257, 257), (128, 128), (1024, 1100)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_long(qmv, n, length, dim):
+    rng = np.random.default_rng(n)
+    cache, twin, table, td = filled(qmv, [length], 2, dim, 64, seed=n)
+    qf, qd = queries(rng, n, 8, dim, True)
+    got = qmv.attend(cache, batch_of(qmv, td, [length], [n]), qd)
+    check(twin, table, [length], [n], qf, got, dim ** -0.5, True, 0, True)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_strides_scale_and_streams(qmv, bf16):
+    """q a slice of a wider row, out a slice too, a scale of its own, another stream."""
+    import torch
+    rng = np.random.default_rng(8)
+    lens, counts, dim = [100, 41], [33, 1], 64
+    cache, twin, table, td = filled(qmv, lens, 2, dim, 32, seed=4)
+    qf, qd = queries(rng, 34, 12, dim, bf16)
+    out = torch.full((34, 10, dim), 7.0, device="cuda", dtype=qd.dtype)
+    s = torch.cuda.Stream()
+    b = batch_of(qmv, td, lens, counts)
+    s.wait_stream(torch.cuda.current_stream())
+    qmv.attend(cache, b, qd[:, 4:8], out=out[:, 2:6], scale=0.3, stream=s)
+    s.synchronize()
+    check(twin, table, lens, counts, qf[:, 4:8], out[:, 2:6], 0.3, True, 0, bf16)
+    assert bool((out[:, :2] == 7).all()) and bool((out[:, 6:] == 7).all())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("n", [1, 40])
+def test_extreme_scales(qmv, bf16, n):
+    """Pages whose values differ by powers of ten, all-zero pages, loud queries and one dominant key."""
+    import torch
+    rng = np.random.default_rng(2)
+    lens = [310]
+    cache, twin, table, td = filled(qmv, lens, 1, 128, 16, seed=6)
+    used = table[0, :20]
+    twin.scale[1][used[:, None], 0] = (10.0 ** rng.uniform(-12, 3, (20, 1))).astype(F)
+    twin.scale[0][used[3]] = 0
+    twin.scale[1][used[5]] = 0
+    twin.lev[1][used[5]] = 0
+    cache.k_scale.copy_(torch.from_numpy(twin.scale[0]))
+    cache.v_scale.copy_(torch.from_numpy(twin.scale[1]))
+    cache.v.copy_(torch.from_numpy(twin.lev[1]))
+    for amp in (1e-6, 1.0, 20.0):
+        qf, qd = queries(rng, n, 4, 128, bf16, amp)
+        got = qmv.attend(cache, batch_of(qmv, td, lens, [n]), qd)
+        check(twin, table, lens, [n], qf, got, 128 ** -0.5, True, 0, bf16, amp)
+    twin.scale[1][used[:, None], 0] = 0
+    twin.lev[1][used] = 0
+    cache.v_scale.copy_(torch.from_numpy(twin.scale[1]))
+    cache.v.copy_(torch.from_numpy(twin.lev[1]))
+    assert not qmv.attend(cache, batch_of(qmv, td, lens, [n]), qd).any()
+
+
+def test_in_a_graph(qmv):
+    """Captured on a stream that the library has not seen, replayed after the lengths moved on."""
+    import torch
+    rng = np.random.default_rng(5)
+    lens = [900, 77]
+    cache, twin, table, td = filled(qmv, lens, 2, 128, 64, seed=8)
+    qf, qd = queries(rng, 2, 8, 128, True)
+    now = ints([850, 50])
+    b = qmv.KvBatch(td, now, max_len=1000)
+    out = torch.empty_like(qd)
+    qmv.attend(cache, b, qd, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qmv.attend(cache, b, qd, out=out)
+    for ls in ([850, 50], lens):
+        now.copy_(ints(ls))
+        g.replay()
+        torch.cuda.synchronize()
+        check(twin, table, ls, [1, 1], qf, out, 128 ** -0.5, True, 0, True)

@@ -38,11 +38,17 @@ constexpr size_t kPrefillWorkspaceBytes = (size_t)32 << 20;
 // bf16 per problem: up to 65,536 columns over the problems of one launch)
 constexpr size_t kSplitBytes = (size_t)2 << 20;
 
+// a stream's workspace of the operators between the products (attention, log probabilities):
+// counters for up to 1024 CTAs, then the parts (the launch keeps its grid to what fits)
+constexpr int kServeCounters = 1024;
+constexpr size_t kServeWorkspaceBytes = (size_t)8 << 20;
+
 namespace {
 std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_pws;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_xws;
+std::map<std::pair<int, cudaStream_t>, Workspace> g_sws;
 
 cudaError_t cached_workspace(std::map<std::pair<int, cudaStream_t>, Workspace>& cache, const DeviceInfo& dev,
                              cudaStream_t stream, size_t bytes, int counters, Workspace* ws) {
@@ -81,6 +87,10 @@ cudaError_t stream_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspa
 
 cudaError_t stream_prefill_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws) {
   return cached_workspace(g_pws, dev, stream, kPrefillWorkspaceBytes, kPrefillCounters, ws);
+}
+
+cudaError_t stream_serve_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws) {
+  return cached_workspace(g_sws, dev, stream, kServeWorkspaceBytes, kServeCounters, ws);
 }
 
 namespace {
@@ -290,7 +300,7 @@ cudaError_t reset_workspaces() {
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  for (auto* cache : {&g_ws, &g_pws}) {
+  for (auto* cache : {&g_ws, &g_pws, &g_sws}) {
     for (auto& kv : *cache) {
       if (kv.first.first != dev) continue;
       err = cudaMemset(kv.second.counters, 0, workspace_counter_bytes(kv.second.max_counters));
@@ -322,7 +332,7 @@ cudaError_t prepare_stream_workspaces(const DeviceInfo& dev, cudaStream_t stream
 cudaError_t release_stream_workspaces(int device, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
   cudaError_t first = cudaSuccess;
-  for (auto* cache : {&g_ws, &g_pws, &g_xws}) {
+  for (auto* cache : {&g_ws, &g_pws, &g_xws, &g_sws}) {
     auto it = cache->find(std::make_pair(device, stream));
     if (it == cache->end()) continue;
     const cudaError_t err = cudaFree(it->second.counters);  // the allocation's base

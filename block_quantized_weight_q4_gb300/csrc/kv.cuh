@@ -30,7 +30,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvRef& c, int s) {
   }
   if (q.len < 0 || q.len > c.max_len || q.len > (long long)c.table_pages * c.page_tokens || q.n < 0 || q.n > c.max_rows ||
       q.n > q.len) {
-    if (threadIdx.x == 0) record_status(c.status, QMV_E_ARG);
+    record_status(c.status, QMV_E_ARG);
     q.n = 0;
     q.len = 0;
     q.row0 = 0;

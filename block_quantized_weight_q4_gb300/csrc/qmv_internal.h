@@ -45,7 +45,9 @@ void workspace_carve(void* base, size_t bytes, int n, Workspace* ws);
 cudaError_t stream_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);
 // The same for the prefill kernel's split tiles (a separate, larger workspace per stream).
 cudaError_t stream_prefill_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);
-// Zero the counters of every workspace (decode and prefill) of the current device (after a kernel gave up on a
+// The same for the operators between the products (attention, log probabilities).
+cudaError_t stream_serve_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);
+// Zero the counters of every workspace of the current device (after a kernel gave up on a
 // bounded wait, a counter may have been left part-way); synchronous.
 cudaError_t reset_workspaces();
 

@@ -613,8 +613,7 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
  * sequence's tokens, and the pages that a window hides whole, do not enter.
  * Scores, softmax and sums are float32.  The levels enter the tensor core as exact halves; q
  * as halves after a power-of-two scale of its row (exact for bfloat16, a pair hi + lo of 22 bits for
- * float32); the weights p rounded to half (a pair hi + lo for float32), scaled so that the
- * largest p * V scale is near 1.  Results do not depend on timing.
+ * float32); the weights p times the V scale as two bfloat16 parts (16 bits; three, 24 bits, for float32).  Results do not depend on timing.
  * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream,
  * allocated on the stream's first such call and kept; while a stream without one is being
  * captured, the call does not split.

@@ -147,8 +147,10 @@ def test_extreme_scales(qmv, bf16, n):
     assert not qmv.attend(cache, batch_of(qmv, td, lens, [n]), qd).any()
 
 
-def test_in_a_graph(qmv):
-    """Captured on a stream that the library has not seen, replayed after the lengths moved on."""
+@pytest.mark.parametrize("warm", [False, True])
+def test_in_a_graph(qmv, warm):
+    """Captured on a stream that the library has not seen, or has (with its workspace), replayed after
+    the lengths moved on."""
     import torch
     rng = np.random.default_rng(5)
     lens = [900, 77]
@@ -157,10 +159,13 @@ def test_in_a_graph(qmv):
     now = ints([850, 50])
     b = qmv.KvBatch(td, now, max_len=1000)
     out = torch.empty_like(qd)
-    qmv.attend(cache, b, qd, out=out)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if warm:
+        qmv.attend(cache, b, qd, out=out, stream=side)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g):
+    with torch.cuda.graph(g, stream=side):
         qmv.attend(cache, b, qd, out=out)
     for ls in ([850, 50], lens):
         now.copy_(ints(ls))

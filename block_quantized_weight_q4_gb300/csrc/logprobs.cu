@@ -1,4 +1,12 @@
 // logprobs.cu -- log probabilities of given tokens, entropy and the top alternatives of rows of logits.
+//
+//   lp_j = x_j - m - log Z,  Z = sum_j e^(x_j - m),  H = log Z - (1 / Z) sum_j e^(x_j - m) (x_j - m).
+//
+// Bound: the logits' bytes, read once.  Each thread keeps a running maximum m, Z and the second sum, moved
+// when a batch of 16 values raises m; each warp keeps the largest n_top keys (value, id) of what it has
+// seen, sorted over its lanes, and a batch touches the list only if its maximum reaches the
+// smallest kept value of any warp of the CTA.  A few rows are cut into parts over many CTAs; the last
+// part of a row to finish joins them in their order.
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
 
@@ -6,94 +14,279 @@ namespace qmv {
 
 namespace {
 
-constexpr int kLpThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 16;  // values a thread takes at a time, as four 16-byte loads
+using Key = unsigned long long;
 
 // A logit and its id as one key that orders as the result does: larger logits first, equal ones
 // by the lower id.  The float's bits are mapped to an unsigned order; -0 counts as +0, NaN as the largest.
-__device__ __forceinline__ unsigned long long lp_key(float x, unsigned id) {
+__device__ __forceinline__ uint32_t ordered(float x) {
   uint32_t b = __float_as_uint(x + 0.0f);
   if ((b & 0x7fffffffu) > 0x7f800000u) b = 0x7fffffffu;
-  b = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((unsigned long long)b << 32) | (0xffffffffu - id);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ Key key_of(float x, uint32_t id) { return ((Key)ordered(x) << 32) | (0xffffffffu - id); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float exp_of(float d) {  // e^d for d <= 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.4426950408889634f));
+  return y;
 }
 
-__device__ __forceinline__ float lp_block_sum(float v, float* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int w = 0; w < kLpThreads / 32; ++w) v += part[w];
-  return v;
+// Running statistics of a row's values: the maximum, sum e^(x - m), sum e^(x - m) (x - m).
+struct Stats {
+  float m, z, zx;
+  __device__ __forceinline__ void move_to(float to) {  // to >= m
+    const float d = m == -INFINITY ? -200.f : fmaxf(m - to, -200.f);
+    const float f = exp_of(d);
+    zx = (zx + z * d) * f;
+    z *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void join(Stats o) {
+    const float to = fmaxf(m, o.m);
+    if (to == -INFINITY) return;
+    move_to(to);
+    o.move_to(to);
+    z += o.z;
+    zx += o.zx;
+  }
+};
+
+// The warp's list: lane i holds the i-th largest key (n_top <= 32 of them count).
+__device__ __forceinline__ void insert(Key& mine, Key k, int lane) {
+  const int at = __popc(__ballot_sync(0xffffffffu, mine > k));
+  const Key up = __shfl_up_sync(0xffffffffu, mine, 1);
+  if (lane == at) {
+    mine = k;
+  } else if (lane > at) {
+    mine = up;
+  }
 }
 
-// One CTA per row: the maximum, then the sums, then one pass over the row for each alternative.
-__global__ void __launch_bounds__(kLpThreads) logprobs_plain_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ float part[kLpThreads / 32];
-  __shared__ unsigned long long keys[kLpThreads / 32];
-  const long long row = blockIdx.x;
+struct Part {  // of one row, in the workspace
+  Stats s;
+  int bad;
+  Key keys[QMV_MAX_TOP];
+};
+
+struct PartArea {
+  unsigned* counters;  // one per row, zero between launches
+  Part* parts;
+};
+
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a, int n_parts,
+                                                            const PartArea area) {
+  __shared__ Stats warp_stats[kWarps];
+  __shared__ Key warp_keys[kWarps][QMV_MAX_TOP];
+  __shared__ uint32_t floor_bits;  // no value below this can be among the largest n_top
+  __shared__ int last_flag;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const long long row = blockIdx.x / n_parts;
+  const int part = blockIdx.x % n_parts;
   const float* x = a.logits + row * a.stride;
   const int n = (int)a.vocab;
-  float m = -INFINITY;
+  const int k = a.n_top;
+  if (tid == 0) floor_bits = k > 0 ? 0u : 0xffffffffu;
+  __syncthreads();
+
+  Stats st{-INFINITY, 0.f, 0.f};
+  Key mine = 0;
   bool bad = false;
-  for (int j = threadIdx.x; j < n; j += kLpThreads) {
-    const float v = x[j];
-    bad |= isnan(v) || v == INFINITY;
-    m = fmaxf(m, v);
-  }
+
+  // 16 values a lane: v[e] is logit first + stride-1 runs of four; absent ones are -inf with id ~0
+  auto take = [&](const float (&v)[kBatch], const uint32_t (&id)[kBatch / 4], int live) {
+    float top = v[0];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-  bad = __syncthreads_or(bad);
-  for (int w = 0; w < kLpThreads / 32; ++w) m = fmaxf(m, part[w]);
-  const bool none = m == -INFINITY && !bad;
-  float z = 0.f, zx = 0.f;
-  if (!none)
-    for (int j = threadIdx.x; j < n; j += kLpThreads) {
-      const float d = x[j] - m;
-      const float e = expf(d);
-      z += e;
-      if (e > 0.f) zx = fmaf(e, d, zx);
+    for (int e = 1; e < kBatch; ++e) top = max_nan(top, v[e]);
+    const uint32_t fb = *reinterpret_cast<volatile uint32_t*>(&floor_bits);
+    const float floor = k > 0 ? (fb == 0u ? -INFINITY : unordered(fb)) : INFINITY;
+    if (__any_sync(0xffffffffu, !(top < floor))) {
+      bad |= !(top < INFINITY);
+      if (k > 0) {
+        Key least = __shfl_sync(0xffffffffu, mine, k - 1);
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const Key ke = key_of(v[e], e < live ? id[e >> 2] + (e & 3) : 0xffffffffu);
+          uint32_t who = __ballot_sync(0xffffffffu, ke > least && !(v[e] < floor));
+          while (who != 0u) {
+            const int src = __ffs(who) - 1;
+            who &= who - 1;
+            const Key c = __shfl_sync(0xffffffffu, ke, src);
+            if (c > least) {
+              insert(mine, c, lane);
+              least = __shfl_sync(0xffffffffu, mine, k - 1);
+            }
+          }
+        }
+        if (lane == 0) atomicMax(&floor_bits, (uint32_t)(least >> 32));
+      }
     }
-  z = lp_block_sum(z, part);
-  zx = lp_block_sum(zx, part);
-  const float lz = bad ? NAN : none ? INFINITY : logf(z);
-  const float lse = none ? INFINITY : m + lz;
-  if (threadIdx.x == 0 && a.entropy != nullptr) a.entropy[row] = bad ? NAN : none ? 0.f : lz - zx / z;
-  for (int g = threadIdx.x; g < a.n_given; g += kLpThreads) {
-    const long long id = a.given[row * a.n_given + g];
-    a.given_logprob[row * a.n_given + g] = id >= 0 && id < a.vocab ? x[id] - lse : NAN;
+    if (top > st.m) st.move_to(top);
+    const float ref = st.m == -INFINITY ? 0.f : st.m;
+    // four chains of sums, joined in a fixed order
+    float z[4] = {0.f, 0.f, 0.f, 0.f}, zx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const float d = fmaxf(v[e] - ref, -200.f);  // e^-200 is 0 in float32
+      const float y = exp_of(d);
+      z[e & 3] += y;
+      zx[e & 3] = fmaf(y, d, zx[e & 3]);
+    }
+    st.z += (z[0] + z[1]) + (z[2] + z[3]);
+    st.zx += (zx[0] + zx[1]) + (zx[2] + zx[3]);
+  };
+
+  // the row from its first 16-byte boundary in batches of 4 x 128 values a warp, cut into n_parts; the up to
+  // three values before it and after the last whole four belong to part 0
+  const int head = min((int)((4 - ((reinterpret_cast<uintptr_t>(x) >> 2) & 3)) & 3), n);
+  const int quads = (n - head) / 4;
+  const float4* xv = reinterpret_cast<const float4*>(x + head);
+  const int q0 = (int)((long long)quads * part / n_parts), q1 = (int)((long long)quads * (part + 1) / n_parts);
+  for (int q = q0 + wid * 128; q < q1; q += kWarps * 128) {
+    float v[kBatch];
+    uint32_t id[kBatch / 4];
+    int live = 0;
+    float4 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int qi = q + 32 * i + lane;
+      f[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      id[i] = (uint32_t)(head + 4 * qi);
+      if (qi < q1) {
+        f[i] = __ldcs(xv + qi);
+        live = 4 * i + 4;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * i] = f[i].x, v[4 * i + 1] = f[i].y, v[4 * i + 2] = f[i].z, v[4 * i + 3] = f[i].w;
+    take(v, id, live);
   }
-  unsigned long long last = ~0ull;
-  for (int t = 0; t < a.n_top; ++t) {
-    unsigned long long best = 0;
-    for (int j = threadIdx.x; j < n; j += kLpThreads) {
-      const unsigned long long k = lp_key(x[j], (unsigned)j);
-      if (k < last && k > best) best = k;
+  if (part == 0 && wid == 0) {
+    const int tail = n - head - 4 * quads;
+    if (head + tail > 0) {
+      float v[kBatch];
+      uint32_t id[kBatch / 4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) v[e] = -INFINITY;
+      const int i = lane < head ? lane : lane - head + n - tail;
+      if (lane < head + tail) {
+        v[0] = x[i];
+        id[0] = (uint32_t)i;
+      }
+      take(v, id, lane < head + tail ? 1 : 0);
     }
+  }
+
+  // the CTA: lanes, then warps, in a fixed order
+  auto join_cta = [&]() {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
-      best = k > best ? k : best;
+      Stats s;
+      s.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+      s.z = __shfl_xor_sync(0xffffffffu, st.z, o);
+      s.zx = __shfl_xor_sync(0xffffffffu, st.zx, o);
+      st.join(s);
+    }
+    if (lane == 0) warp_stats[wid] = st;
+    if (lane < k) warp_keys[wid][lane] = mine;
+    bad = __syncthreads_or(bad);
+    if (wid == 0) {
+      for (int w = 1; w < kWarps; ++w) {
+        st.join(warp_stats[w]);
+        for (int i = 0; i < k; ++i) {
+          const Key c = warp_keys[w][i];
+          if (c <= __shfl_sync(0xffffffffu, mine, k - 1)) break;
+          insert(mine, c, lane);
+        }
+      }
+    }
+  };
+  join_cta();
+
+  if (n_parts > 1) {
+    Part* parts = area.parts + row * n_parts;
+    if (wid == 0) {
+      if (lane == 0) {
+        __stcg(&parts[part].s.m, st.m);
+        __stcg(&parts[part].s.z, st.z);
+        __stcg(&parts[part].s.zx, st.zx);
+        __stcg(&parts[part].bad, (int)bad);
+      }
+      if (lane < k) __stcg(&parts[part].keys[lane], mine);
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) {
+        const unsigned seen = atomicAdd(area.counters + row, 1u);
+        last_flag = seen == (unsigned)(n_parts - 1);
+        if (last_flag) area.counters[row] = 0;
+      }
     }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) keys[threadIdx.x >> 5] = best;
-    __syncthreads();
-    for (int w = 0; w < kLpThreads / 32; ++w) best = keys[w] > best ? keys[w] : best;
-    last = best;
-    if (threadIdx.x == 0) {
-      const unsigned id = 0xffffffffu - (unsigned)best;
-      a.top_ids[row * a.n_top + t] = (int)id;
-      a.top_logprob[row * a.n_top + t] = x[id] - lse;
+    if (!last_flag) return;
+    __threadfence();
+    st = Stats{-INFINITY, 0.f, 0.f};
+    mine = 0;
+    bad = false;
+    for (int p = wid; p < n_parts; p += kWarps) {
+      // lane 0 of each warp joins the statistics, all lanes the keys
+      const Key c = lane < k ? __ldcg(&parts[p].keys[lane]) : 0;
+      bad |= __ldcg(&parts[p].bad) != 0;
+      if (lane == 0) st.join(Stats{__ldcg(&parts[p].s.m), __ldcg(&parts[p].s.z), __ldcg(&parts[p].s.zx)});
+      for (int i = 0; i < k; ++i) {
+        const Key ci = __shfl_sync(0xffffffffu, c, i);
+        if (ci <= __shfl_sync(0xffffffffu, mine, k - 1)) break;
+        insert(mine, ci, lane);
+      }
+    }
+    join_cta();
+  }
+
+  if (wid == 0) {
+    const bool none = st.m == -INFINITY && !bad;
+    const float lz = bad ? NAN : logf(st.z);
+    const float lse = none ? INFINITY : st.m + lz;
+    if (lane == 0 && a.entropy != nullptr) a.entropy[row] = none ? 0.f : lz - st.zx / st.z;
+    for (int i = lane; i < a.n_given; i += 32) {
+      const long long id = a.given[row * a.n_given + i];
+      a.given_logprob[row * a.n_given + i] = id >= 0 && id < a.vocab ? x[id] - lse : NAN;
+    }
+    if (lane < k) {
+      const uint32_t id = 0xffffffffu - (uint32_t)mine;
+      a.top_ids[row * k + lane] = (int)id;
+      a.top_logprob[row * k + lane] = unordered((uint32_t)(mine >> 32)) - lse;
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, const DeviceInfo&, cudaStream_t stream) {
-  logprobs_plain_kernel<<<(unsigned)rows, kLpThreads, 0, stream>>>(a);
+cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, const DeviceInfo& dev, cudaStream_t stream) {
+  PartArea area{nullptr, nullptr};
+  long long parts = 1;
+  // rows cut so that about six CTAs a SM are there, of at least two batches a thread
+  const long long want = (6LL * dev.sm_count + rows - 1) / rows;
+  const long long most = (a.vocab + 8191) / 8192;
+  Workspace ws;
+  if (want > 1 && most > 1 && stream_serve_workspace(dev, stream, &ws) == cudaSuccess) {
+    parts = want < most ? want : most;
+    const long long fit = (long long)(ws.max_partial_floats * sizeof(float) / sizeof(Part)) / rows;
+    if (parts > fit) parts = fit;
+    if (rows > ws.max_counters || parts < 1) parts = 1;
+    area.counters = ws.counters;
+    area.parts = reinterpret_cast<Part*>(ws.partials);
+  }
+  if (rows * parts > INT32_MAX) return cudaErrorInvalidValue;
+  logprobs_kernel<<<(unsigned)(rows * parts), kThreads, 0, stream>>>(a, (int)parts, area);
   return cudaGetLastError();
 }
 

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int j0 = ch * kChunk + 16 * u;
-        ids[u] = ch < ch1 && j0 < sq.len ? kv_page(c, s, j0 / c.page_tokens) : -1;
+        ids[u] = ch < ch1 && j0 < sq.len ? kv_page(c, s, (j0 >> c.page_shift)) : -1;
       }
     };
     auto issue = [&](int ch, int st) {
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
           const int id = ids[u];
           if (id >= 0) {
             const long long at = (long long)id * c.kv_heads + kvh;
-            const long long off = at * head_stride + (long long)(j0 % c.page_tokens) * D;
+            const long long off = at * head_stride + (long long)((j0 & (c.page_tokens - 1))) * D;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
               const int p = i * 32 + lane;
@@ -624,6 +624,7 @@ cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& de
 
 cudaError_t launch_attend(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev,
                           cudaStream_t stream) {
+  if (attend_prompt_supported(c, a, x_bf16, dev)) return launch_attend_prompt(c, a, dev, stream);
   Workspace w;
   const Workspace* ws = stream_serve_workspace(dev, stream, &w) == cudaSuccess ? &w : nullptr;
   switch (c.head_dim) {

@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
   const bool is_v = blockIdx.z & 1;
   const KvSeq q = kv_seq(c, s);
   const int first = q.len - q.n;
-  const int pi = first / c.page_tokens + blockIdx.x;
+  const int pi = (first >> c.page_shift) + blockIdx.x;
   if (pi * c.page_tokens >= q.len || q.n == 0) return;
   const int id = kv_page(c, s, pi);
   if (id < 0) return;
@@ -105,12 +105,12 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
     const int r = p / row_pieces, in_row = p % row_pieces;
     const int head = in_row / ppr, piece = in_row % ppr;
     const int pos = q.len - q.n + r0 + r;
-    const int id = kv_page(c, s, pos / c.page_tokens);
+    const int id = kv_page(c, s, (pos >> c.page_shift));
     if (id < 0) continue;
     const long long at = (long long)id * c.kv_heads + head;
     const float d = __ldg(scale + at);
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-        lev + (at * c.page_tokens + pos % c.page_tokens) * c.head_dim + 16 * piece));
+        lev + (at * c.page_tokens + (pos & (c.page_tokens - 1))) * c.head_dim + 16 * piece));
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     float f[16];
 #pragma unroll

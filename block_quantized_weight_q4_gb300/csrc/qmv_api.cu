@@ -98,6 +98,7 @@ int make_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, KvRef* c) {
   c->kv_heads = cache->kv_heads;
   c->head_dim = cache->head_dim;
   c->page_tokens = cache->page_tokens;
+  c->page_shift = cache->page_tokens == 16 ? 4 : cache->page_tokens == 32 ? 5 : cache->page_tokens == 64 ? 6 : 7;
   c->n_seq = batch->n_seq;
   c->max_rows = batch->starts == nullptr && batch->max_rows > 1 ? 1 : batch->max_rows;
   c->max_len = batch->max_len;

@@ -214,7 +214,8 @@ struct KvRef {
   long long rows;
   int kv_heads;
   int head_dim;
-  int page_tokens;
+  int page_tokens;  // 1 << page_shift
+  int page_shift;
   int n_seq;
   int max_rows;
   int max_len;
@@ -236,6 +237,9 @@ struct AttendArgs {
 };
 cudaError_t launch_attend(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev,
                           cudaStream_t stream);
+// Many rows a sequence, on the tensor-memory kernel.
+bool attend_prompt_supported(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev);
+cudaError_t launch_attend_prompt(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
 struct LogprobArgs {
   const float* logits;

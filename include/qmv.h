@@ -613,7 +613,11 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
  * sequence's tokens, and the pages that a window hides whole, do not enter.
  * Scores, softmax and sums are float32.  The levels enter the tensor core as exact halves; q
  * as halves after a power-of-two scale of its row (exact for bfloat16, a pair hi + lo of 22 bits for
- * float32); the weights p times the V scale as two bfloat16 parts (16 bits; three, 24 bits, for float32).  Results do not depend on timing.
+ * float32); the weights p times the V scale as two bfloat16 parts (16 bits; three, 24 bits, for float32).
+ * Calls with many bfloat16 rows (prompts; heads of 64 or 128) round the weights times the V
+ * scale once to half: 2^-11 relative down to 2^-21 of the row's largest one, below that multiples
+ * of at most 2^-32 of it (a key whose weight times V scale is that far below the row's largest counts only
+ * to that resolution).  Scales are not negative.  Results do not depend on timing.
  * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream,
  * allocated on the stream's first such call and kept; while a stream without one is being
  * captured, the call does not split.

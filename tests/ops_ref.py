@@ -97,6 +97,26 @@ def attend_bound(mag, amp, out, dim, length, bf16):
     return rel[:, :, None] * mag + (2.0 ** -8 * np.abs(out) if bf16 else 0.0) + 1e-30
 
 
+def half_weights(q, k, v_lev, v_scale, first, scale, causal=True, window=0):
+    """What the prompt kernel's rounding to half adds to attend_bound: weights times V scale below 2^-21 of
+    the row's largest are multiples of 2^-32 of it, so each key may be off by that times its level.
+    v_lev, v_scale: levels (length, kv_heads, dim) and scales (length, kv_heads)."""
+    n, heads, dim = q.shape
+    length, kvh = k.shape[0], k.shape[1]
+    pos, j = first + np.arange(n)[:, None], np.arange(length)[None, :]
+    seen = np.ones((n, length), bool) if not causal else j <= pos
+    if window:
+        seen = seen & (j > pos - window)
+    add = np.zeros((n, heads, dim))
+    for h in range(heads):
+        g = h // (heads // kvh)
+        z = np.where(seen, scale * (q[:, h].astype(np.float64) @ k[:, g].astype(np.float64).T), -np.inf)
+        p = np.exp(z - z.max(axis=1, keepdims=True))
+        w = p / p.sum(axis=1, keepdims=True) * v_scale[:, g].astype(np.float64)
+        add[:, h] = 2.0 ** -32 * w.max(axis=1, keepdims=True) * (seen @ np.abs(v_lev[:, g].astype(np.float64)))
+    return add
+
+
 def rmsnorm(x, res, w, eps):
     """64 bits: s, y."""
     s = x.astype(np.float64) + (0.0 if res is None else res.astype(np.float64))

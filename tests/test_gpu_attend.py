@@ -47,7 +47,7 @@ def queries(rng, rows, heads, dim, bf16, amp=1.0):
     return ops_ref.f32_of_bf16(code), dev_x(code)
 
 
-def check(twin, table, lens, counts, qf, got, scale, causal, window, bf16, what=""):
+def check(twin, table, lens, counts, qf, got, scale, causal, window, bf16, what="", halves=False):
     got = got.float().cpu().numpy().astype(np.float64)
     row = 0
     for s, n in enumerate(counts):
@@ -56,6 +56,11 @@ def check(twin, table, lens, counts, qf, got, scale, causal, window, bf16, what=
         k, v = twin.values(0, table[s], lens[s]), twin.values(1, table[s], lens[s])
         ref, mag, amp = ops_ref.attend(qf[row:row + n], k, v, lens[s] - n, scale, causal, window)
         bound = ops_ref.attend_bound(mag, amp, ref, k.shape[2], lens[s], bf16)
+        if halves:
+            pages = np.asarray(table[s][: -(-lens[s] // twin.page)], np.int64)
+            lev = np.moveaxis(twin.lev[1][pages], 1, 2).reshape(-1, v.shape[1], v.shape[2])[:lens[s]]
+            sv = np.repeat(twin.scale[1][pages], twin.page, axis=0)[:lens[s]]
+            bound = bound + ops_ref.half_weights(qf[row:row + n], k, lev, sv, lens[s] - n, scale, causal, window)
         err = np.abs(got[row:row + n] - ref)
         bad = ~(err <= bound)
         assert not bad.any(), (what, s, lens[s], n, int(bad.sum()), np.argwhere(bad)[0], float((err / bound).max()))
@@ -100,6 +105,44 @@ def test_long(qmv, n, length, dim):
     qf, qd = queries(rng, n, 8, dim, True)
     got = qmv.attend(cache, batch_of(qmv, td, [length], [n]), qd)
     check(twin, table, [length], [n], qf, got, dim ** -0.5, True, 0, True)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 200), (False, 0), (False, 77)])
+@pytest.mark.parametrize("heads,kvh,dim,page,lens,counts", [
+    (32, 8, 128, 64, [700], [640]),                        # a chunk over cached tokens
+    (16, 16, 64, 16, [513, 300, 0, 650, 1], [513, 299, 0, 400, 1]),
+    (64, 8, 128, 128, [129, 257, 20], [129, 200, 20]),
+    (24, 8, 64, 32, [1100, 900], [400, 500]),              # a group of three heads
+])
+def test_prompts(qmv, heads, kvh, dim, page, lens, counts, causal, window):
+    """Many rows a sequence, ragged, with rows that fill no tile of 128."""
+    rng = np.random.default_rng(dim + window)
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=page)
+    qf, qd = queries(rng, sum(counts), heads, dim, True)
+    b = batch_of(qmv, td, lens, counts)
+    got = qmv.attend(cache, b, qd, causal=causal, window=window)
+    check(twin, table, lens, counts, qf, got, dim ** -0.5, causal, window, True)
+    again = qmv.attend(cache, b, qd, causal=causal, window=window)
+    assert bool((got == again).all())
+
+
+@pytest.mark.parametrize("scale", [-0.2, 2.0])
+def test_prompts_scale_strides_and_growing_scores(qmv, scale):
+    """Scores that grow along the keys (the running maximum moves at every tile), a negative scale, q and
+    out as slices of wider rows."""
+    import torch
+    rng = np.random.default_rng(3)
+    heads, kvh, dim, lens, counts = 32, 8, 128, [900, 640], [640, 640]
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, 32, seed=1)
+    for s, n in enumerate(lens):
+        for p in range(-(-n // 32)):
+            twin.scale[0][table[s, p]] = 2.0 ** -12 * 1.3 ** p
+    cache.k_scale.copy_(torch.from_numpy(twin.scale[0]))
+    qf, qd = queries(rng, sum(counts), heads + 3, dim, True)
+    out = torch.full((sum(counts), heads + 1, dim), 5.0, device="cuda", dtype=torch.bfloat16)
+    qmv.attend(cache, batch_of(qmv, td, lens, counts), qd[:, 2:2 + heads], out=out[:, :heads], scale=scale)
+    check(twin, table, lens, counts, qf[:, 2:2 + heads], out[:, :heads], scale, True, 0, True, halves=True)
+    assert bool((out[:, heads:] == 5).all())
 
 
 @pytest.mark.parametrize("bf16", [True, False])

@@ -130,10 +130,12 @@ def _check(status: int, where: str):
 
 
 def _stream(stream):
+    """The stream's handle as an integer; the current device's current stream by default (asked for as a
+    handle: making torch's stream object takes about 3 us of the host's time a call)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _x_dtype(x) -> int:
@@ -518,26 +520,34 @@ def rmsnorm(x, weight, eps: float = 1e-5, residual=None, residual_out=None, out=
     update in place), or None.  out: "q8" (the uint8 Q8_0 / f32-scale image that matvec_qx reads),
     "bf16" or "f32".  Returns y."""
     import torch
-    cols = x.shape[-1]
-    rows = x.shape[0] if x.dim() == 2 else 1
-    if x.dim() not in (1, 2) or not x.is_contiguous():
+    shape = x.shape
+    if len(shape) == 2:
+        rows, cols = shape
+    elif len(shape) == 1:
+        rows, cols = 1, shape[0]
+    else:
         raise ValueError("x must be a contiguous (rows, cols) tensor")
-    if weight.dtype != torch.float32 or weight.numel() != cols or not weight.is_contiguous():
+    if not x.is_contiguous():
+        raise ValueError("x must be a contiguous (rows, cols) tensor")
+    f32 = torch.float32
+    if weight.dtype is not f32 or weight.numel() != cols or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous float32 (cols,) tensor")
     for t in (residual, residual_out):
-        if t is not None and (t.dtype != torch.float32 or t.shape != x.shape or not t.is_contiguous()):
+        if t is not None and (t.dtype is not f32 or t.shape != shape or not t.is_contiguous()):
             raise ValueError("residual and residual_out must be contiguous float32 tensors of x's shape")
     if out == "q8":
         code = OUT_Q8
+        # the image's bytes: quants, their padding to 64, a float32 scale for each 32
+        need = (rows * cols + 63) // 64 * 64 + rows * cols // 8
         if y is None:
-            y = torch.empty(weight_bytes(Q8_0, SCALE_F32, rows, cols), dtype=torch.uint8, device=x.device)
-        elif y.dtype != torch.uint8 or y.numel() < weight_bytes(Q8_0, SCALE_F32, rows, cols) or not y.is_contiguous():
+            y = torch.empty(need, dtype=torch.uint8, device=x.device)
+        elif y.dtype is not torch.uint8 or y.numel() < need or not y.is_contiguous():
             raise ValueError("y must be a contiguous uint8 tensor of the image's bytes")
-    elif out in ("bf16", "f32"):
-        code, dtype = (X_BF16, torch.bfloat16) if out == "bf16" else (X_F32, torch.float32)
+    elif out == "bf16" or out == "f32":
+        code, dtype = (X_BF16, torch.bfloat16) if out == "bf16" else (X_F32, f32)
         if y is None:
-            y = torch.empty(x.shape, dtype=dtype, device=x.device)
-        elif y.dtype != dtype or y.shape != x.shape or not y.is_contiguous():
+            y = torch.empty(shape, dtype=dtype, device=x.device)
+        elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape and the output's type")
     else:
         raise ValueError("out must be 'q8', 'bf16' or 'f32'")

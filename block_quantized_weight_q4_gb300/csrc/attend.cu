@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
   constexpr int KS = D / 16;       // 16-dim steps
   constexpr int QP = XB ? 1 : 2;   // parts of q (half): hi (, lo)
   constexpr int PP = XB ? 2 : 3;   // parts of the weights (bfloat16): 16 or 24 bits
+  griddep_launch_dependents();
+  griddep_wait();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scan[kWarps];
   __shared__ int found_seq;
@@ -145,11 +147,11 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
     }
     return total;
   };
-  long long total = 0;
+  long long total = 0, w = 0, before = 0;  // up to 128 sequences: this thread's chunks, and those before them
   for (int s0 = 0; s0 < c.n_seq; s0 += kThreads) {
     const int s = s0 + tid;
-    long long before;
-    total += block_scan(s < c.n_seq ? weight(s) : 0, before);
+    w = s < c.n_seq ? weight(s) : 0;
+    total += block_scan(w, before);
   }
   if (total == 0) return;
   // runs of at least one chunk a warp
@@ -163,9 +165,11 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
   long long base = 0;   // first chunk of sequence s
   for (int s0 = 0; s0 < c.n_seq; s0 += kThreads) {
     const int si = s0 + tid;
-    const long long w = si < c.n_seq ? weight(si) : 0;
-    long long before;
-    const long long sum = block_scan(w, before);
+    long long sum = total;
+    if (c.n_seq > kThreads) {
+      w = si < c.n_seq ? weight(si) : 0;
+      sum = block_scan(w, before);
+    }
     if (base + sum > pos) {
       if (base + before <= pos && pos < base + before + w) {
         found_seq = si;
@@ -546,10 +550,12 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
         for (int i = tid; i < nrows * (D / 4); i += kThreads) {
           const int r = i / (D / 4), d = i % (D / 4) * 4;
           float mm = -INFINITY;
+#pragma unroll 8
           for (long long p = cf; p <= cl; ++p)
             mm = fmaxf(mm, __ldcg(area.parts + (2 * p + (p == cf ? 1 : 0)) * kPart + ROWS * D + r));
           float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
           float ll = 0.f;
+#pragma unroll 4
           for (long long p = cf; p <= cl; ++p) {
             const float* part = area.parts + (2 * p + (p == cf ? 1 : 0)) * kPart;
             const float pm = __ldcg(part + ROWS * D + r);
@@ -606,8 +612,7 @@ cudaError_t launch_rows(const KvRef& c, const AttendArgs& a, const DeviceInfo& d
   const long long span = a.window > 0 && (long long)a.window + c.max_rows < c.max_len ? a.window + c.max_rows : c.max_len;
   const long long most = ((span + kChunk - 1) / kChunk + 1) * blocks * c.kv_heads * c.n_seq / kWarps + 1;
   if (grid > most) grid = most;
-  kern<<<(unsigned)grid, kThreads, kSmem, stream>>>(c, a, area);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3((unsigned)grid), kThreads, kSmem, stream, c, a, area);
 }
 
 template <int D, bool XB>

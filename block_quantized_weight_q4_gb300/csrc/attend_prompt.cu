@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   constexpr int kPieces = D / 16;           // 16-byte pieces of a row of levels
   constexpr int kRowsWarp = 32 / kPieces;   // rows a converting warp takes at a time
   constexpr int kPasses = kKeys / (4 * kRowsWarp);
+  griddep_launch_dependents();
+  griddep_wait();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -588,8 +590,7 @@ cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& de
   }
   const long long blocks = c.rows * (a.heads / c.kv_heads) / (2 * kTileRows) + c.n_seq;
   if (blocks * c.kv_heads > INT32_MAX) return cudaErrorInvalidValue;
-  kern<<<(unsigned)(blocks * c.kv_heads), kThreads, kSmem, stream>>>(c, a);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3((unsigned)(blocks * c.kv_heads)), kThreads, kSmem, stream, c, a);
 }
 
 }  // namespace

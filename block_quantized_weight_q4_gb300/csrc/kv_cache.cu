@@ -1,74 +1,99 @@
 // kv_cache.cu -- the paged cache of keys and values in 8 bits: rows written with one scale for each
 // page and head, and read back.
+#include <type_traits>
+
 #include "kv.cuh"
 
 namespace qmv {
 
 namespace {
 
-constexpr int kWriteThreads = 128;
+constexpr int kWritePieces = 8;  // pieces of 8 values that a thread holds
 
 // One CTA per (page that receives rows, head, K or V).  The page's scale is the largest its tokens
-// have needed: raised by the new rows, the earlier tokens' levels move to it.
-template <bool XB>
-__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ KvRef c,
-                                                                 const void* __restrict__ kx, long long k_stride,
-                                                                 const void* __restrict__ vx, long long v_stride) {
-  __shared__ float part[kWriteThreads / 32];
+// have needed: raised by the new rows, the earlier tokens' levels move to it.  The new rows stay in
+// registers between the maximum and their levels (page_tokens * D / 64 threads), so each is read once.
+template <int D, bool XB>
+__global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ KvRef c, const void* __restrict__ kx,
+                                                       long long k_stride, const void* __restrict__ vx,
+                                                       long long v_stride) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kRow = D / 8;  // pieces of a row
+  __shared__ float part[16];
   const int s = blockIdx.y;
   const int head = blockIdx.z >> 1;
   const bool is_v = blockIdx.z & 1;
+  const int T = blockDim.x;
   const KvSeq q = kv_seq(c, s);
   const int first = q.len - q.n;
   const int pi = (first >> c.page_shift) + blockIdx.x;
-  if (pi * c.page_tokens >= q.len || q.n == 0) return;
+  const int begin = pi << c.page_shift;
+  if (begin >= q.len || q.n == 0) return;
   const int id = kv_page(c, s, pi);
   if (id < 0) return;
-  const int begin = pi * c.page_tokens;
   const int lo = first > begin ? first - begin : 0;
   const int hi = q.len - begin < c.page_tokens ? q.len - begin : c.page_tokens;
   const long long at = (long long)id * c.kv_heads + head;
-  int8_t* lev = (is_v ? c.v : c.k) + at * c.page_tokens * c.head_dim;
+  int8_t* lev = (is_v ? c.v : c.k) + at * c.page_tokens * D;
   float* scale = (is_v ? c.v_scale : c.k_scale) + at;
-  const void* x = is_v ? vx : kx;
+  const float had = lo > 0 ? *scale : 0.f;
   const long long stride = is_v ? v_stride : k_stride;
-  const int ppr = c.head_dim / 8;  // pieces of a row
-  const int pieces = (hi - lo) * ppr;
-  const long long x0 = (q.row0 + (begin + lo - first)) * stride + (long long)head * c.head_dim;
-
-  float amax = 0.f;
-  for (int p = threadIdx.x; p < pieces; p += kWriteThreads) {
-    float v[8];
-    load8<XB>(x, x0 + (p / ppr) * stride + (p % ppr) * 8, v);
+  const int pieces = (hi - lo) * kRow;
+  const long long x0 = (q.row0 + (begin + lo - first)) * stride + (long long)head * D;
+  using Raw = typename std::conditional<XB, uint4, float4>::type;
+  Raw x[kWritePieces][XB ? 1 : 2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  for (int i = 0; i < kWritePieces; ++i) {
+    const int p = threadIdx.x + i * T;
+    if (p < pieces) {
+      const long long e = x0 + (p / kRow) * stride + (p % kRow) * 8;
+      const Raw* g = XB ? reinterpret_cast<const Raw*>(static_cast<const uint16_t*>(is_v ? vx : kx) + e)
+                        : reinterpret_cast<const Raw*>(static_cast<const float*>(is_v ? vx : kx) + e);
+#pragma unroll
+      for (int k = 0; k < (XB ? 1 : 2); ++k) x[i][k] = __ldg(g + k);
+    }
   }
+  // value e of piece i
+  auto value = [&](int i, int e) -> float {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i][0]);
+    return XB ? __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]);
+  };
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWritePieces; ++i)
+    if (threadIdx.x + i * T < pieces) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
+    }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-  const float had = lo > 0 ? *scale : 0.f;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWriteThreads / 32; ++w) amax = fmaxf(amax, part[w]);
+  if (T > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    for (int w = 0; w < (T >> 5); ++w) amax = fmaxf(amax, part[w]);
+  }
   const float want = amax < 1e-30f ? 0.f : __fmul_rn(amax, 1.0f / 127.0f);
   const float d = fmaxf(want, had);
   const float inv = d > 0.f ? __fdiv_rn(1.0f, d) : 0.f;
-
-  for (int p = threadIdx.x; p < pieces; p += kWriteThreads) {
-    float v[8];
-    load8<XB>(x, x0 + (p / ppr) * stride + (p % ppr) * 8, v);
-    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      int l = (int)__fadd_rn(__fmul_rn(v[e], inv), copysignf(0.5f, v[e]));
-      l = l > 127 ? 127 : (l < -127 ? -127 : l);
-      w[e >> 2] |= (uint32_t)(l & 0xFF) << (8 * (e & 3));
+  for (int i = 0; i < kWritePieces; ++i) {
+    const int p = threadIdx.x + i * T;
+    if (p < pieces) {
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = value(i, e);
+        int l = (int)__fadd_rn(__fmul_rn(f, inv), copysignf(0.5f, f));
+        l = l > 127 ? 127 : (l < -127 ? -127 : l);
+        w[e >> 2] |= (uint32_t)(l & 0xFF) << (8 * (e & 3));
+      }
+      *reinterpret_cast<uint2*>(lev + (long long)lo * D + 8 * p) = make_uint2(w[0], w[1]);
     }
-    *reinterpret_cast<uint2*>(lev + (long long)lo * c.head_dim + 8 * p) = make_uint2(w[0], w[1]);
   }
   if (d > had && lo > 0) {
     const float ratio = __fdiv_rn(had, d);
-    for (int p = threadIdx.x; p < lo * ppr; p += kWriteThreads) {
+    for (int p = threadIdx.x; p < lo * kRow; p += T) {
       uint2* g = reinterpret_cast<uint2*>(lev + 8 * p);
       const uint2 u = *g;
       const uint32_t in[2] = {u.x, u.y};
@@ -82,6 +107,8 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
       *g = make_uint2(w[0], w[1]);
     }
   }
+  // (the barrier above came after every thread's read of the old scale; a CTA of one warp runs in step)
+  if (T <= 32) __syncwarp();
   if (threadIdx.x == 0) *scale = d;
 }
 
@@ -91,6 +118,8 @@ constexpr int kReadRows = 32;  // rows of a sequence that one CTA reads back
 template <bool XB>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRef c, void* __restrict__ ko,
                                                       void* __restrict__ vo) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int s = blockIdx.y;
   const bool is_v = blockIdx.z;
   const KvSeq q = kv_seq(c, s);
@@ -137,16 +166,18 @@ cudaError_t launch_kv_write(const KvRef& c, bool x_bf16, const void* k, int64_t 
   // pages that n rows can fall into, wherever they start in the first
   const int pages = (c.max_rows + c.page_tokens - 2) / c.page_tokens + 1;
   const dim3 grid((unsigned)pages, (unsigned)c.n_seq, (unsigned)(2 * c.kv_heads));
-  auto kern = x_bf16 ? kv_write_kernel<true> : kv_write_kernel<false>;
-  kern<<<grid, kWriteThreads, 0, stream>>>(c, k, k_stride, v, v_stride);
-  return cudaGetLastError();
+  int threads = c.page_tokens * c.head_dim / (8 * kWritePieces);
+  if (threads < 32) threads = 32;
+  auto kern = c.head_dim == 64    ? (x_bf16 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
+              : c.head_dim == 128 ? (x_bf16 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>)
+                                  : (x_bf16 ? kv_write_kernel<256, true> : kv_write_kernel<256, false>);
+  return launch_dependent(kern, grid, threads, 0, stream, c, k, k_stride, v, v_stride);
 }
 
 cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, cudaStream_t stream) {
   const dim3 grid((unsigned)((c.max_rows + kReadRows - 1) / kReadRows), (unsigned)c.n_seq, 2u);
   auto kern = out_bf16 ? kv_read_kernel<true> : kv_read_kernel<false>;
-  kern<<<grid, 256, 0, stream>>>(c, k, v);
-  return cudaGetLastError();
+  return launch_dependent(kern, grid, 256, 0, stream, c, k, v);
 }
 
 }  // namespace qmv

@@ -86,6 +86,8 @@ struct PartArea {
 
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a, int n_parts,
                                                             const PartArea area) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ Stats warp_stats[kWarps];
   __shared__ Key warp_keys[kWarps][QMV_MAX_TOP];
   __shared__ uint32_t floor_bits;  // no value below this can be among the largest n_top
@@ -286,8 +288,7 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, const DeviceInfo
     area.parts = reinterpret_cast<Part*>(ws.partials);
   }
   if (rows * parts > INT32_MAX) return cudaErrorInvalidValue;
-  logprobs_kernel<<<(unsigned)(rows * parts), kThreads, 0, stream>>>(a, (int)parts, area);
-  return cudaGetLastError();
+  return launch_dependent(logprobs_kernel, dim3((unsigned)(rows * parts)), kThreads, 0, stream, a, (int)parts, area);
 }
 
 }  // namespace qmv

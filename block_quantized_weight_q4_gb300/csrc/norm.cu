@@ -24,6 +24,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const void* __
                                                                   const float* __restrict__ weight, float eps,
                                                                   void* __restrict__ out, long long out_d_off,
                                                                   long long rows, int cols) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float part[32];
   const long long row = blockIdx.x;
   const int T = blockDim.x;
@@ -142,8 +144,8 @@ cudaError_t launch_typed(int64_t rows, int cols, const void* x, const float* res
   const int ni = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;
   const int threads = ((pieces + ni - 1) / ni + 31) / 32 * 32;
   auto kern = ni == 1 ? rmsnorm_kernel<XB, OUT, 1> : ni == 2 ? rmsnorm_kernel<XB, OUT, 2> : rmsnorm_kernel<XB, OUT, 4>;
-  kern<<<(unsigned)rows, threads, 0, stream>>>(x, residual, residual_out, weight, eps, out, out_d_off, rows, cols);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3((unsigned)rows), threads, 0, stream, x, residual, residual_out, weight, eps, out,
+                          out_d_off, rows, cols);
 }
 
 }  // namespace

@@ -193,6 +193,23 @@ cudaError_t launch_decode_tc_f32(const MatrixRef* ms, const void* const* xs, flo
                                  int act = -1, long long up_batch = 0);
 
 // ---------------------------------------------------------------- between the products
+// Their kernels launch as programmatic dependents: their CTAs may start while the preceding kernel ends, and
+// touch global memory only after griddep_wait().
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Root-mean-square norm (norm.cu): out_dtype QMV_X_F32, QMV_X_BF16, or QMV_OUT_Q8 with the scales at
 // out + out_d_off.
 cudaError_t launch_rmsnorm(bool x_bf16, int64_t rows, int64_t cols, const void* x, const float* residual,

@@ -7,6 +7,8 @@
 // seen, sorted over its lanes, and a batch touches the list only if its maximum reaches the
 // smallest kept value of any warp of the CTA.  A few rows are cut into parts over many CTAs; the last
 // part of a row to finish joins them in their order.
+#include <mutex>
+
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
 
@@ -92,6 +94,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   __shared__ Key warp_keys[kWarps][QMV_MAX_TOP];
   __shared__ uint32_t floor_bits;  // no value below this can be among the largest n_top
   __shared__ int last_flag;
+  __shared__ __align__(16) float stash[kWarps][32][kBatch + 4];  // a batch that may enter the lists
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const long long row = blockIdx.x / n_parts;
   const int part = blockIdx.x % n_parts;
@@ -105,31 +108,60 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   Key mine = 0;
   bool bad = false;
 
-  // 16 values a lane: v[e] is logit first + stride-1 runs of four; absent ones are -inf with id ~0
-  auto take = [&](const float (&v)[kBatch], const uint32_t (&id)[kBatch / 4], int live) {
+  // 16 values a lane, absent ones -inf; id_of(lane, e): the id of a lane's value e; live: a lane's values that are there
+  auto take = [&](const float (&v)[kBatch], int live, auto id_of) {
     float top = v[0];
 #pragma unroll
     for (int e = 1; e < kBatch; ++e) top = max_nan(top, v[e]);
     const uint32_t fb = *reinterpret_cast<volatile uint32_t*>(&floor_bits);
-    const float floor = k > 0 ? (fb == 0u ? -INFINITY : unordered(fb)) : INFINITY;
+    float floor = k > 0 ? (fb == 0u ? -INFINITY : unordered(fb)) : INFINITY;
     if (__any_sync(0xffffffffu, !(top < floor))) {
       bad |= !(top < INFINITY);
       if (k > 0) {
         Key least = __shfl_sync(0xffffffffu, mine, k - 1);
+        if (least == 0) {
+          // nothing kept yet: the k-th largest of the lanes' maxima is a floor to begin with (bitonic sort)
+          uint32_t o = ordered(top);
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const Key ke = key_of(v[e], e < live ? id[e >> 2] + (e & 3) : 0xffffffffu);
-          uint32_t who = __ballot_sync(0xffffffffu, ke > least && !(v[e] < floor));
-          while (who != 0u) {
-            const int src = __ffs(who) - 1;
-            who &= who - 1;
-            const Key c = __shfl_sync(0xffffffffu, ke, src);
+          for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int d = size >> 1; d > 0; d >>= 1) {
+              const uint32_t u = __shfl_xor_sync(0xffffffffu, o, d);
+              o = ((lane & d) == 0) == ((lane & size) == 0) ? max(o, u) : min(o, u);
+            }
+          const float w = unordered(__shfl_sync(0xffffffffu, o, k - 1));
+          floor = w > floor ? w : floor;
+        }
+        // this lane's values that may enter the list: not below the floor, nor equal to the least kept one with
+        // a larger id
+        const float lv = least == 0 ? NAN : unordered((uint32_t)(least >> 32));
+        const uint32_t lid = 0xffffffffu - (uint32_t)least;
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+          if (e < live && !(v[e] < floor) && !(v[e] == lv && id_of(lane, e) >= lid)) m |= 1u << e;
+        uint32_t who = __ballot_sync(0xffffffffu, m != 0u);
+        if (m != 0u) {
+#pragma unroll
+          for (int e = 0; e < kBatch; e += 4)
+            *reinterpret_cast<float4*>(&stash[wid][lane][e]) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+        __syncwarp();
+        while (who != 0u) {
+          const int src = __ffs(who) - 1;
+          who &= who - 1;
+          uint32_t bits = __shfl_sync(0xffffffffu, m, src);
+          while (bits != 0u) {
+            const int e = __ffs(bits) - 1;
+            bits &= bits - 1;
+            const Key c = key_of(stash[wid][src][e], id_of(src, e));
             if (c > least) {
               insert(mine, c, lane);
               least = __shfl_sync(0xffffffffu, mine, k - 1);
             }
           }
         }
+        __syncwarp();  // the stash has been read
         if (lane == 0) atomicMax(&floor_bits, (uint32_t)(least >> 32));
       }
     }
@@ -156,36 +188,28 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   const int q0 = (int)((long long)quads * part / n_parts), q1 = (int)((long long)quads * (part + 1) / n_parts);
   for (int q = q0 + wid * 128; q < q1; q += kWarps * 128) {
     float v[kBatch];
-    uint32_t id[kBatch / 4];
     int live = 0;
-    float4 f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int qi = q + 32 * i + lane;
-      f[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      id[i] = (uint32_t)(head + 4 * qi);
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (qi < q1) {
-        f[i] = __ldcs(xv + qi);
+        f = __ldg(xv + qi);
         live = 4 * i + 4;
       }
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * i] = f[i].x, v[4 * i + 1] = f[i].y, v[4 * i + 2] = f[i].z, v[4 * i + 3] = f[i].w;
-    take(v, id, live);
+    take(v, live, [&](int l, int e) { return (uint32_t)(head + 4 * (q + 32 * (e >> 2) + l) + (e & 3)); });
   }
   if (part == 0 && wid == 0) {
     const int tail = n - head - 4 * quads;
     if (head + tail > 0) {
       float v[kBatch];
-      uint32_t id[kBatch / 4] = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int e = 0; e < kBatch; ++e) v[e] = -INFINITY;
-      const int i = lane < head ? lane : lane - head + n - tail;
-      if (lane < head + tail) {
-        v[0] = x[i];
-        id[0] = (uint32_t)i;
-      }
-      take(v, id, lane < head + tail ? 1 : 0);
+      auto id_of = [&](int l, int) { return (uint32_t)(l < head ? l : l - head + n - tail); };
+      if (lane < head + tail) v[0] = x[id_of(lane, 0)];
+      take(v, lane < head + tail ? 1 : 0, id_of);
     }
   }
 
@@ -274,16 +298,35 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
 
 cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, const DeviceInfo& dev, cudaStream_t stream) {
   PartArea area{nullptr, nullptr};
+  static std::mutex mu;
+  static int ctas_per_sm[64] = {};
+  if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidValue;
+  int per_sm;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (ctas_per_sm[dev.device] == 0) {
+      int k = 0;
+      const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, logprobs_kernel, kThreads, 0);
+      if (err != cudaSuccess) return err;
+      ctas_per_sm[dev.device] = k > 0 ? k : 1;
+    }
+    per_sm = ctas_per_sm[dev.device];
+  }
+  // parts of a row: as many as keep the waves of CTAs times a part's length (with a part's own cost, about as
+  // much as 4096 values) shortest, of 4096 values at least
   long long parts = 1;
-  // rows cut so that about six CTAs a SM are there, of at least two batches a thread
-  const long long want = (6LL * dev.sm_count + rows - 1) / rows;
-  const long long most = (a.vocab + 8191) / 8192;
+  const long long most = (a.vocab + 4095) / 4096, slots = (long long)dev.sm_count * per_sm;
   Workspace ws;
-  if (want > 1 && most > 1 && stream_serve_workspace(dev, stream, &ws) == cudaSuccess) {
-    parts = want < most ? want : most;
+  if (most > 1 && rows < slots && stream_serve_workspace(dev, stream, &ws) == cudaSuccess && rows <= ws.max_counters) {
+    long long best = 0;
     const long long fit = (long long)(ws.max_partial_floats * sizeof(float) / sizeof(Part)) / rows;
-    if (parts > fit) parts = fit;
-    if (rows > ws.max_counters || parts < 1) parts = 1;
+    for (long long p = 1; p <= most && p <= fit && p <= 64; ++p) {
+      const long long cost = (rows * p + slots - 1) / slots * (a.vocab / p + 4096);
+      if (best == 0 || cost < best) {
+        best = cost;
+        parts = p;
+      }
+    }
     area.counters = ws.counters;
     area.parts = reinterpret_cast<Part*>(ws.partials);
   }

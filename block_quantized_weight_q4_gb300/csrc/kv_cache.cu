@@ -68,11 +68,9 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (T > 32) {
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < (T >> 5); ++w) amax = fmaxf(amax, part[w]);
-  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  for (int w = 0; w < (T >> 5); ++w) amax = fmaxf(amax, part[w]);
   const float want = amax < 1e-30f ? 0.f : __fmul_rn(amax, 1.0f / 127.0f);
   const float d = fmaxf(want, had);
   const float inv = d > 0.f ? __fdiv_rn(1.0f, d) : 0.f;
@@ -107,44 +105,59 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
       *g = make_uint2(w[0], w[1]);
     }
   }
-  // (the barrier above came after every thread's read of the old scale; a CTA of one warp runs in step)
-  if (T <= 32) __syncwarp();
+  // (the barrier above came after every thread's read of the old scale)
   if (threadIdx.x == 0) *scale = d;
 }
 
-constexpr int kReadRows = 32;  // rows of a sequence that one CTA reads back
-
-// 16 levels a thread at a time.
-template <bool XB>
+// Rows read back: a CTA takes U * 256 pieces of 16 levels of one (sequence, head, K or V), each thread U of
+// them, whose page ids, then levels and scales, are all asked for before the first is used.
+template <int D, bool XB, int U>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRef c, void* __restrict__ ko,
                                                       void* __restrict__ vo) {
   griddep_launch_dependents();
   griddep_wait();
+  constexpr int kRow = D / 16;  // pieces of a row
+  constexpr int kRows = 256 / kRow;
   const int s = blockIdx.y;
-  const bool is_v = blockIdx.z;
+  // the heads of the same rows lie side by side in the output, so their CTAs follow each other
+  const int head = blockIdx.x % (2 * c.kv_heads) >> 1;
+  const bool is_v = blockIdx.x & 1;
   const KvSeq q = kv_seq(c, s);
-  const int r0 = blockIdx.x * kReadRows;
-  if (r0 >= q.n) return;
-  const int nr = q.n - r0 < kReadRows ? q.n - r0 : kReadRows;
+  const int r0 = blockIdx.x / (2 * c.kv_heads) * (U * kRows) + threadIdx.x / kRow;
+  const int piece = threadIdx.x % kRow;
   const int8_t* lev = is_v ? c.v : c.k;
   const float* scale = is_v ? c.v_scale : c.k_scale;
-  const int ppr = c.head_dim / 16;
-  const int row_pieces = c.kv_heads * ppr;
-  for (int p = threadIdx.x; p < nr * row_pieces; p += 256) {
-    const int r = p / row_pieces, in_row = p % row_pieces;
-    const int head = in_row / ppr, piece = in_row % ppr;
-    const int pos = q.len - q.n + r0 + r;
-    const int id = kv_page(c, s, (pos >> c.page_shift));
-    if (id < 0) continue;
-    const long long at = (long long)id * c.kv_heads + head;
-    const float d = __ldg(scale + at);
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-        lev + (at * c.page_tokens + (pos & (c.page_tokens - 1))) * c.head_dim + 16 * piece));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  const int32_t* pages = c.page_table + (long long)s * c.table_stride;
+  const int first = q.len - q.n;
+  int id[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = r0 + u * kRows;
+    id[u] = r < q.n ? __ldg(pages + ((first + r) >> c.page_shift)) : -1;
+  }
+  uint4 x[U];
+  float d[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = r0 + u * kRows;
+    if ((unsigned)id[u] >= (unsigned)c.n_pages) {
+      if (r < q.n) record_status(c.status, QMV_E_ARG);
+      id[u] = -1;
+      continue;
+    }
+    const long long at = (long long)id[u] * c.kv_heads + head;
+    d[u] = __ldg(scale + at);
+    x[u] = __ldg(reinterpret_cast<const uint4*>(lev + (at * c.page_tokens + ((first + r) & (c.page_tokens - 1))) * D +
+                                                16 * piece));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (id[u] < 0) continue;
+    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
     float f[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), d);
-    const long long o = (q.row0 + r0 + r) * c.kv_heads * c.head_dim + head * c.head_dim + 16 * piece;
+    for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), d[u]);
+    const long long o = ((q.row0 + r0 + u * kRows) * c.kv_heads + head) * D + 16 * piece;
     if (XB) {
       uint4* g = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? vo : ko) + o);
 #pragma unroll
@@ -159,6 +172,19 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
   }
 }
 
+template <int D, bool XB>
+cudaError_t launch_read(const KvRef& c, void* k, void* v, const DeviceInfo& dev, cudaStream_t stream) {
+  constexpr int kRows = 256 / (D / 16);
+  // four pieces a thread where that still leaves every SM several CTAs
+  const long long one = (long long)((c.max_rows + kRows - 1) / kRows) * c.n_seq * 2 * c.kv_heads;
+  const int u = one >= 64LL * dev.sm_count ? 4 : 1;
+  const long long x = (long long)((c.max_rows + u * kRows - 1) / (u * kRows)) * (2 * c.kv_heads);
+  if (x > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)x, (unsigned)c.n_seq);
+  return u == 4 ? launch_dependent(kv_read_kernel<D, XB, 4>, grid, 256, 0, stream, c, k, v)
+                : launch_dependent(kv_read_kernel<D, XB, 1>, grid, 256, 0, stream, c, k, v);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_write(const KvRef& c, bool x_bf16, const void* k, int64_t k_stride, const void* v,
@@ -166,18 +192,24 @@ cudaError_t launch_kv_write(const KvRef& c, bool x_bf16, const void* k, int64_t 
   // pages that n rows can fall into, wherever they start in the first
   const int pages = (c.max_rows + c.page_tokens - 2) / c.page_tokens + 1;
   const dim3 grid((unsigned)pages, (unsigned)c.n_seq, (unsigned)(2 * c.kv_heads));
-  int threads = c.page_tokens * c.head_dim / (8 * kWritePieces);
-  if (threads < 32) threads = 32;
+  // threads for the most rows that a page may receive (64 at least: they also move a raised page's levels)
+  int threads = (c.max_rows < c.page_tokens ? c.max_rows : c.page_tokens) * c.head_dim / (8 * kWritePieces);
+  threads = threads < 64 ? 64 : (threads + 31) / 32 * 32;
   auto kern = c.head_dim == 64    ? (x_bf16 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
               : c.head_dim == 128 ? (x_bf16 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>)
                                   : (x_bf16 ? kv_write_kernel<256, true> : kv_write_kernel<256, false>);
   return launch_dependent(kern, grid, threads, 0, stream, c, k, k_stride, v, v_stride);
 }
 
-cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, cudaStream_t stream) {
-  const dim3 grid((unsigned)((c.max_rows + kReadRows - 1) / kReadRows), (unsigned)c.n_seq, 2u);
-  auto kern = out_bf16 ? kv_read_kernel<true> : kv_read_kernel<false>;
-  return launch_dependent(kern, grid, 256, 0, stream, c, k, v);
+cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, const DeviceInfo& dev,
+                           cudaStream_t stream) {
+  switch (c.head_dim) {
+    case 64: return out_bf16 ? launch_read<64, true>(c, k, v, dev, stream) : launch_read<64, false>(c, k, v, dev, stream);
+    case 128:
+      return out_bf16 ? launch_read<128, true>(c, k, v, dev, stream) : launch_read<128, false>(c, k, v, dev, stream);
+    default:
+      return out_bf16 ? launch_read<256, true>(c, k, v, dev, stream) : launch_read<256, false>(c, k, v, dev, stream);
+  }
 }
 
 }  // namespace qmv

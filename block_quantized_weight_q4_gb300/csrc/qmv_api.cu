@@ -710,7 +710,7 @@ int qmv_kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int out_dt
   DeviceInfo dev;
   if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
   c.status = dev.status;
-  return launch_kv_read(c, out_dtype == QMV_X_BF16, k, v, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
+  return launch_kv_read(c, out_dtype == QMV_X_BF16, k, v, dev, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
 }
 
 int qmv_attend(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int heads, int x_dtype, const void* q,

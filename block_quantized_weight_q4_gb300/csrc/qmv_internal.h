@@ -240,7 +240,8 @@ struct KvRef {
 };
 cudaError_t launch_kv_write(const KvRef& c, bool x_bf16, const void* k, int64_t k_stride, const void* v,
                             int64_t v_stride, cudaStream_t stream);
-cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, const DeviceInfo& dev,
+                           cudaStream_t stream);
 
 struct AttendArgs {
   const void* q;

@@ -22,7 +22,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 32;   // keys of a stage
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 template <int D>
 struct Ring {

@@ -75,6 +75,26 @@ __device__ __forceinline__ void insert(Key& mine, Key k, int lane) {
   }
 }
 
+// The warp's 32 keys in descending order over its lanes (bitonic), and the 32 largest of two such lists.
+__device__ __forceinline__ void sort_keys(Key& v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const Key u = __shfl_xor_sync(0xffffffffu, v, d);
+      v = (((lane & d) == 0) == ((lane & size) == 0)) == (u > v) ? u : v;
+    }
+}
+__device__ __forceinline__ void merge_keys(Key& mine, Key other, int lane) {
+  const Key r = __shfl_sync(0xffffffffu, other, 31 - lane);
+  mine = r > mine ? r : mine;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const Key u = __shfl_xor_sync(0xffffffffu, mine, d);
+    mine = ((lane & d) == 0) == (u > mine) ? u : mine;
+  }
+}
+
 struct Part {  // of one row, in the workspace
   Stats s;
   int bad;
@@ -106,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
 
   Stats st{-INFINITY, 0.f, 0.f};
   Key mine = 0;
-  bool bad = false;
+  bool bad = false, fresh = true;
 
   // 16 values a lane, absent ones -inf; id_of(lane, e): the id of a lane's value e; live: a lane's values that are there
   auto take = [&](const float (&v)[kBatch], int live, auto id_of) {
@@ -119,29 +139,25 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
       bad |= !(top < INFINITY);
       if (k > 0) {
         Key least = __shfl_sync(0xffffffffu, mine, k - 1);
-        if (least == 0) {
-          // nothing kept yet: the k-th largest of the lanes' maxima is a floor to begin with (bitonic sort)
-          uint32_t o = ordered(top);
+        int held = -1;  // this lane's value that is in the list already
+        if (fresh) {
+          fresh = false;
+          // nothing kept yet: the lanes' largest values, sorted, are the list to begin with
 #pragma unroll
-          for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-            for (int d = size >> 1; d > 0; d >>= 1) {
-              const uint32_t u = __shfl_xor_sync(0xffffffffu, o, d);
-              o = ((lane & d) == 0) == ((lane & size) == 0) ? max(o, u) : min(o, u);
-            }
-          const float w = unordered(__shfl_sync(0xffffffffu, o, k - 1));
-          floor = w > floor ? w : floor;
+          for (int e = kBatch - 1; e >= 0; --e)
+            if (v[e] == top || (isnan(top) && isnan(v[e]))) held = e;
+          if (held >= live) held = -1;
+          mine = held >= 0 ? key_of(top, id_of(lane, held)) : 0;
+          sort_keys(mine, lane);
+          least = __shfl_sync(0xffffffffu, mine, k - 1);
         }
-        // this lane's values that may enter the list: not below the floor, nor equal to the least kept one with
-        // a larger id
-        const float lv = least == 0 ? NAN : unordered((uint32_t)(least >> 32));
-        const uint32_t lid = 0xffffffffu - (uint32_t)least;
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e)
-          if (e < live && !(v[e] < floor) && !(v[e] == lv && id_of(lane, e) >= lid)) m |= 1u << e;
-        uint32_t who = __ballot_sync(0xffffffffu, m != 0u);
-        if (m != 0u) {
+        // lanes with a value that may enter the list: not below the floor or the least kept one, nor all equal to
+        // that with larger ids; the warp looks at such a lane's 16 values together
+        const float lv = least == 0 ? -INFINITY : unordered((uint32_t)(least >> 32));
+        floor = lv > floor ? lv : floor;
+        const bool may = live > 0 && !(top < floor) && !(top == lv && id_of(lane, 0) > 0xffffffffu - (uint32_t)least);
+        uint32_t who = __ballot_sync(0xffffffffu, may);
+        if (may) {
 #pragma unroll
           for (int e = 0; e < kBatch; e += 4)
             *reinterpret_cast<float4*>(&stash[wid][lane][e]) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -150,11 +166,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
         while (who != 0u) {
           const int src = __ffs(who) - 1;
           who &= who - 1;
-          uint32_t bits = __shfl_sync(0xffffffffu, m, src);
-          while (bits != 0u) {
-            const int e = __ffs(bits) - 1;
-            bits &= bits - 1;
-            const Key c = key_of(stash[wid][src][e], id_of(src, e));
+          const int n_live = __shfl_sync(0xffffffffu, live, src), skip = __shfl_sync(0xffffffffu, held, src);
+          const int e = lane & (kBatch - 1);
+          const Key mine_key = key_of(stash[wid][src][e], id_of(src, e));
+          uint32_t in = __ballot_sync(0xffffffffu, lane < n_live && lane != skip && mine_key > least);
+          while (in != 0u) {
+            const Key c = __shfl_sync(0xffffffffu, mine_key, __ffs(in) - 1);
+            in &= in - 1;
             if (c > least) {
               insert(mine, c, lane);
               least = __shfl_sync(0xffffffffu, mine, k - 1);
@@ -224,16 +242,21 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
       st.join(s);
     }
     if (lane == 0) warp_stats[wid] = st;
-    if (lane < k) warp_keys[wid][lane] = mine;
+    if (k > 0) warp_keys[wid][lane] = mine;
     bad = __syncthreads_or(bad);
-    if (wid == 0) {
-      for (int w = 1; w < kWarps; ++w) {
-        st.join(warp_stats[w]);
-        for (int i = 0; i < k; ++i) {
-          const Key c = warp_keys[w][i];
-          if (c <= __shfl_sync(0xffffffffu, mine, k - 1)) break;
-          insert(mine, c, lane);
+#pragma unroll
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+      if (wid < half) {
+        st.join(warp_stats[wid + half]);
+        if (k > 0) merge_keys(mine, warp_keys[wid + half][lane], lane);
+      }
+      if (half > 1) {
+        __syncthreads();
+        if (wid < half) {
+          if (lane == 0) warp_stats[wid] = st;
+          if (k > 0) warp_keys[wid][lane] = mine;
         }
+        __syncthreads();
       }
     }
   };
@@ -248,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
         __stcg(&parts[part].s.zx, st.zx);
         __stcg(&parts[part].bad, (int)bad);
       }
-      if (lane < k) __stcg(&parts[part].keys[lane], mine);
+      if (k > 0) __stcg(&parts[part].keys[lane], mine);
       __threadfence();
       __syncwarp();
       if (lane == 0) {
@@ -263,16 +286,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     st = Stats{-INFINITY, 0.f, 0.f};
     mine = 0;
     bad = false;
+#pragma unroll 2
     for (int p = wid; p < n_parts; p += kWarps) {
       // lane 0 of each warp joins the statistics, all lanes the keys
-      const Key c = lane < k ? __ldcg(&parts[p].keys[lane]) : 0;
+      const Key c = k > 0 ? __ldcg(&parts[p].keys[lane]) : 0;
       bad |= __ldcg(&parts[p].bad) != 0;
       if (lane == 0) st.join(Stats{__ldcg(&parts[p].s.m), __ldcg(&parts[p].s.z), __ldcg(&parts[p].s.zx)});
-      for (int i = 0; i < k; ++i) {
-        const Key ci = __shfl_sync(0xffffffffu, c, i);
-        if (ci <= __shfl_sync(0xffffffffu, mine, k - 1)) break;
-        insert(mine, ci, lane);
-      }
+      if (k > 0) merge_keys(mine, c, lane);
     }
     join_cta();
   }

@@ -147,7 +147,8 @@ __device__ __forceinline__ int blocks_of(const KvSeq& q, int group) {
   return (int)(((long long)q.n * group + 2 * kTileRows - 1) / (2 * kTileRows));
 }
 
-template <int D>
+// PG: keys that share a page's scales, 16 or 64 (pages of 64 and 128 tokens).
+template <int D, int PG>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ KvRef c,
                                                                     const __grid_constant__ AttendArgs a) {
   using L = Smem<D>;
@@ -304,21 +305,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             }
         }
         // the tile's maximum (a group's factor is positive, so its largest product is its largest score)
+        constexpr int kGroups = kKeys / PG;
         float mt = -INFINITY;
+        float cg[kGroups], eg[kGroups];
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int x = 0; x < kGroups; ++x) {
+          const GroupScale gs = tab[x * (PG / 16)];
+          cg[x] = group_factor(gs.ks, rowc);
+          eg[x] = gs.e;
+          float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t* w = v[b] + 16 * h;
-            float m0 = max3(w[0], w[1], w[2]), m1 = max3(w[3], w[4], w[5]);
-            m0 = max3(__float_as_uint(m0), w[6], w[7]);
-            m1 = max3(__float_as_uint(m1), w[8], w[9]);
-            m0 = max3(__float_as_uint(m0), w[10], w[11]);
-            m1 = max3(__float_as_uint(m1), w[12], w[13]);
-            m0 = max3(__float_as_uint(m0), w[14], w[15]);
-            const GroupScale gs = tab[2 * b + h];
-            mt = fmaxf(mt, fmaf(fmaxf(m0, m1), group_factor(gs.ks, rowc), gs.e));
+          for (int e = 0; e < PG; e += 2) {
+            const int key = x * PG + e;
+            m[(e >> 1) & 1] = max3(__float_as_uint(m[(e >> 1) & 1]), v[key >> 5][key & 31], v[key >> 5][(key & 31) + 1]);
           }
+          mt = fmaxf(mt, fmaf(fmaxf(m[0], m[1]), cg[x], eg[x]));
+        }
         // the reference follows the maximum when it has fallen 2^8 behind
         const bool move = mt > ref + kSlack;
         if (__any_sync(0xffffffffu, move)) {
@@ -340,28 +342,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         const float base = (ref == -INFINITY ? 0.f : ref) - kWeightBits;
         // the weights, over the scores
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t p[16];
+        for (int x = 0; x < kGroups; ++x) {
+          const uint64_t c2 = pack2(cg[x], cg[x]), e2 = pack2(eg[x] - base, eg[x] - base);
+          uint64_t sum = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const GroupScale gs = tab[2 * b + h];
-            const float cg = group_factor(gs.ks, rowc), eg = gs.e - base;
-            const uint64_t c2 = pack2(cg, cg), e2 = pack2(eg, eg);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float x0, x1;
-              unpack2(fma2(pack2(__uint_as_float(v[b][16 * h + e]), __uint_as_float(v[b][16 * h + e + 1])), c2, e2), x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              sum = add2(sum, pack2(x0, x1));
-              p[8 * h + e / 2] = pack_f16x2(x0, x1);
-            }
-            float s0, s1;
-            unpack2(sum, s0, s1);
-            l = fmaf(s0 + s1, gs.back, l);
+          for (int e = 0; e < PG; e += 2) {
+            const int key = x * PG + e;
+            float x0, x1;
+            unpack2(fma2(pack2(__uint_as_float(v[key >> 5][key & 31]), __uint_as_float(v[key >> 5][(key & 31) + 1])), c2, e2),
+                    x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            sum = add2(sum, pack2(x0, x1));
+            // the pair's halves in place, in the first half of its 32 scores' registers
+            v[key >> 5][(key & 31) >> 1] = pack_f16x2(x0, x1);
+            if ((key & 31) == 30) tmem_st16(sp + 16 * (key >> 5), *reinterpret_cast<uint32_t(*)[16]>(v[key >> 5]));
           }
-          tmem_st16(sp + 16 * b, p);
+          float s0, s1;
+          unpack2(sum, s0, s1);
+          l = fmaf(s0 + s1, tab[x * (PG / 16)].back, l);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -572,9 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   }
 }
 
-template <int D>
+template <int D, int PG>
 cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  auto kern = attend_prompt_kernel<D>;
+  auto kern = attend_prompt_kernel<D, PG>;
   constexpr int kSmem = Smem<D>::kBytes;
   static std::mutex mu;
   static bool ready[64] = {};
@@ -604,7 +603,9 @@ bool attend_prompt_supported(const KvRef& c, const AttendArgs& a, bool x_bf16, c
 }
 
 cudaError_t launch_attend_prompt(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  return c.head_dim == 64 ? launch_dim<64>(c, a, dev, stream) : launch_dim<128>(c, a, dev, stream);
+  if (c.page_tokens >= 64)
+    return c.head_dim == 64 ? launch_dim<64, 64>(c, a, dev, stream) : launch_dim<128, 64>(c, a, dev, stream);
+  return c.head_dim == 64 ? launch_dim<64, 16>(c, a, dev, stream) : launch_dim<128, 16>(c, a, dev, stream);
 }
 
 }  // namespace qmv

@@ -539,7 +539,7 @@ int qmv_rmsnorm(int x_dtype, int64_t rows, int64_t cols, const void *x, const fl
  * page holds, for each of kv_heads heads, page_tokens x head_dim int8 levels, and one float32
  * scale: the value is level * scale.
  *   k, v             : device, n_pages x kv_heads x page_tokens x head_dim int8, 16-byte aligned.
- *   k_scale, v_scale : device, n_pages x kv_heads float32, 4-byte aligned.
+ *   k_scale, v_scale : device, n_pages x kv_heads float32, not negative, 4-byte aligned.
  *   page_tokens is 16, 32, 64 or 128; head_dim 64, 128 or 256; kv_heads 1..1024; n_pages below 2^31. */
 typedef struct qmv_kv_cache {
   int8_t *k;
@@ -617,10 +617,12 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
  * Calls with many bfloat16 rows (prompts; heads of 64 or 128) round the weights times the V
  * scale once to half: 2^-11 relative down to 2^-21 of the row's largest one, below that multiples
  * of at most 2^-32 of it (a key whose weight times V scale is that far below the row's largest counts only
- * to that resolution).  Scales are not negative.  Results do not depend on timing.
- * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream,
- * allocated on the stream's first such call and kept; while a stream without one is being
- * captured, the call does not split.
+ * to that resolution).  Results do not depend on timing.
+ * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream (8 MiB,
+ * shared with qmv_logprobs), allocated on the stream's first such call and kept; while a stream
+ * without one is being captured, the call does not split (slower; call once on the stream before
+ * capturing it).  A captured call keeps to the capturing stream's workspace: its replays must not overlap
+ * in time with other calls that use it.
  * Returns QMV_OK, QMV_E_FORMAT (x_dtype), QMV_E_ARG (null pointer, negative count, window < 0, scale not
  * finite), QMV_E_SHAPE (the cache's or rows' numbers, heads, strides), QMV_E_ALIGN or QMV_E_CUDA. */
 int qmv_attend(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int heads, int x_dtype, const void *q,

@@ -126,6 +126,40 @@ def test_prompts(qmv, heads, kvh, dim, page, lens, counts, causal, window):
     assert bool((got == again).all())
 
 
+def test_many_sequences(qmv):
+    """More sequences than a CTA scans at once, empty ones among them, on both kernels."""
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(0, 90, 300)]
+    cache, twin, table, td = filled(qmv, lens, 2, 64, 16, seed=5)
+    counts = [min(n, 1 + i % 3) for i, n in enumerate(lens)]
+    qf, qd = queries(rng, sum(counts), 6, 64, True)
+    got = qmv.attend(cache, batch_of(qmv, td, lens, counts), qd)
+    check(twin, table, lens, counts, qf, got, 0.125, True, 0, True)
+    lens = [int(x) for x in rng.integers(30, 200, 75)]
+    counts = [min(n, 40) if i % 7 else 0 for i, n in enumerate(lens)]
+    cache, twin, table, td = filled(qmv, lens, 8, 128, 64, seed=6)
+    qf, qd = queries(rng, sum(counts), 64, 128, True)
+    got = qmv.attend(cache, batch_of(qmv, td, lens, counts), qd)
+    check(twin, table, lens, counts, qf, got, 128 ** -0.5, True, 0, True)
+
+
+def test_nothing_to_do(qmv):
+    """Sequences of length zero, and no rows at all."""
+    import torch
+    cache, twin, table, td = filled(qmv, [0, 40], 2, 64, 16, seed=5)
+    out = torch.full((2, 4, 64), 3.0, device="cuda")
+    b = batch_of(qmv, td, [0, 40], [0, 2])
+    q = torch.zeros_like(out)
+    qmv.attend(cache, b, q, out=out)
+    v = torch.from_numpy(twin.values(1, table[1], 40)).cuda()
+    want = torch.stack([v[:39].mean(0), v.mean(0)]).repeat_interleave(2, dim=1)
+    assert float((out - want).abs().max()) < 1e-5  # equal scores: the mean of the values
+    none = batch_of(qmv, td, [0, 40], [0, 0], max_rows=0)
+    assert qmv.attend(cache, none, q[:0]).shape == (0, 4, 64)
+    qmv.kv_write(cache, none, q[:0, :2], q[:0, :2])
+    assert qmv.kv_read(cache, none)[0].shape == (0, 2, 64)
+
+
 @pytest.mark.parametrize("scale", [-0.2, 2.0])
 def test_prompts_scale_strides_and_growing_scores(qmv, scale):
     """Scores that grow along the keys (the running maximum moves at every tile), a negative scale, q and

@@ -131,3 +131,24 @@ def test_another_stream_and_repeat(qmv):
     s.synchronize()
     for u, v, w in zip(a, b, c):
         assert torch.equal(u, v) and torch.equal(u, w)
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_in_a_graph(qmv, warm):
+    """Captured on a stream without a workspace (rows are not cut) and on one with it."""
+    import torch
+    x = (2 * np.random.default_rng(3).standard_normal((2, 60001))).astype(F)
+    xd = torch.zeros((2, 60001), device="cuda")
+    given = torch.tensor([[5], [60000]], device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if warm:
+        qmv.logprobs(xd, given, top=3, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = qmv.logprobs(xd, given, top=3)
+    xd.copy_(torch.from_numpy(x))
+    g.replay()
+    torch.cuda.synchronize()
+    check(x, given.cpu().numpy(), 3, [t.cpu().numpy() for t in got])

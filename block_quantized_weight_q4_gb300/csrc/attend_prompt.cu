@@ -594,12 +594,22 @@ cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& de
 
 }  // namespace
 
-// bfloat16 rows, heads of 64 or 128, and blocks of 256 rows for at least half the SMs (fewer leave the keys
-// unsplit on idle SMs, where the kernel for few rows splits them).
+// bfloat16 rows, heads of 64 or 128, where this kernel's time by the call's bounds is the shorter one.  Its CTAs go
+// through all keys that their 256 rows see (about 1.9 us a tile of 128 keys, 1.5 us with one row tile), in waves
+// over the SMs, from about 8 us on; the kernel for few rows splits the keys and reads them once for each 16
+// rows (about 2 ns for 32 keys of 16 rows over the whole GPU), from about 9 us on.  Measured, that kernel against
+// this one, 32 heads over 8 of 128: one sequence of 2048 tokens, 64 rows 34 against 40 us, 128 rows 47 against
+// 40, 1024 rows 259 against 40; 64 sequences of 4096 tokens, 4 rows each 141 against 203 us, 8 rows 261
+// against 204, 16 rows 498 against 207; 4 prompts of 128 tokens 35 against 15 us.
 bool attend_prompt_supported(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev) {
-  const long long group = a.heads / c.kv_heads;
-  return x_bf16 && c.head_dim <= 128 && c.max_rows * group >= 128 &&
-         c.rows * group / (2 * kTileRows) * c.kv_heads >= dev.sm_count / 2;
+  if (!x_bf16 || c.head_dim > 128) return false;
+  const long long span = a.window > 0 && (long long)a.window + c.max_rows < c.max_len ? a.window + c.max_rows : c.max_len;
+  const long long rows = (c.rows * (a.heads / c.kv_heads) + c.n_seq - 1) / c.n_seq;  // of a sequence and head, on average
+  const long long heads = (long long)c.n_seq * c.kv_heads;
+  const long long waves = (heads * ((rows + 2 * kTileRows - 1) / (2 * kTileRows)) + dev.sm_count - 1) / dev.sm_count;
+  const long long here = 8000 + waves * ((span + kKeys - 1) / kKeys) * (rows > kTileRows ? 1900 : 1500);
+  const long long there = 9000 + 2 * heads * ((rows + 15) / 16) * ((span + 31) / 32);
+  return here < there;
 }
 
 cudaError_t launch_attend_prompt(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {

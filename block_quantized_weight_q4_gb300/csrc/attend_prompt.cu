@@ -220,6 +220,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     fence_mbar_init();
   }
   if (warp == 12) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  // the first loads of the roles are under way while the CTA sets up: a softmax thread's row of q, the page of a
+  // group of keys and its scales
+  const int row_q = rho0 + (warp >> 2) * kTileRows + (threadIdx.x & 127);  // of warps 0-7
+  const bool row_live = warp < 8 && row_q < sq.n * group;
+  const int row_i = row_live ? row_q / group : 0;
+  const int row_head = kvh * group + (row_live ? row_q - row_i * group : 0);
+  uint4 qraw[D / 8];
+  if (row_live) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (sq.row0 + row_i) * a.q_stride +
+                                                      (long long)row_head * D);
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k) qraw[k] = __ldg(src + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k) qraw[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const int32_t* page_row = c.page_table + (long long)s * c.table_stride;
+  auto page_of = [&](int id, int key) {  // a page id outside the cache is recorded and not followed; -1: none
+    if ((unsigned)id < (unsigned)c.n_pages) return id;
+    if (lane < 8 && key < je * kKeys && key < sq.len) record_status(c.status, QMV_E_ARG);
+    return -1;
+  };
+  int id = -1;
+  float gk = 0.f, gv = 0.f;
+  if (warp == 13) {
+    const int key = jb * kKeys + 16 * lane;
+    if (lane < 8 && key < sq.len) id = __ldg(page_row + (key >> c.page_shift));
+    id = page_of(id, key);
+    if (id >= 0) {
+      gk = __ldg(c.k_scale + (long long)id * c.kv_heads + kvh);
+      gv = __ldg(c.v_scale + (long long)id * c.kv_heads + kvh);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -231,9 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     const int q = warp >> 2;
     if (q < n_tiles) {
       const int r = threadIdx.x & 127;
-      const int rho = rho0 + q * kTileRows + r;
-      const bool live = rho < sq.n * group;
-      const int i = live ? rho / group : 0;
+      const bool live = row_live;
+      const int i = row_i;
       const int end = !live ? 0 : a.causal ? first + i + 1 : sq.len;
       const int beg = a.window > 0 ? first + i - a.window + 1 : 0;
       // keys that every row of this tile sees
@@ -246,11 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       float rowc;
       {
         float amax = 0.f;
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) +
-                              (sq.row0 + (live ? rho / group : 0)) * a.q_stride + (long long)(kvh * group + (live ? rho % group : 0)) * D;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
-          const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = qraw[k];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         const uint32_t dst = sbase + L::kQ + q * L::kTile + r * 128;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
-          const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = qraw[k];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
           uint32_t h[4];
 #pragma unroll
@@ -371,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       if (ok) {
         tc_fence_after();
         const float inv = l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l;
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + (sq.row0 + i) * a.out_stride + (long long)(kvh * group + (live ? rho % group : 0)) * D;
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + (sq.row0 + i) * a.out_stride + (long long)row_head * D;
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {
           uint32_t v[16], w[8];
@@ -505,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       // this head's levels of it, one contiguous run
       const bool leader = lane < 8 && ((16 * lane) & (c.page_tokens - 1)) == 0;
       const uint32_t bytes = (uint32_t)(c.page_tokens * D);
-      const int32_t* page_row = c.page_table + (long long)s * c.table_stride;
       const long long page_stride = (long long)c.kv_heads * c.page_tokens * D;
       const int8_t* kbase = c.k + (long long)kvh * c.page_tokens * D;
       const int8_t* vbase = c.v + (long long)kvh * c.page_tokens * D;
@@ -514,14 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         const int key = (jb + n) * kKeys + 16 * lane;
         return lane < 8 && n < keys && key < sq.len ? __ldg(page_row + (key >> c.page_shift)) : -1;
       };
-      auto check = [&](int id, int n) {  // a page id outside the cache is recorded and not followed
-        if ((unsigned)id < (unsigned)c.n_pages) return id;
-        if (lane < 8 && n < keys && (jb + n) * kKeys + 16 * lane < sq.len) record_status(c.status, QMV_E_ARG);
-        return -1;
-      };
-      int id = check(look(0), 0);
-      float gk = id >= 0 ? __ldg(c.k_scale + (long long)id * c.kv_heads + kvh) : 0.f;
-      float gv = id >= 0 ? __ldg(c.v_scale + (long long)id * c.kv_heads + kvh) : 0.f;
       int copied_k = 0, copied_v = 0;
       for (int n = 0; n < keys; ++n) {
         const int next = look(n + 1);
@@ -551,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kTableFull + n % kTableStages);
-        id = check(next, n + 1);
+        id = page_of(next, (jb + n + 1) * kKeys + 16 * lane);
         gk = id >= 0 ? __ldg(c.k_scale + (long long)id * c.kv_heads + kvh) : 0.f;
         gv = id >= 0 ? __ldg(c.v_scale + (long long)id * c.kv_heads + kvh) : 0.f;
       }

@@ -56,6 +56,7 @@ struct Smem {
   static constexpr int kBars = kTable + kTableStages * 8 * 16;
   static constexpr int kMisc = kBars + 24 * 8;
   static constexpr int kBytes = kMisc + 32 + 1024;   // and room to align to 1024
+  static_assert(kBytes <= 227 * 1024, "one CTA's shared memory");
 };
 
 // Barriers.
@@ -247,11 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   if (warp == 13) {
     const int key = jb * kKeys + 16 * lane;
     if (lane < 8 && key < sq.len) id = __ldg(page_row + (key >> c.page_shift));
-    id = page_of(id, key);
-    if (id >= 0) {
-      gk = __ldg(c.k_scale + (long long)id * c.kv_heads + kvh);
-      gv = __ldg(c.v_scale + (long long)id * c.kv_heads + kvh);
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -401,8 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       if (ok) {
         tc_fence_after();
         const float inv = l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l;
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + (sq.row0 + i) * a.out_stride + (long long)row_head * D;
-#pragma unroll
+        // through the rows' place in shared memory, where no product reads any more, so that whole rows leave (a
+        // row a lane takes a pass of the cache's tags for each lane)
+        constexpr int kLanes = D / 8, kStep = 32 / kLanes, kLoads = 32 / kStep;
+        const uint32_t stage = sbase + L::kQ + q * L::kTile + 32 * (warp & 3) * (2 * D);
+#pragma unroll 2
         for (int b = 0; b < D / 16; ++b) {
           uint32_t v[16], w[8];
           tmem_ld16(ot + 16 * b, v);
@@ -410,10 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             w[e] = pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-          if (live) {
-            *reinterpret_cast<uint4*>(dst + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + 16 * b + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+          sts_u32x4(stage + lane * (2 * D) + (((2 * b) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+          sts_u32x4(stage + lane * (2 * D) + (((2 * b + 1) ^ (lane & 7)) << 4), w[4], w[5], w[6], w[7]);
+        }
+        __syncwarp();
+        const long long row_dst = live ? (sq.row0 + i) * a.out_stride + (long long)row_head * D : -1;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+          const int row = x * kStep + lane / kLanes;
+          const long long at = __shfl_sync(0xffffffffu, row_dst, row);
+          uint32_t w[4];
+          lds_u32x4(stage + row * (2 * D) + (((lane % kLanes) ^ (row & 7)) << 4), w);
+          if (at >= 0)
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) + lane % kLanes) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
@@ -543,6 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         const int key = (jb + n) * kKeys + 16 * lane;
         return lane < 8 && n < keys && key < sq.len ? __ldg(page_row + (key >> c.page_shift)) : -1;
       };
+      id = page_of(id, jb * kKeys + 16 * lane);
+      if (id >= 0) {
+        gk = __ldg(c.k_scale + (long long)id * c.kv_heads + kvh);
+        gv = __ldg(c.v_scale + (long long)id * c.kv_heads + kvh);
+      }
       int copied_k = 0, copied_v = 0;
       for (int n = 0; n < keys; ++n) {
         const int next = look(n + 1);

@@ -208,19 +208,26 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   const int quads = (n - head) / 4;
   const float4* xv = reinterpret_cast<const float4*>(x + head);
   const int q0 = (int)((long long)quads * part / n_parts), q1 = (int)((long long)quads * (part + 1) / n_parts);
+  float4 next[4];  // the batch after the one at hand is on its way meanwhile
+  auto load = [&](int q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int qi = q + 32 * i + lane;
+      next[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (qi < q1) next[i] = __ldg(xv + qi);
+    }
+  };
+  load(q0 + wid * 128);
   for (int q = q0 + wid * 128; q < q1; q += kWarps * 128) {
     float v[kBatch];
     int live = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int qi = q + 32 * i + lane;
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (qi < q1) {
-        f = __ldg(xv + qi);
-        live = 4 * i + 4;
-      }
+      const float4 f = next[i];
+      if (q + 32 * i + lane < q1) live = 4 * i + 4;
       v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
     }
+    load(q + kWarps * 128);
     take(v, live, [&](int l, int e) { return (uint32_t)(head + 4 * (q + 32 * (e >> 2) + l) + (e & 3)); });
   }
   if (part == 0 && wid == 0) {

@@ -30,14 +30,10 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
   const int pi = (first >> c.page_shift) + blockIdx.x;
   const int begin = pi << c.page_shift;
   if (begin >= q.len || q.n == 0) return;
-  const int id = kv_page(c, s, pi);
-  if (id < 0) return;
+  // the rows are asked for before the page's id is looked at
+  const int id = __ldg(c.page_table + (long long)s * c.table_stride + pi);
   const int lo = first > begin ? first - begin : 0;
   const int hi = q.len - begin < c.page_tokens ? q.len - begin : c.page_tokens;
-  const long long at = (long long)id * c.kv_heads + head;
-  int8_t* lev = (is_v ? c.v : c.k) + at * c.page_tokens * D;
-  float* scale = (is_v ? c.v_scale : c.k_scale) + at;
-  const float had = lo > 0 ? *scale : 0.f;
   const long long stride = is_v ? v_stride : k_stride;
   const int pieces = (hi - lo) * kRow;
   const long long x0 = (q.row0 + (begin + lo - first)) * stride + (long long)head * D;
@@ -54,6 +50,14 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
       for (int k = 0; k < (XB ? 1 : 2); ++k) x[i][k] = __ldg(g + k);
     }
   }
+  if (id < 0 || id >= c.n_pages) {
+    record_status(c.status, QMV_E_ARG);
+    return;
+  }
+  const long long at = (long long)id * c.kv_heads + head;
+  int8_t* lev = (is_v ? c.v : c.k) + at * c.page_tokens * D;
+  float* scale = (is_v ? c.v_scale : c.k_scale) + at;
+  const float had = lo > 0 ? *scale : 0.f;
   // value e of piece i
   auto value = [&](int i, int e) -> float {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i][0]);

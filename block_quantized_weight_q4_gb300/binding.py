@@ -592,6 +592,7 @@ class KvCache:
         self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.n_pages,
                             self.kv_heads, self.head_dim, self.page_tokens)
         self._p = ctypes.addressof(self._c)
+        self.device = k.device
 
     @classmethod
     def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -636,9 +637,11 @@ class KvBatch:
 
 def _head_rows(t, heads, dim, rows, what):
     """The row stride of a (rows, heads, dim) tensor whose rows are contiguous."""
-    if tuple(t.shape) != (rows, heads, dim) or (rows > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
-        raise ValueError(f"{what} must be a ({rows}, {heads}, {dim}) tensor with contiguous rows")
-    return t.stride(0) if rows > 1 else heads * dim
+    if tuple(t.shape) == (rows, heads, dim):
+        row, head, value = t.stride()
+        if rows == 0 or (value == 1 and (head == dim or heads == 1)):
+            return row if rows > 1 else heads * dim
+    raise ValueError(f"{what} must be a ({rows}, {heads}, {dim}) tensor with contiguous rows")
 
 
 def kv_write(cache: KvCache, batch: KvBatch, k, v, stream=None):
@@ -660,13 +663,13 @@ def kv_read(cache: KvCache, batch: KvBatch, dtype=None, k=None, v=None, stream=N
     if dtype is None:
         dtype = torch.bfloat16 if k is None else k.dtype
     shape = (batch.rows, cache.kv_heads, cache.head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.k.device)
-    if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.k.device)
     for t in (k, v):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous()):
             raise ValueError("k and v must be contiguous (rows, kv_heads, head_dim) tensors of the asked type")
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
     st = load_library().qmv_kv_read(cache._p, batch._p, _x_dtype(k), k.data_ptr(), v.data_ptr(),
                                     _raw_stream(stream, k.get_device()))
     _check(st, "qmv_kv_read")
@@ -684,9 +687,11 @@ def attend(cache: KvCache, batch: KvBatch, q, out=None, scale=None, causal: bool
     qs = _head_rows(q, heads, cache.head_dim, batch.rows, "q")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype:
-        raise ValueError("out must have q's type")
-    os_ = _head_rows(out, heads, cache.head_dim, batch.rows, "out")
+        os_ = heads * cache.head_dim
+    else:
+        if out.dtype != q.dtype:
+            raise ValueError("out must have q's type")
+        os_ = _head_rows(out, heads, cache.head_dim, batch.rows, "out")
     st = load_library().qmv_attend(cache._p, batch._p, heads, _x_dtype(q), q.data_ptr(), qs,
                                    cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
                                    out.data_ptr(), os_, _raw_stream(stream, q.get_device()))

@@ -75,7 +75,12 @@ cudaError_t cached_workspace(std::map<std::pair<int, cudaStream_t>, Workspace>& 
   }
   Workspace w;
   workspace_carve(base, bytes, counters, &w);
-  cache.emplace(key, w);
+  try {
+    cache.emplace(key, w);
+  } catch (...) {  // nothing is thrown through the C entry points
+    cudaFree(base);
+    return cudaErrorMemoryAllocation;
+  }
   *ws = w;
   return cudaSuccess;
 }

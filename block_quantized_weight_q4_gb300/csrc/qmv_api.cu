@@ -722,6 +722,7 @@ int qmv_attend(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int heads, 
   const int st = make_kv(cache, batch, &c);
   if (st != QMV_OK) return st;
   if (heads <= 0 || heads % c.kv_heads != 0 || heads > 65535) return QMV_E_SHAPE;
+  if (c.rows > (INT32_MAX - 4096) / (heads / c.kv_heads)) return QMV_E_SHAPE;
   if (c.rows == 0 || c.max_rows == 0) return QMV_OK;
   if (q == nullptr || out == nullptr) return QMV_E_ARG;
   const int qs = row_stride_status(q, q_stride, heads, c.head_dim, x_dtype, c.rows);

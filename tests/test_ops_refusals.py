@@ -73,6 +73,8 @@ def test_write_read_attend_arguments(lib):
         cp, bp, heads, xd, q, qs, sc, 1, win, o, os, None)
     assert a(xd=2) == FORMAT and a(heads=3) == SHAPE and a(heads=0) == SHAPE and a(heads=70000) == SHAPE
     assert a(q=None) == ARG and a(o=None) == ARG and a(win=-1) == ARG and a(sc=float("inf")) == ARG and a(sc=float("nan")) == ARG
+    c2, b2 = kv(dict(rows=2 ** 30, max_rows=1))
+    assert lib.qmv_attend(ctypes.addressof(c2), ctypes.addressof(b2), 8, 1, P, 512, 0.1, 1, 0, P, 512, None) == SHAPE
     assert a(qs=500) == SHAPE and a(os=8) == SHAPE and a(q=P + 2) == ALIGN and a(qs=516) == ALIGN and a(o=P + 8) == ALIGN
 
 

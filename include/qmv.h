@@ -604,8 +604,9 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
 
 /* Softmax attention of the call's rows over the cache.  q: row r of head h at element
  * r * q_stride + h * head_dim; heads a multiple of kv_heads (at most 65535, and
- * rows * heads / kv_heads below 2^31 - 4096), head h reads key/value head h / (heads / kv_heads); q and out share x_dtype (QMV_X_F32 or QMV_X_BF16); out likewise with
- * out_stride, rows 16-byte aligned; out must not overlap q.
+ * rows * heads / kv_heads below 2^31 - 4096), head h reads key/value head h / (heads / kv_heads);
+ * q and out share x_dtype (QMV_X_F32 or QMV_X_BF16); out likewise with out_stride, rows 16-byte
+ * aligned; out must not overlap q.
  *   z_j = scale * q . K_j,  p = softmax of z over the keys that the mask leaves,  out = sum_j p_j V_j
  * with K_j = level * scale of the cache.  The row at position p sees the keys j <= p (causal != 0)
  * or every key of its sequence (causal = 0), and with window > 0 only those with

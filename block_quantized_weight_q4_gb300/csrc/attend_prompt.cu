@@ -155,10 +155,23 @@ __device__ __forceinline__ int blocks_of(const KvSeq& q, int group) {
   return (int)(((long long)q.n * group + 2 * kTileRows - 1) / (2 * kTileRows));
 }
 
-// PG: keys that share a page's scales, 16 or 64 (pages of 64 and 128 tokens).
-template <int D, int PG>
+// Blocks from `whole` on (in the order of the grid) are cut along their keys into up to `split` parts of at
+// least kMinPart tiles, whose unnormalised outputs meet in the workspace: a part's area is [dim / 4][256 rows] of
+// four floats, then the rows' references and sums.
+struct SplitPlan {
+  int whole;
+  int split;
+  unsigned* counters;  // eight a cut block (one a softmax warp), zero between launches
+  float* parts;
+};
+constexpr int kMinPart = 4;
+
+// PG: keys that share a page's scales, 16 or 64 (pages of 64 and 128 tokens).  CUT: some blocks are cut (the code
+// that joins their parts costs the launches without them 3%: three prompts of up to 2048 tokens 90 against 87 us).
+template <int D, int PG, bool CUT>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ KvRef c,
-                                                                    const __grid_constant__ AttendArgs a) {
+                                                                    const __grid_constant__ AttendArgs a,
+                                                                    const SplitPlan plan) {
   using L = Smem<D>;
   constexpr int kPieces = D / 16;           // 16-byte pieces of a row of levels
   constexpr int kRowsWarp = 32 / kPieces;   // rows a converting warp takes at a time
@@ -177,8 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   const int group = a.heads / c.kv_heads;
 
   // the CTA's block: heads fastest, a sequence's last (longest) blocks first; every warp looks it up
-  const int kvh = blockIdx.x % c.kv_heads;
-  const int want = blockIdx.x / c.kv_heads;
+  const int cut = CUT ? (int)blockIdx.x - plan.whole : -1;  // counted over the parts of cut blocks
+  const int item = cut < 0 ? (int)blockIdx.x : plan.whole + cut / plan.split;
+  const int kvh = item % c.kv_heads;
+  const int want = item / c.kv_heads;
   int s = -1, rb = 0;
   for (int s0 = 0, base = 0; s0 < c.n_seq && s < 0; s0 += 32) {
     const int si = s0 + lane;
@@ -207,7 +222,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   const int i_lo = rho0 / group, i_hi = (rho0 + rows_all - 1) / group;
   const int any_end = a.causal ? first + i_hi + 1 : sq.len;
   const int any_begin = a.window > 0 && first + i_lo - a.window + 1 > 0 ? first + i_lo - a.window + 1 : 0;
-  const int jb = any_begin / kKeys, je = (any_end + kKeys - 1) / kKeys;
+  int jb = any_begin / kKeys, je = (any_end + kKeys - 1) / kKeys;
+  int parts = 1, part = 0;
+  if (CUT && cut >= 0) {
+    const int tiles = je - jb;
+    parts = tiles / kMinPart < plan.split ? (tiles / kMinPart > 1 ? tiles / kMinPart : 1) : plan.split;
+    part = cut % plan.split;
+    if (part >= parts) return;
+    je = jb + tiles * (part + 1) / parts;
+    jb += tiles * part / parts;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -403,32 +427,99 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       if (ok) ok = __all_sync(0xffffffffu, pwait(bars + kDone, 0u, failed));
       if (ok) {
         tc_fence_after();
-        const float inv = l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l;
-        // through the rows' place in shared memory, where no product reads any more, so that whole rows leave (a
-        // row a lane takes a pass of the cache's tags for each lane)
-        constexpr int kLanes = D / 8, kStep = 32 / kLanes, kLoads = 32 / kStep;
-        const uint32_t stage = sbase + L::kQ + q * L::kTile + 32 * (warp & 3) * (2 * D);
+        bool store = true;
+        const float* others = nullptr;
+        float* area = nullptr;
+        constexpr int kPartFloats = 2 * kTileRows * (D + 2);
+        const int row256 = q * kTileRows + r;
+        if (CUT && parts > 1) {
+          // this part's rows; the warp whose rows' last part this is puts them together
+          area = plan.parts + (long long)(cut - part) * kPartFloats;  // of the block's first part
+          float* mine = area + (long long)part * kPartFloats;
 #pragma unroll 2
-        for (int b = 0; b < D / 16; ++b) {
-          uint32_t v[16], w[8];
-          tmem_ld16(ot + 16 * b, v);
-          tmem_ld_wait();
+          for (int b = 0; b < D / 16; ++b) {
+            uint32_t v[16];
+            tmem_ld16(ot + 16 * b, v);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-          sts_u32x4(stage + lane * (2 * D) + (((2 * b) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-          sts_u32x4(stage + lane * (2 * D) + (((2 * b + 1) ^ (lane & 7)) << 4), w[4], w[5], w[6], w[7]);
+            for (int e = 0; e < 4; ++e)
+              __stcg(reinterpret_cast<uint4*>(mine) + (4 * b + e) * (2 * kTileRows) + row256,
+                     make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+          }
+          __stcg(mine + 2 * kTileRows * D + row256, ref);
+          __stcg(mine + 2 * kTileRows * (D + 1) + row256, l);
+          __threadfence();
+          __syncwarp();
+          unsigned seen = 0;
+          if (lane == 0) {
+            unsigned* counter = plan.counters + 8 * (cut / plan.split) + warp;
+            seen = atomicAdd(counter, 1u);
+            if (seen == (unsigned)(parts - 1)) *counter = 0;
+          }
+          store = __shfl_sync(0xffffffffu, seen, 0) == (unsigned)(parts - 1);
+          __threadfence();
+          if (store) {
+            others = area;
+            ref = -INFINITY;
+            for (int p = 0; p < parts; ++p)
+              ref = fmaxf(ref, __ldcg(area + (long long)p * kPartFloats + 2 * kTileRows * D + row256));
+            l = 0.f;
+            for (int p = 0; p < parts; ++p) {
+              const float* from = area + (long long)p * kPartFloats + 2 * kTileRows * D + row256;
+              const float pr = __ldcg(from);
+              if (pr != -INFINITY) l = fmaf(__ldcg(from + 2 * kTileRows), ex2(pr - ref), l);
+            }
+          }
         }
-        __syncwarp();
-        const long long row_dst = live ? (sq.row0 + i) * a.out_stride + (long long)row_head * D : -1;
+        if (store) {
+          const float inv = l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l;
+          // through the rows' place in shared memory, where no product reads any more, so that whole rows leave (a
+          // row a lane takes a pass of the cache's tags for each lane)
+          constexpr int kLanes = D / 8, kStep = 32 / kLanes, kLoads = 32 / kStep;
+          const uint32_t stage = sbase + L::kQ + q * L::kTile + 32 * (warp & 3) * (2 * D);
+#pragma unroll 2
+          for (int b = 0; b < D / 16; ++b) {
+            uint32_t v[16], w[8];
+            if (!CUT || others == nullptr) {
+              tmem_ld16(ot + 16 * b, v);
+              tmem_ld_wait();
+            } else {
+              float y[16];
 #pragma unroll
-        for (int x = 0; x < kLoads; ++x) {
-          const int row = x * kStep + lane / kLanes;
-          const long long at = __shfl_sync(0xffffffffu, row_dst, row);
-          uint32_t w[4];
-          lds_u32x4(stage + row * (2 * D) + (((lane % kLanes) ^ (row & 7)) << 4), w);
-          if (at >= 0)
-            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) + lane % kLanes) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 16; ++e) y[e] = 0.f;
+              for (int p = 0; p < parts; ++p) {
+                const float* from = others + (long long)p * kPartFloats;
+                const float pr = __ldcg(from + 2 * kTileRows * D + row256);
+                const float f = pr == -INFINITY ? 0.f : ex2(pr - ref);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(from) + (4 * b + e) * (2 * kTileRows) + row256);
+                  y[4 * e] = fmaf(x.x, f, y[4 * e]);
+                  y[4 * e + 1] = fmaf(x.y, f, y[4 * e + 1]);
+                  y[4 * e + 2] = fmaf(x.z, f, y[4 * e + 2]);
+                  y[4 * e + 3] = fmaf(x.w, f, y[4 * e + 3]);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(y[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+            sts_u32x4(stage + lane * (2 * D) + (((2 * b) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            sts_u32x4(stage + lane * (2 * D) + (((2 * b + 1) ^ (lane & 7)) << 4), w[4], w[5], w[6], w[7]);
+          }
+          __syncwarp();
+          const long long row_dst = live ? (sq.row0 + i) * a.out_stride + (long long)row_head * D : -1;
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const int row = x * kStep + lane / kLanes;
+            const long long at = __shfl_sync(0xffffffffu, row_dst, row);
+            uint32_t w[4];
+            lds_u32x4(stage + row * (2 * D) + (((lane % kLanes) ^ (row & 7)) << 4), w);
+            if (at >= 0)
+              *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) + lane % kLanes) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
     }
@@ -612,13 +703,46 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   }
 }
 
-template <int D, int PG>
-cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  auto kern = attend_prompt_kernel<D, PG>;
+// How a call's blocks go over the SMs, by its bounds, in ns: about 1.55 us a tile of 128 keys for two row tiles, 1.35 us
+// for one, 6 us more a wave of blocks, 14 us more a wave of cut ones (they write and read their parts).  Blocks that
+// fill whole waves stay whole; the others, or all of a call with fewer blocks than SMs, are cut along the keys
+// where that saves a tenth.  Measured, whole against cut, 32 heads over 8 of 128: 256 rows over 16384 tokens 224 against
+// 74 us, 512 rows over 16384 225 against 126, 64 rows over 2048 40 against 25; 2048 rows over 16384 (256 blocks)
+// 393 against 409, 640 rows over 2048 (80 blocks) 35 against 49.
+struct Estimate {
+  long long items;  // blocks of the grid before any cut, at most: exact for one sequence, else a block more for each
+  long long whole, split, ns;
+};
+long long part_floats(const KvRef& c) { return 2LL * kTileRows * (c.head_dim + 2); }
+Estimate estimate(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev) {
+  const long long group = a.heads / c.kv_heads, all = c.rows * group, block = 2 * kTileRows;
+  const long long items = (c.n_seq == 1 ? (all + block - 1) / block : all / block + c.n_seq) * c.kv_heads;
+  const long long span = a.window > 0 && (long long)a.window + c.max_rows < c.max_len ? a.window + c.max_rows : c.max_len;
+  const long long rows = (all + c.n_seq - 1) / c.n_seq;  // of a sequence and head, on average
+  const long long blocks = (long long)c.n_seq * c.kv_heads * ((rows + block - 1) / block);
+  const long long tiles = (span + kKeys - 1) / kKeys, turn = rows > kTileRows ? 1550 : 1350, sms = dev.sm_count;
+  Estimate best{items, items, 1, 3000 + (blocks + sms - 1) / sms * (tiles * turn + 6000)};
+  // the last blocks of whole prompts are short ones: the order of the grid already evens them out
+  if (blocks >= sms && 2LL * c.max_rows > span) return best;
+  const long long whole = blocks / sms * sms, rest = blocks - whole, before = 3000 + whole / sms * (tiles * turn + 6000);
+  const long long areas = (long long)(kPromptPartialBytes / sizeof(float)) / part_floats(c);
+  const long long most = best.ns / 10 * 9;
+  for (long long s = 2; s <= 16 && tiles >= s * kMinPart; ++s) {
+    if (whole >= items || (items - whole) * s > areas || (items - whole) * 8 > kPromptCounters) break;
+    const long long ns = before + (rest * s + sms - 1) / sms * ((tiles + s - 1) / s * turn + 14000);
+    if (ns < most && ns < best.ns) best = Estimate{items, whole, s, ns};
+  }
+  return best;
+}
+
+template <int D, int PG, bool CUT>
+cudaError_t launch_kernel(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, const SplitPlan& plan, long long grid,
+                          cudaStream_t stream) {
+  auto kern = attend_prompt_kernel<D, PG, CUT>;
   constexpr int kSmem = Smem<D>::kBytes;
   static std::mutex mu;
   static bool ready[64] = {};
-  if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidValue;
+  if (dev.device < 0 || dev.device >= 64 || grid > INT32_MAX) return cudaErrorInvalidValue;
   if ((size_t)kSmem > dev.smem_optin) return cudaErrorInvalidConfiguration;
   {
     std::lock_guard<std::mutex> lock(mu);
@@ -628,29 +752,32 @@ cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& de
       ready[dev.device] = true;
     }
   }
-  const long long blocks = c.rows * (a.heads / c.kv_heads) / (2 * kTileRows) + c.n_seq;
-  if (blocks * c.kv_heads > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_dependent(kern, dim3((unsigned)(blocks * c.kv_heads)), kThreads, kSmem, stream, c, a);
+  return launch_dependent(kern, dim3((unsigned)grid), kThreads, kSmem, stream, c, a, plan);
+}
+
+template <int D, int PG>
+cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  const Estimate e = estimate(c, a, dev);
+  Workspace ws;
+  if (e.split == 1 || stream_prompt_workspace(dev, stream, &ws) != cudaSuccess)
+    return launch_kernel<D, PG, false>(c, a, dev, SplitPlan{}, e.items, stream);
+  return launch_kernel<D, PG, true>(c, a, dev, SplitPlan{(int)e.whole, (int)e.split, ws.counters, ws.partials},
+                                    e.whole + (e.items - e.whole) * e.split, stream);
 }
 
 }  // namespace
 
-// bfloat16 rows, heads of 64 or 128, where this kernel's time by the call's bounds is the shorter one.  Its CTAs go
-// through all keys that their 256 rows see (about 1.9 us a tile of 128 keys, 1.5 us with one row tile), in waves
-// over the SMs, from about 8 us on; the kernel for few rows splits the keys and reads them once for each 16
-// rows (about 2 ns for 32 keys of 16 rows over the whole GPU), from about 9 us on.  Measured, that kernel against
-// this one, 32 heads over 8 of 128: one sequence of 2048 tokens, 64 rows 34 against 40 us, 128 rows 47 against
-// 40, 1024 rows 259 against 40; 64 sequences of 4096 tokens, 4 rows each 141 against 203 us, 8 rows 261
-// against 204, 16 rows 498 against 207; 4 prompts of 128 tokens 35 against 15 us.
+// bfloat16 rows, heads of 64 or 128, where this kernel's estimated time is the shorter one; the kernel for few rows
+// reads the keys once for each 16 rows (over the whole GPU about 2 ns for 32 keys of 16 rows), from about 9 us on.
+// Measured, that kernel against this one, 32 heads over 8 of 128: one sequence of 2048 tokens, 64 rows 34 against
+// 25 us, 1024 rows 259 against 36; 64 sequences of 4096 tokens, 4 rows each 141 against 203 us, 8 rows 261
+// against 206, 16 rows 498 against 207; 4 prompts of 128 tokens 35 against 12 us.
 bool attend_prompt_supported(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev) {
   if (!x_bf16 || c.head_dim > 128) return false;
   const long long span = a.window > 0 && (long long)a.window + c.max_rows < c.max_len ? a.window + c.max_rows : c.max_len;
-  const long long rows = (c.rows * (a.heads / c.kv_heads) + c.n_seq - 1) / c.n_seq;  // of a sequence and head, on average
-  const long long heads = (long long)c.n_seq * c.kv_heads;
-  const long long waves = (heads * ((rows + 2 * kTileRows - 1) / (2 * kTileRows)) + dev.sm_count - 1) / dev.sm_count;
-  const long long here = 8000 + waves * ((span + kKeys - 1) / kKeys) * (rows > kTileRows ? 1900 : 1500);
-  const long long there = 9000 + 2 * heads * ((rows + 15) / 16) * ((span + 31) / 32);
-  return here < there;
+  const long long rows = (c.rows * (a.heads / c.kv_heads) + c.n_seq - 1) / c.n_seq;
+  const long long there = 9000 + 2LL * c.n_seq * c.kv_heads * ((rows + 15) / 16) * ((span + 31) / 32);
+  return estimate(c, a, dev).ns < there;
 }
 
 cudaError_t launch_attend_prompt(const KvRef& c, const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {

@@ -49,6 +49,7 @@ std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_pws;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_xws;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_sws;
+std::map<std::pair<int, cudaStream_t>, Workspace> g_aws;
 
 cudaError_t cached_workspace(std::map<std::pair<int, cudaStream_t>, Workspace>& cache, const DeviceInfo& dev,
                              cudaStream_t stream, size_t bytes, int counters, Workspace* ws) {
@@ -92,6 +93,10 @@ cudaError_t stream_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspa
 
 cudaError_t stream_prefill_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws) {
   return cached_workspace(g_pws, dev, stream, kPrefillWorkspaceBytes, kPrefillCounters, ws);
+}
+
+cudaError_t stream_prompt_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws) {
+  return cached_workspace(g_aws, dev, stream, workspace_counter_bytes(kPromptCounters) + kPromptPartialBytes, kPromptCounters, ws);
 }
 
 cudaError_t stream_serve_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws) {
@@ -305,7 +310,7 @@ cudaError_t reset_workspaces() {
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  for (auto* cache : {&g_ws, &g_pws, &g_sws}) {
+  for (auto* cache : {&g_ws, &g_pws, &g_sws, &g_aws}) {
     for (auto& kv : *cache) {
       if (kv.first.first != dev) continue;
       err = cudaMemset(kv.second.counters, 0, workspace_counter_bytes(kv.second.max_counters));
@@ -337,7 +342,7 @@ cudaError_t prepare_stream_workspaces(const DeviceInfo& dev, cudaStream_t stream
 cudaError_t release_stream_workspaces(int device, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
   cudaError_t first = cudaSuccess;
-  for (auto* cache : {&g_ws, &g_pws, &g_xws, &g_sws}) {
+  for (auto* cache : {&g_ws, &g_pws, &g_xws, &g_sws, &g_aws}) {
     auto it = cache->find(std::make_pair(device, stream));
     if (it == cache->end()) continue;
     const cudaError_t err = cudaFree(it->second.counters);  // the allocation's base

@@ -49,21 +49,6 @@ __device__ __forceinline__ int kv_page(const KvRef& c, int s, int i) {
   return id;
 }
 
-// The sequence that row r of the call belongs to: the last s with starts[s] <= r.
-__device__ __forceinline__ int kv_seq_of_row(const KvRef& c, long long r) {
-  if (c.starts == nullptr) return (int)r;
-  int lo = 0, hi = c.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(c.starts + mid) <= r) {
-      lo = mid;
-    } else {
-      hi = mid - 1;
-    }
-  }
-  return lo;
-}
-
 // Eight consecutive values of a row.
 template <bool XB>
 __device__ __forceinline__ void load8(const void* x, long long at, float (&v)[8]) {

@@ -47,6 +47,10 @@ cudaError_t stream_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspa
 cudaError_t stream_prefill_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);
 // The same for the operators between the products (attention, log probabilities).
 cudaError_t stream_serve_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);
+// And for prompt attention whose blocks are cut along the keys (500 parts of 256 rows of 128 values).
+constexpr int kPromptCounters = 4096;
+constexpr size_t kPromptPartialBytes = (size_t)64 << 20;
+cudaError_t stream_prompt_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);
 // Zero the counters of every workspace of the current device (after a kernel gave up on a
 // bounded wait, a counter may have been left part-way); synchronous.
 cudaError_t reset_workspaces();

@@ -620,10 +620,10 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
  * of at most 2^-32 of it (a key whose weight times V scale is that far below the row's largest counts only
  * to that resolution).  Results do not depend on timing.
  * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream (8 MiB,
- * shared with qmv_logprobs), allocated on the stream's first such call and kept; while a stream
- * without one is being captured, the call does not split (slower; call once on the stream before
- * capturing it).  A captured call keeps to the capturing stream's workspace: its replays must not overlap
- * in time with other calls that use it.
+ * shared with qmv_logprobs; 64 MiB more for prompts of few blocks of rows over many keys), allocated
+ * on the stream's first such call and kept; while a stream without one is being captured, the call
+ * does not split (slower; call once on the stream before capturing it).  A captured call keeps to the
+ * capturing stream's workspace: its replays must not overlap in time with other calls that use it.
  * Returns QMV_OK, QMV_E_FORMAT (x_dtype), QMV_E_ARG (null pointer, negative count, window < 0, scale not
  * finite), QMV_E_SHAPE (the cache's or rows' numbers, heads, strides), QMV_E_ALIGN or QMV_E_CUDA. */
 int qmv_attend(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int heads, int x_dtype, const void *q,

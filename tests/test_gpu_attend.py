@@ -126,6 +126,25 @@ def test_prompts(qmv, heads, kvh, dim, page, lens, counts, causal, window):
     assert bool((got == again).all())
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 1500), (False, 0)])
+@pytest.mark.parametrize("heads,kvh,dim,page,lens,counts", [
+    (8, 2, 128, 64, [5000], [256]),             # few blocks over many keys: each cut along them
+    (32, 8, 64, 16, [2900], [130]),
+    (8, 1, 128, 128, [3000, 40, 2111], [200, 40, 33]),
+    (64, 16, 128, 64, [2100], [700]),           # whole blocks, and the rest cut
+])
+def test_prompts_cut_along_the_keys(qmv, heads, kvh, dim, page, lens, counts, causal, window):
+    rng = np.random.default_rng(dim + window)
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=page)
+    qf, qd = queries(rng, sum(counts), heads, dim, True)
+    b = batch_of(qmv, td, lens, counts)
+    got = qmv.attend(cache, b, qd, causal=causal, window=window)
+    check(twin, table, lens, counts, qf, got, dim ** -0.5, causal, window, True)
+    for _ in range(3):
+        again = qmv.attend(cache, b, qd, causal=causal, window=window)
+        assert bool((got == again).all())
+
+
 def test_many_sequences(qmv):
     """More sequences than a CTA scans at once, empty ones among them, on both kernels."""
     rng = np.random.default_rng(12)

@@ -1,11 +1,12 @@
 // kv_cache.cu -- the paged cache of keys and values in 8 bits: rows written with one scale for each
 // page and head, and read back.
 //
-// Writing is bound by the rows' bytes, and below that by a chain of dependent loads a page (lengths, page id and
-// rows, the old scale) around one reduction: 16384 bfloat16 rows of 8 heads of 128 in 23.4 us (4.3 TB/s, 63% of the
-// measured copy rate; float32 29.3 us, 5.7 TB/s), one row of each of 64 sequences in 3.1 us.  A page, head and
-// side (K or V) is a CTA because its scale is what its rows share.  Reading is a copy that widens: 16 sequences of
-// up to 16384 tokens in 191 us (6.57 TB/s, 97%).
+// Writing is bound by the rows' bytes, and below that by the instructions that a value's level takes (about 7; a third
+// fewer than with conversions, clamps and packs one by one, which took 23.2 us where these take 18.7) and a chain of
+// dependent loads a page (lengths, page id and rows, the old scale) around one reduction: 16384 bfloat16 rows of 8 heads
+// of 128 in 18.7 us (5.4 TB/s, 79% of the measured copy rate; float32 27.5 us, 6.1 TB/s), one row of each of 64
+// sequences in 2.3 us.  A page, head and side (K or V) is a CTA because its scale is what its rows share.  Reading is a
+// copy that widens: 16 sequences of up to 16384 tokens in 191 us (6.57 TB/s, 97%).
 #include <type_traits>
 
 #include "kv.cuh"
@@ -14,12 +15,27 @@ namespace qmv {
 
 namespace {
 
-constexpr int kWritePieces = 8;  // pieces of 8 values that a thread holds
+// Four levels trunc(t) in a word; |t| < 128 (or NaN: 0).
+__device__ __forceinline__ uint32_t pack_levels(float t0, float t1, float t2, float t3) {
+  uint32_t hi, w;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"((int)t3), "r"((int)t2), "r"(0));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w) : "r"((int)t1), "r"((int)t0), "r"(hi));
+  return w;
+}
+// Two values times inv, half a step away from zero.
+__device__ __forceinline__ void step2(float a, float b, uint64_t inv2, float& ta, float& tb) {
+  uint64_t x, h;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(h) : "f"(copysignf(0.5f, a)), "f"(copysignf(0.5f, b)));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(inv2));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(h));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(ta), "=f"(tb) : "l"(x));
+}
 
 // One CTA per (page that receives rows, head, K or V).  The page's scale is the largest its tokens
 // have needed: raised by the new rows, the earlier tokens' levels move to it.  The new rows stay in
-// registers between the maximum and their levels (page_tokens * D / 64 threads), so each is read once.
-template <int D, bool XB>
+// registers between the maximum and their levels (P pieces of 8 values a thread), so each is read once.
+template <int D, bool XB, int P>
 __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ KvRef c, const void* __restrict__ kx,
                                                        long long k_stride, const void* __restrict__ vx,
                                                        long long v_stride) {
@@ -44,9 +60,9 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
   const int pieces = (hi - lo) * kRow;
   const long long x0 = (q.row0 + (begin + lo - first)) * stride + (long long)head * D;
   using Raw = typename std::conditional<XB, uint4, float4>::type;
-  Raw x[kWritePieces][XB ? 1 : 2];
+  Raw x[P][XB ? 1 : 2];
 #pragma unroll
-  for (int i = 0; i < kWritePieces; ++i) {
+  for (int i = 0; i < P; ++i) {
     const int p = threadIdx.x + i * T;
     if (p < pieces) {
       const long long e = x0 + (p / kRow) * stride + (p % kRow) * 8;
@@ -70,12 +86,20 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
     return XB ? __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]);
   };
   float amax = 0.f;
+  uint32_t most = 0u;  // of a thread's bfloat16 values, in pairs
 #pragma unroll
-  for (int i = 0; i < kWritePieces; ++i)
+  for (int i = 0; i < P; ++i)
     if (threadIdx.x + i * T < pieces) {
+      if (XB) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i][0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
+        for (int e = 0; e < 4; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(most) : "r"(w[e] & 0x7fff7fffu));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
+      }
     }
+  if (XB) amax = fmaxf(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
@@ -83,19 +107,18 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
   for (int w = 0; w < (T >> 5); ++w) amax = fmaxf(amax, part[w]);
   const float want = amax < 1e-30f ? 0.f : __fmul_rn(amax, 1.0f / 127.0f);
   const float d = fmaxf(want, had);
-  const float inv = d > 0.f ? __fdiv_rn(1.0f, d) : 0.f;
+  // a scale the cache never gets from its rows (below 1e-30 / 127) leaves no levels
+  const float inv = d > 0x1p-110f ? __fdiv_rn(1.0f, d) : 0.f;
+  uint64_t inv2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
 #pragma unroll
-  for (int i = 0; i < kWritePieces; ++i) {
+  for (int i = 0; i < P; ++i) {
     const int p = threadIdx.x + i * T;
     if (p < pieces) {
-      uint32_t w[2] = {0u, 0u};
+      float t[8];  // (no level passes 127: d is at least the rows' amax * RN(1/127))
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = value(i, e);
-        int l = (int)__fadd_rn(__fmul_rn(f, inv), copysignf(0.5f, f));
-        l = l > 127 ? 127 : (l < -127 ? -127 : l);
-        w[e >> 2] |= (uint32_t)(l & 0xFF) << (8 * (e & 3));
-      }
+      for (int e = 0; e < 8; e += 2) step2(value(i, e), value(i, e + 1), inv2, t[e], t[e + 1]);
+      const uint32_t w[2] = {pack_levels(t[0], t[1], t[2], t[3]), pack_levels(t[4], t[5], t[6], t[7])};
       *reinterpret_cast<uint2*>(lev + (long long)lo * D + 8 * p) = make_uint2(w[0], w[1]);
     }
   }
@@ -183,6 +206,23 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
 }
 
 template <int D, bool XB>
+cudaError_t launch_write(const KvRef& c, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         cudaStream_t stream) {
+  // pages that n rows can fall into, wherever they start in the first
+  const int pages = (c.max_rows + c.page_tokens - 2) / c.page_tokens + 1;
+  const dim3 grid((unsigned)pages, (unsigned)c.n_seq, (unsigned)(2 * c.kv_heads));
+  // pieces of the most rows that a page may receive, over at most 256 threads of 1 or 4, else of 8: 16384 rows of
+  // 8 heads of 128, pages of 16 tokens, 19.3 us with 4 pieces a thread, 23.2 with 8; 256 single rows 4.6 with 1, 6.2
+  // with 8; heads of 256 and pages of 64 (512 threads of 4) 37.0 with 4, 35.0 with 8
+  const int pieces = (c.max_rows < c.page_tokens ? c.max_rows : c.page_tokens) * (D / 8);
+  const int per = pieces <= 64 ? 1 : pieces <= 4 * 256 ? 4 : 8;
+  auto kern = per == 1 ? kv_write_kernel<D, XB, 1> : per == 4 ? kv_write_kernel<D, XB, 4> : kv_write_kernel<D, XB, 8>;
+  // 64 threads at least: they also move a raised page's levels
+  const int threads = pieces <= 64 * per ? 64 : (pieces + 32 * per - 1) / (32 * per) * 32;
+  return launch_dependent(kern, grid, threads, 0, stream, c, k, (long long)k_stride, v, (long long)v_stride);
+}
+
+template <int D, bool XB>
 cudaError_t launch_read(const KvRef& c, void* k, void* v, const DeviceInfo& dev, cudaStream_t stream) {
   constexpr int kRows = 256 / (D / 16);
   // four pieces a thread where that still leaves every SM several CTAs
@@ -199,16 +239,17 @@ cudaError_t launch_read(const KvRef& c, void* k, void* v, const DeviceInfo& dev,
 
 cudaError_t launch_kv_write(const KvRef& c, bool x_bf16, const void* k, int64_t k_stride, const void* v,
                             int64_t v_stride, cudaStream_t stream) {
-  // pages that n rows can fall into, wherever they start in the first
-  const int pages = (c.max_rows + c.page_tokens - 2) / c.page_tokens + 1;
-  const dim3 grid((unsigned)pages, (unsigned)c.n_seq, (unsigned)(2 * c.kv_heads));
-  // threads for the most rows that a page may receive (64 at least: they also move a raised page's levels)
-  int threads = (c.max_rows < c.page_tokens ? c.max_rows : c.page_tokens) * c.head_dim / (8 * kWritePieces);
-  threads = threads < 64 ? 64 : (threads + 31) / 32 * 32;
-  auto kern = c.head_dim == 64    ? (x_bf16 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
-              : c.head_dim == 128 ? (x_bf16 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>)
-                                  : (x_bf16 ? kv_write_kernel<256, true> : kv_write_kernel<256, false>);
-  return launch_dependent(kern, grid, threads, 0, stream, c, k, k_stride, v, v_stride);
+  switch (c.head_dim) {
+    case 64:
+      return x_bf16 ? launch_write<64, true>(c, k, k_stride, v, v_stride, stream)
+                    : launch_write<64, false>(c, k, k_stride, v, v_stride, stream);
+    case 128:
+      return x_bf16 ? launch_write<128, true>(c, k, k_stride, v, v_stride, stream)
+                    : launch_write<128, false>(c, k, k_stride, v, v_stride, stream);
+    default:
+      return x_bf16 ? launch_write<256, true>(c, k, k_stride, v, v_stride, stream)
+                    : launch_write<256, false>(c, k, k_stride, v, v_stride, stream);
+  }
 }
 
 cudaError_t launch_kv_read(const KvRef& c, bool out_bf16, void* k, void* v, const DeviceInfo& dev,

@@ -587,7 +587,8 @@ typedef struct qmv_kv_batch {
  *   had  = the page's scale if it holds tokens from before the call's rows, else 0
  *   d    = max(want, had), stored;  where d > had, the levels of those earlier tokens become
  *          trunc(level * (had / d) + copysign(0.5, level))
- *   level = trunc(x * (1 / d) + copysign(0.5, x)) clamped to +-127, 0 where d is 0.
+ *   level = trunc(x * (1 / d) + copysign(0.5, x)), within +-127; 0 where d is 0 (or below 2^-110, which
+ *          no rows give).
  * A page is written by one sequence only: sequences may share pages that no row of the call falls
  * into.  Each raise of a page's scale moves its earlier levels by at most half a step of the new
  * scale.  x is meant to be finite.  Places of the page after the last row are left as they are.

@@ -145,6 +145,34 @@ def test_prompts_cut_along_the_keys(qmv, heads, kvh, dim, page, lens, counts, ca
         assert bool((got == again).all())
 
 
+def test_cut_prompts_in_captures(qmv):
+    """Captured on a stream that has no workspace the blocks stay whole; after a call on the stream they are
+    cut, in the capture too."""
+    import torch
+    rng = np.random.default_rng(21)
+    lens, counts = [3000], [150]
+    cache, twin, table, td = filled(qmv, lens, 2, 64, 64, seed=9)
+    qf, qd = queries(rng, 150, 8, 64, True)
+    b = batch_of(qmv, td, lens, counts)
+    s = torch.cuda.Stream()
+    got = []
+    for _ in range(2):
+        out = torch.empty_like(qd)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            qmv.attend(cache, b, qd, out=out, stream=s)
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        check(twin, table, lens, counts, qf, out, 64 ** -0.5, True, 0, True)
+        got.append(out)
+        with torch.cuda.stream(s):
+            again = qmv.attend(cache, b, qd, stream=s)
+        torch.cuda.synchronize()
+    assert bool((got[1] == again).all())
+
+
 def test_many_sequences(qmv):
     """More sequences than a CTA scans at once, empty ones among them, on both kernels."""
     rng = np.random.default_rng(12)

@@ -194,3 +194,21 @@ def test_long_cache_offsets_pass_32_bits(qmv):
     step = float(cache.k_scale.max())
     assert float((k - x).abs().max()) <= step * 0.501 and torch.equal(k, v)
     assert not cache.k[1].any() and not cache.k[pages - 2].any()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_scales_that_no_rows_give(qmv, bf16):
+    """A page whose scale was set below 2^-110, and rows too small for one of their own: no levels."""
+    import torch
+    page, heads, dim = 32, 2, 128
+    cache, twin, table, td = make(qmv, [12], heads, dim, page, seed=3)
+    cache.k_scale.fill_(2.0 ** -120)
+    cache.v_scale.fill_(2.0 ** -140)
+    x = torch.full((8, heads, dim), 1e-31, device="cuda", dtype=torch.bfloat16 if bf16 else torch.float32)
+    at = int(table[0, 0])
+    for lev in (cache.k, cache.v):
+        lev[at] = 5
+    qmv.kv_write(cache, batch_of(qmv, td, [12], [8]), x, x)
+    for lev, sc, d in ((cache.k, cache.k_scale, 2.0 ** -120), (cache.v, cache.v_scale, 2.0 ** -140)):
+        assert bool((lev[at, :, 4:12] == 0).all()) and bool((lev[at, :, :4] == 5).all()) and bool((lev[at, :, 12:] == 5).all())
+        assert bool((sc[at] == d).all())

@@ -6,7 +6,8 @@
 // dependent loads a page (lengths, page id and rows, the old scale) around one reduction: 16384 bfloat16 rows of 8 heads
 // of 128 in 18.7 us (5.4 TB/s, 79% of the measured copy rate; float32 27.5 us, 6.1 TB/s), one row of each of 64
 // sequences in 2.3 us.  A page, head and side (K or V) is a CTA because its scale is what its rows share.  Reading is a
-// copy that widens: 16 sequences of up to 16384 tokens in 191 us (6.57 TB/s, 97%).
+// copy that widens: 16 sequences of up to 16384 tokens as bfloat16 in 191 us (6.57 TB/s, 97%), 16 of 8000 as float32 in
+// 196 us (6.69 TB/s; 273 us while a thread stored 64 bytes in a row, so that a warp's store touched 32 lines).
 #include <type_traits>
 
 #include "kv.cuh"
@@ -142,14 +143,17 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
   if (threadIdx.x == 0) *scale = d;
 }
 
-// Rows read back: a CTA takes U * 256 pieces of 16 levels of one (sequence, head, K or V), each thread U of
-// them, whose page ids, then levels and scales, are all asked for before the first is used.
+// Rows read back: a CTA takes U * 256 pieces of one (sequence, head, K or V), each thread U of them, whose page
+// ids, then levels and scales, are all asked for before the first is used.  A piece is 16 levels for bfloat16
+// and 4 for float32, so that a warp's stores leave whole lines.
 template <int D, bool XB, int U>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRef c, void* __restrict__ ko,
                                                       void* __restrict__ vo) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kRow = D / 16;  // pieces of a row
+  using Piece = typename std::conditional<XB, uint4, uint32_t>::type;
+  constexpr int kLevels = (int)sizeof(Piece);
+  constexpr int kRow = D / kLevels;  // pieces of a row
   constexpr int kRows = 256 / kRow;
   const int s = blockIdx.y;
   // the heads of the same rows lie side by side in the output, so their CTAs follow each other
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
     const int r = r0 + u * kRows;
     id[u] = r < q.n ? __ldg(pages + ((first + r) >> c.page_shift)) : -1;
   }
-  uint4 x[U];
+  Piece x[U];
   float d[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -180,27 +184,25 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
     }
     const long long at = (long long)id[u] * c.kv_heads + head;
     d[u] = __ldg(scale + at);
-    x[u] = __ldg(reinterpret_cast<const uint4*>(lev + (at * c.page_tokens + ((first + r) & (c.page_tokens - 1))) * D +
-                                                16 * piece));
+    x[u] = __ldg(reinterpret_cast<const Piece*>(lev + (at * c.page_tokens + ((first + r) & (c.page_tokens - 1))) * D +
+                                                kLevels * piece));
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (id[u] < 0) continue;
-    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-    float f[16];
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
+    float f[kLevels];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), d[u]);
-    const long long o = ((q.row0 + r0 + u * kRows) * c.kv_heads + head) * D + 16 * piece;
-    if (XB) {
+    for (int e = 0; e < kLevels; ++e) f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), d[u]);
+    const long long o = ((q.row0 + r0 + u * kRows) * c.kv_heads + head) * D + kLevels * piece;
+    if constexpr (XB) {
       uint4* g = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? vo : ko) + o);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         g[h] = make_uint4(pack_bf16x2(f[8 * h], f[8 * h + 1]), pack_bf16x2(f[8 * h + 2], f[8 * h + 3]),
                           pack_bf16x2(f[8 * h + 4], f[8 * h + 5]), pack_bf16x2(f[8 * h + 6], f[8 * h + 7]));
     } else {
-      float4* g = reinterpret_cast<float4*>(static_cast<float*>(is_v ? vo : ko) + o);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) g[h] = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+      *reinterpret_cast<float4*>(static_cast<float*>(is_v ? vo : ko) + o) = make_float4(f[0], f[1], f[2], f[3]);
     }
   }
 }
@@ -224,15 +226,16 @@ cudaError_t launch_write(const KvRef& c, const void* k, int64_t k_stride, const 
 
 template <int D, bool XB>
 cudaError_t launch_read(const KvRef& c, void* k, void* v, const DeviceInfo& dev, cudaStream_t stream) {
-  constexpr int kRows = 256 / (D / 16);
-  // four pieces a thread where that still leaves every SM several CTAs
-  const long long one = (long long)((c.max_rows + kRows - 1) / kRows) * c.n_seq * 2 * c.kv_heads;
-  const int u = one >= 64LL * dev.sm_count ? 4 : 1;
+  constexpr int kRows = 256 / (D / (XB ? 16 : 4)), kFew = XB ? 1 : 2, kMany = XB ? 4 : 8;
+  // more pieces a thread where that still leaves every SM several CTAs (float32, 8 heads of 128, with 2 against 4 and
+  // 16: 64 sequences of 33 rows 6.2, 6.5 and 7.6 us; 16 of 8000, with 2 -> 8 and 16 196 and 198 us)
+  const long long one = (long long)((c.max_rows + kFew * kRows - 1) / (kFew * kRows)) * c.n_seq * 2 * c.kv_heads;
+  const int u = one >= (XB ? 64LL : 32LL) * dev.sm_count ? kMany : kFew;
   const long long x = (long long)((c.max_rows + u * kRows - 1) / (u * kRows)) * (2 * c.kv_heads);
   if (x > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)x, (unsigned)c.n_seq);
-  return u == 4 ? launch_dependent(kv_read_kernel<D, XB, 4>, grid, 256, 0, stream, c, k, v)
-                : launch_dependent(kv_read_kernel<D, XB, 1>, grid, 256, 0, stream, c, k, v);
+  return u == kMany ? launch_dependent(kv_read_kernel<D, XB, kMany>, grid, 256, 0, stream, c, k, v)
+                    : launch_dependent(kv_read_kernel<D, XB, kFew>, grid, 256, 0, stream, c, k, v);
 }
 
 }  // namespace

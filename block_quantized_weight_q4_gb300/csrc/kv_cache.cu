@@ -16,23 +16,6 @@ namespace qmv {
 
 namespace {
 
-// Four levels trunc(t) in a word; |t| < 128 (or NaN: 0).
-__device__ __forceinline__ uint32_t pack_levels(float t0, float t1, float t2, float t3) {
-  uint32_t hi, w;
-  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"((int)t3), "r"((int)t2), "r"(0));
-  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w) : "r"((int)t1), "r"((int)t0), "r"(hi));
-  return w;
-}
-// Two values times inv, half a step away from zero.
-__device__ __forceinline__ void step2(float a, float b, uint64_t inv2, float& ta, float& tb) {
-  uint64_t x, h;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(h) : "f"(copysignf(0.5f, a)), "f"(copysignf(0.5f, b)));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(inv2));
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(h));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(ta), "=f"(tb) : "l"(x));
-}
-
 // One CTA per (page that receives rows, head, K or V).  The page's scale is the largest its tokens
 // have needed: raised by the new rows, the earlier tokens' levels move to it.  The new rows stay in
 // registers between the maximum and their levels (P pieces of 8 values a thread), so each is read once.

@@ -9,7 +9,8 @@
 // Nothing is kept but the row itself, in registers, until r is known.
 //
 // Bound by the bytes of the residual stream (read, written) and x: 2048 x 4096 bfloat16 rows into the image
-// 16.2 us, 5.75 TB/s (85% of the measured copy rate), into bfloat16 6.2 TB/s; one row of 4096 2.3 us, which is
+// 15.7 us, 5.94 TB/s (88% of the measured copy rate; 16.2 us with a level's conversion, clamp and pack one by one), into
+// bfloat16 6.2 TB/s; one row of 4096 2.3 us, which is
 // the launch and one chain of loads, the reduction and the stores.
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
@@ -100,19 +101,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const void* __
       for (int o = 1; o <= 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const bool zero = amax < 1e-30f;
       const float inv = zero ? 0.f : __fmul_rn(__frcp_rn(amax), 127.0f);
-      uint32_t w[2];
+      uint64_t inv2;
+      asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
+      float t[8];  // within 127.5: inv is 127 / amax but for two roundings
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t packed = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float t = v[i][4 * g + k];
-          int q = (int)__fadd_rn(__fmul_rn(t, inv), copysignf(0.5f, t));
-          q = q > 127 ? 127 : (q < -127 ? -127 : q);
-          packed |= (uint32_t)(q & 0xFF) << (8 * k);
-        }
-        w[g] = packed;
-      }
+      for (int e = 0; e < 8; e += 2) step2(v[i][e], v[i][e + 1], inv2, t[e], t[e + 1]);
+      const uint32_t w[2] = {pack_levels(t[0], t[1], t[2], t[3]), pack_levels(t[4], t[5], t[6], t[7])};
       if (live) {
         uint8_t* o8 = static_cast<uint8_t*>(out);
         *reinterpret_cast<uint2*>(o8 + at) = make_uint2(w[0], w[1]);
@@ -147,7 +141,7 @@ cudaError_t launch_typed(int64_t rows, int cols, const void* x, const float* res
   const int pieces = cols / 8;
   // up to 512 threads, with up to 4 pieces each before they are more: 512 rows of 16384 float32 columns took 21.0 us
   // with 512 threads x 4 against 25.1 with 1024 x 2 (two CTAs a SM overlap their ends), 256 of 32768 took 22.3 with
-  // 1024 x 4 against 26.6 with 512 x 8
+  // 1024 x 4 against 26.6 with 512 x 8 (19.6 and 20.9 us since levels are packed in steps of two)
   const int ni = pieces <= 512 ? 1 : pieces <= 1024 ? 2 : 4;
   const int threads = ((pieces + ni - 1) / ni + 31) / 32 * 32;
   auto kern = ni == 1 ? rmsnorm_kernel<XB, OUT, 1> : ni == 2 ? rmsnorm_kernel<XB, OUT, 2> : rmsnorm_kernel<XB, OUT, 4>;

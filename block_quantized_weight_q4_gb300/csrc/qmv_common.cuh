@@ -430,4 +430,21 @@ __device__ __forceinline__ void act_q8_lane_quarters(const float (&v)[NCH][8], u
   }
 }
 
+// Four levels trunc(t) in a word; |t| < 128 (or NaN: 0).
+__device__ __forceinline__ uint32_t pack_levels(float t0, float t1, float t2, float t3) {
+  uint32_t hi, w;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"((int)t3), "r"((int)t2), "r"(0));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w) : "r"((int)t1), "r"((int)t0), "r"(hi));
+  return w;
+}
+// Two values times inv, half a step away from zero.
+__device__ __forceinline__ void step2(float a, float b, uint64_t inv2, float& ta, float& tb) {
+  uint64_t x, h;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(h) : "f"(copysignf(0.5f, a)), "f"(copysignf(0.5f, b)));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(inv2));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(h));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(ta), "=f"(tb) : "l"(x));
+}
+
 }  // namespace qmv

@@ -10,8 +10,7 @@
 //
 // Bound by the bytes of the residual stream (read, written) and x: 2048 x 4096 bfloat16 rows into the image
 // 15.7 us, 5.94 TB/s (88% of the measured copy rate; 16.2 us with a level's conversion, clamp and pack one by one), into
-// bfloat16 6.2 TB/s; one row of 4096 2.3 us, which is
-// the launch and one chain of loads, the reduction and the stores.
+// bfloat16 6.2 TB/s; one row of 4096 2.1 us, which is the launch and one chain of loads, the reduction and the stores.
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
 

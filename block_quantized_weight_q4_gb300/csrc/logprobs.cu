@@ -314,16 +314,17 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   if (wid == 0) {
     const bool none = st.m == -INFINITY && !bad;
     const float lz = bad ? NAN : logf(st.z);
-    const float lse = none ? INFINITY : st.m + lz;
+    // the maximum goes first: beside a large one m + log Z would round log Z away
+    auto logprob = [&](float v) { return none ? -INFINITY : (v - st.m) - lz; };
     if (lane == 0 && a.entropy != nullptr) a.entropy[row] = none ? 0.f : lz - st.zx / st.z;
     for (int i = lane; i < a.n_given; i += 32) {
       const long long id = a.given[row * a.n_given + i];
-      a.given_logprob[row * a.n_given + i] = id >= 0 && id < a.vocab ? x[id] - lse : NAN;
+      a.given_logprob[row * a.n_given + i] = id >= 0 && id < a.vocab ? logprob(x[id]) : NAN;
     }
     if (lane < k) {
       const uint32_t id = 0xffffffffu - (uint32_t)mine;
       a.top_ids[row * k + lane] = (int)id;
-      a.top_logprob[row * k + lane] = unordered((uint32_t)(mine >> 32)) - lse;
+      a.top_logprob[row * k + lane] = logprob(unordered((uint32_t)(mine >> 32)));
     }
   }
 }

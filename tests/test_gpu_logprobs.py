@@ -152,3 +152,34 @@ def test_in_a_graph(qmv, warm):
     g.replay()
     torch.cuda.synchronize()
     check(x, given.cpu().numpy(), 3, [t.cpu().numpy() for t in got])
+
+
+@pytest.mark.parametrize("at", [1e5, -1e6, 3e7, "lowest"])
+@pytest.mark.parametrize("n", [3000, 60001])
+def test_large_maximum_keeps_log_z(qmv, at, n):
+    """Rows whose logits are large beside their differences: (x - m) - log Z.  x - m is exact where x and m lie within a
+    factor of two (else rounded once), the sum of n exponentials carries sqrt(n) 2^-24 and 2^-22 an exponential, the
+    logarithm and the two differences a rounding each of at most |lp| 2^-23."""
+    rng = np.random.default_rng(n)
+    if at == "lowest":
+        x = np.full((2, n), np.finfo(F).min, F)
+        x[1, ::3] = -np.inf
+    else:
+        x = (at + 3 * rng.standard_normal((2, n))).astype(F)
+    given = np.array([[0, 1, n - 1], [1, 2, n - 2]])
+    got = run(qmv, x, given, 20)
+    lp, h = ops_ref.logprobs(x)
+
+    def close(a, b):
+        live = np.isfinite(b)
+        assert np.array_equal(np.isneginf(a), np.isneginf(b))
+        tol = np.sqrt(n) * 2.0 ** -24 + 2.0 ** -22 + 3 * 2.0 ** -23 * np.abs(np.where(live, b, 0))
+        assert np.all(np.abs(np.where(live, a, 0).astype(np.float64) - np.where(live, b, 0)) <= tol)
+
+    close(got[0], np.take_along_axis(lp, given, axis=1))
+    ids = ops_ref.top_ids(x, 20)
+    assert np.array_equal(got[2], ids)
+    close(got[3], np.take_along_axis(lp, ids.astype(np.int64), axis=1))
+    # a term of the entropy is an exponential's error times its difference to the maximum, the quotient's and log Z's errors
+    span = np.abs(np.where(np.isfinite(x), x.astype(np.float64) - x.max(axis=1, keepdims=True), 0)).max(axis=1)
+    assert np.all(np.abs(got[1] - h) <= (np.sqrt(n) + 8) * 2.0 ** -23 * (1 + span + np.abs(h)))

@@ -33,9 +33,9 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
   const int T = blockDim.x;
   const KvSeq q = kv_seq(c, s);
   const int first = q.len - q.n;
-  const int pi = (first >> c.page_shift) + blockIdx.x;
+  const int pi = kv_written_page(q.len, q.n, (int)blockIdx.x, c.page_shift);
+  if (pi < 0) return;
   const int begin = pi << c.page_shift;
-  if (begin >= q.len || q.n == 0) return;
   // the rows are asked for before the page's id is looked at
   const int id = __ldg(c.page_table + (long long)s * c.table_stride + pi);
   const int lo = first > begin ? first - begin : 0;
@@ -193,8 +193,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
 template <int D, bool XB>
 cudaError_t launch_write(const KvRef& c, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                          cudaStream_t stream) {
-  // pages that n rows can fall into, wherever they start in the first
-  const int pages = (c.max_rows + c.page_tokens - 2) / c.page_tokens + 1;
+  const int pages = kv_pages_bound(c.max_rows, c.page_tokens);
   const dim3 grid((unsigned)pages, (unsigned)c.n_seq, (unsigned)(2 * c.kv_heads));
   // pieces of the most rows that a page may receive, over at most 256 threads of 1 or 4, else of 8: 16384 rows of
   // 8 heads of 128, pages of 16 tokens, 19.3 us with 4 pieces a thread, 23.2 with 8; 256 single rows 4.6 with 1, 6.2

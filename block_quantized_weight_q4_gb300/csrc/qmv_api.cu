@@ -80,7 +80,7 @@ int make_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, KvRef* c) {
   if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) return QMV_E_SHAPE;
   if (cache->kv_heads < 1 || cache->kv_heads > 1024) return QMV_E_SHAPE;
   if (cache->n_pages < 0 || cache->n_pages > INT32_MAX || batch->n_seq > 65535 || batch->rows > INT32_MAX ||
-      batch->table_stride < batch->table_pages || batch->table_stride > INT32_MAX || batch->max_len > INT32_MAX - 1024)
+      batch->table_stride < batch->table_pages || batch->table_stride > INT32_MAX || batch->max_len > kKvMaxLen)
     return QMV_E_SHAPE;
   if (batch->starts == nullptr && batch->rows != batch->n_seq) return QMV_E_SHAPE;
   c->k = cache->k;
@@ -100,7 +100,7 @@ int make_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, KvRef* c) {
   c->page_tokens = cache->page_tokens;
   c->page_shift = cache->page_tokens == 16 ? 4 : cache->page_tokens == 32 ? 5 : cache->page_tokens == 64 ? 6 : 7;
   c->n_seq = batch->n_seq;
-  c->max_rows = batch->starts == nullptr && batch->max_rows > 1 ? 1 : batch->max_rows;
+  c->max_rows = kv_rows_bound(batch->rows, batch->starts == nullptr && batch->max_rows > 1 ? 1 : batch->max_rows, batch->max_len);
   c->max_len = batch->max_len;
   if (batch->rows == 0 || c->max_rows == 0) return QMV_OK;  // nothing to launch
   if (c->n_seq == 0) return QMV_E_ARG;

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "kv_plan.h"
+
 namespace qmv {
 
 // Validated description of one matrix image (see include/qmv.h).

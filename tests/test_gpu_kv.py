@@ -212,3 +212,27 @@ def test_scales_that_no_rows_give(qmv, bf16):
     for lev, sc, d in ((cache.k, cache.k_scale, 2.0 ** -120), (cache.v, cache.v_scale, 2.0 ** -140)):
         assert bool((lev[at, :, 4:12] == 0).all()) and bool((lev[at, :, :4] == 5).all()) and bool((lev[at, :, 12:] == 5).all())
         assert bool((sc[at] == d).all())
+
+
+def test_loose_bounds(qmv):
+    """max_rows far above the call's rows (up to the type's largest), max_len the largest that is accepted."""
+    import torch
+    page, heads, dim = 16, 2, 64
+    lens, counts = [700, 40, 1], [33, 1, 1]
+    rng = np.random.default_rng(6)
+    cache, twin, table, td = make(qmv, lens, heads, dim, page, seed=7)
+    (k, kd), (v, vd) = rows_of(rng, 35, heads, dim, False), rows_of(rng, 35, heads, dim, False)
+    qmv.kv_write(cache, batch_of(qmv, td, lens, counts), kd, vd)
+    twin.write(table, lens, counts, k, v)
+    same(cache, twin)
+    tight = batch_of(qmv, td, lens, counts)
+    want = qmv.kv_read(cache, tight, torch.float32)
+    out = qmv.attend(cache, tight, kd)
+    for max_rows, max_len in ((2 ** 31 - 1, 700), (2147483000, 2 ** 31 - 1025), (36, 2 ** 31 - 1025)):
+        b = batch_of(qmv, td, lens, counts, max_rows=max_rows, max_len=max_len)
+        qmv.kv_write(cache, b, kd, vd)  # the same rows again: nothing changes
+        same(cache, twin)
+        got = qmv.kv_read(cache, b, torch.float32)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert float((qmv.attend(cache, b, kd) - out).abs().max()) < 1e-4 * float(out.abs().max())
+    assert qmv.last_error() == 0

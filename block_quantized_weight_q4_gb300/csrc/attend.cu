@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
   auto weight = [&](int s) -> long long {
     const KvSeq q = kv_seq(c, s);
     const Shape h = shape_of<ROWS>(c, a, q);
-    return (long long)h.nch * h.nrb * c.kv_heads;
+    return kv_segment_chunks(h.nch, h.nrb, c.kv_heads);
   };
   auto block_scan = [&](long long v, long long& before) -> long long {  // exclusive prefix and total
     long long inc = v;
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
 
   while (pos < my1) {
     // the segment that chunk pos lies in
-    while (pos >= base + (long long)sh.nch * sh.nrb * c.kv_heads && s + 1 < c.n_seq) {
-      base += (long long)sh.nch * sh.nrb * c.kv_heads;
+    while (pos >= base + kv_segment_chunks(sh.nch, sh.nrb, c.kv_heads) && s + 1 < c.n_seq) {
+      base += kv_segment_chunks(sh.nch, sh.nrb, c.kv_heads);
       ++s;
       sq = kv_seq(c, s);
       sh = shape_of<ROWS>(c, a, sq);
     }
-    if (sh.nch * sh.nrb == 0) return;  // lengths that changed under the call
+    if (kv_segment_chunks(sh.nch, sh.nrb, c.kv_heads) == 0) return;  // lengths that changed under the call
     const int seg = (int)((pos - base) / sh.nch);
     const long long seg0 = base + (long long)seg * sh.nch;
     const int kvh = seg / sh.nrb, rb = seg % sh.nrb;

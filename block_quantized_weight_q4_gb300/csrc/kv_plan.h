@@ -35,4 +35,8 @@ QMV_HD int kv_written_page(int len, int n, int i, int page_shift) {
   return i > ((len - 1) >> page_shift) - at ? -1 : at + i;
 }
 
+// Chunks of a sequence's segments in all: n_chunks of keys for each of n_blocks row blocks of each head (past 32 bits from
+// a few hundred thousand rows over as many tokens on).
+QMV_HD long long kv_segment_chunks(int n_chunks, int n_blocks, int heads) { return (long long)n_chunks * n_blocks * heads; }
+
 }  // namespace qmv

@@ -16,6 +16,7 @@ int max_len() { return qmv::kKvMaxLen; }
 int rows_bound(long long rows, int max_rows, int max_len) { return qmv::kv_rows_bound(rows, max_rows, max_len); }
 int pages_bound(int n, int page) { return qmv::kv_pages_bound(n, page); }
 int written_page(int len, int n, int i, int shift) { return qmv::kv_written_page(len, n, i, shift); }
+long long segment_chunks(int n_chunks, int n_blocks, int heads) { return qmv::kv_segment_chunks(n_chunks, n_blocks, heads); }
 }
 """
 
@@ -29,6 +30,7 @@ def plan(tmp_path_factory):
                     str(at / "plan.cpp"), "-o", str(at / "plan.so")], check=True)
     lib = ctypes.CDLL(str(at / "plan.so"))
     lib.rows_bound.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
+    lib.segment_chunks.restype = ctypes.c_longlong
     return lib
 
 
@@ -65,3 +67,10 @@ def test_pages_at_the_largest_bounds(plan, length, n, shift):
         got = plan.written_page(length, n, i, shift)
         assert got == (first + i if first + i <= last else -1)
         assert got * page < 2 ** 31
+
+
+def test_chunks_of_long_prompts(plan):
+    """262144 rows over as many tokens, 16 heads a group of 256: 2^13 chunks for each of 2^19 row blocks is not none."""
+    assert plan.segment_chunks(2 ** 13, 2 ** 19, 1) == 2 ** 32
+    assert plan.segment_chunks(2 ** 26, 2 ** 28, 2) == 2 ** 55
+    assert plan.segment_chunks(0, 7, 8) == plan.segment_chunks(7, 0, 8) == 0

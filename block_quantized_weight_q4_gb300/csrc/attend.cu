@@ -230,11 +230,11 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
     // the ring: chunk ch into stage st
     const long long head_stride = (long long)c.page_tokens * D;
     int ids[2] = {-1, -1};  // the next chunk's pages, looked up one chunk ahead of its copies
-    auto look = [&](int ch) {
+    auto look = [&](int ch, int seen) {  // pages before key `seen` are not looked at
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int j0 = ch * kChunk + 16 * u;
-        ids[u] = ch < ch1 && j0 < sq.len ? kv_page(c, s, (j0 >> c.page_shift)) : -1;
+        ids[u] = ch < ch1 && j0 < sq.len && j0 >= seen ? kv_page(c, s, (j0 >> c.page_shift)) : -1;
       }
     };
     auto issue = [&](int ch, int st) {
@@ -262,9 +262,10 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      look(ch + kWarps);
+      look(ch + kWarps, 0);
     };
-    look(ch0 + wid);
+    // pages that end before any row's first key may be anything; only the first chunk can hold one
+    look(ch0 + wid, any_begin & -c.page_tokens);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(ch0 + wid + i * kWarps, i);
 

@@ -275,10 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
     return -1;
   };
   int id = -1;
+  bool hidden = false;
   float gk = 0.f, gv = 0.f;
   if (warp == 13) {
     const int key = jb * kKeys + 16 * lane;
-    if (lane < 8 && key < sq.len) id = __ldg(page_row + (key >> c.page_shift));
+    // pages that end before any row's first key may be anything: not looked at (only the first tile can hold one)
+    hidden = key < (any_begin & -c.page_tokens);
+    if (lane < 8 && key < sq.len && !hidden) id = __ldg(page_row + (key >> c.page_shift));
   }
   tc_fence_before();
   __syncthreads();
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         const int key = (jb + n) * kKeys + 16 * lane;
         return lane < 8 && n < keys && key < sq.len ? __ldg(page_row + (key >> c.page_shift)) : -1;
       };
-      id = page_of(id, jb * kKeys + 16 * lane);
+      if (!hidden) id = page_of(id, jb * kKeys + 16 * lane);
       if (id >= 0) {
         gk = __ldg(c.k_scale + (long long)id * c.kv_heads + kvh);
         gv = __ldg(c.v_scale + (long long)id * c.kv_heads + kvh);

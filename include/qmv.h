@@ -566,7 +566,8 @@ typedef struct qmv_kv_cache {
  * than max_rows or than kv_len), and a page id outside the cache among the pages it uses, are not
  * followed: nothing out of range is read or written, QMV_E_ARG is recorded in the status word
  * (qmv_check_device) and what the call gives for that sequence is not specified.  Page ids past
- * a sequence's tokens are not looked at. */
+ * a sequence's tokens are not looked at, nor in qmv_attend those of pages that end before the window
+ * of the sequence's first row (pages that a sliding window has left behind may be given away). */
 typedef struct qmv_kv_batch {
   const int32_t *page_table;
   int64_t table_stride;

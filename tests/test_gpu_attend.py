@@ -296,3 +296,55 @@ def test_in_a_graph(qmv, warm):
         g.replay()
         torch.cuda.synchronize()
         check(twin, table, ls, [1, 1], qf, out, 128 ** -0.5, True, 0, True)
+
+
+def hide(cache, twin, table, td, lens, counts, window, page, how):
+    """What a server does with pages that a sliding window has left behind: their table entries cleared, or the pages
+    given to something else (here scales that are no numbers).  Returns the table of the call."""
+    import torch
+    td = td.clone()
+    for s, (n, m) in enumerate(zip(lens, counts)):
+        gone = max(0, n - m - window + 1) // page  # pages that end before any row's first key
+        if how == "cleared":
+            td[s, :gone] = -1
+        else:
+            for scale in (cache.k_scale, cache.v_scale):
+                scale[torch.from_numpy(table[s, :gone].astype(np.int64)).cuda()] = float(how)
+    return td
+
+
+@pytest.mark.parametrize("how", ["cleared", "nan", "inf"])
+@pytest.mark.parametrize("window", [1, 20, 50, 100, 161, 300])
+@pytest.mark.parametrize("heads,kvh,dim,page,lens,counts", [
+    (8, 2, 128, 16, [40, 77, 330, 1000, 18, 551], [1, 1, 1, 1, 1, 1]),
+    (4, 4, 64, 16, [300, 555, 1111, 90], [3, 1, 5, 2]),
+    (4, 2, 256, 32, [200, 390, 1300], [1, 4, 9]),
+    (8, 1, 128, 64, [333, 1000], [2, 1]),
+    (32, 8, 128, 64, [900], [300]),              # from here on the prompt kernel
+    (16, 16, 64, 16, [901, 500], [400, 300]),
+    (32, 8, 64, 32, [1100], [333]),
+    (64, 8, 128, 128, [1000, 700], [300, 200]),
+])
+def test_pages_that_the_window_hides(qmv, heads, kvh, dim, page, lens, counts, window, how):
+    """Pages that no row of a sequence sees into may be anything: neither their table entries nor their scales count."""
+    rng = np.random.default_rng(window)
+    for bf16 in (True, False):
+        cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=window)
+        td = hide(cache, twin, table, td, lens, counts, window, page, how)
+        qf, qd = queries(rng, sum(counts), heads, dim, bf16)
+        got = qmv.attend(cache, batch_of(qmv, td, lens, counts), qd, window=window)
+        assert qmv.last_error() == 0
+        check(twin, table, lens, counts, qf, got, dim ** -0.5, True, window, bf16)
+
+
+@pytest.mark.parametrize("how", ["cleared", "nan"])
+def test_pages_that_the_window_hides_from_cut_prompts(qmv, how):
+    """The same where the blocks are cut along the keys."""
+    rng = np.random.default_rng(4)
+    lens, counts, window, page = [4000], [130], 1500, 16
+    cache, twin, table, td = filled(qmv, lens, 8, 128, page, seed=4)
+    td = hide(cache, twin, table, td, lens, counts, window, page, how)
+    qf, qd = queries(rng, 130, 32, 128, True)
+    got = qmv.attend(cache, batch_of(qmv, td, lens, counts), qd, window=window)
+    assert qmv.last_error() == 0
+    check(twin, table, lens, counts, qf, got, 128 ** -0.5, True, window, True)

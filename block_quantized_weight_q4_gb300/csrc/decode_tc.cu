@@ -1,10 +1,9 @@
 // decode_tc.cu -- entry of the tensor-memory decode product (kernels in decode_tc.cuh) and
 // the per-stream workspace its split tiles use.
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "decode_tc.cuh"
+#include "workspace_cache.h"
 
 namespace qmv {
 
@@ -13,16 +12,6 @@ bool decode_tc_supported(const MatrixRef& m) {
 }
 
 int decode_tc_max_problems() { return dtc::kMaxProblems; }
-
-size_t workspace_counter_bytes(int n) { return ((size_t)n * sizeof(unsigned) + 255) / 256 * 256; }
-
-void workspace_carve(void* base, size_t bytes, int n, Workspace* ws) {
-  const size_t cb = workspace_counter_bytes(n);
-  ws->counters = static_cast<unsigned*>(base);
-  ws->max_counters = n;
-  ws->partials = reinterpret_cast<float*>(static_cast<uint8_t*>(base) + cb);
-  ws->max_partial_floats = bytes > cb ? (bytes - cb) / sizeof(float) : 0;
-}
 
 // a stream's workspace: counters for up to 1024 CTAs, then the parts (2 per CTA of 128
 // rows x up to 16 vectors); the kernel sizes its grid to fit
@@ -45,45 +34,16 @@ constexpr size_t kServeWorkspaceBytes = (size_t)8 << 20;
 
 namespace {
 std::mutex g_ws_mu;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_pws;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_xws;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_sws;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_aws;
+WorkspaceCache g_ws;
+WorkspaceCache g_pws;
+WorkspaceCache g_xws;
+WorkspaceCache g_sws;
+WorkspaceCache g_aws;
 
-cudaError_t cached_workspace(std::map<std::pair<int, cudaStream_t>, Workspace>& cache, const DeviceInfo& dev,
-                             cudaStream_t stream, size_t bytes, int counters, Workspace* ws) {
-  constexpr size_t kMaxEntries = 64;
+cudaError_t cached_workspace(WorkspaceCache& cache, const DeviceInfo& dev, cudaStream_t stream, size_t bytes, int counters,
+                             Workspace* ws) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  const auto key = std::make_pair(dev.device, stream);
-  auto it = cache.find(key);
-  if (it != cache.end()) {
-    *ws = it->second;
-    return cudaSuccess;
-  }
-  if (cache.size() >= kMaxEntries) return cudaErrorMemoryAllocation;
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  cudaError_t err = cudaStreamIsCapturing(stream, &cs);
-  if (err != cudaSuccess) return err;
-  if (cs != cudaStreamCaptureStatusNone) return cudaErrorNotReady;  // no allocation while capturing
-  void* base = nullptr;
-  err = cudaMalloc(&base, bytes);
-  if (err != cudaSuccess) return err;
-  err = cudaMemsetAsync(base, 0, workspace_counter_bytes(counters), stream);
-  if (err != cudaSuccess) {
-    cudaFree(base);
-    return err;
-  }
-  Workspace w;
-  workspace_carve(base, bytes, counters, &w);
-  try {
-    cache.emplace(key, w);
-  } catch (...) {  // nothing is thrown through the C entry points
-    cudaFree(base);
-    return cudaErrorMemoryAllocation;
-  }
-  *ws = w;
-  return cudaSuccess;
+  return qmv::cached_workspace(cache, dev.device, stream, bytes, counters, ws);
 }
 }  // namespace
 

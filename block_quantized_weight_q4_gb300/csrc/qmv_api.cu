@@ -9,6 +9,7 @@
 
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
+#include "workspace_cache.h"
 
 namespace qmv {
 

@@ -38,10 +38,6 @@ struct Workspace {
   float* partials;            // parts of split tiles
   size_t max_partial_floats;
 };
-// Bytes of the counter region for n counters (a multiple of 256); carve `bytes` at `base`
-// into n counters followed by the parts.
-size_t workspace_counter_bytes(int n);
-void workspace_carve(void* base, size_t bytes, int n, Workspace* ws);
 // The workspace of (current device, stream), allocated and zeroed on first use; returns
 // cudaErrorNotReady when there is none yet and the stream is being captured.
 cudaError_t stream_workspace(const DeviceInfo& dev, cudaStream_t stream, Workspace* ws);

@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
   constexpr int KS = D / 16;       // 16-dim steps
   constexpr int QP = XB ? 1 : 2;   // parts of q (half): hi (, lo)
   constexpr int PP = XB ? 2 : 3;   // parts of the weights (bfloat16): 16 or 24 bits
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scan[kWarps];
   __shared__ int found_seq;

@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
   constexpr int kPieces = D / 16;           // 16-byte pieces of a row of levels
   constexpr int kRowsWarp = 32 / kPieces;   // rows a converting warp takes at a time
   constexpr int kPasses = kKeys / (4 * kRowsWarp);
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);

@@ -23,8 +23,8 @@ template <int D, bool XB, int P>
 __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ KvRef c, const void* __restrict__ kx,
                                                        long long k_stride, const void* __restrict__ vx,
                                                        long long v_stride) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   constexpr int kRow = D / 8;  // pieces of a row
   __shared__ float part[16];
   const int s = blockIdx.y;
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(512) kv_write_kernel(const __grid_constant__ K
 template <int D, bool XB, int U>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRef c, void* __restrict__ ko,
                                                       void* __restrict__ vo) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   using Piece = typename std::conditional<XB, uint4, uint32_t>::type;
   constexpr int kLevels = (int)sizeof(Piece);
   constexpr int kRow = D / kLevels;  // pieces of a row

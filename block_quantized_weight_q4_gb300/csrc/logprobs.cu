@@ -115,8 +115,8 @@ struct PartArea {
 
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a, int n_parts,
                                                             const PartArea area) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   __shared__ Stats warp_stats[kWarps];
   __shared__ Key warp_keys[kWarps][QMV_MAX_TOP];
   __shared__ uint32_t floor_bits;  // no value below this can be among the largest n_top

@@ -28,8 +28,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const void* __
                                                                   const float* __restrict__ weight, float eps,
                                                                   void* __restrict__ out, long long out_d_off,
                                                                   long long rows, int cols) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   __shared__ float part[32];
   const long long row = blockIdx.x;
   const int T = blockDim.x;

@@ -196,7 +196,9 @@ cudaError_t launch_decode_tc_f32(const MatrixRef* ms, const void* const* xs, flo
 
 // ---------------------------------------------------------------- between the products
 // Their kernels launch as programmatic dependents: their CTAs may start while the preceding kernel ends, and
-// touch global memory only after griddep_wait().
+// touch global memory only after griddep_wait().  They let their own dependents in only after that wait, too: a product
+// with QMV_FLAG_OVERLAP reads its weights before it waits, and only the kernel right before it may not have
+// written them.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};

@@ -116,3 +116,31 @@ def test_norm_image_feeds_the_quantized_product(qmv):
     wm = qmv.dequant(2, 1, 96, 1024, Wd).cpu().double()
     ref, mag = a @ wm.T, a.abs() @ wm.abs().T
     assert bool(((y - ref).abs() <= 1e-3 * mag).all())
+
+
+def test_weights_written_before_the_norm(qmv):
+    """Weights written by one kernel (a norm's 8-bit image is a Q8_0 / f32 matrix), a norm of the activations, then a product
+    that asks for its weights early: it reads the new ones."""
+    import torch
+    rows, cols = 8192, 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    src = [torch.randn((rows, cols), device="cuda", generator=g) for _ in range(2)]
+    x = torch.randn((1, cols), device="cuda", generator=g)
+    w = torch.ones(cols, device="cuda")
+    h = qmv.rmsnorm(x, w, out="bf16")
+    W = qmv.rmsnorm(src[0], w)
+    want = []
+    for s in src:
+        qmv.rmsnorm(s, w, y=W)
+        torch.cuda.synchronize()
+        want.append(qmv.matvec(qmv.Q8_0, qmv.SCALE_F32, rows, cols, W, h))
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    got = [torch.empty((1, rows), device="cuda") for _ in range(100)]
+    for i, y in enumerate(got):
+        qmv.rmsnorm(src[i & 1], w, y=W)
+        qmv.rmsnorm(x, w, out="bf16", y=h)
+        qmv.matvec_grouped(qmv.Q8_0, qmv.SCALE_F32, [(rows, cols, W, h, y)], overlap=True)
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i & 1]), i

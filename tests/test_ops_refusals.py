@@ -126,3 +126,16 @@ def test_binding_checks_shapes():
         binding.rmsnorm(z((2, 64)), z(64), out="f32")  # not CUDA tensors
     with pytest.raises(TypeError):
         binding.rmsnorm(z((2, 64), dtype=torch.float16), z(64), out="f32")
+
+
+@pytest.mark.parametrize("name", ["attend", "attend_prompt", "kv_cache", "logprobs", "norm"])
+def test_dependents_start_after_the_wait(name):
+    """QMV_FLAG_OVERLAP lets a product read its weights before it waits, so an operator that released it before its own wait
+    would let it read weights that the kernel before the operator is still writing."""
+    import os
+    import re
+    from block_quantized_weight_q4_gb300.build import CSRC
+    text = open(os.path.join(CSRC, name + ".cu")).read()
+    calls = re.findall(r"griddep_(wait|launch_dependents)\(\);", text)
+    kernels = text.count("__global__")
+    assert calls == ["wait", "launch_dependents"] * kernels

@@ -503,14 +503,29 @@ MAX_TOP = 32
 MAX_GIVEN = 64
 
 
-def _raw_stream(stream, device_index):
-    """The stream's handle as an integer; the device's current stream by default."""
+def _raw_stream(stream, device_index, *others):
+    """The stream's handle as an integer; the device's current stream by default.  device_index and others: the
+    devices of the call's tensors (get_device(), -1 on the host), which must be one, the current one: the kernels
+    follow the pointers as they are."""
     if device_index < 0:
         raise ValueError("CUDA tensors are needed")
+    for other in others:
+        if other != device_index:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+    import torch
+    if torch._C._cuda_getDevice() != device_index:
+        raise ValueError("the tensors' device must be the current one (torch.cuda.device)")
     if stream is not None:
         return stream.cuda_stream
-    import torch
     return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def _device_of(tensors, what):
+    """The one device (get_device()) of tensors, None among them left out."""
+    index = {t.get_device() for t in tensors if t is not None}
+    if len(index) != 1:
+        raise ValueError(f"{what} must be on one device")
+    return index.pop()
 
 
 def rmsnorm(x, weight, eps: float = 1e-5, residual=None, residual_out=None, out="q8", y=None, stream=None):
@@ -554,7 +569,9 @@ def rmsnorm(x, weight, eps: float = 1e-5, residual=None, residual_out=None, out=
     st = load_library().qmv_rmsnorm(_x_dtype(x), rows, cols, x.data_ptr(),
                                     None if residual is None else residual.data_ptr(),
                                     None if residual_out is None else residual_out.data_ptr(), weight.data_ptr(), eps,
-                                    code, y.data_ptr(), _raw_stream(stream, x.get_device()))
+                                    code, y.data_ptr(),
+                                    _raw_stream(stream, x.get_device(), weight.get_device(), y.get_device(),
+                                                *[t.get_device() for t in (residual, residual_out) if t is not None]))
     _check(st, "qmv_rmsnorm")
     return y
 
@@ -593,6 +610,7 @@ class KvCache:
                             self.kv_heads, self.head_dim, self.page_tokens)
         self._p = ctypes.addressof(self._c)
         self.device = k.device
+        self._index = _device_of((k, v, k_scale, v_scale), "a cache's tensors")
 
     @classmethod
     def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -633,6 +651,7 @@ class KvBatch:
         self._c = _KvBatchC(page_table.data_ptr(), stride, page_table.shape[1], kv_len.data_ptr(), None if starts is None else starts.data_ptr(),
                             n, rows, max_rows, self.max_len)
         self._p = ctypes.addressof(self._c)
+        self._index = _device_of((page_table, kv_len, starts), "page_table, kv_len and starts")
 
 
 def _head_rows(t, heads, dim, rows, what):
@@ -652,7 +671,7 @@ def kv_write(cache: KvCache, batch: KvBatch, k, v, stream=None):
     ks = _head_rows(k, cache.kv_heads, cache.head_dim, batch.rows, "k")
     vs = _head_rows(v, cache.kv_heads, cache.head_dim, batch.rows, "v")
     st = load_library().qmv_kv_write(cache._p, batch._p, _x_dtype(k), k.data_ptr(), ks, v.data_ptr(), vs,
-                                     _raw_stream(stream, k.get_device()))
+                                     _raw_stream(stream, k.get_device(), v.get_device(), cache._index, batch._index))
     _check(st, "qmv_kv_write")
 
 
@@ -671,7 +690,7 @@ def kv_read(cache: KvCache, batch: KvBatch, dtype=None, k=None, v=None, stream=N
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=cache.device)
     st = load_library().qmv_kv_read(cache._p, batch._p, _x_dtype(k), k.data_ptr(), v.data_ptr(),
-                                    _raw_stream(stream, k.get_device()))
+                                    _raw_stream(stream, k.get_device(), v.get_device(), cache._index, batch._index))
     _check(st, "qmv_kv_read")
     return k, v
 
@@ -694,7 +713,8 @@ def attend(cache: KvCache, batch: KvBatch, q, out=None, scale=None, causal: bool
         os_ = _head_rows(out, heads, cache.head_dim, batch.rows, "out")
     st = load_library().qmv_attend(cache._p, batch._p, heads, _x_dtype(q), q.data_ptr(), qs,
                                    cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-                                   out.data_ptr(), os_, _raw_stream(stream, q.get_device()))
+                                   out.data_ptr(), os_,
+                                   _raw_stream(stream, q.get_device(), out.get_device(), cache._index, batch._index))
     _check(st, "qmv_attend")
     return out
 
@@ -723,7 +743,8 @@ def logprobs(logits, given=None, top: int = 0, entropy: bool = True, stream=None
     st = load_library().qmv_logprobs(rows, vocab, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
                                      None if n == 0 else given.data_ptr(), n, None if n == 0 else glp.data_ptr(),
                                      None if ent is None else ent.data_ptr(), top, None if ids is None else ids.data_ptr(),
-                                     None if tlp is None else tlp.data_ptr(), _raw_stream(stream, logits.get_device()))
+                                     None if tlp is None else tlp.data_ptr(),
+                                     _raw_stream(stream, logits.get_device(), *(() if given is None else (given.get_device(),))))
     _check(st, "qmv_logprobs")
     return glp, ent, ids, tlp
 

@@ -139,3 +139,65 @@ def test_dependents_start_after_the_wait(name):
     calls = re.findall(r"griddep_(wait|launch_dependents)\(\);", text)
     kernels = text.count("__global__")
     assert calls == ["wait", "launch_dependents"] * kernels
+
+
+def test_operands_on_other_devices():
+    """A tensor on the host, or on a device that is not the call's or not current, is refused before anything is launched:
+    its address would be followed.  (Tensors that say they are on a device, so that this runs without one.)"""
+    import torch
+
+    class On(torch.Tensor):
+        index = 0
+
+        def get_device(self):
+            return type(self).index
+
+    class OnOther(On):
+        index = 1
+
+    def z(*shape, dtype=torch.float32, on=On):
+        t = torch.zeros(shape, dtype=dtype)
+        return t if on is None else t.as_subclass(on)
+
+    i32 = torch.int32
+    for bad in (None, OnOther):
+        k = z(2, 1, 16, 64, dtype=torch.int8)
+        with pytest.raises(ValueError, match="device"):
+            binding.KvCache(k, z(2, 1, 16, 64, dtype=torch.int8, on=bad), z(2, 1), z(2, 1))
+        with pytest.raises(ValueError, match="device"):
+            binding.KvCache(k, k, z(2, 1), z(2, 1, on=bad))
+        with pytest.raises(ValueError, match="device"):
+            binding.KvBatch(z(1, 2, dtype=i32), z(1, dtype=i32, on=bad))
+        with pytest.raises(ValueError, match="device"):
+            binding.KvBatch(z(1, 2, dtype=i32), z(1, dtype=i32), starts=z(2, dtype=i32, on=bad), rows=3)
+        cache = binding.KvCache(k, k, z(2, 1), z(2, 1))
+        batch = binding.KvBatch(z(1, 2, dtype=i32), z(1, dtype=i32), starts=z(2, dtype=i32), rows=3)
+        far = binding.KvBatch(z(1, 2, dtype=i32, on=bad), z(1, dtype=i32, on=bad), starts=z(2, dtype=i32, on=bad), rows=3)
+        fc = binding.KvCache(*[t if bad is None else t.as_subclass(bad) for t in
+                               (torch.zeros((2, 1, 16, 64), dtype=torch.int8), torch.zeros((2, 1, 16, 64), dtype=torch.int8),
+                                torch.zeros(2, 1), torch.zeros(2, 1))])
+        x, xb = z(3, 1, 64), z(3, 1, 64, on=bad)
+        for call in (lambda: binding.kv_write(cache, batch, x, xb), lambda: binding.kv_write(cache, far, x, x),
+                     lambda: binding.kv_write(fc, batch, x, x), lambda: binding.kv_read(cache, batch, k=x, v=xb),
+                     lambda: binding.kv_read(cache, far, k=x, v=x), lambda: binding.attend(cache, far, x, out=x),
+                     lambda: binding.attend(fc, batch, x, out=x), lambda: binding.attend(cache, batch, x, out=xb),
+                     lambda: binding.rmsnorm(z(2, 64), z(64, on=bad), y=z(256, dtype=torch.uint8)),
+                     lambda: binding.rmsnorm(z(2, 64), z(64), residual=z(2, 64, on=bad), y=z(256, dtype=torch.uint8)),
+                     lambda: binding.rmsnorm(z(2, 64), z(64), residual_out=z(2, 64, on=bad), y=z(256, dtype=torch.uint8)),
+                     lambda: binding.rmsnorm(z(2, 64), z(64), y=z(256, dtype=torch.uint8, on=bad)),
+                     lambda: binding.logprobs(z(2, 5), z(2, 1, dtype=torch.int64, on=bad))):
+            with pytest.raises(ValueError, match="one CUDA device"):
+                call()
+
+
+def test_operands_on_a_device_that_is_not_current(monkeypatch):
+    import torch
+
+    class On(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    t = torch.zeros(2, 64).as_subclass(On)
+    with pytest.raises(ValueError, match="current"):
+        binding.rmsnorm(t, t[0], out="f32", y=t)

@@ -7,7 +7,9 @@
 // exponent, so that the largest weight * V scale, not the largest weight, sets the range in which
 // the weights are rounded to half: they are formed times 2^7 against a reference that is at most
 // 2^8 behind the running maximum (the output is rescaled only when it falls further back), so they
-// stay under 2^15, and those down to 2^-21 of the largest are normal halves.
+// stay under 2^15, and those down to 2^-21 of the largest are normal halves.  A page whose V scale is 0 has no
+// logarithm: its weights are 0 in P, and its keys' exponentials go to a sum with a reference of its own, on a path
+// that tiles without such pages do not take.
 //
 // A CTA takes two tiles of 128 rows (query token, head of the group) of one key/value head and goes
 // through the keys 128 at a time.  Warps 0-3 and 4-7: one row a thread of the two tiles (softmax);
@@ -45,9 +47,9 @@ constexpr uint32_t kTmemCols = 512;
 // What a group of 16 keys (one page) brings to the softmax.
 struct GroupScale {
   float ks;    // K scale
-  float e;     // log2 of the V scale
-  float back;  // 1 / V scale
-  float pad;
+  float e;     // log2 of the V scale, -infinity for 0
+  float back;  // 1 / V scale, 0 for 0
+  uint32_t zeros;  // which of the tile's groups lie in pages of V scale 0, the same in each group
 };
 
 template <int D>
@@ -341,16 +343,45 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
       const uint32_t sp = tmem + quarter + (uint32_t)(q * kKeys);        // scores, then weights
       const uint32_t ot = tmem + quarter + (uint32_t)(256 + q * 128);    // output
       float ref = -INFINITY, l = 0.f;
+      // keys of zero pages: their largest score and the sum of their exponentials against it, kept out of the registers
+      volatile float zero_ref = -INFINITY, zero_sum = 0.f;
       bool ok = true;
       for (int j = jb; j < je; ++j) {
         const int n = j - jb;
-        ok = pwait(bars + kTableFull + n % kTableStages, (uint32_t)((n / kTableStages) & 1), failed) &&
-             pwait(bars + kSFull + q, (uint32_t)(n & 1), failed);
+        ok = pwait(bars + kTableFull + n % kTableStages, (uint32_t)((n / kTableStages) & 1), failed);
+        const GroupScale* tab = table + (n % kTableStages) * 8;
+        const uint32_t zeros = tab->zeros;
+        ok = ok && pwait(bars + kSFull + q, (uint32_t)(n & 1), failed);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const GroupScale* tab = table + (n % kTableStages) * 8;
         const int j0 = j * kKeys;
+        if (zeros != 0u) {
+#pragma unroll 1
+          for (int b = 0; b < kKeys / 8; ++b) {
+            if (!((zeros >> (b >> 1)) & 1u)) continue;
+            uint32_t o[8];
+            tmem_ld8(sp + 8 * b, o);
+            tmem_ld_wait();
+            const float c = group_factor(tab[b >> 1].ks, rowc);
+            const float was = zero_ref;
+            float m = was, x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int key = j0 + 8 * b + e;
+              x[e] = key < beg || key >= end ? -INFINITY : __uint_as_float(o[e]) * c;
+              m = fmaxf(m, x[e]);
+            }
+            if (m != -INFINITY) {
+              float sum = zero_sum * (m > was ? ex2(was - m) : 1.f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) sum += ex2(x[e] - m);
+              zero_ref = m;
+              zero_sum = sum;
+            }
+            __syncwarp();
+          }
+        }
         uint32_t v[4][32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) tmem_ld32(sp + 32 * b, v[b]);
@@ -435,6 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         float* area = nullptr;
         constexpr int kPartFloats = 2 * kTileRows * (D + 2);
         const int row256 = q * kTileRows + r;
+        float keep = 1.f;  // what the output is moved by when the zero pages' keys join the sum
+        if (zero_sum > 0.f) {
+          const float to = fmaxf(ref, zero_ref);
+          keep = ref == -INFINITY ? 0.f : ex2(ref - to);
+          l = l * keep + zero_sum * ex2(zero_ref - to + kWeightBits);
+          ref = to;
+        }
         if (CUT && parts > 1) {
           // this part's rows; the warp whose rows' last part this is puts them together
           area = plan.parts + (long long)(cut - part) * kPartFloats;  // of the block's first part
@@ -446,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              __stcg(reinterpret_cast<uint4*>(mine) + (4 * b + e) * (2 * kTileRows) + row256,
-                     make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+              __stcg(reinterpret_cast<float4*>(mine) + (4 * b + e) * (2 * kTileRows) + row256,
+                     make_float4(__uint_as_float(v[4 * e]) * keep, __uint_as_float(v[4 * e + 1]) * keep,
+                                 __uint_as_float(v[4 * e + 2]) * keep, __uint_as_float(v[4 * e + 3]) * keep));
           }
           __stcg(mine + 2 * kTileRows * D + row256, ref);
           __stcg(mine + 2 * kTileRows * (D + 1) + row256, l);
@@ -463,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
           __threadfence();
           if (store) {
             others = area;
+            keep = 1.f;  // it is in the parts
             ref = -INFINITY;
             for (int p = 0; p < parts; ++p)
               ref = fmaxf(ref, __ldcg(area + (long long)p * kPartFloats + 2 * kTileRows * D + row256));
@@ -475,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
           }
         }
         if (store) {
-          const float inv = l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l;
+          const float inv = keep * (l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l);
           // through the rows' place in shared memory, where no product reads any more, so that whole rows leave (a
           // row a lane takes a pass of the cache's tags for each lane)
           constexpr int kLanes = D / 8, kStep = 32 / kLanes, kLoads = 32 / kStep;
@@ -675,13 +715,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
         if (copies) bulk_copy(sbase + L::kRawV + 16 * lane * D, vbase + id * page_stride, bytes, bars + kRawVFull);
         copied_v = n + 1;
         // the slot's last readers were done before the levels of tile n - 1 were taken from shared memory
+        const bool zero = gv < 0x1p-113f;  // (or no page)
+        const uint32_t zeros = __ballot_sync(0xffffffffu, zero && id >= 0);
         if (lane < 8) {
           GroupScale gs;
           gs.ks = gk;
-          gs.e = log2f(gv);
-          gs.back = __frcp_rn(gv);
-          if (gv < 0x1p-113f) gs.e = -60.f, gs.back = 0x1p60f;  // a zero page: its levels count for nothing
-          gs.pad = 0.f;
+          gs.e = zero ? -INFINITY : log2f(gv);
+          gs.back = zero ? 0.f : __frcp_rn(gv);
+          gs.zeros = zeros;
           table[(n % kTableStages) * 8 + lane] = gs;
         }
         __syncwarp();

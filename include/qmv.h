@@ -620,7 +620,9 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
  * Calls with many bfloat16 rows (prompts; heads of 64 or 128) round the weights times the V
  * scale once to half: 2^-11 relative down to 2^-21 of the row's largest one, below that multiples
  * of at most 2^-32 of it (a key whose weight times V scale is that far below the row's largest counts only
- * to that resolution).  Results do not depend on timing.
+ * to that resolution; in the sum of the weights, a p below 2^-133 times the row's largest V scale over the
+ * key's is not counted, and a V scale below 2^-113 counts as 0).  What a page of V scale 0 holds is 0
+ * whatever its levels, and its keys weigh in the sum of the weights.  Results do not depend on timing.
  * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream (8 MiB,
  * shared with qmv_logprobs; 64 MiB more for prompts of few blocks of rows over many keys), allocated
  * on the stream's first such call and kept; while a stream without one is being captured, the call

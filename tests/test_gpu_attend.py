@@ -348,3 +348,49 @@ def test_pages_that_the_window_hides_from_cut_prompts(qmv, how):
     got = qmv.attend(cache, batch_of(qmv, td, lens, counts), qd, window=window)
     assert qmv.last_error() == 0
     check(twin, table, lens, counts, qf, got, 128 ** -0.5, True, window, True)
+
+
+SCALE_SHAPES = [
+    (16, 4, 128, 16, [1100], [500]),         # whole blocks on the prompt kernel
+    (32, 8, 64, 64, [900, 700], [400, 300]),
+    (8, 2, 128, 64, [5000], [256]),          # blocks cut along the keys
+    (8, 2, 128, 128, [300, 64, 5], [1, 2, 1]),  # the kernel for few rows
+]
+
+
+@pytest.mark.parametrize("heads,kvh,dim,page,lens,counts", SCALE_SHAPES)
+@pytest.mark.parametrize("amp,lo,hi", [(1e-6, -12, 3), (1.0, -12, 3), (20.0, -12, 3), (1.0, -25, -22), (1.0, 3, 20)])
+@pytest.mark.parametrize("levels", [False, True])
+def test_v_scales_decades_apart_and_zero_pages(qmv, heads, kvh, dim, page, lens, counts, amp, lo, hi, levels):
+    """V scales over many powers of ten, down to values of 1e-23; pages of zero K, and of zero V with and without levels
+    left in them: what a page of scale 0 holds is 0, and its keys weigh in the sum only."""
+    import torch
+    rng = np.random.default_rng(7)
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=3)
+    for s, n in enumerate(lens):
+        used = table[s, :-(-n // page)]
+        twin.scale[1][used] = (10.0 ** rng.uniform(lo, hi, (used.size, kvh))).astype(F)
+        for i, p in enumerate(used):
+            if i % 5 == 2:
+                twin.scale[1][p] = 0
+                if not levels:
+                    twin.lev[1][p] = 0
+            if i % 7 == 3:
+                twin.scale[0][p] = 0
+    for t, a in ((cache.v, twin.lev[1]), (cache.k_scale, twin.scale[0]), (cache.v_scale, twin.scale[1])):
+        t.copy_(torch.from_numpy(a))
+    qf, qd = queries(rng, sum(counts), heads, dim, True, amp)
+    b = batch_of(qmv, td, lens, counts)
+    got = qmv.attend(cache, b, qd)
+    check(twin, table, lens, counts, qf, got, dim ** -0.5, True, 0, True, halves=True)
+    assert bool((got == qmv.attend(cache, b, qd)).all())
+
+
+@pytest.mark.parametrize("heads,kvh,dim,page,lens,counts", SCALE_SHAPES)
+def test_nothing_but_zero_pages(qmv, heads, kvh, dim, page, lens, counts):
+    """Every V scale 0, the levels not: the output is 0 exactly."""
+    rng = np.random.default_rng(8)
+    cache, twin, table, td = filled(qmv, lens, kvh, dim, page, seed=3)
+    cache.v_scale.zero_()
+    _, qd = queries(rng, sum(counts), heads, dim, True)
+    assert not qmv.attend(cache, batch_of(qmv, td, lens, counts), qd).any()

@@ -437,12 +437,14 @@ __device__ __forceinline__ uint32_t pack_levels(float t0, float t1, float t2, fl
   asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w) : "r"((int)t1), "r"((int)t0), "r"(hi));
   return w;
 }
-// Two values times inv, half a step away from zero.
+// Two values times inv, half a step away from zero: two roundings.  The product is an fma with +0: a packed multiply
+// and add in a row are made into one fma (its one rounding gives 0 where the rule gives 1 for a product just below a half),
+// and + 0 cannot be left out (it turns -0 into +0, which the addition after it does not see).
 __device__ __forceinline__ void step2(float a, float b, uint64_t inv2, float& ta, float& tb) {
   uint64_t x, h;
   asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
   asm("mov.b64 %0, {%1, %2};" : "=l"(h) : "f"(copysignf(0.5f, a)), "f"(copysignf(0.5f, b)));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(inv2));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(inv2), "l"(0ull));
   asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(h));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(ta), "=f"(tb) : "l"(x));
 }

@@ -142,3 +142,14 @@ def top_ids(x, n):
     """The n largest of each row, equal ones by the lower id."""
     key = np.where(np.isnan(x), np.inf, x) + 0.0
     return np.stack([np.lexsort((np.arange(r.size), -r))[:n] for r in key])
+
+
+def near_half(inv):
+    """The float32 values below half a step (0.5 / inv) whose level depends on the product's own rounding: rounded before the
+    half is added it gives 1, in one rounding of the whole 0.  May be empty: about three in ten have one."""
+    x = np.full(16, F(np.float64(0.5) / np.float64(inv)))
+    for i in range(1, x.size):
+        x[i] = np.nextafter(x[i - 1], F(0))
+    twice = np.trunc(((x * F(inv)).astype(F) + F(0.5)).astype(F))
+    once = np.trunc((x.astype(np.float64) * np.float64(inv) + 0.5).astype(F))  # 48-bit product, exact in 64 bits
+    return x[twice != once]

@@ -236,3 +236,23 @@ def test_loose_bounds(qmv):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert float((qmv.attend(cache, b, kd) - out).abs().max()) < 1e-4 * float(out.abs().max())
     assert qmv.last_error() == 0
+
+
+@pytest.mark.parametrize("page,heads,dim", [(16, 2, 64), (64, 3, 128), (128, 1, 256)])
+def test_levels_at_half_steps(qmv, page, heads, dim):
+    """Values whose level depends on the product's own rounding: the rule rounds it before the half is added."""
+    import torch
+    rng = np.random.default_rng(page)
+    cache, twin, table, td = make(qmv, [page], heads, dim, page, seed=1)
+    k = np.empty((page, heads, dim), F)
+    for h in range(heads):
+        x = []
+        while len(x) == 0:
+            top = F(rng.uniform(0.5, 50))
+            x = ops_ref.near_half(F(1) / F(top * F(1 / 127)))
+        k[:, h] = rng.choice(np.concatenate([x, -x]), (page, dim))
+        k[rng.integers(page), h, rng.integers(dim)] = top
+    v = -k
+    qmv.kv_write(cache, batch_of(qmv, td, [page], [page]), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda())
+    twin.write(table, [page], [page], k, v)
+    same(cache, twin)

@@ -144,3 +144,22 @@ def test_weights_written_before_the_norm(qmv):
         qmv.matvec_grouped(qmv.Q8_0, qmv.SCALE_F32, [(rows, cols, W, h, y)], overlap=True)
     for i, y in enumerate(got):
         assert torch.equal(y, want[i & 1]), i
+
+
+def test_image_levels_at_half_steps(qmv):
+    """Values whose level depends on the product's own rounding: the rule rounds it before the half is added."""
+    import torch
+    rng = np.random.default_rng(2)
+    rows, cols = 16, 1024
+    x = np.empty((rows, cols // 32, 32), F)
+    for r in range(rows):
+        for b in range(cols // 32):
+            near = []
+            while len(near) == 0:
+                top = F(rng.uniform(0.5, 50))
+                near = ops_ref.near_half(F(127) * (F(1) / top))
+            x[r, b] = rng.choice(np.concatenate([near, -near]), 32)
+            x[r, b, 0] = top
+    lev, _ = _image(qmv, qmv.rmsnorm(torch.from_numpy(x.reshape(rows, cols)).cuda(), torch.ones(cols, device="cuda")), rows, cols)
+    inv = (F(127) * (F(1) / np.abs(x).max(axis=2, keepdims=True))).astype(F)
+    assert np.array_equal(lev.reshape(x.shape), ops_ref.q8_levels(x, inv))

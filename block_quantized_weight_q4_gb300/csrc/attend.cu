@@ -13,9 +13,9 @@
 // maximum, sum and output; the warps of a CTA meet in shared memory, the CTAs that share a
 // sequence in the stream's workspace, added in a fixed order by the last to arrive.
 //
-// Measured: 64 ragged sequences of up to 16384 tokens, 32 heads over 8 of 128, 196 us (6.03 TB/s, 89% of the measured
-// copy rate; issue 53% busy, the ALU work is the levels' conversion, 5 operations for 4 levels of K and 7 of V); 256
-// sequences of 1000 tokens 105 us (5.0 TB/s); one sequence of 1000 tokens 8.4 us, a chain of dependent latencies.
+// Measured: 64 ragged sequences of up to 16384 tokens, 32 heads over 8 of 128, 197 us (6.0 TB/s, 88% of the measured
+// copy rate; issue 54% busy, the ALU work is the levels' conversion, 5 operations for 4 levels of K and 7 of V); 256
+// sequences of 1000 tokens 105 us (5.0 TB/s); one sequence of 1000 tokens 8.6 us, a chain of dependent latencies.
 // Three CTAs of two stages a warp a SM: with three stages only two fit (224 us), with eight warps a CTA 237 us.
 #include <mutex>
 

@@ -22,7 +22,7 @@
 //
 // Bound: 2 x 2 x 128 x 128 x head_dim operations a tile and turn on the tensor core, against one exponential for
 // each score and the softmax's turn, which hides behind the other tile's products only in part.  2048 rows
-// over 16384 tokens (32 heads over 8 of 128) 393 us, 1310 TFLOP/s (69% of the measured bf16 rate; tensor pipe 58%
+// over 16384 tokens (32 heads over 8 of 128) 399 us, 1290 TFLOP/s (69% of the measured bf16 rate; tensor pipe 57%
 // active on a smaller case, issue 48%); three prompts of up to 2048 tokens 87 us.  A turn of one row tile takes
 // about 3500 cycles: softmax 1800, products 1300 (1024 of them at the peak rate), hand-over 400.
 #include <mutex>
@@ -169,7 +169,7 @@ struct SplitPlan {
 constexpr int kMinPart = 4;
 
 // PG: keys that share a page's scales, 16 or 64 (pages of 64 and 128 tokens).  CUT: some blocks are cut (the code
-// that joins their parts costs the launches without them 3%: three prompts of up to 2048 tokens 90 against 87 us).
+// that joins their parts costs the launches without them 3%: prompts of 2048, 1563 and 1278 tokens 98 against 95 us).
 template <int D, int PG, bool CUT>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid_constant__ KvRef c,
                                                                     const __grid_constant__ AttendArgs a,
@@ -750,9 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const __grid
 // How a call's blocks go over the SMs, by its bounds, in ns: about 1.55 us a tile of 128 keys for two row tiles, 1.35 us
 // for one, 6 us more a wave of blocks, 14 us more a wave of cut ones (they write and read their parts).  Blocks that
 // fill whole waves stay whole; the others, or all of a call with fewer blocks than SMs, are cut along the keys
-// where that saves a tenth.  Measured, whole against cut, 32 heads over 8 of 128: 256 rows over 16384 tokens 224 against
-// 74 us, 512 rows over 16384 225 against 126, 64 rows over 2048 40 against 25; 2048 rows over 16384 (256 blocks)
-// 393 against 409, 640 rows over 2048 (80 blocks) 35 against 49.
+// where that saves a tenth.  Measured, whole against cut, 32 heads over 8 of 128: 256 rows over 16384 tokens 213 against
+// 73 us, 512 rows over 16384 212 against 123, 64 rows over 2048 34 against 24; 2048 rows over 16384 (256 blocks)
+// 399 against 399, 640 rows over 2048 (80 blocks) 35 against 49.
 struct Estimate {
   long long items;  // blocks of the grid before any cut, at most: exact for one sequence, else a block more for each
   long long whole, split, ns;
@@ -814,8 +814,9 @@ cudaError_t launch_dim(const KvRef& c, const AttendArgs& a, const DeviceInfo& de
 // bfloat16 rows, heads of 64 or 128, where this kernel's estimated time is the shorter one; the kernel for few rows
 // reads the keys once for each 16 rows (over the whole GPU about 2 ns for 32 keys of 16 rows), from about 9 us on.
 // Measured, that kernel against this one, 32 heads over 8 of 128: one sequence of 2048 tokens, 64 rows 34 against
-// 25 us, 1024 rows 259 against 36; 64 sequences of 4096 tokens, 4 rows each 141 against 203 us, 8 rows 261
-// against 206, 16 rows 498 against 207; 4 prompts of 128 tokens 35 against 12 us.
+// 24 us, 1024 rows 256 against 35; 64 sequences of 4096 tokens, 4 rows each 140 against 207 us, 8 rows 258
+// against 208, 16 rows 494 against 209; 4 prompts of 128 tokens 35 against 12 us.  The choice is the whole call's, by
+// the average of its rows: one chunk of 256 rows among 63 single tokens of 4096 takes 205 us in one call and 33 + 95 in two.
 bool attend_prompt_supported(const KvRef& c, const AttendArgs& a, bool x_bf16, const DeviceInfo& dev) {
   if (!x_bf16 || c.head_dim > 128) return false;
   const long long span = a.window > 0 && (long long)a.window + c.max_rows < c.max_len ? a.window + c.max_rows : c.max_len;

@@ -2,10 +2,11 @@
 // page and head, and read back.
 //
 // Writing is bound by the rows' bytes, and below that by the instructions that a value's level takes (about 7; a third
-// fewer than with conversions, clamps and packs one by one, which took 23.2 us where these take 18.7) and a chain of
+// fewer than with conversions, clamps and packs one by one, which took 23.2 us where these took 18.7) and a chain of
 // dependent loads a page (lengths, page id and rows, the old scale) around one reduction: 16384 bfloat16 rows of 8 heads
-// of 128 in 18.7 us (5.4 TB/s, 79% of the measured copy rate; float32 27.5 us, 6.1 TB/s), one row of each of 64
-// sequences in 2.3 us.  A page, head and side (K or V) is a CTA because its scale is what its rows share.  Reading is a
+// of 128 in 19.2 us (5.2 TB/s, 77% of the measured copy rate; issue 74% busy, ALU 61%; float32 28.2 us, 5.9 TB/s), one row
+// of each of 64 sequences in 2.3 us, 6.5 us where every other one raises a page of 40 earlier tokens, whose levels are then
+// read, moved and written.  A page, head and side (K or V) is a CTA because its scale is what its rows share.  Reading is a
 // copy that widens: 16 sequences of up to 16384 tokens as bfloat16 in 191 us (6.57 TB/s, 97%), 16 of 8000 as float32 in
 // 196 us (6.69 TB/s; 273 us while a thread stored 64 bytes in a row, so that a warp's store touched 32 lines).
 #include <type_traits>
@@ -196,8 +197,8 @@ cudaError_t launch_write(const KvRef& c, const void* k, int64_t k_stride, const 
   const int pages = kv_pages_bound(c.max_rows, c.page_tokens);
   const dim3 grid((unsigned)pages, (unsigned)c.n_seq, (unsigned)(2 * c.kv_heads));
   // pieces of the most rows that a page may receive, over at most 256 threads of 1 or 4, else of 8: 16384 rows of
-  // 8 heads of 128, pages of 16 tokens, 19.3 us with 4 pieces a thread, 23.2 with 8; 256 single rows 4.6 with 1, 6.2
-  // with 8; heads of 256 and pages of 64 (512 threads of 4) 37.0 with 4, 35.0 with 8
+  // 8 heads of 128, pages of 16 tokens, 18.7 us with 4 pieces a thread, 23.6 with 8; 256 single rows 5.1 with 1, 6.8
+  // with 8; heads of 256 and pages of 64 (512 threads of 4) 37.0 with 4, 35.4 with 8
   const int pieces = (c.max_rows < c.page_tokens ? c.max_rows : c.page_tokens) * (D / 8);
   const int per = pieces <= 64 ? 1 : pieces <= 4 * 256 ? 4 : 8;
   auto kern = per == 1 ? kv_write_kernel<D, XB, 1> : per == 4 ? kv_write_kernel<D, XB, 4> : kv_write_kernel<D, XB, 8>;

@@ -8,8 +8,9 @@
 // reaches the smallest kept value of any warp of the CTA.  A few rows are cut into parts over many CTAs; the
 // last part of a row to finish joins them in their order.
 //
-// Measured: 512 rows of 151936 with 5 alternatives 55.1 us (5.64 TB/s, 83% of the measured copy rate; 49.7 us
-// with none, 79.6 with 20), one row with 8 alternatives 10.1 us (7.0 with none): launch, one pass, the join.
+// Measured: 512 rows of 151936 with 5 alternatives 55.7 us (5.59 TB/s, 82% of the measured copy rate; 50 us with none, 60
+// with 8, 80 with 20, 99 with 32: a candidate enters a warp's list by itself, and the floor is a warp's own k-th value), one
+// row with 8 alternatives 10.5 us (7.4 with none): launch, one pass, the join.
 #include <mutex>
 
 #include "qmv_common.cuh"
@@ -22,8 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // What a CTA's part of a row costs besides its values (start, lists, the join), in values: with 4096 the rows of
-// 512 x 151936 are cut in four and take 69.4 us (5 alternatives; 117 us with 20), with 32768 they are whole and
-// take 63.8 (97.9); single rows and 200 x 32000 do not change.
+// 512 x 151936 are cut and take 84.9 us (5 alternatives; 61 us with none, 153 with 20), with 32768 they are whole and
+// take 55.7 (50, 80); 1, 8 and 64 rows of 151936 and 200 of 32000 do not change.
 constexpr long long kPartCost = 32768;
 constexpr int kBatch = 16;  // values a thread takes at a time, as four 16-byte loads
 using Key = unsigned long long;

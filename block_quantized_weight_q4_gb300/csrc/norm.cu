@@ -9,8 +9,9 @@
 // Nothing is kept but the row itself, in registers, until r is known.
 //
 // Bound by the bytes of the residual stream (read, written) and x: 2048 x 4096 bfloat16 rows into the image
-// 15.7 us, 5.94 TB/s (88% of the measured copy rate; 16.2 us with a level's conversion, clamp and pack one by one), into
-// bfloat16 6.2 TB/s; one row of 4096 2.1 us, which is the launch and one chain of loads, the reduction and the stores.
+// 15.6 us, 5.98 TB/s (88% of the measured copy rate; 16.2 us with a level's conversion, clamp and pack one by one), into
+// bfloat16 6.2 TB/s; 700 x 11008 float32 into bfloat16 5.2 TB/s; one row of 4096 2.3 us, which is the launch and one
+// chain of loads, the reduction and the stores.
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
 

@@ -615,18 +615,26 @@ int qmv_kv_read(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int out_dt
  * j > p - window.  A row that sees no key gives zeros.  What the pages hold beyond a
  * sequence's tokens, and the pages that a window hides whole, do not enter.
  * Scores, softmax and sums are float32.  The levels enter the tensor core as exact halves; q
- * as halves after a power-of-two scale of its row (exact for bfloat16, a pair hi + lo of 22 bits for
- * float32); the weights p times the V scale as two bfloat16 parts (16 bits; three, 24 bits, for float32).
+ * as halves after a power-of-two scale of its row (bfloat16 values are exact down to 2^-31 of the row's
+ * largest, smaller ones multiples of at most 2^-38 of it; float32 ones a pair hi + lo of 22 bits);
+ * the weights p times the V scale as two bfloat16 parts (16 bits; three, 24 bits, for float32).
  * Calls with many bfloat16 rows (prompts; heads of 64 or 128) round the weights times the V
  * scale once to half: 2^-11 relative down to 2^-21 of the row's largest one, below that multiples
  * of at most 2^-32 of it (a key whose weight times V scale is that far below the row's largest counts only
  * to that resolution; in the sum of the weights, a p below 2^-133 times the row's largest V scale over the
  * key's is not counted, and a V scale below 2^-113 counts as 0).  What a page of V scale 0 holds is 0
- * whatever its levels, and its keys weigh in the sum of the weights.  Results do not depend on timing.
+ * whatever its levels, and its keys weigh in the sum of the weights.
+ * One kernel takes the whole call, chosen by the estimated times for the average of its rows, the
+ * bounds max_rows and max_len and the heads; how the keys are cut follows from the same
+ * numbers.  So results do not depend on timing, but the last bits of a sequence's rows, and which of
+ * the two roundings above its weights get, depend on what else the call holds.  A prompt chunk and many
+ * single tokens are better given as two calls, which also read the cache at each one's own pace (256 rows and
+ * 63 single tokens over 4096 tokens: 205 us in one call, 33 + 95 in two).
  * May split a long sequence between CTAs: the parts meet in a workspace of the calling stream (8 MiB,
  * shared with qmv_logprobs; 64 MiB more for prompts of few blocks of rows over many keys), allocated
- * on the stream's first such call and kept; while a stream without one is being captured, the call
- * does not split (slower; call once on the stream before capturing it).  A captured call keeps to the
+ * on the stream's first such call and kept; while a stream without one is being captured, or where it
+ * cannot be allocated, the call does not split (much slower for few long sequences: call once on the
+ * stream that will be captured, before the capture).  A captured call keeps to the
  * capturing stream's workspace: its replays must not overlap in time with other calls that use it.
  * Returns QMV_OK, QMV_E_FORMAT (x_dtype), QMV_E_ARG (null pointer, negative count, window < 0, scale not
  * finite), QMV_E_SHAPE (the cache's or rows' numbers, heads, strides), QMV_E_ALIGN or QMV_E_CUDA. */

@@ -109,6 +109,16 @@ def load_library():
     lib.qmv_attend.argtypes = [vp, vp, i32, i32, vp, i64, f32, i32, i32, vp, i64, vp]
     lib.qmv_logprobs.restype = i32
     lib.qmv_logprobs.argtypes = [i64, i64, vp, i64, vp, i32, vp, vp, i32, vp, vp, vp]
+    lib.qmv_sample.restype = i32
+    lib.qmv_sample.argtypes = [i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+    lib.qmv_embed.restype = i32
+    lib.qmv_embed.argtypes = [i32, i32, i64, i64, vp, vp, i64, f32, i32, vp, vp]
+    lib.qmv_qk_rope.restype = i32
+    lib.qmv_qk_rope.argtypes = [i32, i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, f32, vp, vp, i32, i32, f32, i32, vp, i64, vp, i64, vp]
+    lib.qmv_moe_scratch_bytes.restype = sz
+    lib.qmv_moe_scratch_bytes.argtypes = [i64, i32, i64, i32]
+    lib.qmv_moe.restype = i32
+    lib.qmv_moe.argtypes = [vp, i64, vp, i64, i32, i32, f32, i32, i32, vp, i32, vp, vp, vp, vp, vp]
     lib.qmv_check_device.restype = i32
     lib.qmv_check_device.argtypes = []
     lib.qmv_strerror.restype = ctypes.c_char_p
@@ -747,6 +757,199 @@ def logprobs(logits, given=None, top: int = 0, entropy: bool = True, stream=None
                                      _raw_stream(stream, logits.get_device(), *(() if given is None else (given.get_device(),))))
     _check(st, "qmv_logprobs")
     return glp, ent, ids, tlp
+
+
+def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, stream=None):
+    """The next id of each row of logits (qmv_sample): logits and noise (rows, vocab) float32, rows may be strided;
+    noise: exponential random numbers (torch.empty_like(logits).exponential_()).  temperature, top_p, min_p: float32
+    (rows,), top_k int32 (rows,) CUDA tensors, whose contents are read when the call runs on the device, or None.
+    Returns ids, int64 (rows,): what embed() and logprobs() take."""
+    import torch
+    f32 = torch.float32
+    for t in (logits, noise):
+        if t.dim() != 2 or t.dtype is not f32 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError("logits and noise must be float32 (rows, vocab) tensors with contiguous rows")
+    rows, vocab = logits.shape
+    if noise.shape != logits.shape:
+        raise ValueError("noise must have the logits' shape")
+    for t, dtype in ((temperature, f32), (top_k, torch.int32), (top_p, f32), (min_p, f32)):
+        if t is not None and (t.dtype is not dtype or t.shape != (rows,) or not t.is_contiguous()):
+            raise ValueError("temperature, top_p and min_p must be contiguous float32 (rows,) tensors, top_k int32")
+    if ids is None:
+        ids = torch.empty((rows,), dtype=torch.int64, device=logits.device)
+    elif ids.dtype is not torch.int64 or ids.shape != (rows,) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int64 (rows,) tensor")
+    st = load_library().qmv_sample(rows, vocab, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, noise.data_ptr(),
+                                   noise.stride(0) if rows > 1 else vocab,
+                                   None if temperature is None else temperature.data_ptr(),
+                                   None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+                                   None if min_p is None else min_p.data_ptr(), ids.data_ptr(),
+                                   _raw_stream(stream, logits.get_device(), noise.get_device(), ids.get_device(),
+                                               *[t.get_device() for t in (temperature, top_k, top_p, min_p) if t is not None]))
+    _check(st, "qmv_sample")
+    return ids
+
+
+def _out_type(out, what="out"):
+    import torch
+    if out == "f32":
+        return X_F32, torch.float32
+    if out == "bf16":
+        return X_BF16, torch.bfloat16
+    raise ValueError(f"{what} must be 'bf16' or 'f32'")
+
+
+def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: float = 1.0, out="f32", y=None, stream=None):
+    """Rows of a block-quantized token table (qmv_embed): W the uint8 image of the (vocab, cols) matrix, ids an int64 CUDA
+    tensor of any shape.  Returns y, ids.shape + (cols,) of the type `out` ("f32" or "bf16"): the rows times scale, zeros
+    for ids outside the table."""
+    import torch
+    code, dtype = _out_type(out)
+    if ids.dtype is not torch.int64 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int64 tensor")
+    if W.dtype is not torch.uint8 or not W.is_contiguous() or W.numel() < weight_bytes(wtype, scale_dtype, vocab, cols):
+        raise ValueError("W must be a contiguous uint8 tensor of the matrix image's bytes")
+    shape = ids.shape + (cols,)
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=W.device)
+    elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
+        raise ValueError("y must be a contiguous tensor of ids' shape and cols, of the output's type")
+    st = load_library().qmv_embed(wtype, scale_dtype, vocab, cols, W.data_ptr(), ids.data_ptr(), ids.numel(), scale, code,
+                                  y.data_ptr(), _raw_stream(stream, W.get_device(), ids.get_device(), y.get_device()))
+    _check(st, "qmv_embed")
+    return y
+
+
+ROPE_PAIRS = {"neighbours": 0, "halves": 1}
+
+
+def _rope_rows(t, heads, dim, rows, what):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.shape[0] != rows:
+        raise ValueError(f"{what} must be a ({rows}, {heads}, {dim}) tensor")
+    return _head_rows(t, heads, dim, rows, what)
+
+
+def qk_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps: float = 1e-6, pairs="halves", factor: float = 1.0, out=None,
+            q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head and the position rotation, in one pass (qmv_qk_rope).  q (rows, heads, head_dim)
+    and k (rows, kv_heads, head_dim) or None: float32 or bfloat16 CUDA tensors, rows may be strided (slices of a
+    fused projection).  pos: int32 (rows,); freq: float32 (rot_dim / 2,) in radians a position; both None for norms alone.
+    q_weight, k_weight: float32 (head_dim,), or None for no norm.  pairs: "halves" (i and i + rot_dim / 2) or "neighbours"
+    (2i and 2i + 1).  out: "f32" or "bf16" (q's own type by default).  q_out, k_out: where to write (q and k themselves
+    for an update in place).  Returns q_out, k_out."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be a (rows, heads, head_dim) tensor")
+    rows, heads, dim = q.shape
+    x = _x_dtype(q)
+    qs, kvh, ks = _rope_rows(q, heads, dim, rows, "q"), 0, 0
+    if k is not None:
+        if k.dim() != 3 or k.dtype is not q.dtype:
+            raise ValueError("k must be a (rows, kv_heads, head_dim) tensor of q's type")
+        kvh = k.shape[1]
+        ks = _rope_rows(k, kvh, dim, rows, "k")
+    f32 = torch.float32
+    if (pos is None) != (freq is None):
+        raise ValueError("pos and freq go together")
+    rot = 0
+    if freq is not None:
+        if freq.dtype is not f32 or freq.dim() != 1 or not freq.is_contiguous():
+            raise ValueError("freq must be a contiguous float32 (rot_dim / 2,) tensor")
+        if pos.dtype is not torch.int32 or pos.shape != (rows,) or not pos.is_contiguous():
+            raise ValueError("pos must be a contiguous int32 (rows,) tensor")
+        rot = 2 * freq.shape[0]
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not f32 or w.shape != (dim,) or not w.is_contiguous()):
+            raise ValueError("q_weight and k_weight must be contiguous float32 (head_dim,) tensors")
+    if pairs not in ROPE_PAIRS:
+        raise ValueError("pairs must be 'halves' or 'neighbours'")
+    code, dtype = (x, q.dtype) if out is None else _out_type(out)
+    if q_out is None:
+        q_out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device)
+    if k is None:
+        if k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight need k")
+    elif k_out is None:
+        k_out = torch.empty((rows, kvh, dim), dtype=dtype, device=k.device)
+    if q_out.dtype is not dtype or (k_out is not None and k_out.dtype is not dtype):
+        raise ValueError("q_out and k_out must be of the output's type")
+    qos = _rope_rows(q_out, heads, dim, rows, "q_out")
+    kos = 0 if k is None else _rope_rows(k_out, kvh, dim, rows, "k_out")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = load_library().qmv_qk_rope(x, rows, heads, kvh, dim, q.data_ptr(), qs, ptr(k), ks, ptr(q_weight), ptr(k_weight), eps,
+                                    ptr(pos), ptr(freq), rot, ROPE_PAIRS[pairs], factor, code, q_out.data_ptr(), qos, ptr(k_out), kos,
+                                    _raw_stream(stream, q.get_device(), *[t.get_device() for t in
+                                                (k, pos, freq, q_weight, k_weight, q_out, k_out) if t is not None]))
+    _check(st, "qmv_qk_rope")
+    return q_out, k_out
+
+
+class _MoeC(ctypes.Structure):
+    """qmv_moe_layer of include/qmv.h."""
+    _fields_ = [("wtype13", ctypes.c_int), ("wtype2", ctypes.c_int), ("scale_dtype", ctypes.c_int), ("experts", ctypes.c_int),
+                ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64), ("W1", ctypes.c_void_p), ("W3", ctypes.c_void_p),
+                ("W2", ctypes.c_void_p)]
+
+
+class Moe:
+    """A layer of experts (qmv_moe_layer): W1 and W3 the uint8 images of (experts * hidden, dim) matrices of type wtype13, W2
+    that of (experts * dim, hidden) of type wtype2; CUDA tensors, kept with the layer."""
+
+    def __init__(self, wtype13: int, wtype2: int, scale_dtype: int, experts: int, dim: int, hidden: int, W1, W3, W2):
+        import torch
+        for W, wt, rows, cols in ((W1, wtype13, experts * hidden, dim), (W3, wtype13, experts * hidden, dim), (W2, wtype2, experts * dim, hidden)):
+            need = weight_bytes(wt, scale_dtype, rows, cols)
+            if W.dtype is not torch.uint8 or not W.is_contiguous() or need == 0 or W.numel() < need:
+                raise ValueError("W1, W3 and W2 must be contiguous uint8 tensors of the matrix images' bytes")
+        self.experts, self.dim, self.hidden = experts, dim, hidden
+        self.W1, self.W3, self.W2 = W1, W3, W2
+        self._c = _MoeC(wtype13, wtype2, scale_dtype, experts, dim, hidden, W1.data_ptr(), W3.data_ptr(), W2.data_ptr())
+        self._p = ctypes.addressof(self._c)
+        self._index = _device_of((W1, W3, W2), "a layer's matrices")
+
+
+def moe(layer: Moe, x, logits, top: int, renorm: bool = True, scale: float = 1.0, act: str = "silu", out="f32", y=None,
+        routing: bool = False, scratch=None, stream=None):
+    """The layer of experts for a few tokens (qmv_moe): x (tokens, dim) float32/bfloat16, logits (tokens, experts) float32
+    (rows may be strided).  Returns y, (tokens, dim) of the type `out` ("f32" or "bf16"); with routing also the experts
+    (tokens, top) int32 and their shares float32.  scratch: a uint8 CUDA tensor of moe_scratch_bytes(), by default one from
+    torch's allocator for this call (with a stream other than the current one, give it, and keep it until that stream is done)."""
+    import torch
+    code, dtype = _out_type(out)
+    if act not in ACT_CODES:
+        raise ValueError("act must be 'silu' or 'gelu'")
+    if x.dim() != 2 or x.shape[1] != layer.dim or not x.is_contiguous():
+        raise ValueError("x must be a contiguous (tokens, dim) tensor")
+    n = x.shape[0]
+    if logits.dtype is not torch.float32 or logits.shape != (n, layer.experts) or (layer.experts > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a float32 (tokens, experts) tensor with contiguous rows")
+    if y is None:
+        y = torch.empty((n, layer.dim), dtype=dtype, device=x.device)
+    elif y.dtype is not dtype or y.shape != (n, layer.dim) or not y.is_contiguous():
+        raise ValueError("y must be a contiguous (tokens, dim) tensor of the output's type")
+    need = moe_scratch_bytes(n, top, layer.hidden, out)
+    if scratch is None:
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        if stream is not None:
+            scratch.record_stream(stream)
+    elif scratch.dtype is not torch.uint8 or scratch.numel() < need or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous uint8 tensor of moe_scratch_bytes()")
+    ids = shares = None
+    if routing:
+        ids = torch.empty((n, top), dtype=torch.int32, device=x.device)
+        shares = torch.empty((n, top), dtype=torch.float32, device=x.device)
+    st = load_library().qmv_moe(layer._p, n, logits.data_ptr(), logits.stride(0) if n > 1 else layer.experts, top, 1 if renorm else 0,
+                                scale, ACT_CODES[act], _x_dtype(x), x.data_ptr(), code, y.data_ptr(),
+                                None if ids is None else ids.data_ptr(), None if shares is None else shares.data_ptr(),
+                                scratch.data_ptr(),
+                                _raw_stream(stream, x.get_device(), logits.get_device(), y.get_device(), scratch.get_device(), layer._index))
+    _check(st, "qmv_moe")
+    return (y, ids, shares) if routing else y
+
+
+def moe_scratch_bytes(tokens: int, top: int, hidden: int, out="f32") -> int:
+    """Bytes of scratch memory that moe() needs for `tokens` tokens of `top` experts (0 for numbers that it refuses)."""
+    return int(load_library().qmv_moe_scratch_bytes(tokens, top, hidden, _out_type(out)[0]))
 
 
 def last_error() -> int:

@@ -776,6 +776,147 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float* logits, int64_t strid
   return launch_logprobs(a, rows, dev, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
 }
 
+int qmv_sample(int64_t rows, int64_t vocab, const float* logits, int64_t stride, const float* noise, int64_t noise_stride,
+               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int64_t* ids,
+               cudaStream_t stream) {
+  if (rows < 0) return QMV_E_ARG;
+  if (vocab <= 0 || vocab >= QMV_SAMPLE_MAX_VOCAB || stride < vocab || noise_stride < vocab) return QMV_E_SHAPE;
+  if (rows > INT32_MAX / 8 || (rows > 0 && (stride > INT64_MAX / 4 / rows || noise_stride > INT64_MAX / 4 / rows)))
+    return QMV_E_SHAPE;
+  if (rows == 0) return QMV_OK;
+  if (logits == nullptr || noise == nullptr || ids == nullptr) return QMV_E_ARG;
+  if (!aligned(logits, 4) || !aligned(noise, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+      !aligned(min_p, 4) || !aligned(ids, 8))
+    return QMV_E_ALIGN;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
+  SampleArgs a;
+  a.logits = logits;
+  a.noise = noise;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.ids = ids;
+  a.stride = stride;
+  a.noise_stride = noise_stride;
+  a.vocab = vocab;
+  return launch_sample(a, rows, dev, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
+}
+
+int qmv_embed(int wtype, int scale_dtype, int64_t vocab, int64_t cols, const void* W, const int64_t* ids, int64_t rows, float scale,
+              int out_dtype, void* out, cudaStream_t stream) {
+  if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (rows < 0 || !std::isfinite(scale)) return QMV_E_ARG;
+  Layout L;
+  const int lt = make_layout(wtype, scale_dtype, vocab, cols, &L);
+  if (lt != QMV_OK) return lt;
+  if (rows == 0) return QMV_OK;
+  MatrixRef m;
+  const int st = make_ref(wtype, scale_dtype, vocab, cols, W, &m);
+  if (st != QMV_OK) return st;
+  if (cols > INT32_MAX || rows > INT64_MAX / 4 / cols || rows * (cols / 16) > (int64_t)INT32_MAX * 256) return QMV_E_SHAPE;
+  if (ids == nullptr || out == nullptr) return QMV_E_ARG;
+  if (!aligned(ids, 8) || !aligned(out, 16)) return QMV_E_ALIGN;
+  return launch_embed(m, ids, rows, scale, out_dtype == QMV_X_BF16, out, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
+}
+
+int qmv_qk_rope(int x_dtype, int64_t rows, int heads, int kv_heads, int head_dim, const void* q, int64_t q_stride, const void* k,
+                int64_t k_stride, const float* q_weight, const float* k_weight, float eps, const int32_t* pos, const float* freq,
+                int rot_dim, int pairs, float factor, int out_dtype, void* q_out, int64_t q_out_stride, void* k_out,
+                int64_t k_out_stride, cudaStream_t stream) {
+  if (x_dtype != QMV_X_F32 && x_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (pairs != QMV_ROPE_NEIGHBOURS && pairs != QMV_ROPE_HALVES) return QMV_E_FORMAT;
+  if (rows < 0 || !(eps >= 0.f) || std::isinf(eps) || !std::isfinite(factor)) return QMV_E_ARG;
+  if (heads < 1 || heads > 65535 || kv_heads < 0 || kv_heads > 65535) return QMV_E_SHAPE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QMV_E_SHAPE;
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || rows > INT32_MAX) return QMV_E_SHAPE;
+  if (rows == 0) return QMV_OK;
+  if (q == nullptr || q_out == nullptr || (kv_heads > 0 && (k == nullptr || k_out == nullptr)) ||
+      (rot_dim > 0 && (pos == nullptr || freq == nullptr)))
+    return QMV_E_ARG;
+  int st = row_stride_status(q, q_stride, heads, head_dim, x_dtype, rows);
+  if (st == QMV_OK) st = row_stride_status(q_out, q_out_stride, heads, head_dim, out_dtype, rows);
+  if (st == QMV_OK && kv_heads > 0) st = row_stride_status(k, k_stride, kv_heads, head_dim, x_dtype, rows);
+  if (st == QMV_OK && kv_heads > 0) st = row_stride_status(k_out, k_out_stride, kv_heads, head_dim, out_dtype, rows);
+  if (st != QMV_OK) return st;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || (rot_dim > 0 && (!aligned(pos, 4) || !aligned(freq, 4))))
+    return QMV_E_ALIGN;
+  RopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.pos = pos;
+  a.freq = freq;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.rot = rot_dim;
+  a.eps = eps;
+  a.factor = factor;
+  return launch_rope(a, head_dim, x_dtype == QMV_X_BF16, out_dtype == QMV_X_BF16, pairs == QMV_ROPE_HALVES, rows, stream) ==
+                 cudaSuccess
+             ? QMV_OK
+             : QMV_E_CUDA;
+}
+
+size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dtype) {
+  if (tokens < 0 || top < 1 || top > QMV_MOE_MAX_TOP || hidden <= 0 || hidden % 64 != 0 || hidden >= kMoeMaxDim) return 0;
+  if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16) return 0;
+  return moe_scratch_bytes(tokens, top, (int)hidden, out_dtype == QMV_X_BF16);
+}
+
+int qmv_moe(const qmv_moe_layer* layer, int64_t tokens, const float* logits, int64_t logits_stride, int top, int renorm, float scale,
+            int act, int x_dtype, const void* x, int out_dtype, void* out, int32_t* ids, float* shares, void* scratch,
+            cudaStream_t stream) {
+  if (layer == nullptr) return QMV_E_ARG;
+  if (x_dtype != QMV_X_F32 && x_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16) return QMV_E_FORMAT;
+  if (act != QMV_ACT_SILU && act != QMV_ACT_GELU_TANH) return QMV_E_FORMAT;
+  if (tokens < 0 || !std::isfinite(scale)) return QMV_E_ARG;
+  const int64_t e = layer->experts, d = layer->dim, h = layer->hidden;
+  if (e < 1 || e > QMV_MOE_MAX_EXPERTS || d <= 0 || h <= 0 || d % 64 != 0 || h % 64 != 0 || d >= kMoeMaxDim || h >= kMoeMaxDim)
+    return QMV_E_SHAPE;
+  if (top < 1 || top > QMV_MOE_MAX_TOP || top > e || logits_stride < e) return QMV_E_SHAPE;
+  MoeArgs a;
+  int st = make_ref(layer->wtype13, layer->scale_dtype, e * h, d, layer->W1, &a.w1);
+  if (st == QMV_OK) st = make_ref(layer->wtype13, layer->scale_dtype, e * h, d, layer->W3, &a.w3);
+  if (st == QMV_OK) st = make_ref(layer->wtype2, layer->scale_dtype, e * d, h, layer->W2, &a.w2);
+  if (st != QMV_OK) return st;
+  if (tokens > INT64_MAX / 4 / d || (tokens > 0 && logits_stride > INT64_MAX / 4 / tokens)) return QMV_E_SHAPE;
+  if (tokens == 0) return QMV_OK;
+  if (logits == nullptr || x == nullptr || out == nullptr || scratch == nullptr) return QMV_E_ARG;
+  if (!aligned(logits, 4) || !aligned(x, 16) || !aligned(out, 16) || !aligned(ids, 4) || !aligned(shares, 4) || !aligned(scratch, 16))
+    return QMV_E_ALIGN;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
+  a.logits = logits;
+  a.logits_stride = logits_stride;
+  a.x = x;
+  a.out = out;
+  a.scratch = scratch;
+  a.ids = ids;
+  a.shares = shares;
+  a.tokens = tokens;
+  a.experts = (int)e;
+  a.dim = (int)d;
+  a.hidden = (int)h;
+  a.top = top;
+  a.act = act;
+  a.x_bf16 = x_dtype == QMV_X_BF16;
+  a.out_bf16 = out_dtype == QMV_X_BF16;
+  a.renorm = renorm != 0;
+  a.scale = scale;
+  return launch_moe(a, dev, stream) == cudaSuccess ? QMV_OK : QMV_E_CUDA;
+}
+
 int qmv_check_device(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return QMV_E_CUDA;
   DeviceInfo dev;

@@ -277,4 +277,74 @@ struct LogprobArgs {
 };
 cudaError_t launch_logprobs(const LogprobArgs& a, int64_t rows, const DeviceInfo& dev, cudaStream_t stream);
 
+struct SampleArgs {
+  const float* logits;
+  const float* noise;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int64_t* ids;
+  long long stride;
+  long long noise_stride;
+  long long vocab;
+};
+cudaError_t launch_sample(const SampleArgs& a, int64_t rows, const DeviceInfo& dev, cudaStream_t stream);
+
+// Rows `ids` of a token table, scaled.
+cudaError_t launch_embed(const MatrixRef& m, const int64_t* ids, int64_t rows, float scale, bool out_bf16, void* out,
+                         cudaStream_t stream);
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const float* q_weight;  // null: no norm
+  const float* k_weight;
+  const int32_t* pos;
+  const float* freq;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  int heads, kv_heads;
+  int rot;
+  float eps, factor;
+};
+cudaError_t launch_rope(const RopeArgs& a, int head_dim, bool x_bf16, bool out_bf16, bool halves, int64_t rows, cudaStream_t stream);
+
+struct MoeArgs {
+  MatrixRef w1, w3, w2;
+  const float* logits;
+  const void* x;
+  void* out;
+  void* scratch;
+  int32_t* ids;    // null: not asked for
+  float* shares;
+  long long logits_stride;
+  int64_t tokens;
+  int experts, dim, hidden, top, act;
+  bool x_bf16, out_bf16, renorm;
+  float scale;
+};
+// One launch's part (at most 64 tokens), as its kernels get it.
+struct MoeParams {
+  const uint8_t *q1, *d1, *q3, *d3, *q2, *d2;
+  const float* logits;
+  const void* x;
+  void* out;
+  uint16_t* h;
+  int32_t* ids;
+  float* shares;
+  long long logits_stride;
+  long long h_plane;  // elements between h's bfloat16 parts
+  int parts;
+  int tokens, experts, top, dim, hidden;
+  int renorm, act, out_bf16;
+  float scale;
+  int ks;                // warps that share a tile's columns (moe_up)
+  int off_red, off_ring; // places in shared memory
+};
+constexpr int64_t kMoeMaxDim = 1 << 24;
+size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16);
+cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace qmv

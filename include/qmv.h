@@ -664,6 +664,120 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
                  int n_given, float *given_logprob, float *entropy, int n_top, int32_t *top_ids,
                  float *top_logprob, cudaStream_t stream);
 
+#define QMV_SAMPLE_MAX_VOCAB 2147479552 /* 2^31 - 4096 */
+
+/* The next id of each row of logits (float32, as the products leave them), from given random numbers.
+ *   logits : device, row r at element r * stride (stride >= vocab), 4-byte aligned (16-byte aligned rows are read faster).
+ *   noise  : device, row r at element r * noise_stride: exponential random numbers (mean 1), one for each id.
+ *   temperature, top_k, top_p, min_p : device, one value a row (float32, int32, float32, float32), or NULL for
+ *            1, 0, 1, 0: nothing changed or cut off.  They are read when the call runs on the device.
+ *   ids    : device, rows int64, 8-byte aligned.
+ * With w_j = e^((logit_j - max) / temperature), in descending order of the logits (equal ones by the lower id first;
+ * +0 and -0 are equal), a row keeps
+ *   top_k : the first top_k ids (0 or less, or vocab or more: all);
+ *   top_p : of those the smallest first part whose w sum to top_p of their sum at least (1 or more, or NaN: all; 0 or
+ *           less: one id);
+ *   min_p : of those the ids with w_j >= min_p (0 or less, or NaN: all; above 1 as 1),
+ * and its id is the kept one with the largest (logit_j - max) / temperature - ln noise_j, equal ones by the lower id:
+ * a draw from the kept w, each of them chosen with w_j over their sum.  The noise of ids that are cut off does not
+ * matter (and is not read where the cuts leave few).  An id whose noise is not above 0 (or NaN) is not chosen; where
+ * that leaves none, and with a temperature of 2^-100 or less (0, negative or NaN), top_k 1 or top_p 0, the id is that of
+ * the largest logit.  A logit of -infinity is a masked id.  A row that holds NaN, or in which every logit is
+ * -infinity, gives -1; one that holds +infinity the lowest id of those.
+ * The sums that place the top_p border count a w to 2^-32, exactly and in any order.  Scores are compared in
+ * float32 and the closest ones again in 64 bits, so that scores of 2^-30 apart can be told apart, except where
+ * a thread meets three within 2^-12 of the largest.  Results do not depend on timing or on the other rows of the call.
+ * Allocates nothing and uses no workspace.
+ * Returns QMV_OK, QMV_E_ARG (rows < 0, null logits, noise or ids), QMV_E_SHAPE (vocab not within 1..
+ * QMV_SAMPLE_MAX_VOCAB - 1, strides below vocab, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_sample(int64_t rows, int64_t vocab, const float *logits, int64_t stride, const float *noise,
+               int64_t noise_stride, const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, int64_t *ids, cudaStream_t stream);
+
+/* Rows of a token table (Krafla page, "Body": tok_emb, vocab x cols), read from its quants:
+ *   out[r][c] = level * d * scale  of row ids[r] of W (two float32 products, each rounded to nearest; rounded once
+ *   more to bfloat16 for QMV_X_BF16).
+ *   W   : device, the vocab x cols matrix image (qmv_matvec).  ids: device, rows int64, 8-byte aligned; an id
+ *         outside 0..vocab-1 (the -1 of qmv_sample among them) gives a row of zeros.
+ *   out : device, rows x cols of out_dtype (QMV_X_F32 or QMV_X_BF16), contiguous, 16-byte aligned; fully written.
+ * rows 0 launches nothing.  Returns as qmv_dequant, QMV_E_FORMAT for out_dtype, QMV_E_ARG for rows < 0 or a scale that is
+ * not finite. */
+int qmv_embed(int wtype, int scale_dtype, int64_t vocab, int64_t cols, const void *W, const int64_t *ids, int64_t rows,
+              float scale, int out_dtype, void *out, cudaStream_t stream);
+
+/* pairs of qmv_qk_rope: which two values of a head turn together. */
+#define QMV_ROPE_NEIGHBOURS 0 /* 2i and 2i + 1 */
+#define QMV_ROPE_HALVES 1     /* i and i + rot_dim / 2 */
+
+/* Queries and keys between their products and qmv_kv_write / qmv_attend: norms for each head and the position rotation
+ * (Krafla page, "RoPE"; the frequency tables of its variants are the caller's), in one pass.  For each head of each row:
+ *   s = x * weight / sqrt(mean(x^2) + eps)     (float32; s = x where the weight is NULL)
+ *   for pair i of the first rot_dim values, with t = pos[row] * freq[i]:
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t) * factor;  the values past rot_dim are s.
+ * t is formed in 64 bits, so a far position costs no accuracy.
+ *   q : device, row r of head h at element r * q_stride + h * head_dim, x_dtype QMV_X_F32 or QMV_X_BF16; k likewise with
+ *       kv_heads heads.  kv_heads 0: no keys (k and k_out are not looked at).  q_out, k_out likewise with their
+ *       strides, out_dtype QMV_X_F32 or QMV_X_BF16; each row 16-byte aligned.  An output may be its input (the same
+ *       pointer, stride and type); otherwise outputs must not overlap anything else of the call.
+ *   q_weight, k_weight : device, head_dim float32, 16-byte aligned, or NULL.
+ *   pos  : device, rows int32 (any value).  freq: device, rot_dim / 2 float32, radians a position.  4-byte aligned; not looked
+ *          at with rot_dim 0.
+ *   head_dim 64, 128 or 256; rot_dim a multiple of 16, 0..head_dim.
+ * rows 0 launches nothing.  Returns QMV_OK, QMV_E_FORMAT (dtypes, pairs), QMV_E_ARG (rows < 0, null pointer, eps negative
+ * or not finite, factor not finite), QMV_E_SHAPE (heads not 1..65535, kv_heads not 0..65535, head_dim, rot_dim, strides),
+ * QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_qk_rope(int x_dtype, int64_t rows, int heads, int kv_heads, int head_dim, const void *q, int64_t q_stride,
+                const void *k, int64_t k_stride, const float *q_weight, const float *k_weight, float eps,
+                const int32_t *pos, const float *freq, int rot_dim, int pairs, float factor, int out_dtype, void *q_out,
+                int64_t q_out_stride, void *k_out, int64_t k_out_stride, cudaStream_t stream);
+
+#define QMV_MOE_MAX_EXPERTS 256
+#define QMV_MOE_MAX_TOP 16
+
+/* A layer of experts: matrix images (qmv_matvec) whose rows are the experts' matrices one after the other.
+ *   W1, W3 : (experts * hidden) x dim, gate and up, both of type wtype13 (class w1/w3 of a mixed file).
+ *   W2     : (experts * dim) x hidden, down, of type wtype2.  All with scales of scale_dtype.
+ *   experts 1..QMV_MOE_MAX_EXPERTS; dim and hidden multiples of 64, below 2^24. */
+typedef struct qmv_moe_layer {
+  int wtype13;
+  int wtype2;
+  int scale_dtype;
+  int experts;
+  int64_t dim;
+  int64_t hidden;
+  const void *W1;
+  const void *W3;
+  const void *W2;
+} qmv_moe_layer;
+
+/* Bytes of the scratch memory of a qmv_moe call (0 for arguments that it refuses).  Host only. */
+size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dtype);
+
+/* The layer's feed-forward for a few tokens, from the router's logits (which are one of this library's products).  Token
+ * t uses the `top` experts of its largest logits (equal ones: the lower expert), and
+ *   out[t] = scale * sum_e p_e W2_e (act(W1_e x_t) * (W3_e x_t)),
+ * p_e the softmax of the token's logits over the experts that it uses (renorm != 0) or over all of them (renorm = 0).
+ *   logits : device, float32, token t at element t * logits_stride (at least experts), 4-byte aligned.
+ *   x      : device, tokens x dim, x_dtype QMV_X_F32 or QMV_X_BF16, contiguous, 16-byte aligned.
+ *   act    : QMV_ACT_SILU or QMV_ACT_GELU_TANH.
+ *   out    : device, tokens x dim of out_dtype (QMV_X_F32 or QMV_X_BF16), contiguous, 16-byte aligned, fully written.
+ *   ids, shares : device, tokens x top int32 / float32: the experts and their p in descending order; each may be NULL.
+ *   scratch : device, qmv_moe_scratch_bytes(), 16-byte aligned: h between the call's launches.  Calls that may overlap in
+ *            time need scratch memory of their own, captured graphs too.
+ * An expert of logit -infinity is not used (where that leaves fewer than top, ids of -1 with p 0; a token without
+ * experts gives zeros).  A token whose logits hold NaN or +infinity gives NaN, and ids of -1.
+ * The sums are float32 in an order that follows from the sizes and the routing alone: results do not depend on
+ * timing, the last bits of a token may depend on the other tokens of its block of 64.  Levels are exact; x enters as it is
+ * (float32 in three bfloat16 parts, 24 bits), act(gate) * up in three bfloat16 parts for float32 outputs and in two (16 bits) for
+ * bfloat16 ones.  Activations and act(gate) * up are meant to be below 3.38e38.
+ * Tokens go in blocks of 64, each of two launches that read every used expert's weights: for prompts of many tokens
+ * the weights' bytes are read once a block.
+ * tokens 0 launches nothing.  Returns QMV_OK, QMV_E_FORMAT (types, act), QMV_E_ARG (null pointer, tokens < 0, scale not finite), QMV_E_SHAPE
+ * (the layer's numbers, top not 1..min(experts, QMV_MOE_MAX_TOP), logits_stride, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */
+int qmv_moe(const qmv_moe_layer *layer, int64_t tokens, const float *logits, int64_t logits_stride, int top, int renorm,
+            float scale, int act, int x_dtype, const void *x, int out_dtype, void *out, int32_t *ids, float *shares,
+            void *scratch, cudaStream_t stream);
+
 /* Synchronizes the current device, then returns and clears the status word that the
  * kernels set when a bounded wait runs out (QMV_E_TIMEOUT); QMV_OK when none was set,
  * QMV_E_CUDA when the device reports a CUDA error.  When the word was set it also zeroes the

@@ -7,11 +7,14 @@
 // needed: the parts of a row join by a maximum, whose result does not depend on how the row is cut.
 //
 // The cuts are prefixes of the descending order (larger logits first, equal ones by the lower id), so each is one
-// border.  Keys: a logit mapped to an unsigned order, then the id's complement: 64 bits, no two equal.  A pass over
-// the row adds count and weight of 1024 buckets of (max - x) / T in shared memory (integers, so the order of the atomics
-// does not matter); the bucket that holds the border, with all above it where that is few enough, is collected, sorted
-// and walked.  A bucket that holds more than the list (equal or nearly equal logits) is cut again by its keys' bits.
+// border.  One pass over the row leaves the maxima of its chunks of 128 logits (and the sum of the w, where top-p stands alone).
+// k chunks whose maxima reach a value hold k logits that do, and the w of chunk maxima sum to no more than those of all logits: so
+// the maxima alone give a value that the kept logits reach.  The few chunks that hold such logits are read again (from L2) and
+// those logits collected, sorted by keys (value, id; no two equal) and walked.  Where they are too many (flat rows), a second pass adds
+// count and weight of 1024 buckets of (max - x) / T in shared memory (integers, so the order of the atomics does not matter),
+// and only the bucket that holds the border is collected, after cutting it again by its keys' bits where it holds too many.
 //
+// Scores are float32; those close to the best are formed again in 64 bits, so equal draws are told apart as the definition does.
 // A row is one cluster's: 1, 2, 4 or 8 CTAs, which join in distributed shared memory; no workspace.
 #include <cooperative_groups.h>
 
@@ -30,12 +33,16 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBuckets = 1024;  // two a thread
 constexpr int kList = 2048;     // keys that are collected and sorted
+constexpr int kChunks = 2048;   // of a row at most
+constexpr int kClose = 64;      // candidates of the last comparison that are listed
 constexpr int kMaxRanks = 8;
+constexpr int kBatch = 8;       // loads of 16 bytes that a thread has on their way
 using Key = unsigned long long;
 
-// (as in logprobs.cu) larger logits first, equal ones by the lower id; -0 counts as +0
+// (as in logprobs.cu) larger logits first, equal ones by the lower id; -0 counts as +0, NaN as the largest
 __device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);
+  uint32_t b = __float_as_uint(x + 0.0f);
+  if ((b & 0x7fffffffu) > 0x7f800000u) b = 0x7fffffffu;
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
@@ -43,15 +50,25 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 }
 __device__ __forceinline__ Key key_of(float x, uint32_t id) { return ((Key)ordered(x) << 32) | (0xffffffffu - id); }
 __device__ __forceinline__ uint32_t id_of(Key k) { return 0xffffffffu - (uint32_t)k; }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// One row as its CTA sees it.
+constexpr uint32_t kMasked = 0x007fffffu;   // ordered(-infinity)
+constexpr uint32_t kInfinite = 0xff800000u; // ordered(+infinity); NaN is above
+
+// One row as its CTA sees it: quads of 16 bytes from the row's first 16-byte boundary, q0 .. q1 - 1 the CTA's; 32 << shift
+// quads are a chunk.  `ends`: this CTA also has the up to 6 values before the first and after the last whole quad, as its last chunk.
 struct Row {
   const float* x;
   const float* e;
   int n;
-  int head, quads, q0, q1;  // quads of 16 bytes from the row's first 16-byte boundary; the CTA's are q0 .. q1 - 1
-  bool ends;                // this CTA also has the values before the first and after the last whole four
-  float max, scale;         // scale: log2 e / T
+  int head, quads, q0, q1;
+  int shift, chunks;  // the CTA's chunks, without the ends
+  bool ends;
+  float max, scale;   // scale: log2 e / T
 };
 
 // A logit's distance below the maximum in powers of two, its bucket and its weight.
@@ -59,52 +76,49 @@ __device__ __forceinline__ float below(const Row& r, float x) { return (r.max - 
 __device__ __forceinline__ int bucket_of(float t) {  // (NaN, of 0 * inf, gives 0)
   return min((int)(t * 32.f), kBuckets - 1);
 }
-__device__ __forceinline__ float weight_of(float t) {
+__device__ __forceinline__ float exp2_of(float t) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-t));
-  return t == 0.f ? 1.f : y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+  return y;
 }
+__device__ __forceinline__ float weight_of(float t) { return t > 0.f ? exp2_of(-t) : 1.f; }
 // The weight as an integer in units of 2^-31: sums of them are exact, so no order of adding matters.  An id counts
 // to 2^-32 of the largest.
-__device__ __forceinline__ uint32_t mass_of(float t) { return t > 0.f ? __float2uint_rn(weight_of(t) * 0x1p31f) : 0x80000000u; }
+__device__ __forceinline__ uint32_t mass_of(float t) { return t > 0.f ? __float2uint_rn(exp2_of(-t) * 0x1p31f) : 0x80000000u; }
 
-// f(x, id) for each of the CTA's logits, a thread's ids in rising order; four loads of 16 bytes are on their way at a time.
+// f(x, id, local chunk) for the logits of the CTA's chunks whose maximum reaches `least` (mapped; 0: of all).  Whole warps
+// take part: f may use neither shuffles nor barriers.
 template <typename F>
-__device__ __forceinline__ void for_each(const Row& r, F f) {
-  if (r.ends && (int)threadIdx.x < r.head) f(__ldg(r.x + threadIdx.x), (int)threadIdx.x);
+__device__ __forceinline__ void for_each(const Row& r, const uint32_t* chunk_max, uint32_t least, F f) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
-  for (int q = r.q0 + threadIdx.x; q < r.q1; q += 4 * kThreads) {
+  const int subs = (r.q1 - r.q0 + 31) / 32;
+  for (int s = wid; s < subs; s += 4 * kWarps) {
     float4 v[4];
+    bool in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int sub = s + i * kWarps, q = r.q0 + 32 * sub + lane;
+      in[i] = q < r.q1 && (least == 0 || chunk_max[sub >> r.shift] >= least);
+      if (in[i]) v[i] = __ldg(xv + q);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (q + i * kThreads < r.q1) v[i] = __ldg(xv + q + i * kThreads);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (q + i * kThreads < r.q1) {
-        const int id = r.head + 4 * (q + i * kThreads);
-        f(v[i].x, id);
-        f(v[i].y, id + 1);
-        f(v[i].z, id + 2);
-        f(v[i].w, id + 3);
+      if (in[i]) {
+        const int sub = s + i * kWarps, id = r.head + 4 * (r.q0 + 32 * sub + lane);
+        f(v[i].x, id, sub >> r.shift);
+        f(v[i].y, id + 1, sub >> r.shift);
+        f(v[i].z, id + 2, sub >> r.shift);
+        f(v[i].w, id + 3, sub >> r.shift);
       }
   }
-  const int id = r.head + 4 * r.quads + (int)threadIdx.x;
-  if (r.ends && id < r.n) f(__ldg(r.x + id), id);
+  const int tail = r.n - r.head - 4 * r.quads;
+  if (r.ends && (int)threadIdx.x < r.head + tail) {
+    const int id = (int)threadIdx.x < r.head ? (int)threadIdx.x : (int)threadIdx.x - r.head + r.n - tail;
+    f(__ldg(r.x + id), id, r.chunks);
+  }
 }
 
-// The two best scores that a thread has seen: float32, so a draw that is close is decided again in 64 bits.
-struct Best {
-  float s0 = -INFINITY, s1 = -INFINITY;
-  int i0 = -1, i1 = -1;
-  __device__ __forceinline__ void take(float s, int id) {
-    if (s > s0) {
-      s1 = s0, i1 = i0;
-      s0 = s, i0 = id;
-    } else if (s > s1) {
-      s1 = s, i1 = id;
-    }
-  }
-};
 struct Draw {  // a candidate's score in 64 bits; the larger wins, then the lower id
   double s;
   int id;
@@ -114,35 +128,44 @@ __device__ __forceinline__ Draw better(Draw a, Draw b) {
   if (a.id < 0 || b.s > a.s || (b.s == a.s && b.id < a.id)) return b;
   return a;
 }
-
-__device__ __forceinline__ float ln_of(float e) {
+__device__ __forceinline__ float log2_of(float e) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(e));
-  return y * 0.6931471805599453f;
+  return y;
+}
+__device__ __forceinline__ float log2_of_normal(float e) {  // (-infinity for subnormal numbers)
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(e));
+  return y;
 }
 
 struct Shared {
   uint32_t count[kBuckets], low[kBuckets], high[kBuckets];
   Key list[kList];
-  uint32_t listed;
+  uint32_t chunk[kChunks + 1];  // the maxima of the CTA's chunks, mapped
+  uint32_t listed, close;
+  int close_id[kClose];
   // each rank's part of what is joined
-  float rank_max;
-  Key rank_key;
-  int rank_bad;
+  uint32_t rank_max;
+  Key rank_sum;
   float rank_best;
   Draw rank_draw;
+  int rank_id;
   // what rank 0 or every rank found
+  float reach;  // what the chunks' maxima tell: every kept logit reaches it (NaN: they do not tell)
   int bucket;
   uint32_t above_count, in_count;
-  Key above_mass, total_mass;
+  Key above_mass;
   Key border;
   Key border_mass;
-  Key part_key[kWarps];
+  int kept;
   Key scan_mass[kWarps];
   uint32_t scan_count[kWarps];
   float part[kWarps];
   Draw part_draw[kWarps];
+  __device__ __forceinline__ float* best() { return reinterpret_cast<float*>(count); }  // a chunk's best score, once the buckets have done
 };
+static_assert(sizeof(float) * (kChunks + 1) <= 3 * sizeof(uint32_t) * kBuckets, "the buckets' room holds the chunks' best scores");
 
 __device__ __forceinline__ float block_max(Shared& sh, float v) {
 #pragma unroll
@@ -189,40 +212,37 @@ __device__ __forceinline__ void add(Shared& sh, int b, uint32_t mass) {
 
 __device__ __forceinline__ void clear(Shared& sh) {
   for (int i = threadIdx.x; i < kBuckets; i += kThreads) sh.count[i] = sh.low[i] = sh.high[i] = 0u;
-  if (threadIdx.x == 0) sh.listed = 0u;
 }
 
 // A thread's two buckets over all ranks.
 __device__ __forceinline__ void gather(cg::cluster_group& cl, Shared& sh, int ranks, uint32_t (&c)[2], Key (&m)[2]) {
   c[0] = c[1] = 0;
   m[0] = m[1] = 0;
+#pragma unroll 2
   for (int r = 0; r < ranks; ++r) {
     const Shared* o = ranks == 1 ? &sh : cl.map_shared_rank(&sh, r);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int b = 2 * threadIdx.x + k;
-      c[k] += o->count[b];
-      m[k] += ((Key)o->high[b] << 32) + o->low[b];
-    }
+    const uint2 n = reinterpret_cast<const uint2*>(o->count)[threadIdx.x], l = reinterpret_cast<const uint2*>(o->low)[threadIdx.x],
+                h = reinterpret_cast<const uint2*>(o->high)[threadIdx.x];
+    c[0] += n.x, c[1] += n.y;
+    m[0] += ((Key)h.x << 32) + l.x, m[1] += ((Key)h.y << 32) + l.y;
   }
 }
 
 // Which bucket (or bin) holds the border: the first at which the count reaches `want_count`, or (want_count 0) the last whose
-// exclusive mass is below `want_mass`.  Leaves it, what lies above it and what it holds in sh; every rank finds the same.
-__device__ void find_border(cg::cluster_group& cl, Shared& sh, int ranks, uint32_t base_count, Key base_mass, uint32_t want_count,
+// exclusive mass is below `want_mass`.  c, m: a thread's two buckets.  Leaves it, what lies above it and what it holds in sh.  False
+// where all buckets together do not reach the border.
+__device__ bool find_border(Shared& sh, const uint32_t (&c)[2], const Key (&m)[2], uint32_t base_count, Key base_mass, uint32_t want_count,
                             double want_mass) {
-  uint32_t c[2], all_c;
-  Key m[2], all_m;
-  gather(cl, sh, ranks, c, m);
-  uint32_t pc = c[0] + c[1];
-  Key pm = m[0] + m[1];
+  uint32_t all_c, pc = c[0] + c[1];
+  Key all_m, pm = m[0] + m[1];
   block_scan(sh, pc, pm, all_c, all_m);
   pc += base_count;
   pm += base_mass;
+  const bool found = want_count != 0 ? base_count + all_c >= want_count : (double)(base_mass + all_m) >= want_mass;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const bool here = want_count != 0 ? pc < want_count && pc + c[k] >= want_count
-                                      : c[k] != 0 && (double)pm < want_mass && (double)(pm + m[k]) >= want_mass;
+                                      : m[k] != 0 && (double)pm < want_mass && (double)(pm + m[k]) >= want_mass;
     if (here) {
       sh.bucket = 2 * threadIdx.x + k;
       sh.above_count = pc;
@@ -232,8 +252,8 @@ __device__ void find_border(cg::cluster_group& cl, Shared& sh, int ranks, uint32
     pc += c[k];
     pm += m[k];
   }
-  if (threadIdx.x == 0) sh.total_mass = all_m;
   __syncthreads();
+  return found;
 }
 
 // The smallest mapped logit whose bucket is at most b (buckets fall as logits rise).
@@ -296,14 +316,47 @@ __device__ int prefix_by_mass(const Row& r, Shared& sh, int n, Key above_mass, d
 }
 
 struct Border {
-  Key key;        // kept: keys of at least this
-  Key mass;       // the kept keys' weight
-  int listed;     // > 0: the first `listed` of rank 0's sorted list are all that is kept
+  Key key;     // kept: keys of at least this
+  Key mass;    // the kept keys' weight
+  int listed;  // > 0: the first `listed` of rank 0's sorted list are all that is kept
 };
 
-// The border in the bucket that find_border left in sh, among keys of at least `floor`.  want_count: that many stay; else those of exclusive mass below
-// want_mass.  more_p > 0, where the list holds everything kept: the top-p cut is made in it, too.
-__device__ Border resolve(cg::cluster_group& cl, const Row& r, Shared& sh, int rank, int ranks, Key floor, uint32_t want_count, double want_mass, float more_p) {
+// Keys of lo .. hi go to rank 0's list, in no order.  Returns how many there are (the list holds the first kList).
+__device__ uint32_t collect(cg::cluster_group& cl, const Row& r, Shared& sh, Shared* home, Key lo, Key hi) {
+  const uint32_t least = (uint32_t)(lo >> 32);
+  for_each(r, sh.chunk, least, [&](float x, int id, int) {
+    if (ordered(x) < least) return;
+    const Key k = key_of(x, (uint32_t)id);
+    if (k >= lo && k <= hi) {
+      const uint32_t at = atomicAdd(&home->listed, 1u);
+      if (at < (uint32_t)kList) home->list[at] = k;
+    }
+  });
+  cl.sync();
+  return home->listed;
+}
+
+// Rank 0's list, sorted and cut: the first `count` of it (all of it for 0), of those the part whose exclusive mass, over
+// above_mass, is below want_mass, of those the part whose exclusive mass is below top_p of what is left.  weigh: the kept keys'
+// mass is wanted.
+__device__ void cut_list(const Row& r, Shared& sh, uint32_t listed, uint32_t count, Key above_mass, double want_mass, float top_p, bool weigh) {
+  const int n = (int)listed;
+  sort_list(sh, n);
+  Key mass = 0;
+  int stay = count != 0 ? min(n, (int)count) : n;
+  if (weigh || top_p < 1.f || want_mass < INFINITY) stay = prefix_by_mass(r, sh, stay, above_mass, want_mass, mass);
+  if (top_p < 1.f) stay = prefix_by_mass(r, sh, stay, 0, (double)top_p * (double)mass, mass);
+  if (threadIdx.x == 0) {
+    sh.kept = stay;
+    sh.border = stay > 0 ? sh.list[stay - 1] : ~(Key)0;
+    sh.border_mass = mass;
+  }
+}
+
+// The border in the bucket that find_border left in sh, among keys of at least `floor`.  want_count: that many stay; else those of exclusive
+// mass below want_mass.  more_p < 1, where the list holds everything kept: the top-p cut is made in it, too.
+__device__ Border resolve(cg::cluster_group& cl, const Row& r, Shared& sh, Shared* home, int rank, int ranks, Key floor, uint32_t want_count,
+                          double want_mass, float more_p) {
   uint32_t above = sh.above_count, inside = sh.in_count;
   Key above_mass = sh.above_mass;
   Key lo, hi;
@@ -324,12 +377,15 @@ __device__ Border resolve(cg::cluster_group& cl, const Row& r, Shared& sh, int r
     cl.sync();  // every rank has read the histograms
     clear(sh);
     __syncthreads();
-    for_each(r, [&](float x, int id) {
+    for_each(r, sh.chunk, (uint32_t)(lo >> 32), [&](float x, int id, int) {
       const Key k = key_of(x, (uint32_t)id);
       if (k >= lo && k <= hi) add(sh, (int)((hi - k) >> shift), mass_of(below(r, x)));
     });
     cl.sync();
-    find_border(cl, sh, ranks, above, above_mass, want_count, want_mass);
+    uint32_t c[2];
+    Key m[2];
+    gather(cl, sh, ranks, c, m);
+    find_border(sh, c, m, above, above_mass, want_count, want_mass);
     above = sh.above_count;
     above_mass = sh.above_mass;
     inside = sh.in_count;
@@ -337,38 +393,18 @@ __device__ Border resolve(cg::cluster_group& cl, const Row& r, Shared& sh, int r
     const Key low = hi - (((Key)1 << shift) - 1);
     lo = low > lo && low <= hi ? low : lo;
   }
-  // collected at rank 0, in no order
   cl.sync();
   if (threadIdx.x == 0) sh.listed = 0u;
   cl.sync();
-  Shared* home = ranks == 1 ? &sh : cl.map_shared_rank(&sh, 0);
-  for_each(r, [&](float x, int id) {
-    if (ordered(x) < (uint32_t)(lo >> 32)) return;
-    const Key k = key_of(x, (uint32_t)id);
-    if (k >= lo && k <= hi) {
-      const uint32_t at = atomicAdd(&home->listed, 1u);
-      if (at < (uint32_t)kList) home->list[at] = k;
-    }
-  });
-  cl.sync();
-  if (rank == 0) {
-    const int n = min((int)sh.listed, kList);
-    sort_list(sh, n);
-    Key mass;
-    int stay = want_count != 0 ? min(n, (int)(want_count - above)) : n;
-    stay = prefix_by_mass(r, sh, stay, above_mass, want_count != 0 ? INFINITY : want_mass, mass);
-    if (whole && more_p < 1.f) stay = prefix_by_mass(r, sh, stay, 0, (double)more_p * (double)mass, mass);
-    if (threadIdx.x == 0) {
-      sh.border = sh.list[max(stay, 1) - 1];
-      sh.border_mass = mass;
-      sh.bucket = max(stay, 1);
-    }
-  }
+  const uint32_t listed = collect(cl, r, sh, home, lo, hi);
+  if (rank == 0)
+    cut_list(r, sh, min(listed, (uint32_t)kList), want_count != 0 ? want_count - above : 0, above_mass, want_count != 0 ? INFINITY : want_mass,
+             whole ? more_p : 1.f, true);
   cl.sync();
   Border b;
   b.key = home->border;
   b.mass = home->border_mass;
-  b.listed = whole ? home->bucket : 0;
+  b.listed = whole ? home->kept : 0;
   return b;
 }
 
@@ -384,12 +420,273 @@ struct SampleParams {
   int64_t* ids;
 };
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p, int ranks) {
+// The pass over the row: the maxima of its chunks, and with SUM each thread's largest logit and sum of 2^((x - it) scale).
+template <bool SUM>
+__device__ __forceinline__ uint32_t first_pass(const Row& r, Shared& sh, float& own_max, float& own_sum) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
+  const int subs = (r.q1 - r.q0 + 31) / 32;
+  uint32_t most = 0;
+  float m = -INFINITY, sum[kBatch] = {};
+  auto take = [&](const float (&v)[4 * kBatch], float top) {
+    if (!(top > -INFINITY)) return;  // (NaN: the row is refused)
+    if (top > m) {
+      const float f = m > -INFINITY ? exp2_of((m - top) * r.scale) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) sum[i] *= f;
+      m = top;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * kBatch; ++i) sum[i % kBatch] += v[i] < m ? exp2_of((v[i] - m) * r.scale) : 1.f;
+  };
+  for (int s = wid; s < subs; s += kBatch * kWarps) {
+    float v[4 * kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int q = r.q0 + 32 * (s + i * kWarps) + lane;
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (q < r.q1) f = __ldg(xv + q);
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float t = max_nan(max_nan(v[4 * i], v[4 * i + 1]), max_nan(v[4 * i + 2], v[4 * i + 3]));
+      if (SUM) top = fmaxf(top, t);
+      const uint32_t o = __reduce_max_sync(0xffffffffu, ordered(t));
+      most = max(most, o);
+      if (lane == 0 && s + i * kWarps < subs) {
+        uint32_t* at = &sh.chunk[(s + i * kWarps) >> r.shift];
+        if (r.shift == 0)
+          *at = o;
+        else
+          atomicMax(at, o);
+      }
+    }
+    if (SUM) take(v, top);
+  }
+  if (r.ends) {
+    const int tail = r.n - r.head - 4 * r.quads;
+    float v[4 * kBatch];
+#pragma unroll
+    for (int i = 0; i < 4 * kBatch; ++i) v[i] = -INFINITY;
+    if (wid == 0) {
+      if (lane < r.head + tail) v[0] = __ldg(r.x + (lane < r.head ? lane : lane - r.head + r.n - tail));
+      const uint32_t o = __reduce_max_sync(0xffffffffu, ordered(v[0]));
+      most = max(most, o);
+      if (lane == 0) sh.chunk[r.chunks] = o;
+      if (SUM) take(v, v[0]);
+    }
+  }
+  if (SUM) {
+    own_max = m;
+    own_sum = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+    static_assert(kBatch == 8, "eight chains");
+  }
+  return most;
+}
+
+// Count or weight of the row's logits in the buckets.
+template <bool MASS>
+__device__ __forceinline__ void bucket_pass(const Row& r, Shared& sh) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
+  const int subs = (r.q1 - r.q0 + 31) / 32;
+  uint32_t far = 0;  // the last bucket takes most of a sharp row: in a register (a weight of at most 1 each)
+  auto put = [&](const float (&v)[8]) {
+    int b[8];
+    uint32_t m[8], old[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = below(r, v[i]);
+      b[i] = v[i] > -INFINITY ? bucket_of(t) : kBuckets;
+      m[i] = MASS ? mass_of(t) : 1u;
+      if (b[i] == kBuckets - 1) far += m[i];
+    }
+    // the additions first, what they carry after: none waits for another
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      old[i] = 0;
+      if (b[i] < kBuckets - 1) old[i] = atomicAdd(MASS ? &sh.low[b[i]] : &sh.count[b[i]], m[i]);
+    }
+    if (MASS) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (b[i] < kBuckets - 1 && old[i] + m[i] < old[i]) atomicAdd(&sh.high[b[i]], 1u);
+    }
+  };
+  for (int s = wid; s < subs; s += 4 * kWarps) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = r.q0 + 32 * (s + i * kWarps) + lane;
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (q < r.q1) f = __ldg(xv + q);
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float(&half)[8] = *reinterpret_cast<const float(*)[8]>(v + 8 * h);
+      put(half);
+    }
+  }
+  if (r.ends && wid == 0) {
+    const int tail = r.n - r.head - 4 * r.quads;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = -INFINITY;
+    if (lane < r.head + tail) v[0] = __ldg(r.x + (lane < r.head ? lane : lane - r.head + r.n - tail));
+    put(v);
+  }
+  far = __reduce_add_sync(0xffffffffu, far);
+  if (lane == 0 && far != 0) {
+    const uint32_t old = atomicAdd(MASS ? &sh.low[kBuckets - 1] : &sh.count[kBuckets - 1], far);
+    if (MASS && old + far < old) atomicAdd(&sh.high[kBuckets - 1], 1u);
+  }
+}
+
+__device__ __forceinline__ int mapped(float v) {  // an integer that orders as the float does
+  return v >= 0.f ? __float_as_int(v) : __float_as_int(v) ^ 0x7fffffff;
+}
+
+// The draw over the chunks whose maximum reaches `least`: kind(x, id) is 1 for a logit that takes part, 2 for one that goes to rank 0's
+// list, else 0.  Leaves each chunk's best score; returns the thread's.
+template <typename K, typename S>
+__device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* home, uint32_t least, K kind, S score) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
+  const bool wide = ((reinterpret_cast<uintptr_t>(r.e + r.head)) & 15) == 0;
+  const int subs = (r.q1 - r.q0 + 31) / 32;
+  int* best = reinterpret_cast<int*>(sh.best());
+  float most = -INFINITY;
+  constexpr int B = 2;
+  for (int s = wid; s < subs; s += B * kWarps) {
+    float v[4 * B], e[4 * B];
+    int part[B];  // two bits a logit
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int sub = s + i * kWarps, q = r.q0 + 32 * sub + lane;
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (q < r.q1 && sh.chunk[sub >> r.shift] >= least) f = __ldg(xv + q);
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int id = r.head + 4 * (r.q0 + 32 * (s + i * kWarps) + lane);
+      part[i] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (v[4 * i + k] > -INFINITY) part[i] |= kind(v[4 * i + k], id + k) << (2 * k);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if ((part[i] & 0x55) != 0) {
+        if (wide)
+          f = __ldg(reinterpret_cast<const float4*>(r.e + id));
+        else
+          f = make_float4(__ldg(r.e + id), __ldg(r.e + id + 1), __ldg(r.e + id + 2), __ldg(r.e + id + 3));
+      }
+      e[4 * i] = f.x, e[4 * i + 1] = f.y, e[4 * i + 2] = f.z, e[4 * i + 3] = f.w;
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int sub = s + i * kWarps, id = r.head + 4 * (r.q0 + 32 * sub + lane);
+      float t = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int what = part[i] >> (2 * k) & 3;
+        if (what == 1) t = fmaxf(t, score(v[4 * i + k], e[4 * i + k]));
+        if (what == 2) {
+          const uint32_t at = atomicAdd(&home->listed, 1u);
+          if (at < (uint32_t)kList) home->list[at] = key_of(v[4 * i + k], (uint32_t)(id + k));
+        }
+      }
+      t = unordered(__reduce_max_sync(0xffffffffu, ordered(t)));
+      most = fmaxf(most, t);
+      if (lane == 0 && sub < subs) {
+        if (r.shift == 0)
+          best[sub] = mapped(t);
+        else
+          atomicMax(best + (sub >> r.shift), mapped(t));
+      }
+    }
+  }
+  if (r.ends && wid == 0) {
+    const int tail = r.n - r.head - 4 * r.quads;
+    float t = -INFINITY;
+    if (lane < r.head + tail) {
+      const int id = lane < r.head ? lane : lane - r.head + r.n - tail;
+      const float x = __ldg(r.x + id);
+      const int what = x > -INFINITY ? kind(x, id) : 0;
+      if (what == 1) t = score(x, __ldg(r.e + id));
+      if (what == 2) {
+        const uint32_t at = atomicAdd(&home->listed, 1u);
+        if (at < (uint32_t)kList) home->list[at] = key_of(x, (uint32_t)id);
+      }
+    }
+    t = unordered(__reduce_max_sync(0xffffffffu, ordered(t)));
+    most = fmaxf(most, t);
+    if (lane == 0) best[r.chunks] = mapped(t);
+  }
+  return most;
+}
+
+// The pass of a draw from the whole row: each chunk's best score (in powers of two, nothing subtracted), and whether the row holds NaN.
+// A random number that is not above 0, subnormal ones among them, makes a score that is infinite or NaN: the caller looks again.
+__device__ __forceinline__ bool free_pass(const Row& r, Shared& sh, float& most) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
+  const float4* ev = reinterpret_cast<const float4*>(r.e + r.head);
+  const int subs = (r.q1 - r.q0 + 31) / 32;
+  int* best = reinterpret_cast<int*>(sh.best());
+  float nan = 0.f;
+  most = -INFINITY;
+  auto score = [&](float x, float e) {
+    nan = max_nan(nan, x);
+    return fmaf(x, r.scale, -log2_of_normal(e));
+  };
+  for (int s = wid; s < subs; s += 4 * kWarps) {
+    float4 v[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = r.q0 + 32 * (s + i * kWarps) + lane;
+      v[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      u[i] = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (q < r.q1) v[i] = __ldg(xv + q), u[i] = __ldg(ev + q);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float t = fmaxf(fmaxf(score(v[i].x, u[i].x), score(v[i].y, u[i].y)), fmaxf(score(v[i].z, u[i].z), score(v[i].w, u[i].w)));
+      const float o = unordered(__reduce_max_sync(0xffffffffu, ordered(t)));
+      most = max_nan(most, o);
+      if (lane == 0 && s + i * kWarps < subs) {
+        if (r.shift == 0)
+          best[s + i * kWarps] = mapped(o);
+        else
+          atomicMax(best + ((s + i * kWarps) >> r.shift), mapped(o));
+      }
+    }
+  }
+  if (r.ends && wid == 0) {
+    const int tail = r.n - r.head - 4 * r.quads;
+    float t = -INFINITY;
+    if (lane < r.head + tail) {
+      const int id = lane < r.head ? lane : lane - r.head + r.n - tail;
+      t = score(__ldg(r.x + id), __ldg(r.e + id));
+    }
+    const float o = unordered(__reduce_max_sync(0xffffffffu, ordered(t)));
+    most = max_nan(most, o);
+    if (lane == 0) best[r.chunks] = mapped(o);
+  }
+  return nan != nan;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p, int ranks) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int rank = ranks == 1 ? 0 : (int)cl.block_rank();
+  Shared* home = ranks == 1 ? &sh : cl.map_shared_rank(&sh, 0);
   const long long row = blockIdx.x / ranks;
   Row r;
   r.x = p.logits + row * p.stride;
@@ -400,112 +697,266 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   r.q0 = (int)((long long)r.quads * rank / ranks);
   r.q1 = (int)((long long)r.quads * (rank + 1) / ranks);
   r.ends = rank == 0;
+  r.shift = 0;
+  while (((long long)r.quads >> (5 + r.shift)) + kMaxRanks > kChunks) ++r.shift;
+  r.chunks = (((r.q1 - r.q0 + 31) / 32) + (1 << r.shift) - 1) >> r.shift;
 
-  const float T = p.temperature != nullptr ? __ldg(p.temperature + row) : 1.f;
+  const float asked = p.temperature != nullptr ? __ldg(p.temperature + row) : 1.f;
+  const float T = asked > 0x1p100f ? 0x1p100f : asked;
   const int k = p.top_k != nullptr ? __ldg(p.top_k + row) : 0;
   const float top_p = p.top_p != nullptr ? __ldg(p.top_p + row) : 1.f;
   const float min_p = p.min_p != nullptr ? __ldg(p.min_p + row) : 0.f;
   const bool by_k = k > 0 && k < r.n, by_p = top_p < 1.f, by_m = min_p > 0.f;
   const bool greedy = !(T > 0x1p-100f) || k == 1 || top_p <= 0.f;
-  const bool free_draw = !greedy && !by_k && !by_p && !by_m;
-
-  // ---- the row's maximum and its id, and whether it holds NaN
-  Key top = 0;
-  bool bad = false;
-  Best best;
+  const bool whole_row = !greedy && !by_k && !by_p && !by_m;
   const float inv_t = __fdiv_rn(1.f, T);
-  if (free_draw) {
-    // nothing is cut off: the draw needs no maximum (scores are compared, whatever is subtracted from all)
-    const float* e = r.e;
-    const bool wide = ((reinterpret_cast<uintptr_t>(e + r.head)) & 15) == 0;
-    auto take = [&](float x, float ex, int id) {
-      const Key kx = key_of(x, (uint32_t)id);
-      top = kx > top ? kx : top;
-      bad |= x != x;
-      if (ex > 0.f && x > -INFINITY) best.take(x * inv_t - ln_of(ex), id);
+  r.scale = __fmul_rn(1.4426950408889634f, inv_t);
+  r.max = 0.f;
+  // a score is float32: its logarithm is off by 2^-21 of |log2 e| (< 150) at most, the difference, product and sum by a few 2^-24
+  // of their own size; candidates as close to the best as that are looked at again
+  auto margin_of = [&](float most, float size) { return 4e-4f + 0x1p-20f * (fabsf(most) + size); };
+
+  // each CTA's part of the row is joined by what: a maximum of mapped values
+  auto over_ranks = [&](uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
+    if (lane == 0) sh.scan_count[wid] = v;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) v = max(v, sh.scan_count[w]);
+    if (ranks > 1) {
+      if (threadIdx.x == 0) sh.rank_max = v;
+      cl.sync();
+      for (int i = 0; i < ranks; ++i) v = max(v, cl.map_shared_rank(&sh, i)->rank_max);
+    }
+    return v;
+  };
+  // the comparison in 64 bits of the logits that visit(least, f) hands to f: those whose score reaches most - margin; writes the
+  // row's id.  all_ranks: every rank calls it (else rank 0 alone)
+  auto decide = [&](float most, float margin, auto visit, auto score, bool all_ranks) {
+    auto meet = [&]() {
+      if (all_ranks)
+        cl.sync();
+      else
+        __syncthreads();
     };
-    if (wide) {
-      if (r.ends && (int)threadIdx.x < r.head) take(__ldg(r.x + threadIdx.x), __ldg(e + threadIdx.x), (int)threadIdx.x);
-      const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
-      const float4* ev = reinterpret_cast<const float4*>(e + r.head);
-      for (int q = r.q0 + threadIdx.x; q < r.q1; q += 4 * kThreads) {
-        float4 v[4], u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (q + i * kThreads < r.q1) v[i] = __ldg(xv + q + i * kThreads), u[i] = __ldg(ev + q + i * kThreads);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (q + i * kThreads < r.q1) {
-            const int id = r.head + 4 * (q + i * kThreads);
-            take(v[i].x, u[i].x, id);
-            take(v[i].y, u[i].y, id + 1);
-            take(v[i].z, u[i].z, id + 2);
-            take(v[i].w, u[i].w, id + 3);
-          }
+    if (rank == 0 && threadIdx.x == 0) sh.close = 0u;
+    meet();
+    const float least = most - margin;
+    visit(least, [&](float x, float e, int id) {
+      if (score(x, e) >= least) {
+        const uint32_t at = atomicAdd(&home->close, 1u);
+        if (at < (uint32_t)kClose) home->close_id[at] = id;
       }
-      const int id = r.head + 4 * r.quads + (int)threadIdx.x;
-      if (r.ends && id < r.n) take(__ldg(r.x + id), __ldg(e + id), id);
-    } else {
-      for_each(r, [&](float x, int id) { take(x, __ldg(e + id), id); });
-    }
-  } else {
-    for_each(r, [&](float x, int id) {
-      const Key kx = key_of(x, (uint32_t)id);
-      top = kx > top ? kx : top;
-      bad |= x != x;
     });
-  }
+    meet();
+    const uint32_t n = home->close;
+    if (n == 1) {
+      if (rank == 0 && threadIdx.x == 0) p.ids[row] = sh.close_id[0];
+      return;
+    }
+    auto exact = [&](float x, float e, int id) { return Draw{((double)x - (double)r.max) / (double)T - log((double)e), id}; };
+    Draw d{0.0, -1};
+    if (n > (uint32_t)kClose) {
+      visit(least, [&](float x, float e, int id) {
+        if (score(x, e) >= least) d = better(d, exact(x, e, id));
+      });
+    } else if (rank == 0 && threadIdx.x < n) {
+      const int id = sh.close_id[threadIdx.x];
+      d = exact(__ldg(r.x + id), __ldg(r.e + id), id);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Key u = __shfl_xor_sync(0xffffffffu, top, o);
-    top = u > top ? u : top;
+    for (int o = 16; o > 0; o >>= 1) {
+      Draw u;
+      u.s = __shfl_xor_sync(0xffffffffu, d.s, o);
+      u.id = __shfl_xor_sync(0xffffffffu, d.id, o);
+      d = better(d, u);
+    }
+    if (lane == 0) sh.part_draw[wid] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kWarps; ++w) d = better(d, sh.part_draw[w]);
+      sh.rank_draw = d;
+    }
+    meet();
+    if (rank == 0 && threadIdx.x == 0) {
+      if (all_ranks)
+        for (int i = 1; i < ranks; ++i) d = better(d, cl.map_shared_rank(&sh, i)->rank_draw);
+      p.ids[row] = d.id;
+    }
+  };
+  // f(x, e, id) for the logits of chunks whose best score reaches `least`
+  auto chunks_reaching = [&](float least, auto f) {
+    const int* best = reinterpret_cast<const int*>(sh.best());
+    const int reach = mapped(least);
+    for (int c = wid; c < r.chunks + r.ends; c += kWarps) {
+      if (best[c] < reach) continue;
+      if (c == r.chunks) {
+        const int tail = r.n - r.head - 4 * r.quads;
+        if (lane < r.head + tail) {
+          const int id = lane < r.head ? lane : lane - r.head + r.n - tail;
+          f(__ldg(r.x + id), __ldg(r.e + id), id);
+        }
+        continue;
+      }
+      for (int j = 0; j < 1 << r.shift; ++j) {
+        const int q = r.q0 + 32 * ((c << r.shift) + j) + lane;
+        if (q >= r.q1) break;
+        const int id = r.head + 4 * q;
+        for (int i = 0; i < 4; ++i) f(__ldg(r.x + id + i), __ldg(r.e + id + i), id + i);
+      }
+    }
+  };
+  // the lowest id of the largest logit, `top` mapped; every rank calls it
+  auto largest = [&](uint32_t top) {
+    int id = INT32_MAX;
+    __syncthreads();
+    if (top <= kInfinite && top > kMasked)
+      for_each(r, sh.chunk, top, [&](float x, int i, int) {
+        if (ordered(x) == top) id = min(id, i);
+      });
+    id = __reduce_min_sync(0xffffffffu, id);
+    if (lane == 0) sh.scan_count[wid] = (uint32_t)id;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) id = min(id, (int)sh.scan_count[w]);
+    if (ranks > 1) {
+      if (threadIdx.x == 0) sh.rank_id = id;
+      cl.sync();
+      for (int i = 0; i < ranks; ++i) id = min(id, cl.map_shared_rank(&sh, i)->rank_id);
+    }
+    if (rank == 0 && threadIdx.x == 0) p.ids[row] = id == INT32_MAX ? -1 : id;
+  };
+
+  if (r.shift > 0) {
+    for (int i = threadIdx.x; i <= r.chunks; i += kThreads) sh.chunk[i] = 0u, reinterpret_cast<int*>(sh.best())[i] = INT32_MIN;
+    __syncthreads();
   }
-  if ((threadIdx.x & 31) == 0) sh.part_key[threadIdx.x >> 5] = top;
-  bad = __syncthreads_or(bad);
-  for (int w = 0; w < kWarps; ++w) top = sh.part_key[w] > top ? sh.part_key[w] : top;
-  if (ranks > 1) {
-    if (threadIdx.x == 0) sh.rank_key = top, sh.rank_bad = bad;
-    cl.sync();
-    for (int i = 0; i < ranks; ++i) {
-      const Shared* o = cl.map_shared_rank(&sh, i);
-      top = o->rank_key > top ? o->rank_key : top;
-      bad |= o->rank_bad != 0;
+  // ---- a draw from the whole row: one pass over logits and random numbers, then the chunks with the best scores
+  if (whole_row) {
+    const bool wide = ((reinterpret_cast<uintptr_t>(r.e + r.head)) & 15) == 0;
+    if (wide) {
+      float most;
+      const bool nan = free_pass(r, sh, most);
+      // NaN, infinite scores and those so large that float32 leaves them coarse are left to the passes by the maximum
+      const float m = unordered(over_ranks(nan || !(most < INFINITY) ? 0xffffffffu : ordered(most)));
+      if (fabsf(m) < 2048.f) {
+        auto score = [&](float x, float e) { return fmaf(x, r.scale, -log2_of_normal(e)); };
+        // |x scale| is at most that of the score and |log2 e| together
+        decide(m, margin_of(m, 150.f), chunks_reaching, score, true);
+        if (ranks > 1) cl.sync();
+        return;
+      }
+      if (ranks > 1) cl.sync();  // rank_max is written again
+      if (r.shift > 0) {
+        for (int i = threadIdx.x; i <= r.chunks; i += kThreads) reinterpret_cast<int*>(sh.best())[i] = INT32_MIN;
+        __syncthreads();
+      }
     }
   }
-  r.max = unordered((uint32_t)(top >> 32));
-  if (bad || r.max == -INFINITY || greedy || r.max == INFINITY) {
-    if (rank == 0 && threadIdx.x == 0) p.ids[row] = bad || r.max == -INFINITY ? -1 : (int64_t)id_of(top);
+
+  // (rank 0's, for the chunks' maxima: cleared before the ranks meet over the row's maximum)
+  clear(sh);
+  if (threadIdx.x == 0) sh.listed = 0u;
+  // ---- the row's maximum, its chunks' maxima, and the sum of the weights where top-p stands alone
+  const bool sum_first = !greedy && by_p && !by_k;
+  float own_max = -INFINITY, own_sum = 0.f;
+  const uint32_t own_top = sum_first ? first_pass<true>(r, sh, own_max, own_sum) : first_pass<false>(r, sh, own_max, own_sum);
+  const uint32_t top = over_ranks(own_top);
+  r.max = unordered(top);
+  if (top >= kInfinite || top <= kMasked || greedy) {
+    largest(top);
     if (ranks > 1) cl.sync();  // no rank leaves while another reads its shared memory
     return;
   }
-  r.scale = __fmul_rn(1.4426950408889634f, inv_t);
+
+  // scores in powers of two below the maximum's
+  auto kept_by_m = [&](float x) { return !by_m || x == r.max || weight_of(below(r, x)) >= min_p; };
+  auto score = [&](float x, float e) { return e > 0.f ? (x - r.max) * r.scale - log2_of(e) : -INFINITY; };
 
   // ---- the borders of top-k and top-p
   Border border{0, 0, 0};
+  int bucket = -1;  // the draw's pass takes the logits above this bucket and collects it
+  double want = 0.0;
+  uint32_t first = 0;
   if (by_k || by_p) {
-    clear(sh);
-    __syncthreads();
-    uint32_t far_count = 0, far_mass = 0;  // the last bucket takes most of a sharp row: in registers
-    for_each(r, [&](float x, int id) {
-      if (!(x > -INFINITY)) return;
-      const float t = below(r, x);
-      const int b = bucket_of(t);
-      if (b == kBuckets - 1) {
-        far_count += 1;
-        far_mass += mass_of(t);  // at most 1 each
-      } else {
-        add(sh, b, mass_of(t));
+    // what the chunks' maxima tell: a value that k logits, or logits of top_p of the weight, reach.  Rank 0's buckets take
+    // all ranks' maxima.
+    if (sum_first) {
+      Key sum = own_max > -INFINITY ? __double2ull_rn((double)(own_sum * (own_max < r.max ? exp2_of((own_max - r.max) * r.scale) : 1.f)) * 0x1p31) : 0;
+      uint32_t none = 0, all_c;
+      Key all;
+      block_scan(sh, none, sum, all_c, all);
+      if (threadIdx.x == 0) sh.rank_sum = all;
+    }
+    for (int c = threadIdx.x; c < r.chunks + r.ends; c += kThreads) {
+      const uint32_t o = sh.chunk[c];
+      if (o > kMasked) {
+        const float t = below(r, unordered(o));
+        add(*home, bucket_of(t), mass_of(t));
       }
-    });
-    far_count = __reduce_add_sync(0xffffffffu, far_count);
-    far_mass = __reduce_add_sync(0xffffffffu, far_mass);
-    if ((threadIdx.x & 31) == 0 && far_count != 0) {
-      atomicAdd(&sh.count[kBuckets - 1], far_count);
-      const uint32_t old = atomicAdd(&sh.low[kBuckets - 1], far_mass);
-      if (old + far_mass < old) atomicAdd(&sh.high[kBuckets - 1], 1u);
     }
     cl.sync();
-    // the total first: a row may hold fewer finite logits than k
+    if (rank == 0) {
+      uint32_t c[2];
+      Key m[2], sum = 0;
+      gather(cl, sh, 1, c, m);
+      if (sum_first) {
+        for (int i = 0; i < ranks; ++i) sum += (ranks == 1 ? &sh : cl.map_shared_rank(&sh, i))->rank_sum;
+        want = (double)top_p * (double)sum;
+      }
+      uint32_t need = 0;
+      if (by_k) {
+        // k chunks hold k logits that reach their maxima; in a flat row fewer chunks do: where a share f of N chunks reaches a value, about
+        // -ln(1 - f) N logits do.  (Too few of them collected: the passes below.)
+        const float chunks = (float)((r.quads >> (5 + r.shift)) + 1);
+        const float few = chunks * (1.f - expf(-(1.25f * (float)k + 32.f) / chunks));
+        need = (uint32_t)max(1, min(k, (int)few));
+      }
+      const bool found = find_border(sh, c, m, 0, 0, need, want);
+      // the bucket's lower end, and a little below: a logit more in the list does no harm
+      const float edge = (float)(sh.bucket + 1) / (32.f * r.scale);
+      if (threadIdx.x == 0)
+        sh.reach = found && sh.bucket < kBuckets - 1 ? r.max - edge * (1.f + 0x1p-18f) - 0x1p-20f * fabsf(r.max) : NAN;
+    }
+    cl.sync();
+    const float reach = home->reach;
+    bool fast = reach > -INFINITY;  // (not NaN)
+    if (fast) {
+      const uint32_t listed = collect(cl, r, sh, home, (Key)ordered(reach) << 32, ~(Key)0);
+      fast = listed <= (uint32_t)kList && (!by_k || listed >= (uint32_t)k);
+    }
+    if (fast) {
+      if (rank != 0) {  // the rest is rank 0's list
+        cl.sync();
+        return;
+      }
+      cut_list(r, sh, home->listed, by_k ? (uint32_t)k : 0u, 0, by_k ? INFINITY : want, by_k ? top_p : 1.f, false);
+      __syncthreads();
+      const int kept = max(sh.kept, 1);
+      auto listed = [&](float, auto f) {
+        for (int i = threadIdx.x; i < kept; i += kThreads) {
+          const float x = unordered((uint32_t)(sh.list[i] >> 32));
+          const int id = (int)id_of(sh.list[i]);
+          if (kept_by_m(x)) f(x, __ldg(r.e + id), id);
+        }
+      };
+      float most = -INFINITY;
+      listed(0.f, [&](float x, float e, int) { most = fmaxf(most, score(x, e)); });
+      most = block_max(sh, most);
+      if (most > -INFINITY)
+        decide(most, margin_of(most, 150.f), listed, score, false);
+      else if (threadIdx.x == 0)  // no random number to choose by: the largest logit
+        p.ids[row] = (int64_t)id_of(sh.list[0]);
+      if (ranks > 1) cl.sync();  // (the others have read this CTA's shared memory by now)
+      return;
+    }
+    // the buckets of all logits
+    const bool both = by_k && by_p;
+    cl.sync();
+    clear(sh);
+    __syncthreads();
+    if (by_k) bucket_pass<false>(r, sh);
+    if (by_p) bucket_pass<true>(r, sh);
+    cl.sync();
     uint32_t c[2], all_c;
     Key m[2], all_m;
     gather(cl, sh, ranks, c, m);
@@ -513,90 +964,115 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     Key pm = m[0] + m[1];
     block_scan(sh, pc, pm, all_c, all_m);
     __syncthreads();
-    const bool cut_k = by_k && (uint32_t)k < all_c;
-    if (cut_k) {
-      find_border(cl, sh, ranks, 0, 0, (uint32_t)k, 0.0);
-      border = resolve(cl, r, sh, rank, ranks, 0, (uint32_t)k, 0.0, by_p ? top_p : 1.f);
-    }
-    if (by_p && border.listed == 0) {
-      if (cut_k) {
-        // the buckets again (the list and finer bins took their place)
+    const bool cut_k = by_k && (uint32_t)k < all_c;  // (a row may hold fewer finite logits)
+    want = (double)top_p * (double)all_m;
+    if (cut_k && both) {
+      // the k-th logit itself, then the buckets of those above it
+      find_border(sh, c, m, 0, 0, (uint32_t)k, 0.0);
+      border = resolve(cl, r, sh, home, rank, ranks, 0, (uint32_t)k, 0.0, top_p);
+      if (border.listed == 0) {
         cl.sync();
         clear(sh);
         __syncthreads();
-        for_each(r, [&](float x, int id) {
+        for_each(r, sh.chunk, (uint32_t)(border.key >> 32), [&](float x, int id, int) {
           if (key_of(x, (uint32_t)id) >= border.key) add(sh, bucket_of(below(r, x)), mass_of(below(r, x)));
         });
         cl.sync();
+        gather(cl, sh, ranks, c, m);
+        find_border(sh, c, m, 0, 0, 0, (double)top_p * (double)border.mass);
+        const Border bp = resolve(cl, r, sh, home, rank, ranks, border.key, 0, (double)top_p * (double)border.mass, 1.f);
+        border.key = bp.key > border.key ? bp.key : border.key;
       }
-      const double want = (double)top_p * (double)(cut_k ? border.mass : all_m);
-      find_border(cl, sh, ranks, 0, 0, 0, want);
-      const Border bp = resolve(cl, r, sh, rank, ranks, border.key, 0, want, 1.f);
-      border.key = bp.key > border.key ? bp.key : border.key;
-      border.listed = bp.listed;
+    } else if (cut_k || by_p) {
+      first = cut_k ? (uint32_t)k : 0u;
+      find_border(sh, c, m, 0, 0, first, want);
+      bucket = sh.bucket;
     }
   }
 
-  // ---- the draw among what is kept
-  // (a maximum that is large beside T: scores without it would be coarse, or overflow)
-  const bool far = free_draw && !(fabsf(r.max * inv_t) < 1024.f);
-  if (far) best = Best{};
-  auto score = [&](float x, float ex) { return (x - r.max) * inv_t - ln_of(ex); };
-  auto kept_by_m = [&](float x) { return !by_m || weight_of(below(r, x)) >= min_p || x == r.max; };
-  if (border.listed > 0) {
-    if (rank == 0) {
-      for (int i = threadIdx.x; i < border.listed; i += kThreads) {
-        const float x = unordered((uint32_t)(sh.list[i] >> 32));
-        const int id = (int)id_of(sh.list[i]);
-        if (kept_by_m(x)) {
-          const float ex = __ldg(r.e + id);
-          if (ex > 0.f) best.take(score(x, ex), id);
-        }
-      }
-    }
-  } else if (!free_draw || far) {
-    for_each(r, [&](float x, int id) {
-      if (x > -INFINITY && key_of(x, (uint32_t)id) >= border.key && kept_by_m(x)) {
-        const float ex = __ldg(r.e + id);
-        if (ex > 0.f) best.take(score(x, ex), id);
-      }
-    });
+  // ---- the draw's pass, over the chunks that hold logits of min-p's weight
+  uint32_t least = kMasked + 1;
+  if (by_m) {
+    const float edge = -log2_of(fminf(min_p, 1.f)) / r.scale;
+    const float reach = r.max - edge * (1.f + 0x1p-18f) - 0x1p-20f * fabsf(r.max);
+    if (reach > -INFINITY) least = max(least, ordered(reach));
   }
-  const bool join = ranks > 1 && border.listed == 0;
-  float most = block_max(sh, best.s0);
-  if (join) {
-    if (threadIdx.x == 0) sh.rank_best = most;
+  cl.sync();  // the buckets have been read
+  if (r.shift > 0)
+    for (int i = threadIdx.x; i <= r.chunks; i += kThreads) reinterpret_cast<int*>(sh.best())[i] = INT32_MIN;
+  if (threadIdx.x == 0) sh.listed = 0u;
+  cl.sync();
+  float most = -INFINITY;
+  if (bucket >= 0) {
+    const uint32_t above_count = sh.above_count;
+    const Key above_mass = sh.above_mass;
+    auto kind = [&](float x, int) {
+      const int b = bucket_of(below(r, x));
+      return b < bucket ? (int)kept_by_m(x) : b == bucket ? 2 : 0;
+    };
+    most = draw_pass(r, sh, home, kMasked + 1, kind, score);  // (the bucket is collected whole, whatever min-p keeps)
     cl.sync();
-    for (int i = 0; i < ranks; ++i) most = fmaxf(most, cl.map_shared_rank(&sh, i)->rank_best);
+    const uint32_t n = home->listed;
+    if (n <= (uint32_t)kList) {
+      // the bucket's logits that stay take part, too
+      int kept = 0;
+      auto listed = [&](float, auto f) {
+        for (int i = threadIdx.x; i < kept; i += kThreads) {
+          const float x = unordered((uint32_t)(sh.list[i] >> 32));
+          const int id = (int)id_of(sh.list[i]);
+          if (kept_by_m(x)) f(x, __ldg(r.e + id), id);
+        }
+      };
+      if (rank == 0) {
+        cut_list(r, sh, n, first != 0 ? first - above_count : 0u, above_mass, first != 0 ? INFINITY : want, 1.f, false);
+        __syncthreads();
+        kept = sh.kept;
+        listed(0.f, [&](float x, float e, int) { most = fmaxf(most, score(x, e)); });
+      }
+      most = unordered(over_ranks(ordered(most)));
+      if (most > -INFINITY) {
+        auto visit = [&](float least, auto f) {
+          chunks_reaching(least, [&](float x, float e, int id) {
+            if (x > -INFINITY && kind(x, id) == 1) f(x, e, id);
+          });
+          listed(least, f);
+        };
+        decide(most, margin_of(most, 150.f), visit, score, true);
+      } else {
+        largest(top);
+      }
+      if (ranks > 1) cl.sync();
+      return;
+    }
+    // more than the list holds (equal or nearly equal logits): count and weight of all, and the border by keys
+    cl.sync();
+    clear(sh);
+    __syncthreads();
+    bucket_pass<false>(r, sh);
+    bucket_pass<true>(r, sh);
+    cl.sync();
+    uint32_t c[2];
+    Key m[2];
+    gather(cl, sh, ranks, c, m);
+    find_border(sh, c, m, 0, 0, first, want);
+    border = resolve(cl, r, sh, home, rank, ranks, 0, first, want, 1.f);
+    cl.sync();
+    if (r.shift > 0)
+      for (int i = threadIdx.x; i <= r.chunks; i += kThreads) reinterpret_cast<int*>(sh.best())[i] = INT32_MIN;
+    cl.sync();
   }
-  // candidates near the best, again in 64 bits.  A float32 score is off by its logarithm's 2^-21 or so of |ln e| (< 100) at the
-  // worst, the difference's and the product's roundings: a few 2^-24 of |x / T|.
-  const float margin = 2e-4f + 0x1p-21f * fabsf(most) + (free_draw && !far ? 0x1p-21f * fabsf(r.max * inv_t) : 0.f);
-  Draw d{0.0, -1};
-  auto again = [&](float s, int id) {
-    if (id >= 0 && s >= most - margin)
-      d = better(d, Draw{((double)__ldg(r.x + id) - (double)r.max) / (double)T - log((double)__ldg(r.e + id)), id});
-  };
-  again(best.s0, best.i0);
-  again(best.s1, best.i1);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Draw u;
-    u.s = __shfl_xor_sync(0xffffffffu, d.s, o);
-    u.id = __shfl_xor_sync(0xffffffffu, d.id, o);
-    d = better(d, u);
-  }
-  if ((threadIdx.x & 31) == 0) sh.part_draw[threadIdx.x >> 5] = d;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) d = better(d, sh.part_draw[w]);
-    sh.rank_draw = d;
-  }
-  if (ranks > 1) cl.sync();
-  if (rank == 0 && threadIdx.x == 0) {
-    if (join)
-      for (int i = 1; i < ranks; ++i) d = better(d, cl.map_shared_rank(&sh, i)->rank_draw);
-    p.ids[row] = d.id >= 0 ? (int64_t)d.id : (int64_t)id_of(top);
+  auto kind = [&](float x, int id) { return (int)(key_of(x, (uint32_t)id) >= border.key && kept_by_m(x)); };
+  most = draw_pass(r, sh, home, max(least, (uint32_t)(border.key >> 32)), kind, score);
+  most = unordered(over_ranks(ordered(most)));
+  if (most > -INFINITY) {
+    auto visit = [&](float least, auto f) {
+      chunks_reaching(least, [&](float x, float e, int id) {
+        if (x > -INFINITY && kind(x, id) == 1) f(x, e, id);
+      });
+    };
+    decide(most, margin_of(most, 150.f), visit, score, true);
+  } else {
+    largest(top);
   }
   if (ranks > 1) cl.sync();
 }

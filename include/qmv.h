@@ -684,9 +684,9 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
  * that leaves none, and with a temperature of 2^-100 or less (0, negative or NaN), top_k 1 or top_p 0, the id is that of
  * the largest logit.  A logit of -infinity is a masked id.  A row that holds NaN, or in which every logit is
  * -infinity, gives -1; one that holds +infinity the lowest id of those.
- * The sums that place the top_p border count a w to 2^-32, exactly and in any order.  Scores are compared in
- * float32 and the closest ones again in 64 bits, so that scores of 2^-30 apart can be told apart, except where
- * a thread meets three within 2^-12 of the largest.  Results do not depend on timing or on the other rows of the call.
+ * (A temperature above 2^100 counts as that.)  The sums that place the top_p border are float32 sums of a few terms
+ * each, then exact: a border may be off by 2^-20 of the mass.  Scores near the largest are compared in 64 bits.  Results
+ * do not depend on timing or on the other rows of the call.
  * Allocates nothing and uses no workspace.
  * Returns QMV_OK, QMV_E_ARG (rows < 0, null logits, noise or ids), QMV_E_SHAPE (vocab not within 1..
  * QMV_SAMPLE_MAX_VOCAB - 1, strides below vocab, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */

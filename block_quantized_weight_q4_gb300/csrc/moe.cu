@@ -4,16 +4,22 @@
 //   h_e  = act(W1_e x_t) * (W3_e x_t),   out_t = scale * sum_{e in E(t)} p_e W2_e h_e.
 //
 // Two launches.  Every CTA of both works out the routing itself from the logits (a maximum over a warp's lanes `top` times
-// a token): a launch of its own would cost more.  A unit is an expert with as many of its tokens as the 8 columns
-// of an m16n8k16 MMA take: a bfloat16 activation is one column, an h of two or three parts two or four.  An expert that
-// more tokens chose has more units, whose weights come from L2 after the first.
-//   moe_up:   items of (unit, rows of W1 and the same rows of W3); a CTA's warps share an item's columns and meet in shared
-//             memory, where gate and up become h, written as bfloat16 parts (hi, lo; three for float32 outputs).
+// a token): a launch of its own would cost more.  A unit is an expert with up to 4 of its tokens (2 where they are float32: a value
+// is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after the first.
+//   moe_up:   items of (unit, 32 rows of W1 and of W3), each CTA a run of them; a CTA's warps share an item's columns and meet in
+//             shared memory, where gate and up become h.
 //   moe_down: a cluster holds 32 rows of the output; its warps share the (unit, columns) stages of all units evenly, each
 //             adds share * W2_e h_e into a tile of its own, and the tiles are added in a fixed order at the end.  Launched as a
 //             dependent of moe_up: routing and the first weights are read while that one ends.
-// Weights reach each warp through a ring of its own (cp.async, 32 rows of 128 bytes of quants a stage); levels enter the tensor core as exact
-// bfloat16, a block's dot product is scaled in float32 (as in decode_mma.cu).
+// Weights reach each warp through a ring of its own (cp.async, 32 rows of 128 bytes of quants a stage).
+//
+// Products: m16n8k16 with IEEE halves.  Lane t of a row's four lanes takes a whole block of 32 weights (one or two 16-byte loads), so an
+// MMA's k slots hold four different blocks; the columns are 2 vectors x those 4 blocks, and a lane's B values are
+// zero but for its own block's column.  After the 8 MMAs of four blocks a lane holds the dot products of two blocks for two
+// rows, scaled by the weights' and the activations' scales in float32: a quarter of the loads and scalings that
+// one block an MMA would take, and 2 vectors fill the 8 columns.  Levels are exact halves.  An activation is a half after the power of two
+// that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16 down to 2^-31 of the largest; float32 values (and h for
+// float32 outputs) are two halves, 22 bits; h for bfloat16 outputs one, 2^-11 relative.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -32,7 +38,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTokens = 64;    // of a launch
 constexpr int kExperts = QMV_MOE_MAX_EXPERTS;
 constexpr int kTop = QMV_MOE_MAX_TOP;
-constexpr int kCols = 8;       // columns of an MMA
+constexpr int kVectors = 4;    // of a unit: two to an MMA
 constexpr int kUnits = kExperts + kTokens * kTop / 2;  // experts, and one more for each 2 tokens or more
 constexpr int kRowsStage = 32;
 
@@ -172,23 +178,29 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Layout of a stage: q (32 rows of 128 bytes, their 16-byte pieces exchanged by row & 7), the rows' scales, then the
-// activations of MMA columns (a column's values and 16 bytes, so that the 8 columns' words lie in different banks).
-template <int WT, bool F16, bool XF32>
+// Layout of a stage: q (32 rows of 128 bytes), then the rows' scales.  A row's 16-byte pieces are exchanged between even and
+// odd rows, so that the 16-byte loads of two rows' four blocks lie in different banks.
+template <int WT, bool F16>
 struct Stage {
   static constexpr int kChunk = WT == QMV_Q4_0 ? 256 : 128;  // weights of a row
+  static constexpr int kBlocks = kChunk / 32;
+  static constexpr int kTurn = WT == QMV_Q4_0 ? 4 : 1;       // what an odd row's piece numbers are exchanged by
   static constexpr int kQ = kRowsStage * 128;
-  static constexpr int kScaleRow = kChunk / 32 * (F16 ? 2 : 4);
-  static constexpr int kD = kRowsStage * kScaleRow;
-  static constexpr int kXCol = kChunk * (XF32 ? 4 : 2) + 16;
-  static __host__ __device__ int bytes(int mma_cols) { return kQ + kD + mma_cols * kXCol; }
+  static constexpr int kScaleRow = kBlocks * (F16 ? 2 : 4);
+  static constexpr int kBytes = kQ + kRowsStage * kScaleRow;
+  // a vector's chunk: its blocks' halves, 64 of 80 bytes a block, and 64 bytes between vectors: the 8 lanes that read a set's two
+  // vectors lie in different banks.  Then the blocks' scales.
+  static constexpr int kBlock = 80;
+  static constexpr int kVector = kBlocks * kBlock + (WT == QMV_Q4_0 ? 64 : 0);
+  static_assert(kVector % 128 == 64, "the second vector's banks");
+  static __host__ __device__ constexpr int columns(int vectors) { return vectors * (kVector + kBlocks * 4); }
 };
 
 // Rows row_a .. row_a + 15 of one matrix image and row_b .. row_b + 15 of another (or of the same), chunk c of `cols` columns.
 template <int WT, bool F16>
 __device__ __forceinline__ void load_weights(uint32_t stage, const uint8_t* qa, const uint8_t* da, const uint8_t* qb, const uint8_t* db,
                                              long long row_a, long long row_b, int c, int cols) {
-  using S = Stage<WT, F16, false>;
+  using S = Stage<WT, F16>;
   const int lane = threadIdx.x & 31;
   const long long row_bytes = WT == QMV_Q4_0 ? cols / 2 : cols;
   const int piece = lane & 7;
@@ -198,7 +210,7 @@ __device__ __forceinline__ void load_weights(uint32_t stage, const uint8_t* qa, 
   for (int i = 0; i < kRowsStage / 4; ++i) {
     const int row = i * 4 + (lane >> 3);
     const uint8_t* src = row < 16 ? qa + (row_a + row) * row_bytes : qb + (row_b + row - 16) * row_bytes;
-    copy_async<16>(stage + row * 128 + ((piece ^ (row & 7)) << 4), src + off, live);
+    copy_async<16>(stage + row * 128 + ((piece ^ ((row & 1) * S::kTurn)) << 4), src + off, live);
   }
   // scales
   constexpr int kSize = F16 ? 2 : 4;
@@ -223,210 +235,324 @@ __device__ __forceinline__ void load_weights(uint32_t stage, const uint8_t* qa, 
   }
 }
 
-// Chunk c of the activations of `n` tokens (lane k: the row of token k): token k's part p is MMA column k * SPAN + p, and lies
-// p * plane elements after its first part.
-template <typename S, int SPAN, int PARTS, bool XF32>
-__device__ __forceinline__ void load_columns(uint32_t at, const void* x, long long plane, int row, int n, int c, int cols) {
-  const int lane = threadIdx.x & 31;
-  constexpr int kSize = XF32 ? 4 : 2;
-  constexpr int kPieces = S::kChunk * kSize / 16;  // of a column: 16, 32 or 64
-  for (int k = 0; k < n; ++k) {
-    const long long base = (long long)__shfl_sync(0xffffffffu, row, k) * cols;
+// The power of two that brings amax into [2^14, 2^15), and its inverse (1 for amax 0, below 2^-112 or not finite).
+// Eight values of a block of 32 that four neighbouring lanes hold, as halves at that scale: hi, and with LO what hi leaves (11 more bits).
+template <bool LO>
+__device__ __forceinline__ float to_halves(const float (&v)[8], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < (PARTS * kPieces + 31) / 32; ++i) {
-      const int j = lane + 32 * i, part = j / kPieces, piece = j % kPieces;
-      if (PARTS * kPieces % 32 != 0 && part >= PARTS) continue;
-      const int v = c * S::kChunk + piece * (16 / kSize);  // the piece's first value
-      const bool live = v < cols;
-      copy_async<16>(at + (k * SPAN + part) * S::kXCol + piece * 16,
-                     static_cast<const uint8_t*>(x) + (base + part * plane + (live ? v : 0)) * kSize, live);
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  float up, down;
+  half_stage_scale(amax, up, down);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a = v[2 * e] * up, b = v[2 * e + 1] * up;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi[e]) : "f"(b), "f"(a));
+    if (LO) {
+      const float ra = a - __half2float(__ushort_as_half((unsigned short)(hi[e] & 0xffffu)));
+      const float rb = b - __half2float(__ushort_as_half((unsigned short)(hi[e] >> 16)));
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(rb), "f"(ra));
     }
   }
+  return down;
 }
 
-// Three bfloat16 parts of two float32 values: together 24 bits.
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  hi = pack_bf16x2(a, b);
-  const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
-  mid = pack_bf16x2(ra, rb);
-  lo = pack_bf16x2(ra - __uint_as_float(mid << 16), rb - __uint_as_float(mid & 0xffff0000u));
-}
-
-// One stage's products: acc[m] += the 16 x 8 products of row tile m (m = 0, 1) with the MMA columns.  live: this lane's
-// column (lane / 4) is there.
-template <int WT, bool F16, bool XF32>
-__device__ __forceinline__ void consume(uint32_t stage, bool live, float (&acc)[2][4]) {
-  using S = Stage<WT, F16, XF32>;
+// One stage's products: acc[m][set] += what row tile m (rows g and g + 8 of it) gives for this lane's two blocks and vector.
+// b: this lane's column (its vector and block of the first four blocks), moving by `step` from set to set and by `group` from four blocks to
+// the next (both 0 at zeros, for lanes without a column); xs: the vector's scales of the lane's two blocks.
+template <int WT, bool F16>
+__device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t step, uint32_t group, uint32_t xs, uint32_t xs_step, int sets,
+                                        float (&acc)[2][2][2]) {
+  using S = Stage<WT, F16>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int lm = lane >> 3, lrow = (lane & 7) + ((lm & 1) << 3), lsub = lm >> 1, sw = lrow & 7;
-  const uint32_t xs = stage + S::kQ + S::kD + (live ? g * S::kXCol : 0) + t * (XF32 ? 16 : 8);
-  constexpr int kParts = XF32 ? 3 : 1;
+  constexpr int kGroups = S::kBlocks / 4;
+  constexpr int kPieces = WT == QMV_Q4_0 ? 1 : 2;  // of 16 bytes, of a block
+  const uint32_t turn = (g & 1) * S::kTurn;
 #pragma unroll
-  for (int bp = 0; bp < S::kChunk / 64; ++bp) {
-    uint32_t w[2][4];
-    if (WT == QMV_Q4_0) {
+  for (int i = 0; i < kGroups; ++i) {
+    float c[2][2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) c[m][v][0] = c[m][v][1] = c[m][v][2] = c[m][v][3] = 0.f;
+    uint32_t q[2][2][4 * kPieces];  // [tile][row g, g + 8][word]
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          uint32_t w[4];
+          lds_u32x4(stage + (16 * m + 8 * h + g) * 128 + ((((4 * i + t) * kPieces + j) ^ turn) << 4), w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[m][h][4 * j + k] = w[k];
+        }
+    // eight elements of a block at a time: one load of B (two for Q4_0, whose words hold elements 16 apart)
+#pragma unroll
+    for (int j = 0; j < 2 * kPieces; ++j) {
+      uint32_t x[2][2][4];  // [set][first, elements 16 further][halves]
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        if (v < sets) {
+          lds_u32x4(b + v * step + i * group + j * 16, x[v][0]);
+          if (WT == QMV_Q4_0) lds_u32x4(b + v * step + i * group + 32 + j * 16, x[v][1]);
+        }
 #pragma unroll
       for (int m = 0; m < 2; ++m)
-        ldmatrix_x4(w[m][0], w[m][1], w[m][2], w[m][3], stage + (16 * m + lrow) * 128 + (((2 * bp + lsub) ^ sw) << 4));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t wg = q[m][0][2 * j + k], wh = q[m][1][2 * j + k];
+          if (WT == QMV_Q4_0) {
+            uint32_t g01, g23, gh01, gh23, h01, h23, hh01, hh23;
+            q4_word_to_f16_levels(wg, g01, g23, gh01, gh23);
+            q4_word_to_f16_levels(wh, h01, h23, hh01, hh23);
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+              if (v < sets) {
+                mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
+                mma_f16_16816(c[m][v], gh01, hh01, gh23, hh23, x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
+              }
+          } else {
+            uint32_t g01, g23, h01, h23;
+            q8_word_to_f16_levels(wg, g01, g23);
+            q8_word_to_f16_levels(wh, h01, h23);
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+              if (v < sets) mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
+          }
+        }
     }
-    float d[2][2][2];  // [tile][row g, g + 8][block]
+    // columns 2 t and 2 t + 1: vector t / 2 of the set, blocks 2 (t & 1) and the next
+    float xd[2][2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      if (v < sets) {
+        uint32_t u0, u1;
+        lds_u32x2(xs + v * xs_step + i * 16, u0, u1);
+        xd[v][0] = __uint_as_float(u0), xd[v][1] = __uint_as_float(u1);
+      }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t at = stage + S::kQ + (16 * m + 8 * h + g) * S::kScaleRow + bp * (F16 ? 4 : 8);
+        const uint32_t at = stage + S::kQ + (16 * m + 8 * h + g) * S::kScaleRow + (4 * i + 2 * (t & 1)) * (F16 ? 2 : 4);
+        float d0, d1;
         if (F16) {
-          const uint32_t v = lds_u32(at);
-          d[m][h][0] = f16_bits_to_f32((uint16_t)(v & 0xFFFF));
-          d[m][h][1] = f16_bits_to_f32((uint16_t)(v >> 16));
+          const uint32_t u = lds_u32(at);
+          d0 = f16_bits_to_f32((uint16_t)(u & 0xFFFF));
+          d1 = f16_bits_to_f32((uint16_t)(u >> 16));
         } else {
-          uint32_t a, b;
-          lds_u32x2(at, a, b);
-          d[m][h][0] = __uint_as_float(a);
-          d[m][h][1] = __uint_as_float(b);
+          uint32_t u0, u1;
+          lds_u32x2(at, u0, u1);
+          d0 = __uint_as_float(u0);
+          d1 = __uint_as_float(u1);
         }
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          if (v < sets) acc[m][v][h] = fmaf(d0 * xd[v][0], c[m][v][2 * h], fmaf(d1 * xd[v][1], c[m][v][2 * h + 1], acc[m][v][h]));
       }
+  }
+}
+
+__device__ __forceinline__ void wait_ring(int ring) {  // all but the newest ring - 1 groups of copies have landed
+  if (ring == 2)
+    copies_wait<1>();
+  else if (ring == 3)
+    copies_wait<2>();
+  else
+    copies_wait<3>();
+}
+
+// Where a lane reads B from: `columns` holds the unit's vectors (then their blocks' scales), `zeros` 128 bytes of zeros.
+struct Columns {
+  uint32_t b, step, group, xs, xs_step;
+};
+template <typename S>
+__device__ __forceinline__ Columns columns_of(uint32_t columns, uint32_t zeros, int max_vectors) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int v = g >> 2;
+  const bool mine = (g & 3) == t && v < max_vectors;
+  Columns c;
+  c.b = mine ? columns + v * S::kVector + t * S::kBlock : zeros;
+  c.step = mine && 2 + v < max_vectors ? 2 * S::kVector : 0;
+  c.group = mine ? 4 * S::kBlock : 0;
+  const int sv = t >> 1;
+  c.xs = sv < max_vectors ? columns + max_vectors * S::kVector + sv * S::kBlocks * 4 + 2 * (t & 1) * 4 : zeros;
+  c.xs_step = 2 + sv < max_vectors ? 2 * S::kBlocks * 4 : 0;  // (what is read for a vector that is not there goes nowhere)
+  return c;
+}
+
+// ------------------------------------------------------------------------------------------ gate and up
+// A warp's columns of chunk c, converted: `vectors` halves of up to kVectors vectors, then their scales, at `to`.
+template <typename S, bool XF32>
+__device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, const void* x, const Unit& u, int c, int cols) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPieces = S::kChunk / 8;  // of a token
+  float* scales = reinterpret_cast<float*>(to + max_vectors * S::kVector);
+#pragma unroll 2
+  for (int i = 0; i < u.cols * kPieces; i += 32) {
+    const int k = (i + lane) / kPieces, piece = (i + lane) % kPieces;
+    const int tok = __shfl_sync(0xffffffffu, u.tok, k & 31);
+    const bool in = k < u.cols;
+    const int at = c * S::kChunk + 8 * piece;
+    float v[8];
 #pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-      const int k = 2 * bp + hb;
-      uint32_t b[kParts][2][2];  // [part][half block][pair]
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (in && at < cols) {
+      if (XF32) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + (long long)tok * cols + at);
+        const float4 a = __ldg(f), b = __ldg(f + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      } else {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + (long long)tok * cols + at));
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (XF32) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          if (live) lds_f32x4(xs + (k * 32 + h * 16) * 4, v);
-          split3(v[0], v[1], b[0][h][0], b[kParts / 3][h][0], b[kParts / 3 * 2][h][0]);
-          split3(v[2], v[3], b[0][h][1], b[kParts / 3][h][1], b[kParts / 3 * 2][h][1]);
-        } else {
-          b[0][h][0] = b[0][h][1] = 0u;
-          if (live) lds_u32x2(xs + (k * 32 + h * 16) * 2, b[0][h][0], b[0][h][1]);
-        }
+        for (int e = 0; e < 4; ++e) v[2 * e] = __uint_as_float(ww[e] << 16), v[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
       }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t a[2][4];  // [half block][fragment]
-        if (WT == QMV_Q4_0) {
-          q4_word_to_bf16_levels(w[m][2 * hb], a[0][0], a[0][2], a[1][0], a[1][2]);
-          q4_word_to_bf16_levels(w[m][2 * hb + 1], a[0][1], a[0][3], a[1][1], a[1][3]);
-        } else {
-          uint32_t q[4];  // row g half 0, row g + 8 half 0, row g half 1, row g + 8 half 1
-          ldmatrix_x4(q[0], q[1], q[2], q[3], stage + (16 * m + lrow) * 128 + (((2 * k + lsub) ^ sw) << 4));
-          q8_word_to_bf16_levels(q[0], a[0][0], a[0][2]);
-          q8_word_to_bf16_levels(q[1], a[0][1], a[0][3]);
-          q8_word_to_bf16_levels(q[2], a[1][0], a[1][2]);
-          q8_word_to_bf16_levels(q[3], a[1][1], a[1][3]);
-        }
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = kParts - 1; p >= 0; --p)  // the small parts first
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_bf16_16816(c, a[h][0], a[h][1], a[h][2], a[h][3], b[p][h][0], b[p][h][1], c);
-        acc[m][0] = fmaf(d[m][0][hb], c[0], acc[m][0]);
-        acc[m][1] = fmaf(d[m][0][hb], c[1], acc[m][1]);
-        acc[m][2] = fmaf(d[m][1][hb], c[2], acc[m][2]);
-        acc[m][3] = fmaf(d[m][1][hb], c[3], acc[m][3]);
+    }
+    uint32_t hi[4], lo[4];
+    const float down = to_halves<XF32>(v, hi, lo);
+    if (in) {
+      const int vec = XF32 ? 2 * k : k;
+      uint8_t* at16 = to + vec * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16;
+      *reinterpret_cast<uint4*>(at16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (XF32) *reinterpret_cast<uint4*>(at16 + S::kVector) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if ((piece & 3) == 0) {
+        scales[vec * S::kBlocks + (piece >> 2)] = down;
+        if (XF32) scales[(vec + 1) * S::kBlocks + (piece >> 2)] = down;
       }
     }
   }
 }
 
-// ------------------------------------------------------------------------------------------ gate and up
-constexpr int kRing = 2;
-
 template <int WT, bool F16, bool XF32>
 __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_constant__ MoeParams p) {
-  using S = Stage<WT, F16, XF32>;
-  constexpr int kUnit = XF32 ? 4 : 8;  // tokens of a unit (float32 activations take twice the room)
+  using S = Stage<WT, F16>;
+  constexpr int kUnit = XF32 ? kVectors / 2 : kVectors;  // tokens of a unit
   extern __shared__ __align__(1024) uint8_t smem[];
   Routing& r = *reinterpret_cast<Routing*>(smem);
-  float* red = reinterpret_cast<float*>(smem + p.off_red);  // 32 rows x 8 columns a warp
+  float* red = reinterpret_cast<float*>(smem + p.off_red);  // a warp's gate and up: [token][gate, up][32 rows]
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int stage_bytes = S::bytes(min(p.tokens, kUnit));
-  const uint32_t ring = smem_u32(smem + p.off_ring) + wid * kRing * stage_bytes;
+  const int max_tokens = min(p.tokens, kUnit), max_vectors = XF32 ? 2 * max_tokens : max_tokens;
+  const uint32_t ring = smem_u32(smem + p.off_ring) + wid * p.ring * S::kBytes;
+  const int cache_bytes = S::columns(max_vectors);
+  uint8_t* cache = smem + p.off_cols + wid * p.cached * cache_bytes;  // the warp's columns, of p.cached chunks
   griddep_wait();
   griddep_launch_dependents();
+  if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
   route(r, p, kUnit);
+  const uint32_t zeros = smem_u32(smem + p.off_zero);
 
-  const int tiles = p.hidden / 16, chunks = (p.dim + S::kChunk - 1) / S::kChunk;
+  const int tiles = p.hidden / 32, chunks = (p.dim + S::kChunk - 1) / S::kChunk;
   const int tiles_item = kWarps / p.ks;
   const int items_unit = (tiles + tiles_item - 1) / tiles_item;
   const int items = r.units * items_unit;
+  // a run of items: mostly one unit's, so that its columns are converted once
+  const int item0 = (int)((long long)items * blockIdx.x / gridDim.x), item1 = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
   const int slice = wid % p.ks, tile_local = wid / p.ks;
   const int c0 = slice * chunks / p.ks, n = (slice + 1) * chunks / p.ks - c0;
 
-  // the producer's place: stage j of the warp's columns of an item
-  int pi = blockIdx.x, pj = 0, ps = 0;
-  Unit pu{};
-  int p_tile = 0;
+  // the producer's place: chunk j of the warp's columns of an item, rows 16 m .. of its tile
+  int pi = item0, pj = 0, pm = 0, ps = 0;
+  int p_tile = 0, p_expert = 0;
   auto settle = [&]() {  // on to an item in which the warp has rows
-    while (pi < items) {
+    while (pi < item1) {
       p_tile = pi % items_unit * tiles_item + tile_local;
       if (p_tile < tiles) break;
-      pi += gridDim.x;
+      ++pi;
     }
-    if (pi < items) pu = unit_of(r, p, pi / items_unit, kUnit);
+    if (pi < item1) p_expert = r.unit[pi / items_unit] & 255;
   };
   settle();
   auto issue = [&]() {
-    if (pi < items) {
-      const uint32_t st = ring + ps * stage_bytes;
-      const long long row = (long long)pu.expert * p.hidden + 16LL * p_tile;
-      load_weights<WT, F16>(st, p.q1, p.d1, p.q3, p.d3, row, row, c0 + pj, p.dim);
-      load_columns<S, 1, 1, XF32>(st + S::kQ + S::kD, p.x, 0, pu.tok, pu.cols, c0 + pj, p.dim);
-      ps = ps + 1 == kRing ? 0 : ps + 1;
-      if (++pj == n) {
+    if (pi < item1) {
+      const long long row = (long long)p_expert * p.hidden + 32LL * p_tile + 16 * pm;
+      load_weights<WT, F16>(ring + ps * S::kBytes, p.q1, p.d1, p.q3, p.d3, row, row, c0 + pj, p.dim);
+      ps = ps + 1 == p.ring ? 0 : ps + 1;
+      pm ^= 1;
+      if (pm == 0 && ++pj == n) {
         pj = 0;
-        pi += gridDim.x;
+        ++pi;
         settle();
       }
     }
     copies_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) issue();
+  for (int i = 0; i < p.ring - 1; ++i) issue();
 
-  int cs = 0;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int tile = item % items_unit * tiles_item + tile_local;
-    const Unit u = unit_of(r, p, item / items_unit, kUnit);
-    float acc[2][4] = {};
+  int cs = 0, held = -1;  // held: the unit whose columns the cache has
+  for (int item = item0; item < item1; ++item) {
+    const int unit = item / items_unit, tile = item % items_unit * tiles_item + tile_local;
+    const Unit u = unit_of(r, p, unit, kUnit);
+    const int vectors = XF32 ? 2 * u.cols : u.cols, sets = (vectors + 1) / 2;
+    float acc[2][2][2][2] = {};  // [rows 16 m][W1, W3][set][row g, g + 8]
     if (tile < tiles) {
-      for (int j = 0; j < n; ++j) {
-        __syncwarp();  // every lane is done with the slot that is filled next
-        issue();
-        copies_wait<kRing - 1>();
+      if (held != unit && n <= p.cached) {
         __syncwarp();
-        consume<WT, F16, XF32>(ring + cs * stage_bytes, g < u.cols, acc);
-        cs = cs + 1 == kRing ? 0 : cs + 1;
+        for (int j = 0; j < n; ++j) convert_columns<S, XF32>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
+        __syncwarp();
+        held = unit;
+      }
+      for (int j = 0; j < n; ++j) {
+        if (n > p.cached) {
+          __syncwarp();
+          convert_columns<S, XF32>(cache, max_vectors, p.x, u, c0 + j, p.dim);
+        }
+        const Columns c = columns_of<S>(smem_u32(cache) + (n > p.cached ? 0 : j * cache_bytes), zeros, max_vectors);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          __syncwarp();  // every lane is done with the slot that is filled next
+          issue();
+          wait_ring(p.ring);
+          __syncwarp();
+          consume<WT, F16>(ring + cs * S::kBytes, c.b, c.step, c.group, c.xs, c.xs_step, sets, acc[m]);
+          cs = cs + 1 == p.ring ? 0 : cs + 1;
+        }
       }
     }
-    float* my = red + wid * (kRowsStage * kCols);
+    // a vector's two lanes hold two blocks each; float32 tokens: hi and lo are the set's two vectors
+    float* my = red + wid * (kUnit * 64);
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      *reinterpret_cast<float2*>(my + (16 * m + g) * kCols + 2 * t) = make_float2(acc[m][0], acc[m][1]);
-      *reinterpret_cast<float2*>(my + (16 * m + g + 8) * kCols + 2 * t) = make_float2(acc[m][2], acc[m][3]);
-    }
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float a = acc[m][w][v][h];
+            a += __shfl_xor_sync(0xffffffffu, a, 1);
+            if (XF32) a += __shfl_xor_sync(0xffffffffu, a, 2);
+            const int tok = XF32 ? v : 2 * v + (t >> 1);
+            if (XF32 ? t == 0 : (t & 1) == 0) my[tok * 64 + w * 32 + 16 * m + 8 * h + g] = a;
+          }
     __syncthreads();
-    for (int i = threadIdx.x; i < tiles_item * 16 * kCols; i += kThreads) {  // whole warps: tiles_item * 128 is a multiple of 32
-      const int tl = i / (16 * kCols), col = i / 16 % kCols, row = i % 16;
+    for (int i = wid; i < tiles_item * u.cols; i += kWarps) {
+      const int tl = i / u.cols, col = i % u.cols;
       const int ht = item % items_unit * tiles_item + tl;
       const int slot = __shfl_sync(0xffffffffu, u.slot, col);
-      if (col < u.cols && ht < tiles) {
+      if (ht < tiles) {
         float gate = 0.f, up = 0.f;
         for (int k = 0; k < p.ks; ++k) {
-          const float* part = red + (tl * p.ks + k) * (kRowsStage * kCols);
-          gate += part[row * kCols + col];
-          up += part[(16 + row) * kCols + col];
+          const float* part = red + (tl * p.ks + k) * (kUnit * 64) + col * 64;
+          gate += part[lane];
+          up += part[32 + lane];
         }
+        // the tile's 32 rows are a block of W2's columns: halves at a power of two of the block's own
         const float h = glu(p.act, gate, up);
-        uint16_t* out = p.h + (long long)slot * p.hidden + 16 * ht + row;
-        uint32_t hi, mid, lo;
-        split3(h, 0.f, hi, mid, lo);
-        if (!isfinite(h)) mid = lo = 0u;  // (infinity less itself)
-        out[0] = (uint16_t)hi;
-        out[p.h_plane] = (uint16_t)mid;
-        if (p.parts > 2) out[2 * p.h_plane] = (uint16_t)lo;
+        float amax = fabsf(h);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float to, down;
+        half_stage_scale(amax, to, down);
+        const float v = h * to;
+        const __half hi = __float2half_rn(v);
+        __half* out = reinterpret_cast<__half*>(p.h) + (long long)slot * p.hidden + 32 * ht + lane;
+        out[0] = hi;
+        if (p.parts > 1) out[p.h_plane] = __float2half_rn(isfinite(v) ? v - __half2float(hi) : 0.f);
+        if (lane == 0) p.h_scale[(long long)slot * (p.hidden / 32) + ht] = down;
       }
     }
     __syncthreads();
@@ -436,19 +562,21 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
 // ------------------------------------------------------------------------------------------ down
 template <int WT, bool F16, int PARTS>
 __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_constant__ MoeParams p, int ranks) {
-  using S = Stage<WT, F16, false>;
-  constexpr int kSpan = PARTS == 2 ? 2 : 4;   // MMA columns of a token
-  constexpr int kUnit = kCols / kSpan;        // tokens of a unit
+  using S = Stage<WT, F16>;
+  constexpr int kUnit = kVectors / PARTS;  // tokens of a unit
   extern __shared__ __align__(1024) uint8_t smem[];
   Routing& r = *reinterpret_cast<Routing*>(smem);
-  float* tiles = reinterpret_cast<float*>(smem + p.off_red);  // a warp's 32 rows x tokens
+  float* tiles = reinterpret_cast<float*>(smem + p.off_red);  // a warp's tokens x 32 rows
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int stage_bytes = S::bytes(min(p.tokens, kUnit) * kSpan);
-  const uint32_t ring = smem_u32(smem + p.off_ring) + wid * kRing * stage_bytes;
+  const int max_vectors = min(p.tokens, kUnit) * PARTS;
+  const int stage_bytes = S::kBytes + S::columns(max_vectors);
+  const uint32_t ring = smem_u32(smem + p.off_ring) + wid * p.ring * stage_bytes;
+  const uint32_t zeros = smem_u32(smem + p.off_zero);
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank();
   const int row0 = (int)(blockIdx.x / ranks) * kRowsStage;
   // launched by moe_up after its own wait: what came before that, the logits and the weights among it, is complete
+  if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
   route(r, p, kUnit);
   float* my = tiles + wid * kRowsStage * p.tokens;
   for (int i = lane; i < kRowsStage * p.tokens; i += 32) my[i] = 0.f;
@@ -457,73 +585,119 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   const int chunks = (p.hidden + S::kChunk - 1) / S::kChunk;
   const int total = r.units * chunks, warps = ranks * kWarps, me = rank * kWarps + wid;
   const int s0 = (int)((long long)total * me / warps), s1 = (int)((long long)total * (me + 1) / warps);
-  int ps = s0, slot_p = 0;
+  int ps = s0, ps_c = s0 % chunks, ps_u = s0 / chunks, slot_p = 0;
   Unit pu{};
-  int p_unit = -1;
-  auto weights = [&]() {
-    const int u = ps / chunks, c = ps % chunks;
-    if (u != p_unit) pu = unit_of(r, p, u, kUnit), p_unit = u;
+  if (s0 < s1) pu = unit_of(r, p, ps_u, kUnit);
+  auto weights = [&](int at) {
     const long long row = (long long)pu.expert * p.dim + row0;
-    load_weights<WT, F16>(ring + slot_p * stage_bytes, p.q2, p.d2, p.q2, p.d2, row, row + 16, c, p.hidden);
+    load_weights<WT, F16>(ring + at * stage_bytes, p.q2, p.d2, p.q2, p.d2, row, row + 16, ps_c, p.hidden);
   };
-  auto columns = [&]() {
-    load_columns<S, kSpan, PARTS, false>(ring + slot_p * stage_bytes + S::kQ + S::kD, p.h, p.h_plane, pu.slot, pu.cols, ps % chunks, p.hidden);
+  // the vectors' halves and scales: a piece of 16 bytes a lane and vector
+  auto columns = [&](int at) {
+    const uint32_t to = ring + at * stage_bytes + S::kBytes;
+    constexpr int kPieces = S::kChunk / 8;  // of a vector
+    const int n = pu.cols * PARTS * kPieces;
+    for (int i = lane; i < (n + 31) / 32 * 32; i += 32) {
+      const int v = i / kPieces, piece = i % kPieces;
+      const long long slot = __shfl_sync(0xffffffffu, pu.slot, v / PARTS & 31);
+      if (i >= n) continue;
+      const int first = ps_c * S::kChunk + piece * 8;
+      const bool live = first < p.hidden;
+      copy_async<16>(to + v * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16,
+                     p.h + (v % PARTS) * p.h_plane + slot * p.hidden + (live ? first : 0), live);
+      if ((piece & 3) == 0)
+        copy_async<4>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 4, p.h_scale + slot * (p.hidden / 32) + (live ? first / 32 : 0), live);
+    }
+  };
+  auto advance = [&]() {
     ++ps;
-    slot_p = slot_p + 1 == kRing ? 0 : slot_p + 1;
+    slot_p = slot_p + 1 == p.ring ? 0 : slot_p + 1;
+    if (++ps_c == chunks) {
+      ps_c = 0;
+      if (ps < s1) pu = unit_of(r, p, ++ps_u, kUnit);
+    }
   };
-  static_assert(kRing == 2, "one stage's weights are asked for ahead of the wait");
-  if (ps < s1) weights();
+  // the first stage's weights are asked for while moe_up ends
+  if (ps < s1) weights(0);
   griddep_wait();
   griddep_launch_dependents();
-  if (ps < s1) columns();
+  if (ps < s1) {
+    columns(0);
+    advance();
+  }
   copies_commit();
+  for (int i = 0; i < p.ring - 2; ++i) {
+    if (ps < s1) {
+      weights(slot_p);
+      columns(slot_p);
+      advance();
+    }
+    copies_commit();
+  }
 
-  float acc[2][4] = {};
-  int cs = 0, c_unit = -1;
+  float acc[2][2][2] = {};  // [tile][set][row g, g + 8]
+  int cs = 0, cc = s0 % chunks, cu = s0 / chunks;
   Unit u{};
+  if (s0 < s1) u = unit_of(r, p, cu, kUnit);
   auto flush = [&]() {
-    if (c_unit < 0) return;
-    // a token's parts lie side by side: in this lane's two columns, and for three parts in its neighbour's
-    const int col = 2 * t / kSpan;
-    const int tok = __shfl_sync(0xffffffffu, u.tok, col);
-    const float share = __shfl_sync(0xffffffffu, u.share, col);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int v = 0; v < 2; ++v) {
+      const int col = PARTS == 2 ? v : 2 * v + (t >> 1);
+      const int tok = __shfl_sync(0xffffffffu, u.tok, col);
+      const float share = __shfl_sync(0xffffffffu, u.share, col);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v = acc[m][2 * h] + acc[m][2 * h + 1];
-        if (PARTS == 3) v += __shfl_xor_sync(0xffffffffu, v, 1);
-        if (col < u.cols && 2 * t % kSpan == 0) my[(16 * m + 8 * h + g) * p.tokens + tok] += share * v;
-      }
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+          float a = acc[m][v][h];
+          a += __shfl_xor_sync(0xffffffffu, a, 1);
+          if (PARTS == 2) a += __shfl_xor_sync(0xffffffffu, a, 2);
+          if (col < u.cols && (PARTS == 2 ? t == 0 : (t & 1) == 0)) my[tok * kRowsStage + 16 * m + 8 * h + g] += share * a;
+          acc[m][v][h] = 0.f;
+        }
+    }
+    __syncwarp();
   };
   for (int s = s0; s < s1; ++s) {
     __syncwarp();
-    if (ps < s1) weights(), columns();
-    copies_commit();
-    const int uu = s / chunks;
-    if (uu != c_unit) {
-      flush();
-      u = unit_of(r, p, uu, kUnit);
-      c_unit = uu;
+    if (ps < s1) {
+      weights(slot_p);
+      columns(slot_p);
+      advance();
     }
-    copies_wait<kRing - 1>();
+    copies_commit();
+    wait_ring(p.ring);
     __syncwarp();
-    consume<WT, F16, false>(ring + cs * stage_bytes, g / kSpan < u.cols && g % kSpan < PARTS, acc);
-    cs = cs + 1 == kRing ? 0 : cs + 1;
+    const Columns c = columns_of<S>(ring + cs * stage_bytes + S::kBytes, zeros, max_vectors);
+    consume<WT, F16>(ring + cs * stage_bytes, c.b, c.step, c.group, c.xs, c.xs_step, (u.cols * PARTS + 1) / 2, acc);
+    cs = cs + 1 == p.ring ? 0 : cs + 1;
+    if (++cc == chunks) {
+      flush();
+      cc = 0;
+      if (s + 1 < s1) u = unit_of(r, p, ++cu, kUnit);
+    }
   }
-  flush();
-  cl.sync();
-  // the cluster's tiles: its CTAs share the sums, each in rank, then warp order
+  if (s0 < s1 && cc != 0) flush();
+  __syncthreads();
+  // this CTA's tiles in warp order, then the cluster's in rank order, its CTAs sharing the sums
   const int values = kRowsStage * p.tokens;
+  for (int i = threadIdx.x; i < values; i += kThreads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += tiles[w * values + i];
+    tiles[i] = sum;
+  }
+  if (ranks > 1)
+    cl.sync();
+  else
+    __syncthreads();
   for (int i = rank * kThreads + threadIdx.x; i < values; i += ranks * kThreads) {
     const int row = i % kRowsStage, tok = i / kRowsStage;
-    float sum = 0.f;
-    for (int k = 0; k < ranks; ++k) {
-      const float* o = cl.map_shared_rank(tiles, k);
-      for (int w = 0; w < kWarps; ++w) sum += o[(w * kRowsStage + row) * p.tokens + tok];
-    }
+    float v[8], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < ranks ? cl.map_shared_rank(tiles, k)[i] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += v[k];
     sum *= p.scale;
     if (r.bad >> tok & 1) sum = NAN;
     const long long at = (long long)tok * p.dim + row0 + row;
@@ -538,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
       if (p.shares != nullptr) p.shares[i] = r.share[i];
     }
   }
-  cl.sync();  // no CTA leaves while another reads its tiles
+  if (ranks > 1) cl.sync();  // no CTA leaves while another reads its tiles
 }
 
 cudaError_t allow_smem(const void* kern, int device, size_t bytes) {
@@ -548,38 +722,75 @@ cudaError_t allow_smem(const void* kern, int device, size_t bytes) {
 
 constexpr size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
+// Shared memory of an SM's CTA, with what the system keeps, where `n` are to fit.
+size_t room(const DeviceInfo& dev, int n) {
+  const size_t each = dev.smem_per_sm / n;
+  const size_t have = each > dev.smem_reserved ? each - dev.smem_reserved : 0;
+  return have < dev.smem_optin ? have : dev.smem_optin;
+}
+
 template <int WT, bool F16>
 cudaError_t launch_up(MoeParams p, bool x_f32, const DeviceInfo& dev, cudaStream_t stream) {
-  const int unit = x_f32 ? 4 : 8, cols = p.tokens < unit ? p.tokens : unit;
-  const int stage = x_f32 ? Stage<WT, F16, true>::bytes(cols) : Stage<WT, F16, false>::bytes(cols);
-  p.off_red = (int)round_up(sizeof(Routing), 128);
-  p.off_ring = (int)round_up(p.off_red + kWarps * kRowsStage * kCols * 4, 1024);
-  const size_t smem = p.off_ring + (size_t)kWarps * kRing * stage;
-  const int chunk = Stage<WT, F16, false>::kChunk, chunks = (p.dim + chunk - 1) / chunk;
+  using S = Stage<WT, F16>;
+  const int unit = x_f32 ? kVectors / 2 : kVectors, tokens = p.tokens < unit ? p.tokens : unit;
+  const int columns = S::columns(x_f32 ? 2 * tokens : tokens);
+  const int chunks = (p.dim + S::kChunk - 1) / S::kChunk;
   p.ks = 1;
   while (p.ks < kWarps && 2 * p.ks <= chunks) p.ks *= 2;
+  const int slice = (chunks + p.ks - 1) / p.ks;
+  p.off_zero = (int)round_up(sizeof(Routing), 128);
+  p.off_red = p.off_zero + 128;
+  p.off_cols = p.off_red + kWarps * unit * 64 * 4;
+  // the warps' columns are kept where they leave room for the rings; two CTAs a SM with rings of two stages before one with more
+  size_t smem = 0;
+  int per_sm = 2;
+  for (;; --per_sm) {
+    for (p.cached = slice; p.cached >= 1; p.cached = p.cached > 1 ? 1 : 0) {
+      p.off_ring = (int)round_up(p.off_cols + (size_t)kWarps * p.cached * columns, 128);
+      for (p.ring = per_sm == 2 ? 2 : 4; p.ring >= 2; --p.ring) {
+        smem = p.off_ring + (size_t)kWarps * p.ring * S::kBytes;
+        if (smem <= room(dev, per_sm)) break;
+      }
+      if (p.ring >= 2) break;
+    }
+    if (p.cached >= 1) break;
+    if (per_sm == 1) return cudaErrorInvalidValue;
+  }
   const int tiles_item = kWarps / p.ks;
   const long long units = (p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) + p.tokens * p.top / unit;
-  const long long items = units * ((p.hidden / 16 + tiles_item - 1) / tiles_item);
-  const long long slots = (long long)dev.sm_count * (2 * (smem + dev.smem_reserved) <= dev.smem_per_sm ? 2 : 1);
+  const long long items = units * ((p.hidden / 32 + tiles_item - 1) / tiles_item);
+  const long long slots = (long long)dev.sm_count * per_sm;
   auto kern = x_f32 ? moe_up_kernel<WT, F16, true> : moe_up_kernel<WT, F16, false>;
-  cudaError_t err = allow_smem((const void*)kern, dev.device, smem);
+  const cudaError_t err = allow_smem((const void*)kern, dev.device, smem);
   if (err != cudaSuccess) return err;
   return launch_dependent(kern, dim3((unsigned)(items < slots ? items : slots)), kThreads, smem, stream, p);
 }
 
 template <int WT, bool F16>
 cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream) {
-  const int span = p.parts == 2 ? 2 : 4, unit = kCols / span, cols = (p.tokens < unit ? p.tokens : unit) * span;
-  const int stage = Stage<WT, F16, false>::bytes(cols);
-  p.off_red = (int)round_up(sizeof(Routing), 128);
-  p.off_ring = (int)round_up(p.off_red + (size_t)kWarps * kRowsStage * p.tokens * 4, 1024);
-  const size_t smem = p.off_ring + (size_t)kWarps * kRing * stage;
-  const int tiles = p.dim / kRowsStage;
+  using S = Stage<WT, F16>;
+  const int unit = kVectors / p.parts, vectors = (p.tokens < unit ? p.tokens : unit) * p.parts;
+  const int stage = S::kBytes + S::columns(vectors);
+  p.off_zero = (int)round_up(sizeof(Routing), 128);
+  p.off_red = p.off_zero + 128;
+  p.off_ring = (int)round_up(p.off_red + (size_t)kWarps * kRowsStage * p.tokens * 4, 128);
+  size_t smem = 0;
+  int per_sm = 2;
+  for (; per_sm >= 1; --per_sm) {
+    for (p.ring = per_sm == 2 ? 2 : 4; p.ring >= 2; --p.ring) {
+      smem = p.off_ring + (size_t)kWarps * p.ring * stage;
+      if (smem <= room(dev, per_sm)) break;
+    }
+    if (p.ring >= 2) break;
+  }
+  if (per_sm < 1) return cudaErrorInvalidValue;
+  // CTAs of a cluster: as many as the SMs take, with a stage for each of their warps
+  const int tiles = p.dim / kRowsStage, chunks = (p.hidden + S::kChunk - 1) / S::kChunk;
+  const long long stages = (long long)(p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) * chunks;
   int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= 2 * dev.sm_count) ranks *= 2;
-  auto kern = p.parts == 3 ? moe_down_kernel<WT, F16, 3> : moe_down_kernel<WT, F16, 2>;
-  cudaError_t err = allow_smem((const void*)kern, dev.device, smem);
+  while (ranks < 8 && tiles * ranks * 2 <= per_sm * dev.sm_count && stages >= 2 * ranks * kWarps) ranks *= 2;
+  auto kern = p.parts == 2 ? moe_down_kernel<WT, F16, 2> : moe_down_kernel<WT, F16, 1>;
+  const cudaError_t err = allow_smem((const void*)kern, dev.device, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * ranks));
@@ -602,7 +813,7 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
 
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16) {
   const size_t t = tokens < kTokens ? tokens : kTokens;
-  return t * top * hidden * 2 * (out_bf16 ? 2 : 3);
+  return t * top * (hidden * 2 * (out_bf16 ? 1 : 2) + hidden / 32 * 4);
 }
 
 cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -617,7 +828,8 @@ cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t str
     p.out_bf16 = a.out_bf16;
     p.h = static_cast<uint16_t*>(a.scratch);
     p.h_plane = (long long)p.tokens * a.top * a.hidden;
-    p.parts = a.out_bf16 ? 2 : 3;
+    p.parts = a.out_bf16 ? 1 : 2;
+    p.h_scale = reinterpret_cast<float*>(p.h + p.parts * p.h_plane);
     p.ids = a.ids == nullptr ? nullptr : a.ids + t0 * a.top;
     p.shares = a.shares == nullptr ? nullptr : a.shares + t0 * a.top;
     p.experts = a.experts;

@@ -331,17 +331,20 @@ struct MoeParams {
   const float* logits;
   const void* x;
   void* out;
-  uint16_t* h;
+  uint16_t* h;        // halves of act(gate) * up, tokens * top rows of `hidden`, `parts` times
+  float* h_scale;     // of each 32 of a row
   int32_t* ids;
   float* shares;
   long long logits_stride;
-  long long h_plane;  // elements between h's bfloat16 parts
+  long long h_plane;  // elements between h's parts
   int parts;
   int tokens, experts, top, dim, hidden;
   int renorm, act, out_bf16;
   float scale;
   int ks;                // warps that share a tile's columns (moe_up)
-  int off_red, off_ring; // places in shared memory
+  int cached;            // chunks of the warps' columns that shared memory keeps (moe_up)
+  int ring;              // stages of a warp's ring, 2 to 4
+  int off_zero, off_red, off_cols, off_ring;  // places in shared memory
 };
 constexpr int64_t kMoeMaxDim = 1 << 24;
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16);

@@ -152,6 +152,7 @@ struct Shared {
   Draw rank_draw;
   int rank_id;
   // what rank 0 or every rank found
+  uint32_t reaching;  // rank 0's: chunks whose maxima reach min-p's value
   float reach;  // what the chunks' maxima tell: every kept logit reaches it (NaN: they do not tell)
   int bucket;
   uint32_t above_count, in_count;
@@ -321,17 +322,61 @@ struct Border {
   int listed;  // > 0: the first `listed` of rank 0's sorted list are all that is kept
 };
 
+// A warp's logits x[0 .. N - 1] of ids id, id + 1 .. a lane that `takes` go to rank 0's list: one addition to its length for all.
+template <int N, typename F>
+__device__ __forceinline__ void list_keys(Shared* home, const float (&x)[N], int id, F takes) {
+  const int lane = threadIdx.x & 31;
+  uint32_t in[N], total = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    in[k] = __ballot_sync(0xffffffffu, takes(x[k], id + k));
+    total += __popc(in[k]);
+  }
+  if (total == 0) return;
+  uint32_t at = 0;
+  if (lane == 0) at = atomicAdd(&home->listed, total);
+  at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t mine = at + __popc(in[k] & ((1u << lane) - 1u));
+    if ((in[k] >> lane & 1u) && mine < (uint32_t)kList) home->list[mine] = key_of(x[k], (uint32_t)(id + k));
+    at += __popc(in[k]);
+  }
+}
+
 // Keys of lo .. hi go to rank 0's list, in no order.  Returns how many there are (the list holds the first kList).
 __device__ uint32_t collect(cg::cluster_group& cl, const Row& r, Shared& sh, Shared* home, Key lo, Key hi) {
   const uint32_t least = (uint32_t)(lo >> 32);
-  for_each(r, sh.chunk, least, [&](float x, int id, int) {
-    if (ordered(x) < least) return;
-    const Key k = key_of(x, (uint32_t)id);
-    if (k >= lo && k <= hi) {
-      const uint32_t at = atomicAdd(&home->listed, 1u);
-      if (at < (uint32_t)kList) home->list[at] = k;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
+  const int subs = (r.q1 - r.q0 + 31) / 32;
+  for (int s = wid; s < subs; s += 4 * kWarps) {
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int sub = s + i * kWarps, q = r.q0 + 32 * sub + lane;
+      v[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (q < r.q1 && sh.chunk[sub >> r.shift] >= least) v[i] = __ldg(xv + q);
     }
-  });
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = r.head + 4 * (r.q0 + 32 * (s + i * kWarps) + lane);
+      const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      list_keys<4>(home, x, id, [&](float y, int j) {
+        const Key k = key_of(y, (uint32_t)j);
+        return y > -INFINITY && k >= lo && k <= hi;
+      });
+    }
+  }
+  if (r.ends && wid == 0) {
+    const int tail = r.n - r.head - 4 * r.quads;
+    const int id = lane < r.head ? lane : lane - r.head + r.n - tail;
+    const float x[1] = {lane < r.head + tail ? __ldg(r.x + id) : -INFINITY};
+    list_keys<1>(home, x, id, [&](float y, int j) {
+      const Key k = key_of(y, (uint32_t)j);
+      return y > -INFINITY && k >= lo && k <= hi;
+    });
+  }
   cl.sync();
   return home->listed;
 }
@@ -550,25 +595,34 @@ __device__ __forceinline__ int mapped(float v) {  // an integer that orders as t
 }
 
 // The draw over the chunks whose maximum reaches `least`: kind(x, id) is 1 for a logit that takes part, 2 for one that goes to rank 0's
-// list, else 0.  Leaves each chunk's best score; returns the thread's.
+// list (where the pass `collects`), else 0.  Leaves each chunk's best score; returns the thread's.
 template <typename K, typename S>
-__device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* home, uint32_t least, K kind, S score) {
+__device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* home, uint32_t least, bool collects, K kind, S score) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
   const bool wide = ((reinterpret_cast<uintptr_t>(r.e + r.head)) & 15) == 0;
   const int subs = (r.q1 - r.q0 + 31) / 32;
   int* best = reinterpret_cast<int*>(sh.best());
   float most = -INFINITY;
-  constexpr int B = 2;
+  constexpr int B = 3;
   for (int s = wid; s < subs; s += B * kWarps) {
     float v[4 * B], e[4 * B];
     int part[B];  // two bits a logit
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       const int sub = s + i * kWarps, q = r.q0 + 32 * sub + lane;
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (q < r.q1 && sh.chunk[sub >> r.shift] >= least) f = __ldg(xv + q);
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), u = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q < r.q1 && sh.chunk[sub >> r.shift] >= least) {
+        // the random numbers at once: they come from memory, and chunks that get here hold kept logits
+        const int id = r.head + 4 * q;
+        f = __ldg(xv + q);
+        if (wide)
+          u = __ldg(reinterpret_cast<const float4*>(r.e + id));
+        else
+          u = make_float4(__ldg(r.e + id), __ldg(r.e + id + 1), __ldg(r.e + id + 2), __ldg(r.e + id + 3));
+      }
       v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+      e[4 * i] = u.x, e[4 * i + 1] = u.y, e[4 * i + 2] = u.z, e[4 * i + 3] = u.w;
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -577,14 +631,6 @@ __device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* hom
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (v[4 * i + k] > -INFINITY) part[i] |= kind(v[4 * i + k], id + k) << (2 * k);
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((part[i] & 0x55) != 0) {
-        if (wide)
-          f = __ldg(reinterpret_cast<const float4*>(r.e + id));
-        else
-          f = make_float4(__ldg(r.e + id), __ldg(r.e + id + 1), __ldg(r.e + id + 2), __ldg(r.e + id + 3));
-      }
-      e[4 * i] = f.x, e[4 * i + 1] = f.y, e[4 * i + 2] = f.z, e[4 * i + 3] = f.w;
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -594,10 +640,10 @@ __device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* hom
       for (int k = 0; k < 4; ++k) {
         const int what = part[i] >> (2 * k) & 3;
         if (what == 1) t = fmaxf(t, score(v[4 * i + k], e[4 * i + k]));
-        if (what == 2) {
-          const uint32_t at = atomicAdd(&home->listed, 1u);
-          if (at < (uint32_t)kList) home->list[at] = key_of(v[4 * i + k], (uint32_t)(id + k));
-        }
+      }
+      if (collects) {
+        const float x[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        list_keys<4>(home, x, id, [&](float, int j) { return (part[i] >> (2 * (j - id)) & 3) == 2; });
       }
       t = unordered(__reduce_max_sync(0xffffffffu, ordered(t)));
       most = fmaxf(most, t);
@@ -855,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // (rank 0's, for the chunks' maxima: cleared before the ranks meet over the row's maximum)
   clear(sh);
-  if (threadIdx.x == 0) sh.listed = 0u;
+  if (threadIdx.x == 0) sh.listed = sh.reaching = 0u;
   // ---- the row's maximum, its chunks' maxima, and the sum of the weights where top-p stands alone
   const bool sum_first = !greedy && by_p && !by_k;
   float own_max = -INFINITY, own_sum = 0.f;
@@ -872,12 +918,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto kept_by_m = [&](float x) { return !by_m || x == r.max || weight_of(below(r, x)) >= min_p; };
   auto score = [&](float x, float e) { return e > 0.f ? (x - r.max) * r.scale - log2_of(e) : -INFINITY; };
 
+  // a value that all logits of min-p's weight reach (a little low: what is kept is asked of each)
+  float reach_m = -INFINITY;
+  if (by_m) {
+    const float edge = -log2_of(fminf(min_p, 1.f)) / r.scale;
+    reach_m = r.max - edge * (1.f + 0x1p-18f) - 0x1p-20f * fabsf(r.max);
+  }
+  const uint32_t least = reach_m > -INFINITY ? ordered(reach_m) : kMasked + 1;
+
   // ---- the borders of top-k and top-p
   Border border{0, 0, 0};
   int bucket = -1;  // the draw's pass takes the logits above this bucket and collects it
   double want = 0.0;
   uint32_t first = 0;
-  if (by_k || by_p) {
+  if (by_k || by_p || reach_m > -INFINITY) {
     // what the chunks' maxima tell: a value that k logits, or logits of top_p of the weight, reach.  Rank 0's buckets take
     // all ranks' maxima.
     if (sum_first) {
@@ -887,15 +941,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       block_scan(sh, none, sum, all_c, all);
       if (threadIdx.x == 0) sh.rank_sum = all;
     }
+    uint32_t reaching = 0;
     for (int c = threadIdx.x; c < r.chunks + r.ends; c += kThreads) {
       const uint32_t o = sh.chunk[c];
       if (o > kMasked) {
         const float t = below(r, unordered(o));
-        add(*home, bucket_of(t), mass_of(t));
+        if (by_k || by_p) add(*home, bucket_of(t), mass_of(t));
+        reaching += o >= least;
       }
     }
+    if (by_m) {
+      reaching = __reduce_add_sync(0xffffffffu, reaching);
+      if (lane == 0) atomicAdd(&home->reaching, reaching);
+    }
     cl.sync();
-    if (rank == 0) {
+    if (rank == 0 && (by_k || by_p)) {
       uint32_t c[2];
       Key m[2], sum = 0;
       gather(cl, sh, 1, c, m);
@@ -917,19 +977,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (threadIdx.x == 0)
         sh.reach = found && sh.bucket < kBuckets - 1 ? r.max - edge * (1.f + 0x1p-18f) - 0x1p-20f * fabsf(r.max) : NAN;
     }
-    cl.sync();
-    const float reach = home->reach;
-    bool fast = reach > -INFINITY;  // (not NaN)
+    if (by_k || by_p) cl.sync();
+    // the list from the higher of both values: top-p's sums are over what lies above, so what min-p cuts off below does not matter
+    // (with top-k they need all of the k: its own value)
+    const float reach_kp = by_k || by_p ? home->reach : -INFINITY;
+    const float reach = by_k && (reach_kp > -INFINITY || by_p) ? reach_kp : fmaxf(reach_kp, reach_m);  // (fmaxf passes over NaN)
+    const float share = (float)home->reaching / ((float)(r.quads >> (5 + r.shift)) + 1.f);
+    // (where most chunks reach min-p's value the list would not hold the logits that do)
+    bool fast = reach > -INFINITY && !(reach == reach_m && !by_k && share > 0.6f);
     if (fast) {
       const uint32_t listed = collect(cl, r, sh, home, (Key)ordered(reach) << 32, ~(Key)0);
-      fast = listed <= (uint32_t)kList && (!by_k || listed >= (uint32_t)k);
+      fast = listed <= (uint32_t)kList && (!by_k || listed >= (uint32_t)k || (!by_p && reach == reach_m));
     }
     if (fast) {
       if (rank != 0) {  // the rest is rank 0's list
         cl.sync();
         return;
       }
-      cut_list(r, sh, home->listed, by_k ? (uint32_t)k : 0u, 0, by_k ? INFINITY : want, by_k ? top_p : 1.f, false);
+      cut_list(r, sh, home->listed, by_k ? (uint32_t)k : 0u, 0, by_k || !by_p ? INFINITY : want, by_k ? top_p : 1.f, false);
       __syncthreads();
       const int kept = max(sh.kept, 1);
       auto listed = [&](float, auto f) {
@@ -949,7 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (ranks > 1) cl.sync();  // (the others have read this CTA's shared memory by now)
       return;
     }
-    // the buckets of all logits
+    // the buckets of all logits (min-p alone: the pass below)
+    if (by_k || by_p) {
     const bool both = by_k && by_p;
     cl.sync();
     clear(sh);
@@ -988,15 +1054,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       find_border(sh, c, m, 0, 0, first, want);
       bucket = sh.bucket;
     }
+    }
   }
 
-  // ---- the draw's pass, over the chunks that hold logits of min-p's weight
-  uint32_t least = kMasked + 1;
-  if (by_m) {
-    const float edge = -log2_of(fminf(min_p, 1.f)) / r.scale;
-    const float reach = r.max - edge * (1.f + 0x1p-18f) - 0x1p-20f * fabsf(r.max);
-    if (reach > -INFINITY) least = max(least, ordered(reach));
-  }
+  // ---- the draw's pass
   cl.sync();  // the buckets have been read
   if (r.shift > 0)
     for (int i = threadIdx.x; i <= r.chunks; i += kThreads) reinterpret_cast<int*>(sh.best())[i] = INT32_MIN;
@@ -1010,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int b = bucket_of(below(r, x));
       return b < bucket ? (int)kept_by_m(x) : b == bucket ? 2 : 0;
     };
-    most = draw_pass(r, sh, home, kMasked + 1, kind, score);  // (the bucket is collected whole, whatever min-p keeps)
+    most = draw_pass(r, sh, home, kMasked + 1, true, kind, score);  // (the bucket is collected whole, whatever min-p keeps)
     cl.sync();
     const uint32_t n = home->listed;
     if (n <= (uint32_t)kList) {
@@ -1062,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cl.sync();
   }
   auto kind = [&](float x, int id) { return (int)(key_of(x, (uint32_t)id) >= border.key && kept_by_m(x)); };
-  most = draw_pass(r, sh, home, max(least, (uint32_t)(border.key >> 32)), kind, score);
+  most = draw_pass(r, sh, home, max(least, (uint32_t)(border.key >> 32)), false, kind, score);
   most = unordered(over_ranks(ordered(most)));
   if (most > -INFINITY) {
     auto visit = [&](float least, auto f) {

@@ -767,9 +767,10 @@ size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dt
  * An expert of logit -infinity is not used (where that leaves fewer than top, ids of -1 with p 0; a token without
  * experts gives zeros).  A token whose logits hold NaN or +infinity gives NaN, and ids of -1.
  * The sums are float32 in an order that follows from the sizes and the routing alone: results do not depend on
- * timing, the last bits of a token may depend on the other tokens of its block of 64.  Levels are exact; x enters as it is
- * (float32 in three bfloat16 parts, 24 bits), act(gate) * up in three bfloat16 parts for float32 outputs and in two (16 bits) for
- * bfloat16 ones.  Activations and act(gate) * up are meant to be below 3.38e38.
+ * timing, the last bits of a token may depend on the other tokens of its block of 64.  Levels enter the tensor core as exact
+ * halves, an activation as a half after the power of two that brings the largest of its 32 columns into [2^14, 2^15) (bfloat16 values are
+ * exact down to 2^-31 of that largest; float32 ones two halves, 22 bits), act(gate) * up likewise: two halves (22 bits) for float32
+ * outputs, one (2^-11 relative) for bfloat16 ones; values below 2^-28 of their block's largest are multiples of 2^-39 of it.
  * Tokens go in blocks of 64, each of two launches that read every used expert's weights: for prompts of many tokens
  * the weights' bytes are read once a block.
  * tokens 0 launches nothing.  Returns QMV_OK, QMV_E_FORMAT (types, act), QMV_E_ARG (null pointer, tokens < 0, scale not finite), QMV_E_SHAPE

@@ -45,7 +45,7 @@ def _x(rng, tokens, dim, bf16, amp=1.0):
 
 def _check(layer, got, x, logits, top, renorm, scale, act, bf16_out):
     y, ids, shares = got
-    want, bound, wi, ws, rel = step_ref.moe(layer.w1, layer.w3, layer.w2, x, logits, top, renorm, scale, act, 2 if bf16_out else 3)
+    want, bound, wi, ws, rel = step_ref.moe(layer.w1, layer.w3, layer.w2, x, logits, top, renorm, scale, act, 1 if bf16_out else 2)
     assert np.array_equal(ids.cpu().numpy(), wi)
     s = shares.cpu().numpy().astype(np.float64)
     assert np.array_equal(np.isnan(s), np.isnan(ws)) and np.all((np.abs(s - ws) <= rel * ws + 1e-38) | np.isnan(ws))

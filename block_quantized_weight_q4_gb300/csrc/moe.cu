@@ -22,6 +22,7 @@
 // float32 outputs) are two halves, 22 bits; h for bfloat16 outputs one, 2^-11 relative.
 #include <cooperative_groups.h>
 
+#include <cstddef>
 #include <mutex>
 
 #include "qmv_common.cuh"
@@ -33,25 +34,25 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kMaxWarps = 16;
 constexpr int kTokens = 64;    // of a launch
 constexpr int kExperts = QMV_MOE_MAX_EXPERTS;
 constexpr int kTop = QMV_MOE_MAX_TOP;
 constexpr int kVectors = 4;    // of a unit: two to an MMA
-constexpr int kUnits = kExperts + kTokens * kTop / 2;  // experts, and one more for each 2 tokens or more
+constexpr int kUnits = kTokens * kTop;  // at most one a token and expert
 constexpr int kRowsStage = 32;
 
 // ------------------------------------------------------------------------------------------ routing
 struct Routing {
   unsigned long long mask[kExperts];  // tokens of an expert
   unsigned long long bad;             // tokens whose logits hold NaN or +infinity
-  float share[kTokens * kTop];
   uint16_t sel[kTokens * kTop];       // experts of a token, 0xffff: none
   uint16_t unit[kUnits];              // expert | pass << 8
   int units;
-  int part[kWarps];
+  int part[kMaxWarps];
+  float share[kTokens * kTop];  // moe_down's alone (moe_up's shared memory ends before it)
 };
+constexpr size_t kRoutingUp = offsetof(Routing, share);
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -61,13 +62,14 @@ __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// unit_cols: tokens of a unit
+// W: the CTA's warps (8 or more: a thread for each expert); unit_cols: tokens of a unit
+template <int W, bool SHARES>
 __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < kExperts; e += kThreads) r.mask[e] = 0;
+  for (int e = threadIdx.x; e < kExperts; e += 32 * W) r.mask[e] = 0;
   if (threadIdx.x == 0) r.bad = 0;
   __syncthreads();
-  for (int tok = wid; tok < p.tokens; tok += kWarps) {
+  for (int tok = wid; tok < p.tokens; tok += W) {
     uint32_t key[kExperts / 32];
     float most = -INFINITY;
     bool bad = false;
@@ -86,7 +88,7 @@ __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     bad = __any_sync(0xffffffffu, bad);
     float sum = 0.f;
-    if (!p.renorm) {
+    if (SHARES && !p.renorm) {
 #pragma unroll
       for (int i = 0; i < kExperts / 32; ++i)
         if (key[i] != 0) sum += expf(unordered(key[i]) - most);
@@ -104,9 +106,11 @@ __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
       int e = 0xffff;
       if (high != 0) {
         e = (int)__reduce_min_sync(0xffffffffu, best == high ? (unsigned)at : 0xffffu);
-        const float w = expf(unordered(high) - most);
-        if (lane == k) mine = w;
-        if (p.renorm) sum += w;
+        if (SHARES) {
+          const float w = expf(unordered(high) - most);
+          if (lane == k) mine = w;
+          if (p.renorm) sum += w;
+        }
 #pragma unroll
         for (int i = 0; i < kExperts / 32; ++i)
           if (e == lane + 32 * i) key[i] = 0;
@@ -115,7 +119,7 @@ __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
       if (lane == 0) r.sel[tok * p.top + k] = (uint16_t)e;
     }
     if (bad && lane == 0) atomicOr(&r.bad, 1ull << tok);
-    if (lane < p.top) r.share[tok * p.top + lane] = bad ? NAN : mine == 0.f ? 0.f : __fdiv_rn(mine, sum);
+    if (SHARES && lane < p.top) r.share[tok * p.top + lane] = bad ? NAN : mine == 0.f ? 0.f : __fdiv_rn(mine, sum);
   }
   __syncthreads();
   // units: experts in rising order, each with ceil(tokens / unit_cols) passes
@@ -129,7 +133,7 @@ __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
   if (lane == 31) r.part[wid] = upto;
   __syncthreads();
   int all = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w == wid) upto += all;
     all += r.part[w];
   }
@@ -138,11 +142,10 @@ __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
   __syncthreads();
 }
 
-// A unit as a warp holds it: lane n < cols has column n's token, its row of h (token * top + place) and its share.
+// A unit as a warp holds it: lane n < cols has token n of it and that token's row of h (token * top + place).
 struct Unit {
   int expert, cols;
   int tok, slot;
-  float share;
 };
 __device__ __forceinline__ Unit unit_of(const Routing& r, const MoeParams& p, int u, int unit_cols) {
   const int lane = threadIdx.x & 31;
@@ -152,13 +155,11 @@ __device__ __forceinline__ Unit unit_of(const Routing& r, const MoeParams& p, in
   unsigned long long m = r.mask[c.expert];
   c.cols = min(__popcll(m) - unit_cols * pass, unit_cols);
   c.tok = c.slot = 0;
-  c.share = 0.f;
   if (lane < c.cols) {
     for (int i = 0; i < unit_cols * pass + lane; ++i) m &= m - 1;
     c.tok = __ffsll((long long)m) - 1;
     c.slot = c.tok * p.top;
     while (r.sel[c.slot] != c.expert) ++c.slot;  // (it is there: the mask says so)
-    c.share = r.share[c.slot];
   }
   return c;
 }
@@ -188,52 +189,64 @@ struct Stage {
   static constexpr int kQ = kRowsStage * 128;
   static constexpr int kScaleRow = kBlocks * (F16 ? 2 : 4);
   static constexpr int kBytes = kQ + kRowsStage * kScaleRow;
-  // a vector's chunk: its blocks' halves, 64 of 80 bytes a block, and 64 bytes between vectors: the 8 lanes that read a set's two
-  // vectors lie in different banks.  Then the blocks' scales.
+  // a vector's chunk: its blocks' halves, 64 of 80 bytes a block, so that the lanes that read four blocks lie in different banks.
+  // Then the blocks' scales.
   static constexpr int kBlock = 80;
-  static constexpr int kVector = kBlocks * kBlock + (WT == QMV_Q4_0 ? 64 : 0);
-  static_assert(kVector % 128 == 64, "the second vector's banks");
+  static constexpr int kVector = kBlocks * kBlock;
   static __host__ __device__ constexpr int columns(int vectors) { return vectors * (kVector + kBlocks * 4); }
 };
 
-// Rows row_a .. row_a + 15 of one matrix image and row_b .. row_b + 15 of another (or of the same), chunk c of `cols` columns.
+// Where a lane reads a stage's rows: 16 rows of one matrix image and 16 of another (or of the same, at another place).  Moving to
+// another chunk or 16 rows further is an offset to all of them.
 template <int WT, bool F16>
-__device__ __forceinline__ void load_weights(uint32_t stage, const uint8_t* qa, const uint8_t* da, const uint8_t* qb, const uint8_t* db,
-                                             long long row_a, long long row_b, int c, int cols) {
+struct Rows {
   using S = Stage<WT, F16>;
-  const int lane = threadIdx.x & 31;
-  const long long row_bytes = WT == QMV_Q4_0 ? cols / 2 : cols;
-  const int piece = lane & 7;
-  const bool live = c * 128 + piece * 16 < row_bytes;
-  const long long off = live ? (long long)c * 128 + piece * 16 : 0;
-#pragma unroll
-  for (int i = 0; i < kRowsStage / 4; ++i) {
-    const int row = i * 4 + (lane >> 3);
-    const uint8_t* src = row < 16 ? qa + (row_a + row) * row_bytes : qb + (row_b + row - 16) * row_bytes;
-    copy_async<16>(stage + row * 128 + ((piece ^ ((row & 1) * S::kTurn)) << 4), src + off, live);
+  const uint8_t *qa, *qb;  // this lane's piece of rows (lane / 8) of both
+  const uint8_t *da, *db;  // the scales of the rows' first blocks: of row lane % 16 (whole chunks), else of row 0
+  __device__ __forceinline__ void set(const uint8_t* q_a, const uint8_t* d_a, const uint8_t* q_b, const uint8_t* d_b, long long row_a,
+                                      long long row_b, int cols) {
+    const int lane = threadIdx.x & 31;
+    const long long row_bytes = WT == QMV_Q4_0 ? cols / 2 : cols, scale_bytes = cols / 32 * (F16 ? 2 : 4);
+    qa = q_a + (row_a + (lane >> 3)) * row_bytes + (lane & 7) * 16;
+    qb = q_b + (row_b + (lane >> 3)) * row_bytes + (lane & 7) * 16;
+    const int row = cols % S::kChunk == 0 ? lane & 15 : 0;
+    da = d_a + (row_a + row) * scale_bytes;
+    db = d_b + (row_b + row) * scale_bytes;
   }
-  // scales
-  constexpr int kSize = F16 ? 2 : 4;
-  const long long scale_bytes = cols / 32 * kSize;  // of a row
-  const uint32_t sd = stage + S::kQ;
-  if (cols % S::kChunk == 0) {
-    const uint8_t* src = (lane < 16 ? da + (row_a + lane) * scale_bytes : db + (row_b + lane - 16) * scale_bytes) + c * S::kScaleRow;
-    constexpr int kPiece = S::kScaleRow < 16 ? S::kScaleRow : 16;
+  // Chunk c of the rows `down` rows further.
+  __device__ __forceinline__ void load(uint32_t stage, int c, int down, int cols) const {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const int row_bytes = WT == QMV_Q4_0 ? cols / 2 : cols, scale_bytes = cols / 32 * (F16 ? 2 : 4);
+    const bool live = c * 128 + piece * 16 < row_bytes;
+    const long long off = (long long)down * row_bytes + (live ? c * 128 : -piece * 16);  // (a piece past the row: its first bytes, not copied)
+    const uint8_t *a = qa + off, *b = qb + off;
+    const uint32_t to = stage + (lane >> 3) * 128 + ((piece ^ (((lane >> 3) & 1) * S::kTurn)) << 4);  // (rows 4 apart are both even or odd)
 #pragma unroll
-    for (int i = 0; i < S::kScaleRow / kPiece; ++i)
-      copy_async<kPiece>(sd + lane * S::kScaleRow + kPiece * i, src + kPiece * i, true);
-  } else {  // rows on 4-byte boundaries (columns are a multiple of 64)
-    constexpr int kWords = S::kScaleRow / 4;
+    for (int i = 0; i < 4; ++i) {
+      copy_async<16>(to + i * 512, a, live);
+      copy_async<16>(to + i * 512 + 2048, b, live);
+      a += 4 * row_bytes;
+      b += 4 * row_bytes;
+    }
+    const uint32_t sd = stage + S::kQ;
+    const long long s_off = (long long)down * scale_bytes + c * S::kScaleRow;
+    if (cols % S::kChunk == 0) {
+      const uint8_t* src = (lane < 16 ? da : db) + s_off;
+      constexpr int kPiece = S::kScaleRow < 16 ? S::kScaleRow : 16;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int at = lane + 32 * i, row = at / kWords, word = at % kWords;
-      const bool there = c * S::kScaleRow + 4 * word < scale_bytes;
-      const uint8_t* src = (row < 16 ? da + (row_a + row) * scale_bytes : db + (row_b + row - 16) * scale_bytes) +
-                           (there ? c * S::kScaleRow + 4 * word : 0);
-      copy_async<4>(sd + row * S::kScaleRow + 4 * word, src, there);
+      for (int i = 0; i < S::kScaleRow / kPiece; ++i) copy_async<kPiece>(sd + lane * S::kScaleRow + kPiece * i, src + kPiece * i, true);
+    } else {  // rows on 4-byte boundaries (columns are a multiple of 64)
+      constexpr int kWords = S::kScaleRow / 4;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int at = lane + 32 * i, row = at / kWords, word = at % kWords;
+        const bool there = c * S::kScaleRow + 4 * word < scale_bytes;
+        const uint8_t* src = (row < 16 ? da : db) + (long long)(row & 15) * scale_bytes + s_off + 4 * word;
+        copy_async<4>(sd + row * S::kScaleRow + 4 * word, there ? src : (row < 16 ? da : db), there);
+      }
     }
   }
-}
+};
 
 // The power of two that brings amax into [2^14, 2^15), and its inverse (1 for amax 0, below 2^-112 or not finite).
 // Eight values of a block of 32 that four neighbouring lanes hold, as halves at that scale: hi, and with LO what hi leaves (11 more bits).
@@ -262,8 +275,8 @@ __device__ __forceinline__ float to_halves(const float (&v)[8], uint32_t (&hi)[4
 // One stage's products: acc[m][set] += what row tile m (rows g and g + 8 of it) gives for this lane's two blocks and vector.
 // b: this lane's column (its vector and block of the first four blocks), moving by `step` from set to set and by `group` from four blocks to
 // the next (both 0 at zeros, for lanes without a column); xs: the vector's scales of the lane's two blocks.
-template <int WT, bool F16>
-__device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t step, uint32_t group, uint32_t xs, uint32_t xs_step, int sets,
+template <int WT, bool F16, int SETS>
+__device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t step, uint32_t group, uint32_t xs, uint32_t xs_step,
                                         float (&acc)[2][2][2]) {
   using S = Stage<WT, F16>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -272,11 +285,11 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
   const uint32_t turn = (g & 1) * S::kTurn;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    float c[2][2][4];
+    float c[2][SETS][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) c[m][v][0] = c[m][v][1] = c[m][v][2] = c[m][v][3] = 0.f;
+      for (int v = 0; v < SETS; ++v) c[m][v][0] = c[m][v][1] = c[m][v][2] = c[m][v][3] = 0.f;
     uint32_t q[2][2][4 * kPieces];  // [tile][row g, g + 8][word]
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -292,10 +305,9 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
     // eight elements of a block at a time: one load of B (two for Q4_0, whose words hold elements 16 apart)
 #pragma unroll
     for (int j = 0; j < 2 * kPieces; ++j) {
-      uint32_t x[2][2][4];  // [set][first, elements 16 further][halves]
+      uint32_t x[SETS][2][4];  // [set][first, elements 16 further][halves]
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        if (v < sets) {
+      for (int v = 0; v < SETS; ++v) {
           lds_u32x4(b + v * step + i * group + j * 16, x[v][0]);
           if (WT == QMV_Q4_0) lds_u32x4(b + v * step + i * group + 32 + j * 16, x[v][1]);
         }
@@ -309,8 +321,7 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
             q4_word_to_f16_levels(wg, g01, g23, gh01, gh23);
             q4_word_to_f16_levels(wh, h01, h23, hh01, hh23);
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
-              if (v < sets) {
+            for (int v = 0; v < SETS; ++v) {
                 mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
                 mma_f16_16816(c[m][v], gh01, hh01, gh23, hh23, x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
               }
@@ -319,16 +330,14 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
             q8_word_to_f16_levels(wg, g01, g23);
             q8_word_to_f16_levels(wh, h01, h23);
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
-              if (v < sets) mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
+            for (int v = 0; v < SETS; ++v) mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
           }
         }
     }
     // columns 2 t and 2 t + 1: vector t / 2 of the set, blocks 2 (t & 1) and the next
-    float xd[2][2];
+    float xd[SETS][2];
 #pragma unroll
-    for (int v = 0; v < 2; ++v)
-      if (v < sets) {
+    for (int v = 0; v < SETS; ++v) {
         uint32_t u0, u1;
         lds_u32x2(xs + v * xs_step + i * 16, u0, u1);
         xd[v][0] = __uint_as_float(u0), xd[v][1] = __uint_as_float(u1);
@@ -350,8 +359,7 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
           d1 = __uint_as_float(u1);
         }
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-          if (v < sets) acc[m][v][h] = fmaf(d0 * xd[v][0], c[m][v][2 * h], fmaf(d1 * xd[v][1], c[m][v][2 * h + 1], acc[m][v][h]));
+        for (int v = 0; v < SETS; ++v) acc[m][v][h] = fmaf(d0 * xd[v][0], c[m][v][2 * h], fmaf(d1 * xd[v][1], c[m][v][2 * h + 1], acc[m][v][h]));
       }
   }
 }
@@ -382,6 +390,15 @@ __device__ __forceinline__ Columns columns_of(uint32_t columns, uint32_t zeros, 
   c.xs = sv < max_vectors ? columns + max_vectors * S::kVector + sv * S::kBlocks * 4 + 2 * (t & 1) * 4 : zeros;
   c.xs_step = 2 + sv < max_vectors ? 2 * S::kBlocks * 4 : 0;  // (what is read for a vector that is not there goes nowhere)
   return c;
+}
+
+// A unit of one or two vectors, or of three or four.
+template <int WT, bool F16>
+__device__ __forceinline__ void consume_any(uint32_t stage, const Columns& c, int sets, float (&acc)[2][2][2]) {
+  if (sets == 1)
+    consume<WT, F16, 1>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
+  else
+    consume<WT, F16, 2>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
 }
 
 // ------------------------------------------------------------------------------------------ gate and up
@@ -427,54 +444,59 @@ __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, co
   }
 }
 
+constexpr int kUpWarps = 16, kUpThreads = kUpWarps * 32;
+
 template <int WT, bool F16, bool XF32>
-__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_constant__ MoeParams p) {
+__global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_constant__ MoeParams p) {
   using S = Stage<WT, F16>;
-  constexpr int kUnit = XF32 ? kVectors / 2 : kVectors;  // tokens of a unit
+  constexpr int kUnit = XF32 ? kVectors / 2 : kVectors;  // tokens of a unit at most
   extern __shared__ __align__(1024) uint8_t smem[];
   Routing& r = *reinterpret_cast<Routing*>(smem);
   float* red = reinterpret_cast<float*>(smem + p.off_red);  // a warp's gate and up: [token][gate, up][32 rows]
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int max_tokens = min(p.tokens, kUnit), max_vectors = XF32 ? 2 * max_tokens : max_tokens;
+  const int max_vectors = min(p.tokens, p.unit) * (XF32 ? 2 : 1);
   const uint32_t ring = smem_u32(smem + p.off_ring) + wid * p.ring * S::kBytes;
   const int cache_bytes = S::columns(max_vectors);
   uint8_t* cache = smem + p.off_cols + wid * p.cached * cache_bytes;  // the warp's columns, of p.cached chunks
   griddep_wait();
   griddep_launch_dependents();
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
-  route(r, p, kUnit);
+  route<kUpWarps, false>(r, p, p.unit);
   const uint32_t zeros = smem_u32(smem + p.off_zero);
 
   const int tiles = p.hidden / 32, chunks = (p.dim + S::kChunk - 1) / S::kChunk;
-  const int tiles_item = kWarps / p.ks;
-  const int items_unit = (tiles + tiles_item - 1) / tiles_item;
+  const int items_unit = (tiles + p.tiles_item - 1) / p.tiles_item;
   const int items = r.units * items_unit;
   // a run of items: mostly one unit's, so that its columns are converted once
   const int item0 = (int)((long long)items * blockIdx.x / gridDim.x), item1 = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
   const int slice = wid % p.ks, tile_local = wid / p.ks;
+  const bool works = tile_local < p.tiles_item;
   const int c0 = slice * chunks / p.ks, n = (slice + 1) * chunks / p.ks - c0;
 
   // the producer's place: chunk j of the warp's columns of an item, rows 16 m .. of its tile
   int pi = item0, pj = 0, pm = 0, ps = 0;
-  int p_tile = 0, p_expert = 0;
+  int p_unit = item0 / items_unit, p_first = item0 % items_unit * p.tiles_item;  // the item's unit and first tile
+  Rows<WT, F16> rows;
   auto settle = [&]() {  // on to an item in which the warp has rows
-    while (pi < item1) {
-      p_tile = pi % items_unit * tiles_item + tile_local;
-      if (p_tile < tiles) break;
+    while (pi < item1 && !(works && p_first + tile_local < tiles)) {
       ++pi;
+      if ((p_first += p.tiles_item) >= tiles) p_first = 0, ++p_unit;
     }
-    if (pi < item1) p_expert = r.unit[pi / items_unit] & 255;
+    if (pi < item1) {
+      const long long row = (long long)(r.unit[p_unit] & 255) * p.hidden + 32LL * (p_first + tile_local);
+      rows.set(p.q1, p.d1, p.q3, p.d3, row, row, p.dim);
+    }
   };
   settle();
   auto issue = [&]() {
     if (pi < item1) {
-      const long long row = (long long)p_expert * p.hidden + 32LL * p_tile + 16 * pm;
-      load_weights<WT, F16>(ring + ps * S::kBytes, p.q1, p.d1, p.q3, p.d3, row, row, c0 + pj, p.dim);
+      rows.load(ring + ps * S::kBytes, c0 + pj, 16 * pm, p.dim);
       ps = ps + 1 == p.ring ? 0 : ps + 1;
       pm ^= 1;
       if (pm == 0 && ++pj == n) {
         pj = 0;
         ++pi;
+        if ((p_first += p.tiles_item) >= tiles) p_first = 0, ++p_unit;
         settle();
       }
     }
@@ -482,69 +504,79 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   };
   for (int i = 0; i < p.ring - 1; ++i) issue();
 
-  int cs = 0, held = -1;  // held: the unit whose columns the cache has
+  int cs = 0, held = -1;  // held: the unit that u is, and whose columns the cache has
+  int unit = item0 / items_unit, first = item0 % items_unit * p.tiles_item;
+  Unit u{};
+  const Columns col0 = columns_of<S>(smem_u32(cache), zeros, max_vectors);
   for (int item = item0; item < item1; ++item) {
-    const int unit = item / items_unit, tile = item % items_unit * tiles_item + tile_local;
-    const Unit u = unit_of(r, p, unit, kUnit);
-    const int vectors = XF32 ? 2 * u.cols : u.cols, sets = (vectors + 1) / 2;
-    float acc[2][2][2][2] = {};  // [rows 16 m][W1, W3][set][row g, g + 8]
-    if (tile < tiles) {
-      if (held != unit && n <= p.cached) {
+    const int tile = first + tile_local;
+    if (held != unit) {
+      u = unit_of(r, p, unit, p.unit);
+      if (works && n <= p.cached) {
         __syncwarp();
         for (int j = 0; j < n; ++j) convert_columns<S, XF32>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
         __syncwarp();
-        held = unit;
       }
+      held = unit;
+    }
+    const int sets = XF32 ? u.cols : (u.cols + 1) / 2;
+    float acc[2][2][2][2] = {};  // [rows 16 m][W1, W3][set][row g, g + 8]
+    if (works && tile < tiles) {
       for (int j = 0; j < n; ++j) {
+        Columns c = col0;
         if (n > p.cached) {
           __syncwarp();
           convert_columns<S, XF32>(cache, max_vectors, p.x, u, c0 + j, p.dim);
+        } else {
+          c.b += c.b == zeros ? 0 : j * cache_bytes;
+          c.xs += c.xs == zeros ? 0 : j * cache_bytes;
         }
-        const Columns c = columns_of<S>(smem_u32(cache) + (n > p.cached ? 0 : j * cache_bytes), zeros, max_vectors);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           __syncwarp();  // every lane is done with the slot that is filled next
           issue();
           wait_ring(p.ring);
           __syncwarp();
-          consume<WT, F16>(ring + cs * S::kBytes, c.b, c.step, c.group, c.xs, c.xs_step, sets, acc[m]);
+          consume_any<WT, F16>(ring + cs * S::kBytes, c, sets, acc[m]);
           cs = cs + 1 == p.ring ? 0 : cs + 1;
         }
       }
     }
     // a vector's two lanes hold two blocks each; float32 tokens: hi and lo are the set's two vectors
-    float* my = red + wid * (kUnit * 64);
+    float* area = red + (item & 1) * (kUpWarps * kUnit * 64);  // (two, so that one barrier an item does)
+    float* my = area + wid * (kUnit * 64);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int v = 0; v < 2; ++v)
+      if (v < sets) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float a = acc[m][w][v][h];
-            a += __shfl_xor_sync(0xffffffffu, a, 1);
-            if (XF32) a += __shfl_xor_sync(0xffffffffu, a, 2);
-            const int tok = XF32 ? v : 2 * v + (t >> 1);
-            if (XF32 ? t == 0 : (t & 1) == 0) my[tok * 64 + w * 32 + 16 * m + 8 * h + g] = a;
-          }
+            for (int h = 0; h < 2; ++h) {
+              float a = acc[m][w][v][h];
+              a += __shfl_xor_sync(0xffffffffu, a, 1);
+              if (XF32) a += __shfl_xor_sync(0xffffffffu, a, 2);
+              const int tok = XF32 ? v : 2 * v + (t >> 1);
+              if (XF32 ? t == 0 : (t & 1) == 0) my[tok * 64 + w * 32 + 16 * m + 8 * h + g] = a;
+            }
+      }
     __syncthreads();
-    for (int i = wid; i < tiles_item * u.cols; i += kWarps) {
-      const int tl = i / u.cols, col = i % u.cols;
-      const int ht = item % items_unit * tiles_item + tl;
+    // the item's tiles and tokens over the warps, another one first each time
+    for (int i = (wid + item * 5) % kUpWarps; i < p.tiles_item * u.cols; i += kUpWarps) {
+      const int tl = i / u.cols, col = i % u.cols, ht = first + tl;
       const int slot = __shfl_sync(0xffffffffu, u.slot, col);
       if (ht < tiles) {
+        const float* part = area + tl * p.ks * (kUnit * 64) + col * 64 + lane;
         float gate = 0.f, up = 0.f;
+#pragma unroll 4
         for (int k = 0; k < p.ks; ++k) {
-          const float* part = red + (tl * p.ks + k) * (kUnit * 64) + col * 64;
-          gate += part[lane];
-          up += part[32 + lane];
+          gate += part[k * (kUnit * 64)];
+          up += part[k * (kUnit * 64) + 32];
         }
         // the tile's 32 rows are a block of W2's columns: halves at a power of two of the block's own
         const float h = glu(p.act, gate, up);
-        float amax = fabsf(h);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(isnan(h) ? 0.f : fabsf(h))));
         float to, down;
         half_stage_scale(amax, to, down);
         const float v = h * to;
@@ -555,13 +587,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         if (lane == 0) p.h_scale[(long long)slot * (p.hidden / 32) + ht] = down;
       }
     }
-    __syncthreads();
+    if ((first += p.tiles_item) >= tiles) first = 0, ++unit;
   }
 }
 
 // ------------------------------------------------------------------------------------------ down
+constexpr int kDownWarps = 8, kDownThreads = kDownWarps * 32;
+
 template <int WT, bool F16, int PARTS>
-__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_constant__ MoeParams p, int ranks) {
+__global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_constant__ MoeParams p, int ranks) {
   using S = Stage<WT, F16>;
   constexpr int kUnit = kVectors / PARTS;  // tokens of a unit
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -577,44 +611,54 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   const int row0 = (int)(blockIdx.x / ranks) * kRowsStage;
   // launched by moe_up after its own wait: what came before that, the logits and the weights among it, is complete
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
-  route(r, p, kUnit);
+  route<kDownWarps, true>(r, p, kUnit);
   float* my = tiles + wid * kRowsStage * p.tokens;
   for (int i = lane; i < kRowsStage * p.tokens; i += 32) my[i] = 0.f;
   __syncwarp();
 
   const int chunks = (p.hidden + S::kChunk - 1) / S::kChunk;
-  const int total = r.units * chunks, warps = ranks * kWarps, me = rank * kWarps + wid;
+  const int total = r.units * chunks, warps = ranks * kDownWarps, me = rank * kDownWarps + wid;
   const int s0 = (int)((long long)total * me / warps), s1 = (int)((long long)total * (me + 1) / warps);
   int ps = s0, ps_c = s0 % chunks, ps_u = s0 / chunks, slot_p = 0;
   Unit pu{};
-  if (s0 < s1) pu = unit_of(r, p, ps_u, kUnit);
-  auto weights = [&](int at) {
+  Rows<WT, F16> rows;
+  uint32_t h_at = 0;  // lane v: vector v's row of h, in 64 halves
+  auto next_unit = [&]() {
+    pu = unit_of(r, p, ps_u, kUnit);
     const long long row = (long long)pu.expert * p.dim + row0;
-    load_weights<WT, F16>(ring + at * stage_bytes, p.q2, p.d2, p.q2, p.d2, row, row + 16, ps_c, p.hidden);
+    rows.set(p.q2, p.d2, p.q2, p.d2, row, row + 16, p.hidden);
+    const int slot = __shfl_sync(0xffffffffu, pu.slot, lane / PARTS);
+    h_at = (uint32_t)((lane % PARTS * p.h_plane + (long long)slot * p.hidden) / 64);
   };
+  if (s0 < s1) next_unit();
   // the vectors' halves and scales: a piece of 16 bytes a lane and vector
   auto columns = [&](int at) {
     const uint32_t to = ring + at * stage_bytes + S::kBytes;
-    constexpr int kPieces = S::kChunk / 8;  // of a vector
-    const int n = pu.cols * PARTS * kPieces;
-    for (int i = lane; i < (n + 31) / 32 * 32; i += 32) {
-      const int v = i / kPieces, piece = i % kPieces;
-      const long long slot = __shfl_sync(0xffffffffu, pu.slot, v / PARTS & 31);
-      if (i >= n) continue;
-      const int first = ps_c * S::kChunk + piece * 8;
-      const bool live = first < p.hidden;
-      copy_async<16>(to + v * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16,
-                     p.h + (v % PARTS) * p.h_plane + slot * p.hidden + (live ? first : 0), live);
+    constexpr int kPieces = S::kChunk / 8;       // of a vector
+    constexpr int kTogether = 32 / kPieces;      // vectors of one instruction
+    const int vectors = pu.cols * PARTS, piece = lane % kPieces;
+    const int first = ps_c * S::kChunk + piece * 8;
+    const bool live = first < p.hidden;
+#pragma unroll
+    for (int i = 0; i < kVectors; i += kTogether) {
+      if (i >= vectors) break;
+      const int v = i + lane / kPieces;
+      const uint32_t row = __shfl_sync(0xffffffffu, h_at, v);
+      const int slot = __shfl_sync(0xffffffffu, pu.slot, v / PARTS);
+      if (v >= vectors) continue;
+      copy_async<16>(to + v * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16, p.h + (long long)row * 64 + (live ? first : 0), live);
       if ((piece & 3) == 0)
-        copy_async<4>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 4, p.h_scale + slot * (p.hidden / 32) + (live ? first / 32 : 0), live);
+        copy_async<4>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 4, p.h_scale + (long long)slot * (p.hidden / 32) + (live ? first / 32 : 0), live);
     }
   };
+  auto weights = [&](int at) { rows.load(ring + at * stage_bytes, ps_c, 0, p.hidden); };
   auto advance = [&]() {
     ++ps;
     slot_p = slot_p + 1 == p.ring ? 0 : slot_p + 1;
     if (++ps_c == chunks) {
       ps_c = 0;
-      if (ps < s1) pu = unit_of(r, p, ++ps_u, kUnit);
+      ++ps_u;
+      if (ps < s1) next_unit();
     }
   };
   // the first stage's weights are asked for while moe_up ends
@@ -635,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     copies_commit();
   }
 
+  const Columns col0 = columns_of<S>(ring + S::kBytes, zeros, max_vectors);
   float acc[2][2][2] = {};  // [tile][set][row g, g + 8]
   int cs = 0, cc = s0 % chunks, cu = s0 / chunks;
   Unit u{};
@@ -644,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     for (int v = 0; v < 2; ++v) {
       const int col = PARTS == 2 ? v : 2 * v + (t >> 1);
       const int tok = __shfl_sync(0xffffffffu, u.tok, col);
-      const float share = __shfl_sync(0xffffffffu, u.share, col);
+      const float share = r.share[__shfl_sync(0xffffffffu, u.slot, col)];  // (lanes without a token: of the first, unused)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -668,8 +713,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     copies_commit();
     wait_ring(p.ring);
     __syncwarp();
-    const Columns c = columns_of<S>(ring + cs * stage_bytes + S::kBytes, zeros, max_vectors);
-    consume<WT, F16>(ring + cs * stage_bytes, c.b, c.step, c.group, c.xs, c.xs_step, (u.cols * PARTS + 1) / 2, acc);
+    Columns c = col0;
+    c.b += c.b == zeros ? 0 : cs * stage_bytes;
+    c.xs += c.xs == zeros ? 0 : cs * stage_bytes;
+    consume_any<WT, F16>(ring + cs * stage_bytes, c, (u.cols * PARTS + 1) / 2, acc);
     cs = cs + 1 == p.ring ? 0 : cs + 1;
     if (++cc == chunks) {
       flush();
@@ -681,17 +728,17 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   __syncthreads();
   // this CTA's tiles in warp order, then the cluster's in rank order, its CTAs sharing the sums
   const int values = kRowsStage * p.tokens;
-  for (int i = threadIdx.x; i < values; i += kThreads) {
+  for (int i = threadIdx.x; i < values; i += kDownThreads) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += tiles[w * values + i];
+    for (int w = 0; w < kDownWarps; ++w) sum += tiles[w * values + i];
     tiles[i] = sum;
   }
   if (ranks > 1)
     cl.sync();
   else
     __syncthreads();
-  for (int i = rank * kThreads + threadIdx.x; i < values; i += ranks * kThreads) {
+  for (int i = rank * kDownThreads + threadIdx.x; i < values; i += ranks * kDownThreads) {
     const int row = i % kRowsStage, tok = i / kRowsStage;
     float v[8], sum = 0.f;
 #pragma unroll
@@ -707,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
       static_cast<float*>(p.out)[at] = sum;
   }
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < p.tokens * p.top; i += kThreads) {
+    for (int i = threadIdx.x; i < p.tokens * p.top; i += kDownThreads) {
       if (p.ids != nullptr) p.ids[i] = r.sel[i] == 0xffff ? -1 : (int)r.sel[i];
       if (p.shares != nullptr) p.shares[i] = r.share[i];
     }
@@ -715,9 +762,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   if (ranks > 1) cl.sync();  // no CTA leaves while another reads its tiles
 }
 
-cudaError_t allow_smem(const void* kern, int device, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// A kernel's dynamic shared-memory limit raised to all that a CTA may have, once for each kernel and device.
+template <typename K>
+cudaError_t allow_smem(K kern, const DeviceInfo& dev, bool (&done)[64]) {
+  static std::mutex mu;
+  if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidValue;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev.device]) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dev.smem_optin);
+  done[dev.device] = err == cudaSuccess;
+  return err;
 }
 
 constexpr size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
@@ -732,38 +786,40 @@ size_t room(const DeviceInfo& dev, int n) {
 template <int WT, bool F16>
 cudaError_t launch_up(MoeParams p, bool x_f32, const DeviceInfo& dev, cudaStream_t stream) {
   using S = Stage<WT, F16>;
-  const int unit = x_f32 ? kVectors / 2 : kVectors, tokens = p.tokens < unit ? p.tokens : unit;
-  const int columns = S::columns(x_f32 ? 2 * tokens : tokens);
+  const int most = x_f32 ? kVectors / 2 : kVectors;
   const int chunks = (p.dim + S::kChunk - 1) / S::kChunk;
   p.ks = 1;
-  while (p.ks < kWarps && 2 * p.ks <= chunks) p.ks *= 2;
+  while (p.ks < kUpWarps && 2 * p.ks <= chunks) p.ks *= 2;
   const int slice = (chunks + p.ks - 1) / p.ks;
-  p.off_zero = (int)round_up(sizeof(Routing), 128);
+  p.off_zero = (int)round_up(kRoutingUp, 128);
   p.off_red = p.off_zero + 128;
-  p.off_cols = p.off_red + kWarps * unit * 64 * 4;
-  // the warps' columns are kept where they leave room for the rings; two CTAs a SM with rings of two stages before one with more
+  p.off_cols = p.off_red + 2 * kUpWarps * most * 64 * 4;
+  // the warps' columns are kept where they leave room for the rings; units of fewer tokens where they do not (Q4_0 with float32 scales)
   size_t smem = 0;
-  int per_sm = 2;
-  for (;; --per_sm) {
-    for (p.cached = slice; p.cached >= 1; p.cached = p.cached > 1 ? 1 : 0) {
-      p.off_ring = (int)round_up(p.off_cols + (size_t)kWarps * p.cached * columns, 128);
-      for (p.ring = per_sm == 2 ? 2 : 4; p.ring >= 2; --p.ring) {
-        smem = p.off_ring + (size_t)kWarps * p.ring * S::kBytes;
-        if (smem <= room(dev, per_sm)) break;
+  bool fits = false;
+  for (p.unit = most; p.unit >= 1 && !fits; p.unit -= fits ? 0 : 1) {
+    const int tokens = p.tokens < p.unit ? p.tokens : p.unit, columns = S::columns(x_f32 ? 2 * tokens : tokens);
+    for (int keep = 0; keep < 2 && !fits; ++keep) {
+      p.cached = keep == 0 ? slice : 1;
+      p.off_ring = (int)round_up(p.off_cols + (size_t)kUpWarps * p.cached * columns, 128);
+      for (p.ring = 4; p.ring >= 2 && !fits; p.ring -= fits ? 0 : 1) {
+        smem = p.off_ring + (size_t)kUpWarps * p.ring * S::kBytes;
+        fits = smem <= dev.smem_optin;
       }
-      if (p.ring >= 2) break;
     }
-    if (p.cached >= 1) break;
-    if (per_sm == 1) return cudaErrorInvalidValue;
+    if (fits) break;
   }
-  const int tiles_item = kWarps / p.ks;
-  const long long units = (p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) + p.tokens * p.top / unit;
-  const long long items = units * ((p.hidden / 32 + tiles_item - 1) / tiles_item);
-  const long long slots = (long long)dev.sm_count * per_sm;
+  if (!fits) return cudaErrorInvalidValue;
+  // an item: as many tiles as the warps take, or fewer where that would leave SMs without one
+  const long long units = (p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) + p.tokens * p.top / p.unit;
+  const int tiles = p.hidden / 32;
+  for (p.tiles_item = kUpWarps / p.ks; p.tiles_item > 1 && units * ((tiles + p.tiles_item - 1) / p.tiles_item) < dev.sm_count;) p.tiles_item /= 2;
+  const long long items = units * ((tiles + p.tiles_item - 1) / p.tiles_item);
   auto kern = x_f32 ? moe_up_kernel<WT, F16, true> : moe_up_kernel<WT, F16, false>;
-  const cudaError_t err = allow_smem((const void*)kern, dev.device, smem);
+  static bool done[2][64] = {};
+  const cudaError_t err = allow_smem(kern, dev, done[x_f32]);
   if (err != cudaSuccess) return err;
-  return launch_dependent(kern, dim3((unsigned)(items < slots ? items : slots)), kThreads, smem, stream, p);
+  return launch_dependent(kern, dim3((unsigned)(items < dev.sm_count ? items : dev.sm_count)), kUpThreads, smem, stream, p);
 }
 
 template <int WT, bool F16>
@@ -773,12 +829,12 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
   const int stage = S::kBytes + S::columns(vectors);
   p.off_zero = (int)round_up(sizeof(Routing), 128);
   p.off_red = p.off_zero + 128;
-  p.off_ring = (int)round_up(p.off_red + (size_t)kWarps * kRowsStage * p.tokens * 4, 128);
+  p.off_ring = (int)round_up(p.off_red + (size_t)kDownWarps * kRowsStage * p.tokens * 4, 128);
   size_t smem = 0;
   int per_sm = 2;
   for (; per_sm >= 1; --per_sm) {
     for (p.ring = per_sm == 2 ? 2 : 4; p.ring >= 2; --p.ring) {
-      smem = p.off_ring + (size_t)kWarps * p.ring * stage;
+      smem = p.off_ring + (size_t)kDownWarps * p.ring * stage;
       if (smem <= room(dev, per_sm)) break;
     }
     if (p.ring >= 2) break;
@@ -788,13 +844,14 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
   const int tiles = p.dim / kRowsStage, chunks = (p.hidden + S::kChunk - 1) / S::kChunk;
   const long long stages = (long long)(p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) * chunks;
   int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= per_sm * dev.sm_count && stages >= 2 * ranks * kWarps) ranks *= 2;
+  while (ranks < 8 && tiles * ranks * 2 <= per_sm * dev.sm_count && stages >= 2 * ranks * kDownWarps) ranks *= 2;
   auto kern = p.parts == 2 ? moe_down_kernel<WT, F16, 2> : moe_down_kernel<WT, F16, 1>;
-  const cudaError_t err = allow_smem((const void*)kern, dev.device, smem);
+  static bool done[2][64] = {};
+  const cudaError_t err = allow_smem(kern, dev, done[p.parts - 1]);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * ranks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kDownThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

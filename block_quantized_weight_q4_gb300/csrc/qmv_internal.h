@@ -341,6 +341,8 @@ struct MoeParams {
   int tokens, experts, top, dim, hidden;
   int renorm, act, out_bf16;
   float scale;
+  int unit;              // tokens of a unit at most (moe_up)
+  int tiles_item;        // tiles of 32 rows of an item (moe_up)
   int ks;                // warps that share a tile's columns (moe_up)
   int cached;            // chunks of the warps' columns that shared memory keeps (moe_up)
   int ring;              // stages of a warp's ring, 2 to 4

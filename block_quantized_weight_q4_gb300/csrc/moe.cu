@@ -17,9 +17,15 @@
 // MMA's k slots hold four different blocks; the columns are 2 vectors x those 4 blocks, and a lane's B values are
 // zero but for its own block's column.  After the 8 MMAs of four blocks a lane holds the dot products of two blocks for two
 // rows, scaled by the weights' and the activations' scales in float32: a quarter of the loads and scalings that
-// one block an MMA would take, and 2 vectors fill the 8 columns.  Levels are exact halves.  An activation is a half after the power of two
-// that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16 down to 2^-31 of the largest; float32 values (and h for
-// float32 outputs) are two halves, 22 bits; h for bfloat16 outputs one, 2^-11 relative.
+// one block an MMA would take, and 2 vectors fill the 8 columns.
+//
+// Levels: a Q4_0 nibble n in the lowest bits of a half is the subnormal number n 2^-24, in the next four bits n 2^-20: masks make
+// MMA operands of a word of 8 nibbles, without arithmetic.  Values 16 .. 31 of a block's activations are kept as a 16th, and the level's
+// -8 is taken from the block's sum: sum (n - 8) x = sum n x - 8 sum x (the two are at most twice what the sum's terms weigh, so
+// no accuracy goes).  Q8_0 quants become exact halves by a magic number.
+// An activation is a half after the power of two that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16
+// down to 2^-27 of the largest; float32 values (and h for float32 outputs) are two halves, 22 bits; h for bfloat16 outputs one, 2^-11
+// relative.
 #include <cooperative_groups.h>
 
 #include <cstddef>
@@ -190,10 +196,10 @@ struct Stage {
   static constexpr int kScaleRow = kBlocks * (F16 ? 2 : 4);
   static constexpr int kBytes = kQ + kRowsStage * kScaleRow;
   // a vector's chunk: its blocks' halves, 64 of 80 bytes a block, so that the lanes that read four blocks lie in different banks.
-  // Then the blocks' scales.
+  // Then for each block what a sum of products is multiplied by and what is taken off it then.
   static constexpr int kBlock = 80;
   static constexpr int kVector = kBlocks * kBlock;
-  static __host__ __device__ constexpr int columns(int vectors) { return vectors * (kVector + kBlocks * 4); }
+  static __host__ __device__ constexpr int columns(int vectors) { return vectors * (kVector + kBlocks * 8); }
 };
 
 // Where a lane reads a stage's rows: 16 rows of one matrix image and 16 of another (or of the same, at another place).  Moving to
@@ -201,32 +207,40 @@ struct Stage {
 template <int WT, bool F16>
 struct Rows {
   using S = Stage<WT, F16>;
-  const uint8_t *qa, *qb;  // this lane's piece of rows (lane / 8) of both
+  const uint8_t *qa, *qb;  // this lane's first piece (lane % 4, and the fourth after it) of rows lane / 4 (and 8 further) of both
   const uint8_t *da, *db;  // the scales of the rows' first blocks: of row lane % 16 (whole chunks), else of row 0
   __device__ __forceinline__ void set(const uint8_t* q_a, const uint8_t* d_a, const uint8_t* q_b, const uint8_t* d_b, long long row_a,
                                       long long row_b, int cols) {
     const int lane = threadIdx.x & 31;
     const long long row_bytes = WT == QMV_Q4_0 ? cols / 2 : cols, scale_bytes = cols / 32 * (F16 ? 2 : 4);
-    qa = q_a + (row_a + (lane >> 3)) * row_bytes + (lane & 7) * 16;
-    qb = q_b + (row_b + (lane >> 3)) * row_bytes + (lane & 7) * 16;
+    qa = q_a + (row_a + (lane >> 2)) * row_bytes + (lane & 3) * 16;
+    qb = q_b + (row_b + (lane >> 2)) * row_bytes + (lane & 3) * 16;
     const int row = cols % S::kChunk == 0 ? lane & 15 : 0;
     da = d_a + (row_a + row) * scale_bytes;
     db = d_b + (row_b + row) * scale_bytes;
   }
   // Chunk c of the rows `down` rows further.
   __device__ __forceinline__ void load(uint32_t stage, int c, int down, int cols) const {
-    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const int lane = threadIdx.x & 31, piece = lane & 3;
     const int row_bytes = WT == QMV_Q4_0 ? cols / 2 : cols, scale_bytes = cols / 32 * (F16 ? 2 : 4);
-    const bool live = c * 128 + piece * 16 < row_bytes;
-    const long long off = (long long)down * row_bytes + (live ? c * 128 : -piece * 16);  // (a piece past the row: its first bytes, not copied)
-    const uint8_t *a = qa + off, *b = qb + off;
-    const uint32_t to = stage + (lane >> 3) * 128 + ((piece ^ (((lane >> 3) & 1) * S::kTurn)) << 4);  // (rows 4 apart are both even or odd)
+    const long long off = (long long)down * row_bytes + c * 128;
+    const uint8_t* from[4] = {qa + off, qa + off + 8 * row_bytes, qb + off, qb + off + 8 * row_bytes};
+    // piece numbers are exchanged by the row's lowest bit
+    const uint32_t odd = (lane >> 2 & 1) * S::kTurn;
+    const uint32_t to = stage + (lane >> 2) * 128, near = (piece ^ odd) << 4, far = ((piece + 4) ^ odd) << 4;
+    if ((c + 1) * 128 <= row_bytes) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      copy_async<16>(to + i * 512, a, live);
-      copy_async<16>(to + i * 512 + 2048, b, live);
-      a += 4 * row_bytes;
-      b += 4 * row_bytes;
+      for (int i = 0; i < 4; ++i) {
+        copy_async<16>(to + i * 1024 + near, from[i], true);
+        copy_async<16>(to + i * 1024 + far, from[i] + 64, true);
+      }
+    } else {  // the row ends in this chunk: zeros after it
+      const int left = row_bytes - c * 128 - piece * 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        copy_async<16>(to + i * 1024 + near, left > 0 ? from[i] : qa, left > 0);
+        copy_async<16>(to + i * 1024 + far, left > 64 ? from[i] + 64 : qa, left > 64);
+      }
     }
     const uint32_t sd = stage + S::kQ;
     const long long s_off = (long long)down * scale_bytes + c * S::kScaleRow;
@@ -248,10 +262,12 @@ struct Rows {
   }
 };
 
-// The power of two that brings amax into [2^14, 2^15), and its inverse (1 for amax 0, below 2^-112 or not finite).
-// Eight values of a block of 32 that four neighbouring lanes hold, as halves at that scale: hi, and with LO what hi leaves (11 more bits).
-template <bool LO>
-__device__ __forceinline__ float to_halves(const float (&v)[8], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+// Eight values of a block of 32 (elements 8 piece ..) that four neighbouring lanes hold, as halves at the power of two that brings the block's
+// largest into [2^14, 2^15): hi, and with LO what hi leaves (11 more bits).  For Q4_0 in the order in which masks take a word's nibbles (0, 2,
+// 1, 3 of each four), the block's second half as a 16th.  mul, off: what the products' sum is multiplied by and what is taken off
+// then (hi's, then lo's).
+template <int WT, bool LO>
+__device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32_t (&hi)[4], uint32_t (&lo)[4], float (&mul)[2], float (&off)[2]) {
   float amax = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
@@ -259,22 +275,38 @@ __device__ __forceinline__ float to_halves(const float (&v)[8], uint32_t (&hi)[4
   for (int o = 1; o <= 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   float up, down;
   half_stage_scale(amax, up, down);
+  const float part = WT == QMV_Q4_0 && piece >= 2 ? 0.0625f : 1.f, back = WT == QMV_Q4_0 && piece >= 2 ? 16.f : 1.f;
+  float sum = 0.f, sum_lo = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float a = v[2 * e] * up, b = v[2 * e + 1] * up;
+    const int i = WT == QMV_Q4_0 ? (e & 2) * 2 + (e & 1) : 2 * e, j = WT == QMV_Q4_0 ? i + 2 : i + 1;
+    const float a = v[i] * up * part, b = v[j] * up * part;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi[e]) : "f"(b), "f"(a));
+    const float ha = __half2float(__ushort_as_half((unsigned short)(hi[e] & 0xffffu)));
+    const float hb = __half2float(__ushort_as_half((unsigned short)(hi[e] >> 16)));
+    sum += ha + hb;
     if (LO) {
-      const float ra = a - __half2float(__ushort_as_half((unsigned short)(hi[e] & 0xffffu)));
-      const float rb = b - __half2float(__ushort_as_half((unsigned short)(hi[e] >> 16)));
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(rb), "f"(ra));
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(b - hb), "f"(a - ha));
+      sum_lo += __half2float(__ushort_as_half((unsigned short)(lo[e] & 0xffffu))) + __half2float(__ushort_as_half((unsigned short)(lo[e] >> 16)));
     }
   }
-  return down;
+  mul[0] = mul[1] = down;
+  off[0] = off[1] = 0.f;
+  if (WT == QMV_Q4_0) {
+    sum *= back, sum_lo *= back;
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (LO) sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
+    }
+    mul[0] = mul[1] = down * 0x1p24f;
+    off[0] = 8.f * sum * down, off[1] = 8.f * sum_lo * down;
+  }
 }
 
 // One stage's products: acc[m][set] += what row tile m (rows g and g + 8 of it) gives for this lane's two blocks and vector.
 // b: this lane's column (its vector and block of the first four blocks), moving by `step` from set to set and by `group` from four blocks to
-// the next (both 0 at zeros, for lanes without a column); xs: the vector's scales of the lane's two blocks.
+// the next (both 0 at zeros, for lanes without a column); xs: the vector's factors of the lane's two blocks.
 template <int WT, bool F16, int SETS>
 __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t step, uint32_t group, uint32_t xs, uint32_t xs_step,
                                         float (&acc)[2][2][2]) {
@@ -282,7 +314,10 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   constexpr int kGroups = S::kBlocks / 4;
   constexpr int kPieces = WT == QMV_Q4_0 ? 1 : 2;  // of 16 bytes, of a block
-  const uint32_t turn = (g & 1) * S::kTurn;
+  // this lane's piece of row g: the other four pieces (Q4_0), or the other one of two (Q8_0), lie where the exchange puts them
+  const uint32_t near = ((t * kPieces) ^ ((g & 1) * S::kTurn)) << 4;
+  const uint32_t q0 = stage + g * 128 + near, q1 = stage + g * 128 + (near ^ (WT == QMV_Q4_0 ? 64 : 16));
+  const uint32_t d0 = stage + S::kQ + g * S::kScaleRow + 2 * (t & 1) * (F16 ? 2 : 4);
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
     float c[2][SETS][4];
@@ -298,7 +333,7 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
           uint32_t w[4];
-          lds_u32x4(stage + (16 * m + 8 * h + g) * 128 + ((((4 * i + t) * kPieces + j) ^ turn) << 4), w);
+          lds_u32x4(((WT == QMV_Q4_0 ? i : j) == 0 ? q0 : q1) + (16 * m + 8 * h) * 128, w);
 #pragma unroll
           for (int k = 0; k < 4; ++k) q[m][h][4 * j + k] = w[k];
         }
@@ -308,23 +343,23 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
       uint32_t x[SETS][2][4];  // [set][first, elements 16 further][halves]
 #pragma unroll
       for (int v = 0; v < SETS; ++v) {
-          lds_u32x4(b + v * step + i * group + j * 16, x[v][0]);
-          if (WT == QMV_Q4_0) lds_u32x4(b + v * step + i * group + 32 + j * 16, x[v][1]);
-        }
+        lds_u32x4(b + v * step + i * group + j * 16, x[v][0]);
+        if (WT == QMV_Q4_0) lds_u32x4(b + v * step + i * group + 32 + j * 16, x[v][1]);
+      }
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t wg = q[m][0][2 * j + k], wh = q[m][1][2 * j + k];
           if (WT == QMV_Q4_0) {
-            uint32_t g01, g23, gh01, gh23, h01, h23, hh01, hh23;
-            q4_word_to_f16_levels(wg, g01, g23, gh01, gh23);
-            q4_word_to_f16_levels(wh, h01, h23, hh01, hh23);
+            // nibbles of bytes 0 and 2, then of bytes 1 and 3
+            constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+            const uint32_t sg = wg >> 8, sh = wh >> 8;
 #pragma unroll
             for (int v = 0; v < SETS; ++v) {
-                mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
-                mma_f16_16816(c[m][v], gh01, hh01, gh23, hh23, x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
-              }
+              mma_f16_16816(c[m][v], wg & kLow, wh & kLow, sg & kLow, sh & kLow, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
+              mma_f16_16816(c[m][v], wg & kHigh, wh & kHigh, sg & kHigh, sh & kHigh, x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
+            }
           } else {
             uint32_t g01, g23, h01, h23;
             q8_word_to_f16_levels(wg, g01, g23);
@@ -335,31 +370,29 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
         }
     }
     // columns 2 t and 2 t + 1: vector t / 2 of the set, blocks 2 (t & 1) and the next
-    float xd[SETS][2];
+    float f[SETS][4];  // multiplied by, taken off; of both blocks
 #pragma unroll
-    for (int v = 0; v < SETS; ++v) {
-        uint32_t u0, u1;
-        lds_u32x2(xs + v * xs_step + i * 16, u0, u1);
-        xd[v][0] = __uint_as_float(u0), xd[v][1] = __uint_as_float(u1);
-      }
+    for (int v = 0; v < SETS; ++v) lds_f32x4(xs + v * xs_step + i * 32, f[v]);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t at = stage + S::kQ + (16 * m + 8 * h + g) * S::kScaleRow + (4 * i + 2 * (t & 1)) * (F16 ? 2 : 4);
-        float d0, d1;
+        const uint32_t at = d0 + (16 * m + 8 * h) * S::kScaleRow + 4 * i * (F16 ? 2 : 4);
+        float2 d;
         if (F16) {
           const uint32_t u = lds_u32(at);
-          d0 = f16_bits_to_f32((uint16_t)(u & 0xFFFF));
-          d1 = f16_bits_to_f32((uint16_t)(u >> 16));
+          d = __half22float2(*reinterpret_cast<const __half2*>(&u));
         } else {
           uint32_t u0, u1;
           lds_u32x2(at, u0, u1);
-          d0 = __uint_as_float(u0);
-          d1 = __uint_as_float(u1);
+          d = make_float2(__uint_as_float(u0), __uint_as_float(u1));
         }
 #pragma unroll
-        for (int v = 0; v < SETS; ++v) acc[m][v][h] = fmaf(d0 * xd[v][0], c[m][v][2 * h], fmaf(d1 * xd[v][1], c[m][v][2 * h + 1], acc[m][v][h]));
+        for (int v = 0; v < SETS; ++v) {
+          const float s0 = WT == QMV_Q4_0 ? fmaf(c[m][v][2 * h], f[v][0], -f[v][1]) : c[m][v][2 * h] * f[v][0];
+          const float s1 = WT == QMV_Q4_0 ? fmaf(c[m][v][2 * h + 1], f[v][2], -f[v][3]) : c[m][v][2 * h + 1] * f[v][2];
+          acc[m][v][h] = fmaf(d.x, s0, fmaf(d.y, s1, acc[m][v][h]));
+        }
       }
   }
 }
@@ -387,8 +420,8 @@ __device__ __forceinline__ Columns columns_of(uint32_t columns, uint32_t zeros, 
   c.step = mine && 2 + v < max_vectors ? 2 * S::kVector : 0;
   c.group = mine ? 4 * S::kBlock : 0;
   const int sv = t >> 1;
-  c.xs = sv < max_vectors ? columns + max_vectors * S::kVector + sv * S::kBlocks * 4 + 2 * (t & 1) * 4 : zeros;
-  c.xs_step = 2 + sv < max_vectors ? 2 * S::kBlocks * 4 : 0;  // (what is read for a vector that is not there goes nowhere)
+  c.xs = sv < max_vectors ? columns + max_vectors * S::kVector + sv * S::kBlocks * 8 + 2 * (t & 1) * 8 : zeros;
+  c.xs_step = 2 + sv < max_vectors ? 2 * S::kBlocks * 8 : 0;  // (what is read for a vector that is not there goes nowhere)
   return c;
 }
 
@@ -403,11 +436,11 @@ __device__ __forceinline__ void consume_any(uint32_t stage, const Columns& c, in
 
 // ------------------------------------------------------------------------------------------ gate and up
 // A warp's columns of chunk c, converted: `vectors` halves of up to kVectors vectors, then their scales, at `to`.
-template <typename S, bool XF32>
+template <typename S, int WT, bool XF32>
 __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, const void* x, const Unit& u, int c, int cols) {
   const int lane = threadIdx.x & 31;
   constexpr int kPieces = S::kChunk / 8;  // of a token
-  float* scales = reinterpret_cast<float*>(to + max_vectors * S::kVector);
+  float2* factors = reinterpret_cast<float2*>(to + max_vectors * S::kVector);
 #pragma unroll 2
   for (int i = 0; i < u.cols * kPieces; i += 32) {
     const int k = (i + lane) / kPieces, piece = (i + lane) % kPieces;
@@ -430,15 +463,16 @@ __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, co
       }
     }
     uint32_t hi[4], lo[4];
-    const float down = to_halves<XF32>(v, hi, lo);
+    float mul[2], off[2];
+    to_halves<WT, XF32>(v, piece & 3, hi, lo, mul, off);
     if (in) {
       const int vec = XF32 ? 2 * k : k;
       uint8_t* at16 = to + vec * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16;
       *reinterpret_cast<uint4*>(at16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if (XF32) *reinterpret_cast<uint4*>(at16 + S::kVector) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       if ((piece & 3) == 0) {
-        scales[vec * S::kBlocks + (piece >> 2)] = down;
-        if (XF32) scales[(vec + 1) * S::kBlocks + (piece >> 2)] = down;
+        factors[vec * S::kBlocks + (piece >> 2)] = make_float2(mul[0], off[0]);
+        if (XF32) factors[(vec + 1) * S::kBlocks + (piece >> 2)] = make_float2(mul[1], off[1]);
       }
     }
   }
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       u = unit_of(r, p, unit, p.unit);
       if (works && n <= p.cached) {
         __syncwarp();
-        for (int j = 0; j < n; ++j) convert_columns<S, XF32>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
+        for (int j = 0; j < n; ++j) convert_columns<S, WT, XF32>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
         __syncwarp();
       }
       held = unit;
@@ -526,7 +560,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         Columns c = col0;
         if (n > p.cached) {
           __syncwarp();
-          convert_columns<S, XF32>(cache, max_vectors, p.x, u, c0 + j, p.dim);
+          convert_columns<S, WT, XF32>(cache, max_vectors, p.x, u, c0 + j, p.dim);
         } else {
           c.b += c.b == zeros ? 0 : j * cache_bytes;
           c.xs += c.xs == zeros ? 0 : j * cache_bytes;
@@ -579,12 +613,26 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(isnan(h) ? 0.f : fabsf(h))));
         float to, down;
         half_stage_scale(amax, to, down);
-        const float v = h * to;
-        const __half hi = __float2half_rn(v);
-        __half* out = reinterpret_cast<__half*>(p.h) + (long long)slot * p.hidden + 32 * ht + lane;
+        // as to_halves() leaves activations, for W2's type
+        const bool split = p.w2_q4 && lane >= 16;
+        const float v = h * to * (split ? 0.0625f : 1.f);
+        const __half hi = __float2half_rn(v), lo = __float2half_rn(isfinite(v) ? v - __half2float(hi) : 0.f);
+        const int place = p.w2_q4 ? (lane & ~3) | (lane & 1) << 1 | (lane >> 1 & 1) : lane;
+        __half* out = reinterpret_cast<__half*>(p.h) + (long long)slot * p.hidden + 32 * ht + place;
         out[0] = hi;
-        if (p.parts > 1) out[p.h_plane] = __float2half_rn(isfinite(v) ? v - __half2float(hi) : 0.f);
-        if (lane == 0) p.h_scale[(long long)slot * (p.hidden / 32) + ht] = down;
+        if (p.parts > 1) out[p.h_plane] = lo;
+        float sum = 0.f, sum_lo = 0.f;
+        if (p.w2_q4) {
+          sum = __half2float(hi) * (split ? 16.f : 1.f), sum_lo = __half2float(lo) * (split ? 16.f : 1.f);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
+          }
+        }
+        if (lane < p.parts)
+          p.h_factor[((long long)lane * p.tokens * p.top + slot) * (p.hidden / 32) + ht] =
+              make_float2(p.w2_q4 ? down * 0x1p24f : down, 8.f * (lane == 0 ? sum : sum_lo) * down);
       }
     }
     if ((first += p.tiles_item) >= tiles) first = 0, ++unit;
@@ -648,7 +696,8 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
       if (v >= vectors) continue;
       copy_async<16>(to + v * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16, p.h + (long long)row * 64 + (live ? first : 0), live);
       if ((piece & 3) == 0)
-        copy_async<4>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 4, p.h_scale + (long long)slot * (p.hidden / 32) + (live ? first / 32 : 0), live);
+        copy_async<8>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 8,
+                      p.h_factor + ((long long)(v % PARTS) * p.tokens * p.top + slot) * (p.hidden / 32) + (live ? first / 32 : 0), live);
     }
   };
   auto weights = [&](int at) { rows.load(ring + at * stage_bytes, ps_c, 0, p.hidden); };
@@ -870,7 +919,7 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
 
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16) {
   const size_t t = tokens < kTokens ? tokens : kTokens;
-  return t * top * (hidden * 2 * (out_bf16 ? 1 : 2) + hidden / 32 * 4);
+  return t * top * (hidden * 2 + hidden / 32 * 8) * (out_bf16 ? 1 : 2);
 }
 
 cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -886,7 +935,8 @@ cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t str
     p.h = static_cast<uint16_t*>(a.scratch);
     p.h_plane = (long long)p.tokens * a.top * a.hidden;
     p.parts = a.out_bf16 ? 1 : 2;
-    p.h_scale = reinterpret_cast<float*>(p.h + p.parts * p.h_plane);
+    p.h_factor = reinterpret_cast<float2*>(p.h + p.parts * p.h_plane);
+    p.w2_q4 = a.w2.wtype == QMV_Q4_0;
     p.ids = a.ids == nullptr ? nullptr : a.ids + t0 * a.top;
     p.shares = a.shares == nullptr ? nullptr : a.shares + t0 * a.top;
     p.experts = a.experts;

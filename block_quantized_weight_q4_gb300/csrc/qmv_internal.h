@@ -332,14 +332,14 @@ struct MoeParams {
   const void* x;
   void* out;
   uint16_t* h;        // halves of act(gate) * up, tokens * top rows of `hidden`, `parts` times
-  float* h_scale;     // of each 32 of a row
+  float2* h_factor;   // of each 32 of a row: what products with them are multiplied by, what is taken off then
   int32_t* ids;
   float* shares;
   long long logits_stride;
   long long h_plane;  // elements between h's parts
   int parts;
   int tokens, experts, top, dim, hidden;
-  int renorm, act, out_bf16;
+  int renorm, act, out_bf16, w2_q4;
   float scale;
   int unit;              // tokens of a unit at most (moe_up)
   int tiles_item;        // tiles of 32 rows of an item (moe_up)

@@ -83,7 +83,7 @@ def moe(w1, w3, w2, x, logits, top, renorm, scale, name, parts):
     Bound.  A product's sum of n terms: blocks of 32 on the tensor core, then n / 32 float32 additions, each at most 2^-23 of
     the sum of magnitudes A (whatever the rounding inside an MMA): (n / 32 + 40) 2^-23 A; x itself in 22 bits (2^-22 A).  h = act(g) u:
     |dh| <= 1.13 |u| dg + |act(g)| du (the slope of either activation is below 1.13) + 2^-20 (1 + |g|) |h| for the float32 functions, and
-    its halves' rounding, 2^-11 |h| for one and 2^-22 for two, or 2^-39 of the largest where that is more.  The shares: 2^-20 relative (exponentials, sums, a quotient), and the
+    its halves' rounding, 2^-11 |h| for one and 2^-22 for two, or 2^-35 of the largest where that is more (a block's second half keeps four bits fewer of its small values).  The shares: 2^-20 relative (exponentials, sums, a quotient), and the
     difference of a logit and the maximum, d, rounded to float32: e^(d (1 + 2^-24)) is off by |d| 2^-24.  The shares' relative bound is
     the fifth result."""
     tokens, experts = logits.shape
@@ -112,7 +112,7 @@ def moe(w1, w3, w2, x, logits, top, renorm, scale, name, parts):
             c = (dim / 32 + 42) * 2.0 ** -23
             h = act(name, g) * u
             dh = (1.13 * np.abs(u) * c * ga + np.abs(act(name, g)) * c * ua + 1.13 * c * c * ga * ua +
-                  (2.0 ** -20 * (1 + np.abs(g)) + (2.0 ** -11 if parts == 1 else 2.0 ** -22)) * np.abs(h) + 2.0 ** -39 * np.abs(h).max() + 1e-33)
+                  (2.0 ** -20 * (1 + np.abs(g)) + (2.0 ** -11 if parts == 1 else 2.0 ** -22)) * np.abs(h) + 2.0 ** -35 * np.abs(h).max() + 1e-33)
             a2 = np.abs(w2[e].astype(np.float64))
             out[t] += pe * scale * (w2[e].astype(np.float64) @ h)
             bound[t] += pe * abs(scale) * (a2 @ dh + ((hidden / 32 + 40) * 2.0 ** -23 + re) * (a2 @ np.abs(h)))

@@ -28,7 +28,6 @@
 // relative.
 #include <cooperative_groups.h>
 
-#include <cstddef>
 #include <mutex>
 
 #include "qmv_common.cuh"
@@ -45,20 +44,25 @@ constexpr int kTokens = 64;    // of a launch
 constexpr int kExperts = QMV_MOE_MAX_EXPERTS;
 constexpr int kTop = QMV_MOE_MAX_TOP;
 constexpr int kVectors = 4;    // of a unit: two to an MMA
-constexpr int kUnits = kTokens * kTop;  // at most one a token and expert
 constexpr int kRowsStage = 32;
 
 // ------------------------------------------------------------------------------------------ routing
+// What a CTA knows of the routing, in shared memory; the arrays after it have the lengths that the call bounds.
 struct Routing {
-  unsigned long long mask[kExperts];  // tokens of an expert
-  unsigned long long bad;             // tokens whose logits hold NaN or +infinity
-  uint16_t sel[kTokens * kTop];       // experts of a token, 0xffff: none
-  uint16_t unit[kUnits];              // expert | pass << 8
+  uint32_t mask[2][kExperts];    // tokens of an expert, 32 a word
+  uint32_t bad[2];               // tokens whose logits hold NaN or +infinity
   int units;
   int part[kMaxWarps];
-  float share[kTokens * kTop];  // moe_down's alone (moe_up's shared memory ends before it)
+  uint16_t base[kExperts];       // an expert's first unit
+  uint16_t sel[kTokens * kTop];  // experts of a token, 0xffff: none
 };
-constexpr size_t kRoutingUp = offsetof(Routing, share);
+struct Units {
+  uint2* entry;    // a unit's tokens: four of 16 bits, token << 10 | token * top + place
+  uint16_t* head;  // expert | tokens << 8
+  static __host__ __device__ int bytes(int n) { return n * 8 + (n * 2 + 15) / 16 * 16; }
+  __device__ __forceinline__ Units(uint8_t* at, int n) : entry(reinterpret_cast<uint2*>(at)), head(reinterpret_cast<uint16_t*>(at + n * 8)) {}
+};
+static_assert(kTokens * kTop <= 1024 && kTokens <= 64, "a token and its place in 16 bits");
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -68,68 +72,77 @@ __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// W: the CTA's warps (8 or more: a thread for each expert); unit_cols: tokens of a unit
+// W: the CTA's warps (8 or more: a thread for each expert); unit_cols: tokens of a unit.  share: where the shares go (moe_down).
 template <int W, bool SHARES>
-__device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
+__device__ void route(Routing& r, const Units& units, const MoeParams& p, int unit_cols, float* share) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < kExperts; e += 32 * W) r.mask[e] = 0;
-  if (threadIdx.x == 0) r.bad = 0;
+  constexpr int kEach = kExperts / 32;
+  // a token's logits are asked for while the token before it is routed
+  float l[kEach];
+  auto ask = [&](int tok) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      l[i] = -INFINITY;
+      if (32 * i < p.experts && tok < p.tokens && lane + 32 * i < p.experts) l[i] = __ldg(p.logits + tok * p.logits_stride + lane + 32 * i);
+    }
+  };
+  ask(wid);
+  for (int e = threadIdx.x; e < 2 * kExperts; e += 32 * W) r.mask[0][e] = 0u;
+  if (threadIdx.x < 2) r.bad[threadIdx.x] = 0u;
   __syncthreads();
   for (int tok = wid; tok < p.tokens; tok += W) {
-    uint32_t key[kExperts / 32];
-    float most = -INFINITY;
+    uint32_t key[kEach];
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kExperts / 32; ++i) {
-      key[i] = 0;
-      const int e = lane + 32 * i;
-      if (e < p.experts) {
-        const float l = __ldg(p.logits + tok * p.logits_stride + e);
-        bad |= !(l < INFINITY);
-        if (l > -INFINITY) key[i] = ordered(l);
-        most = fmaxf(most, l);
-      }
+    for (int i = 0; i < kEach; ++i) {
+      bad |= !(l[i] < INFINITY);
+      key[i] = l[i] > -INFINITY ? ordered(l[i]) : 0u;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    ask(tok + W);
     bad = __any_sync(0xffffffffu, bad);
-    float sum = 0.f;
-    if (SHARES && !p.renorm) {
-#pragma unroll
-      for (int i = 0; i < kExperts / 32; ++i)
-        if (key[i] != 0) sum += expf(unordered(key[i]) - most);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    float mine = 0.f;  // lane k: the share of the k-th
+    uint32_t top = 0;  // the token's largest
+    float sum = 0.f, mine = 0.f;  // lane k: what the k-th weighs
     for (int k = 0; k < p.top; ++k) {
-      uint32_t best = 0;
-      int at = 0;
+      // the lane's best: the larger key, then the lower expert
+      uint32_t best = key[0];
+      int at = lane;
 #pragma unroll
-      for (int i = 0; i < kExperts / 32; ++i)
-        if (key[i] > best) best = key[i], at = lane + 32 * i;
+      for (int i = 1; i < kEach; ++i)
+        if (32 * i < p.experts && key[i] > best) best = key[i], at = lane + 32 * i;
       const uint32_t high = bad ? 0u : __reduce_max_sync(0xffffffffu, best);
       int e = 0xffff;
       if (high != 0) {
         e = (int)__reduce_min_sync(0xffffffffu, best == high ? (unsigned)at : 0xffffu);
+        if (k == 0) {
+          top = high;
+          if (SHARES && !p.renorm) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+              if (32 * i < p.experts && key[i] != 0) sum += expf(unordered(key[i]) - unordered(top));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          }
+        }
         if (SHARES) {
-          const float w = expf(unordered(high) - most);
+          const float w = expf(unordered(high) - unordered(top));
           if (lane == k) mine = w;
           if (p.renorm) sum += w;
         }
 #pragma unroll
-        for (int i = 0; i < kExperts / 32; ++i)
+        for (int i = 0; i < kEach; ++i)
           if (e == lane + 32 * i) key[i] = 0;
-        if (lane == 0) atomicOr(&r.mask[e], 1ull << tok);
+        if (lane == 0) atomicOr(&r.mask[tok >> 5][e], 1u << (tok & 31));
       }
       if (lane == 0) r.sel[tok * p.top + k] = (uint16_t)e;
     }
-    if (bad && lane == 0) atomicOr(&r.bad, 1ull << tok);
-    if (SHARES && lane < p.top) r.share[tok * p.top + lane] = bad ? NAN : mine == 0.f ? 0.f : __fdiv_rn(mine, sum);
+    if (bad && lane == 0) atomicOr(&r.bad[tok >> 5], 1u << (tok & 31));
+    if (SHARES && lane < p.top) share[tok * p.top + lane] = bad ? NAN : mine == 0.f ? 0.f : __fdiv_rn(mine, sum);
   }
   __syncthreads();
-  // units: experts in rising order, each with ceil(tokens / unit_cols) passes
-  const int passes = (int)threadIdx.x < p.experts ? (__popcll(r.mask[threadIdx.x]) + unit_cols - 1) / unit_cols : 0;
+  // units: experts in rising order, an expert's tokens in theirs
+  const int e = threadIdx.x;
+  int tokens = e < p.experts ? __popc(r.mask[0][e]) + __popc(r.mask[1][e]) : 0;
+  const int passes = (tokens + unit_cols - 1) / unit_cols;
   int upto = passes;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -139,12 +152,23 @@ __device__ void route(Routing& r, const MoeParams& p, int unit_cols) {
   if (lane == 31) r.part[wid] = upto;
   __syncthreads();
   int all = 0;
+#pragma unroll
   for (int w = 0; w < W; ++w) {
     if (w == wid) upto += all;
     all += r.part[w];
   }
-  for (int i = 0; i < passes; ++i) r.unit[upto - passes + i] = (uint16_t)(threadIdx.x | i << 8);
+  if (e < p.experts) r.base[e] = (uint16_t)(upto - passes);
+  for (int i = upto - passes; i < upto; ++i, tokens -= unit_cols) units.head[i] = (uint16_t)(e | min(tokens, unit_cols) << 8);
   if (threadIdx.x == 0) r.units = all;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.tokens * p.top; i += 32 * W) {
+    const int x = r.sel[i];
+    if (x == 0xffff) continue;
+    const int tok = i / p.top;
+    const uint32_t before = (1u << (tok & 31)) - 1u;
+    const int place = tok < 32 ? __popc(r.mask[0][x] & before) : __popc(r.mask[0][x]) + __popc(r.mask[1][x] & before);
+    reinterpret_cast<uint16_t*>(units.entry + r.base[x] + place / unit_cols)[place % unit_cols] = (uint16_t)(tok << 10 | i);
+  }
   __syncthreads();
 }
 
@@ -153,21 +177,21 @@ struct Unit {
   int expert, cols;
   int tok, slot;
 };
-__device__ __forceinline__ Unit unit_of(const Routing& r, const MoeParams& p, int u, int unit_cols) {
+__device__ __forceinline__ Unit unit_of(const Units& units, int u) {
   const int lane = threadIdx.x & 31;
+  const int head = units.head[u];
   Unit c;
-  c.expert = r.unit[u] & 255;
-  const int pass = r.unit[u] >> 8;
-  unsigned long long m = r.mask[c.expert];
-  c.cols = min(__popcll(m) - unit_cols * pass, unit_cols);
-  c.tok = c.slot = 0;
-  if (lane < c.cols) {
-    for (int i = 0; i < unit_cols * pass + lane; ++i) m &= m - 1;
-    c.tok = __ffsll((long long)m) - 1;
-    c.slot = c.tok * p.top;
-    while (r.sel[c.slot] != c.expert) ++c.slot;  // (it is there: the mask says so)
-  }
+  c.expert = head & 255;
+  c.cols = head >> 8;
+  const int entry = lane < c.cols ? reinterpret_cast<const uint16_t*>(units.entry + u)[lane] : 0;
+  c.tok = entry >> 10;
+  c.slot = entry & 1023;
   return c;
+}
+// An even share of n for each of `of`: the first of share i.
+__device__ __forceinline__ int share_of(int n, int i, int of) {
+  const int each = n / of, more = n - each * of;
+  return i * each + min(i, more);
 }
 
 // ------------------------------------------------------------------------------------------ stages
@@ -495,15 +519,16 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   griddep_wait();
   griddep_launch_dependents();
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
-  route<kUpWarps, false>(r, p, p.unit);
+  const Units units(smem + p.off_units, p.max_units);
+  route<kUpWarps, false>(r, units, p, p.unit, nullptr);
   const uint32_t zeros = smem_u32(smem + p.off_zero);
 
   const int tiles = p.hidden / 32, chunks = (p.dim + S::kChunk - 1) / S::kChunk;
   const int items_unit = (tiles + p.tiles_item - 1) / p.tiles_item;
   const int items = r.units * items_unit;
   // a run of items: mostly one unit's, so that its columns are converted once
-  const int item0 = (int)((long long)items * blockIdx.x / gridDim.x), item1 = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
-  const int slice = wid % p.ks, tile_local = wid / p.ks;
+  const int item0 = share_of(items, blockIdx.x, gridDim.x), item1 = share_of(items, blockIdx.x + 1, gridDim.x);
+  const int slice = wid & (p.ks - 1), tile_local = wid / p.ks;  // (ks is a power of two)
   const bool works = tile_local < p.tiles_item;
   const int c0 = slice * chunks / p.ks, n = (slice + 1) * chunks / p.ks - c0;
 
@@ -517,7 +542,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       if ((p_first += p.tiles_item) >= tiles) p_first = 0, ++p_unit;
     }
     if (pi < item1) {
-      const long long row = (long long)(r.unit[p_unit] & 255) * p.hidden + 32LL * (p_first + tile_local);
+      const long long row = (long long)(units.head[p_unit] & 255) * p.hidden + 32LL * (p_first + tile_local);
       rows.set(p.q1, p.d1, p.q3, p.d3, row, row, p.dim);
     }
   };
@@ -545,7 +570,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   for (int item = item0; item < item1; ++item) {
     const int tile = first + tile_local;
     if (held != unit) {
-      u = unit_of(r, p, unit, p.unit);
+      u = unit_of(units, unit);
       if (works && n <= p.cached) {
         __syncwarp();
         for (int j = 0; j < n; ++j) convert_columns<S, WT, XF32>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
@@ -659,20 +684,22 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   const int row0 = (int)(blockIdx.x / ranks) * kRowsStage;
   // launched by moe_up after its own wait: what came before that, the logits and the weights among it, is complete
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
-  route<kDownWarps, true>(r, p, kUnit);
+  const Units units(smem + p.off_units, p.max_units);
+  float* share = reinterpret_cast<float*>(smem + p.off_share);
+  route<kDownWarps, true>(r, units, p, kUnit, share);
   float* my = tiles + wid * kRowsStage * p.tokens;
   for (int i = lane; i < kRowsStage * p.tokens; i += 32) my[i] = 0.f;
   __syncwarp();
 
   const int chunks = (p.hidden + S::kChunk - 1) / S::kChunk;
   const int total = r.units * chunks, warps = ranks * kDownWarps, me = rank * kDownWarps + wid;
-  const int s0 = (int)((long long)total * me / warps), s1 = (int)((long long)total * (me + 1) / warps);
+  const int s0 = share_of(total, me, warps), s1 = share_of(total, me + 1, warps);
   int ps = s0, ps_c = s0 % chunks, ps_u = s0 / chunks, slot_p = 0;
   Unit pu{};
   Rows<WT, F16> rows;
   uint32_t h_at = 0;  // lane v: vector v's row of h, in 64 halves
   auto next_unit = [&]() {
-    pu = unit_of(r, p, ps_u, kUnit);
+    pu = unit_of(units, ps_u);
     const long long row = (long long)pu.expert * p.dim + row0;
     rows.set(p.q2, p.d2, p.q2, p.d2, row, row + 16, p.hidden);
     const int slot = __shfl_sync(0xffffffffu, pu.slot, lane / PARTS);
@@ -732,13 +759,13 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   float acc[2][2][2] = {};  // [tile][set][row g, g + 8]
   int cs = 0, cc = s0 % chunks, cu = s0 / chunks;
   Unit u{};
-  if (s0 < s1) u = unit_of(r, p, cu, kUnit);
+  if (s0 < s1) u = unit_of(units, cu);
   auto flush = [&]() {
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const int col = PARTS == 2 ? v : 2 * v + (t >> 1);
       const int tok = __shfl_sync(0xffffffffu, u.tok, col);
-      const float share = r.share[__shfl_sync(0xffffffffu, u.slot, col)];  // (lanes without a token: of the first, unused)
+      const float part = share[__shfl_sync(0xffffffffu, u.slot, col)];  // (lanes without a token: of the first, unused)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -746,7 +773,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
           float a = acc[m][v][h];
           a += __shfl_xor_sync(0xffffffffu, a, 1);
           if (PARTS == 2) a += __shfl_xor_sync(0xffffffffu, a, 2);
-          if (col < u.cols && (PARTS == 2 ? t == 0 : (t & 1) == 0)) my[tok * kRowsStage + 16 * m + 8 * h + g] += share * a;
+          if (col < u.cols && (PARTS == 2 ? t == 0 : (t & 1) == 0)) my[tok * kRowsStage + 16 * m + 8 * h + g] += part * a;
           acc[m][v][h] = 0.f;
         }
     }
@@ -770,7 +797,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     if (++cc == chunks) {
       flush();
       cc = 0;
-      if (s + 1 < s1) u = unit_of(r, p, ++cu, kUnit);
+      if (s + 1 < s1) u = unit_of(units, ++cu);
     }
   }
   if (s0 < s1 && cc != 0) flush();
@@ -795,7 +822,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += v[k];
     sum *= p.scale;
-    if (r.bad >> tok & 1) sum = NAN;
+    if (r.bad[tok >> 5] >> (tok & 31) & 1u) sum = NAN;
     const long long at = (long long)tok * p.dim + row0 + row;
     if (p.out_bf16)
       static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(sum);
@@ -805,7 +832,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < p.tokens * p.top; i += kDownThreads) {
       if (p.ids != nullptr) p.ids[i] = r.sel[i] == 0xffff ? -1 : (int)r.sel[i];
-      if (p.shares != nullptr) p.shares[i] = r.share[i];
+      if (p.shares != nullptr) p.shares[i] = share[i];
     }
   }
   if (ranks > 1) cl.sync();  // no CTA leaves while another reads its tiles
@@ -825,6 +852,12 @@ cudaError_t allow_smem(K kern, const DeviceInfo& dev, bool (&done)[64]) {
 
 constexpr size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
+// Units of a launch at most: an expert's last one may be part full.
+int max_units(const MoeParams& p, int used) {
+  const int pairs = p.tokens * p.top, n = used + pairs / p.unit;
+  return n < pairs ? n : pairs;
+}
+
 // Shared memory of an SM's CTA, with what the system keeps, where `n` are to fit.
 size_t room(const DeviceInfo& dev, int n) {
   const size_t each = dev.smem_per_sm / n;
@@ -840,14 +873,17 @@ cudaError_t launch_up(MoeParams p, bool x_f32, const DeviceInfo& dev, cudaStream
   p.ks = 1;
   while (p.ks < kUpWarps && 2 * p.ks <= chunks) p.ks *= 2;
   const int slice = (chunks + p.ks - 1) / p.ks;
-  p.off_zero = (int)round_up(kRoutingUp, 128);
-  p.off_red = p.off_zero + 128;
-  p.off_cols = p.off_red + 2 * kUpWarps * most * 64 * 4;
+  const int used = p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top;
+  p.off_units = (int)round_up(sizeof(Routing), 16);
   // the warps' columns are kept where they leave room for the rings; units of fewer tokens where they do not (Q4_0 with float32 scales)
   size_t smem = 0;
   bool fits = false;
   for (p.unit = most; p.unit >= 1 && !fits; p.unit -= fits ? 0 : 1) {
     const int tokens = p.tokens < p.unit ? p.tokens : p.unit, columns = S::columns(x_f32 ? 2 * tokens : tokens);
+    p.max_units = max_units(p, used);
+    p.off_zero = (int)round_up(p.off_units + Units::bytes(p.max_units), 128);
+    p.off_red = p.off_zero + 128;
+    p.off_cols = p.off_red + 2 * kUpWarps * most * 64 * 4;
     for (int keep = 0; keep < 2 && !fits; ++keep) {
       p.cached = keep == 0 ? slice : 1;
       p.off_ring = (int)round_up(p.off_cols + (size_t)kUpWarps * p.cached * columns, 128);
@@ -860,7 +896,7 @@ cudaError_t launch_up(MoeParams p, bool x_f32, const DeviceInfo& dev, cudaStream
   }
   if (!fits) return cudaErrorInvalidValue;
   // an item: as many tiles as the warps take, or fewer where that would leave SMs without one
-  const long long units = (p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) + p.tokens * p.top / p.unit;
+  const long long units = p.max_units;
   const int tiles = p.hidden / 32;
   for (p.tiles_item = kUpWarps / p.ks; p.tiles_item > 1 && units * ((tiles + p.tiles_item - 1) / p.tiles_item) < dev.sm_count;) p.tiles_item /= 2;
   const long long items = units * ((tiles + p.tiles_item - 1) / p.tiles_item);
@@ -876,7 +912,11 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
   using S = Stage<WT, F16>;
   const int unit = kVectors / p.parts, vectors = (p.tokens < unit ? p.tokens : unit) * p.parts;
   const int stage = S::kBytes + S::columns(vectors);
-  p.off_zero = (int)round_up(sizeof(Routing), 128);
+  p.unit = unit;
+  p.max_units = max_units(p, p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top);
+  p.off_units = (int)round_up(sizeof(Routing), 16);
+  p.off_share = p.off_units + Units::bytes(p.max_units);
+  p.off_zero = (int)round_up(p.off_share + (size_t)p.tokens * p.top * 4, 128);
   p.off_red = p.off_zero + 128;
   p.off_ring = (int)round_up(p.off_red + (size_t)kDownWarps * kRowsStage * p.tokens * 4, 128);
   size_t smem = 0;

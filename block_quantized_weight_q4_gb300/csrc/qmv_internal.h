@@ -341,12 +341,13 @@ struct MoeParams {
   int tokens, experts, top, dim, hidden;
   int renorm, act, out_bf16, w2_q4;
   float scale;
-  int unit;              // tokens of a unit at most (moe_up)
+  int unit;              // tokens of a unit at most
   int tiles_item;        // tiles of 32 rows of an item (moe_up)
   int ks;                // warps that share a tile's columns (moe_up)
   int cached;            // chunks of the warps' columns that shared memory keeps (moe_up)
   int ring;              // stages of a warp's ring, 2 to 4
-  int off_zero, off_red, off_cols, off_ring;  // places in shared memory
+  int max_units;
+  int off_units, off_share, off_zero, off_red, off_cols, off_ring;  // places in shared memory
 };
 constexpr int64_t kMoeMaxDim = 1 << 24;
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16);

@@ -3,14 +3,14 @@
 //   E(t) = the `top` largest of token t's router logits (equal ones: the lower expert),  p = their softmax share,
 //   h_e  = act(W1_e x_t) * (W3_e x_t),   out_t = scale * sum_{e in E(t)} p_e W2_e h_e.
 //
-// Two launches.  Every CTA of both works out the routing itself from the logits (a maximum over a warp's lanes `top` times
-// a token): a launch of its own would cost more.  A unit is an expert with up to 4 of its tokens (2 where they are float32: a value
-// is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after the first.
+// Two launches.  Every CTA of the first works out the routing itself from the logits (a maximum over a warp's lanes `top` times
+// a token: a launch of its own would cost more), and one of them leaves it for the second.  A unit is an expert with up to 4 of its tokens (2
+// where they are float32: a value is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after
+// the first.
 //   moe_up:   items of (unit, 32 rows of W1 and of W3), each CTA a run of them; a CTA's warps share an item's columns and meet in
 //             shared memory, where gate and up become h.
 //   moe_down: a cluster holds 32 rows of the output; its warps share the (unit, columns) stages of all units evenly, each
-//             adds share * W2_e h_e into a tile of its own, and the tiles are added in a fixed order at the end.  Launched as a
-//             dependent of moe_up: routing and the first weights are read while that one ends.
+//             adds share * W2_e h_e into a tile of its own, and the tiles are added in a fixed order at the end.
 // Weights reach each warp through a ring of its own (cp.async, 32 rows of 128 bytes of quants a stage).
 //
 // Products: m16n8k16 with IEEE halves.  Lane t of a row's four lanes takes a whole block of 32 weights (one or two 16-byte loads), so an
@@ -35,6 +35,13 @@
 
 namespace qmv {
 
+// What moe_down gets of it, in the call's scratch memory: this, the units as moe_down forms them, the shares of tokens * top places.
+struct MoeTable {
+  int units;
+  uint32_t bad[2];
+  int none;
+};
+
 namespace {
 
 namespace cg = cooperative_groups;
@@ -47,7 +54,7 @@ constexpr int kVectors = 4;    // of a unit: two to an MMA
 constexpr int kRowsStage = 32;
 
 // ------------------------------------------------------------------------------------------ routing
-// What a CTA knows of the routing, in shared memory; the arrays after it have the lengths that the call bounds.
+// What moe_up's CTAs know of the routing, in shared memory; the arrays after it have the lengths that the call bounds.
 struct Routing {
   uint32_t mask[2][kExperts];    // tokens of an expert, 32 a word
   uint32_t bad[2];               // tokens whose logits hold NaN or +infinity
@@ -59,11 +66,10 @@ struct Routing {
 struct Units {
   uint2* entry;    // a unit's tokens: four of 16 bits, token << 10 | token * top + place
   uint16_t* head;  // expert | tokens << 8
-  static __host__ __device__ int bytes(int n) { return n * 8 + (n * 2 + 15) / 16 * 16; }
+  static __host__ __device__ int bytes(int n) { return n * 8 + (n * 2 + 7) / 8 * 8; }
   __device__ __forceinline__ Units(uint8_t* at, int n) : entry(reinterpret_cast<uint2*>(at)), head(reinterpret_cast<uint16_t*>(at + n * 8)) {}
 };
 static_assert(kTokens * kTop <= 1024 && kTokens <= 64, "a token and its place in 16 bits");
-
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
@@ -72,74 +78,106 @@ __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// W: the CTA's warps (8 or more: a thread for each expert); unit_cols: tokens of a unit.  share: where the shares go (moe_down).
-template <int W, bool SHARES>
-__device__ void route(Routing& r, const Units& units, const MoeParams& p, int unit_cols, float* share) {
+// The experts of the tokens that this warp routes, two tokens at a time (each step waits for the one before it).  EACH: experts a lane
+// has.  share, where it is wanted, gets the tokens' shares.
+template <int W, int EACH>
+__device__ __forceinline__ void choose(Routing& r, const MoeParams& p, float* share) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  constexpr int kEach = kExperts / 32;
-  // a token's logits are asked for while the token before it is routed
-  float l[kEach];
-  auto ask = [&](int tok) {
+  for (int tok0 = wid; tok0 < p.tokens; tok0 += 2 * W) {
+    uint32_t key[2][EACH];
+    bool bad[2];
+    float sum[2], most[2];
+    uint32_t mine[2] = {0u, 0u};  // lane k: the k-th's key
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      l[i] = -INFINITY;
-      if (32 * i < p.experts && tok < p.tokens && lane + 32 * i < p.experts) l[i] = __ldg(p.logits + tok * p.logits_stride + lane + 32 * i);
+    for (int s = 0; s < 2; ++s) {
+      const int tok = tok0 + s * W;
+      bool odd = false;
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        const int e = lane + 32 * i;
+        float l = -INFINITY;
+        if (tok < p.tokens && e < p.experts) l = __ldg(p.logits + tok * p.logits_stride + e);
+        odd |= !(l < INFINITY);
+        key[s][i] = l > -INFINITY ? ordered(l) : 0u;
+        best = max(best, key[s][i]);
+      }
+      bad[s] = __any_sync(0xffffffffu, odd);
+      sum[s] = most[s] = 0.f;
+      if (share != nullptr) {
+        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+        most[s] = high != 0 ? unordered(high) : 0.f;
+        if (!p.renorm) {
+#pragma unroll
+          for (int i = 0; i < EACH; ++i) sum[s] += key[s][i] != 0 ? expf(unordered(key[s][i]) - most[s]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) key[s][i] = bad[s] ? 0u : key[s][i];
     }
-  };
-  ask(wid);
+    for (int k = 0; k < p.top; ++k) {
+      // the lane's best: the larger key, then the lower expert
+      uint32_t best[2], high[2];
+      int at[2], e[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        best[s] = key[s][0];
+        at[s] = lane;
+#pragma unroll
+        for (int i = 1; i < EACH; ++i) {
+          at[s] = key[s][i] > best[s] ? lane + 32 * i : at[s];
+          best[s] = max(best[s], key[s][i]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) high[s] = __reduce_max_sync(0xffffffffu, best[s]);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) e[s] = (int)__reduce_min_sync(0xffffffffu, best[s] == high[s] && high[s] != 0 ? (unsigned)at[s] : 0xffffu);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        mine[s] = lane == k ? high[s] : mine[s];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) key[s][i] = e[s] == lane + 32 * i ? 0u : key[s][i];
+        if (lane == s && tok0 + s * W < p.tokens) r.sel[(tok0 + s * W) * p.top + k] = (uint16_t)e[s];
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int tok = tok0 + s * W;
+      if (tok >= p.tokens) continue;
+      if (bad[s] && lane == 0) atomicOr(&r.bad[tok >> 5], 1u << (tok & 31));
+      if (share != nullptr) {
+        const float w = mine[s] != 0 ? expf(unordered(mine[s]) - most[s]) : 0.f;
+        float total = p.renorm ? w : sum[s];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane < p.top) share[tok * p.top + lane] = bad[s] ? NAN : w == 0.f ? 0.f : __fdiv_rn(w, total);
+      }
+    }
+  }
+}
+
+// The tokens' experts, and the experts' tokens.  W: the CTA's warps (8 or more: a thread for each expert).
+template <int W>
+__device__ __forceinline__ void route(Routing& r, const MoeParams& p, float* share) {
   for (int e = threadIdx.x; e < 2 * kExperts; e += 32 * W) r.mask[0][e] = 0u;
   if (threadIdx.x < 2) r.bad[threadIdx.x] = 0u;
   __syncthreads();
-  for (int tok = wid; tok < p.tokens; tok += W) {
-    uint32_t key[kEach];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      bad |= !(l[i] < INFINITY);
-      key[i] = l[i] > -INFINITY ? ordered(l[i]) : 0u;
-    }
-    ask(tok + W);
-    bad = __any_sync(0xffffffffu, bad);
-    uint32_t top = 0;  // the token's largest
-    float sum = 0.f, mine = 0.f;  // lane k: what the k-th weighs
-    for (int k = 0; k < p.top; ++k) {
-      // the lane's best: the larger key, then the lower expert
-      uint32_t best = key[0];
-      int at = lane;
-#pragma unroll
-      for (int i = 1; i < kEach; ++i)
-        if (32 * i < p.experts && key[i] > best) best = key[i], at = lane + 32 * i;
-      const uint32_t high = bad ? 0u : __reduce_max_sync(0xffffffffu, best);
-      int e = 0xffff;
-      if (high != 0) {
-        e = (int)__reduce_min_sync(0xffffffffu, best == high ? (unsigned)at : 0xffffu);
-        if (k == 0) {
-          top = high;
-          if (SHARES && !p.renorm) {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-              if (32 * i < p.experts && key[i] != 0) sum += expf(unordered(key[i]) - unordered(top));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          }
-        }
-        if (SHARES) {
-          const float w = expf(unordered(high) - unordered(top));
-          if (lane == k) mine = w;
-          if (p.renorm) sum += w;
-        }
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          if (e == lane + 32 * i) key[i] = 0;
-        if (lane == 0) atomicOr(&r.mask[tok >> 5][e], 1u << (tok & 31));
-      }
-      if (lane == 0) r.sel[tok * p.top + k] = (uint16_t)e;
-    }
-    if (bad && lane == 0) atomicOr(&r.bad[tok >> 5], 1u << (tok & 31));
-    if (SHARES && lane < p.top) share[tok * p.top + lane] = bad ? NAN : mine == 0.f ? 0.f : __fdiv_rn(mine, sum);
+  if (p.experts <= 128)
+    choose<W, 4>(r, p, share);
+  else
+    choose<W, kExperts / 32>(r, p, share);
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.tokens * p.top; i += 32 * W) {
+    const int x = r.sel[i], tok = i / p.top;
+    if (x != 0xffff) atomicOr(&r.mask[tok >> 5][x], 1u << (tok & 31));
   }
   __syncthreads();
-  // units: experts in rising order, an expert's tokens in theirs
+}
+// The units of up to unit_cols tokens: experts in rising order, an expert's tokens in theirs.
+template <int W>
+__device__ __forceinline__ void form_units(Routing& r, const Units& units, const MoeParams& p, int unit_cols) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int e = threadIdx.x;
   int tokens = e < p.experts ? __popc(r.mask[0][e]) + __popc(r.mask[1][e]) : 0;
   const int passes = (tokens + unit_cols - 1) / unit_cols;
@@ -154,8 +192,9 @@ __device__ void route(Routing& r, const Units& units, const MoeParams& p, int un
   int all = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    if (w == wid) upto += all;
-    all += r.part[w];
+    const int n = r.part[w];
+    upto += w < wid ? n : 0;
+    all += n;
   }
   if (e < p.experts) r.base[e] = (uint16_t)(upto - passes);
   for (int i = upto - passes; i < upto; ++i, tokens -= unit_cols) units.head[i] = (uint16_t)(e | min(tokens, unit_cols) << 8);
@@ -520,7 +559,29 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   griddep_launch_dependents();
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
   const Units units(smem + p.off_units, p.max_units);
-  route<kUpWarps, false>(r, units, p, p.unit, nullptr);
+  // the last CTA (whose run of items is none of the longer ones) leaves the routing for moe_down, in units of its own size, and the call's
+  // ids and shares.  (The rings' room is free as yet.)
+  const bool leaves = blockIdx.x == gridDim.x - 1;
+  float* share = leaves ? reinterpret_cast<float*>(smem + p.off_ring) : nullptr;
+  route<kUpWarps>(r, p, share);
+  for (int rounds = leaves && p.down_unit != p.unit ? 2 : 1; rounds > 0; --rounds) {
+    form_units<kUpWarps>(r, units, p, rounds == 2 ? p.down_unit : p.unit);
+    if (share != nullptr) {
+      uint8_t* at = reinterpret_cast<uint8_t*>(p.table);
+      if (threadIdx.x == 0) *p.table = MoeTable{r.units, {r.bad[0], r.bad[1]}, 0};
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + p.off_units);
+      uint32_t* to = reinterpret_cast<uint32_t*>(at + sizeof(MoeTable));
+      for (int i = threadIdx.x; i < Units::bytes(p.max_units) / 4; i += kUpThreads) to[i] = from[i];
+      float* shares = reinterpret_cast<float*>(at + sizeof(MoeTable) + Units::bytes(p.max_units));
+      for (int i = threadIdx.x; i < p.tokens * p.top; i += kUpThreads) {
+        shares[i] = share[i];
+        if (p.ids != nullptr) p.ids[i] = r.sel[i] == 0xffff ? -1 : (int)r.sel[i];
+        if (p.shares != nullptr) p.shares[i] = share[i];
+      }
+      share = nullptr;
+      __syncthreads();
+    }
+  }
   const uint32_t zeros = smem_u32(smem + p.off_zero);
 
   const int tiles = p.hidden / 32, chunks = (p.dim + S::kChunk - 1) / S::kChunk;
@@ -672,7 +733,6 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   using S = Stage<WT, F16>;
   constexpr int kUnit = kVectors / PARTS;  // tokens of a unit
   extern __shared__ __align__(1024) uint8_t smem[];
-  Routing& r = *reinterpret_cast<Routing*>(smem);
   float* tiles = reinterpret_cast<float*>(smem + p.off_red);  // a warp's tokens x 32 rows
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int max_vectors = min(p.tokens, kUnit) * PARTS;
@@ -682,17 +742,25 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank();
   const int row0 = (int)(blockIdx.x / ranks) * kRowsStage;
-  // launched by moe_up after its own wait: what came before that, the logits and the weights among it, is complete
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
-  const Units units(smem + p.off_units, p.max_units);
-  float* share = reinterpret_cast<float*>(smem + p.off_share);
-  route<kDownWarps, true>(r, units, p, kUnit, share);
+  griddep_wait();
+  griddep_launch_dependents();
+  // the routing as moe_up left it
+  {
+    const int words = (int)(sizeof(MoeTable) + Units::bytes(p.max_units) + p.tokens * p.top * 4) / 4;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p.table);
+    for (int i = threadIdx.x; i < words; i += kDownThreads) reinterpret_cast<uint32_t*>(smem)[i] = __ldcg(from + i);
+  }
+  const MoeTable& table = *reinterpret_cast<const MoeTable*>(smem);
+  const Units units(smem + sizeof(MoeTable), p.max_units);
+  const float* share = reinterpret_cast<const float*>(smem + sizeof(MoeTable) + Units::bytes(p.max_units));
+  __syncthreads();
   float* my = tiles + wid * kRowsStage * p.tokens;
   for (int i = lane; i < kRowsStage * p.tokens; i += 32) my[i] = 0.f;
   __syncwarp();
 
   const int chunks = (p.hidden + S::kChunk - 1) / S::kChunk;
-  const int total = r.units * chunks, warps = ranks * kDownWarps, me = rank * kDownWarps + wid;
+  const int total = table.units * chunks, warps = ranks * kDownWarps, me = rank * kDownWarps + wid;
   const int s0 = share_of(total, me, warps), s1 = share_of(total, me + 1, warps);
   int ps = s0, ps_c = s0 % chunks, ps_u = s0 / chunks, slot_p = 0;
   Unit pu{};
@@ -737,16 +805,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
       if (ps < s1) next_unit();
     }
   };
-  // the first stage's weights are asked for while moe_up ends
-  if (ps < s1) weights(0);
-  griddep_wait();
-  griddep_launch_dependents();
-  if (ps < s1) {
-    columns(0);
-    advance();
-  }
-  copies_commit();
-  for (int i = 0; i < p.ring - 2; ++i) {
+  for (int i = 0; i < p.ring - 1; ++i) {
     if (ps < s1) {
       weights(slot_p);
       columns(slot_p);
@@ -822,18 +881,12 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += v[k];
     sum *= p.scale;
-    if (r.bad[tok >> 5] >> (tok & 31) & 1u) sum = NAN;
+    if (table.bad[tok >> 5] >> (tok & 31) & 1u) sum = NAN;
     const long long at = (long long)tok * p.dim + row0 + row;
     if (p.out_bf16)
       static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(sum);
     else
       static_cast<float*>(p.out)[at] = sum;
-  }
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < p.tokens * p.top; i += kDownThreads) {
-      if (p.ids != nullptr) p.ids[i] = r.sel[i] == 0xffff ? -1 : (int)r.sel[i];
-      if (p.shares != nullptr) p.shares[i] = share[i];
-    }
   }
   if (ranks > 1) cl.sync();  // no CTA leaves while another reads its tiles
 }
@@ -852,9 +905,9 @@ cudaError_t allow_smem(K kern, const DeviceInfo& dev, bool (&done)[64]) {
 
 constexpr size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-// Units of a launch at most: an expert's last one may be part full.
-int max_units(const MoeParams& p, int used) {
-  const int pairs = p.tokens * p.top, n = used + pairs / p.unit;
+// Units of a launch at most (both kernels' arrays have this length): an expert's last one may be part full.
+int max_units(int tokens, int top, int experts, int unit) {
+  const int pairs = tokens * top, used = experts < pairs ? experts : pairs, n = used + pairs / unit;
   return n < pairs ? n : pairs;
 }
 
@@ -865,22 +918,22 @@ size_t room(const DeviceInfo& dev, int n) {
   return have < dev.smem_optin ? have : dev.smem_optin;
 }
 
+// (sets p.max_units, for launch_down as well)
 template <int WT, bool F16>
-cudaError_t launch_up(MoeParams p, bool x_f32, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStream_t stream) {
   using S = Stage<WT, F16>;
   const int most = x_f32 ? kVectors / 2 : kVectors;
   const int chunks = (p.dim + S::kChunk - 1) / S::kChunk;
   p.ks = 1;
   while (p.ks < kUpWarps && 2 * p.ks <= chunks) p.ks *= 2;
   const int slice = (chunks + p.ks - 1) / p.ks;
-  const int used = p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top;
   p.off_units = (int)round_up(sizeof(Routing), 16);
   // the warps' columns are kept where they leave room for the rings; units of fewer tokens where they do not (Q4_0 with float32 scales)
   size_t smem = 0;
   bool fits = false;
   for (p.unit = most; p.unit >= 1 && !fits; p.unit -= fits ? 0 : 1) {
     const int tokens = p.tokens < p.unit ? p.tokens : p.unit, columns = S::columns(x_f32 ? 2 * tokens : tokens);
-    p.max_units = max_units(p, used);
+    p.max_units = max_units(p.tokens, p.top, p.experts, p.unit < p.down_unit ? p.unit : p.down_unit);
     p.off_zero = (int)round_up(p.off_units + Units::bytes(p.max_units), 128);
     p.off_red = p.off_zero + 128;
     p.off_cols = p.off_red + 2 * kUpWarps * most * 64 * 4;
@@ -910,13 +963,9 @@ cudaError_t launch_up(MoeParams p, bool x_f32, const DeviceInfo& dev, cudaStream
 template <int WT, bool F16>
 cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream) {
   using S = Stage<WT, F16>;
-  const int unit = kVectors / p.parts, vectors = (p.tokens < unit ? p.tokens : unit) * p.parts;
+  const int vectors = (p.tokens < p.down_unit ? p.tokens : p.down_unit) * p.parts;
   const int stage = S::kBytes + S::columns(vectors);
-  p.unit = unit;
-  p.max_units = max_units(p, p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top);
-  p.off_units = (int)round_up(sizeof(Routing), 16);
-  p.off_share = p.off_units + Units::bytes(p.max_units);
-  p.off_zero = (int)round_up(p.off_share + (size_t)p.tokens * p.top * 4, 128);
+  p.off_zero = (int)round_up(sizeof(MoeTable) + Units::bytes(p.max_units) + (size_t)p.tokens * p.top * 4, 128);
   p.off_red = p.off_zero + 128;
   p.off_ring = (int)round_up(p.off_red + (size_t)kDownWarps * kRowsStage * p.tokens * 4, 128);
   size_t smem = 0;
@@ -959,7 +1008,8 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
 
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16) {
   const size_t t = tokens < kTokens ? tokens : kTokens;
-  return t * top * (hidden * 2 + hidden / 32 * 8) * (out_bf16 ? 1 : 2);
+  const int pairs = (int)t * top;
+  return (size_t)pairs * (hidden * 2 + hidden / 32 * 8) * (out_bf16 ? 1 : 2) + sizeof(MoeTable) + Units::bytes(pairs) + (size_t)pairs * 4;
 }
 
 cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -972,17 +1022,19 @@ cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t str
     p.x = static_cast<const uint8_t*>(a.x) + t0 * a.dim * (a.x_bf16 ? 2 : 4);
     p.out = static_cast<uint8_t*>(a.out) + t0 * a.dim * (a.out_bf16 ? 2 : 4);
     p.out_bf16 = a.out_bf16;
+    p.hidden = a.hidden;
+    p.top = a.top;
     p.h = static_cast<uint16_t*>(a.scratch);
     p.h_plane = (long long)p.tokens * a.top * a.hidden;
     p.parts = a.out_bf16 ? 1 : 2;
     p.h_factor = reinterpret_cast<float2*>(p.h + p.parts * p.h_plane);
+    p.table = reinterpret_cast<MoeTable*>(p.h_factor + (size_t)p.parts * p.tokens * p.top * (p.hidden / 32));
+    p.down_unit = kVectors / p.parts;
     p.w2_q4 = a.w2.wtype == QMV_Q4_0;
     p.ids = a.ids == nullptr ? nullptr : a.ids + t0 * a.top;
     p.shares = a.shares == nullptr ? nullptr : a.shares + t0 * a.top;
     p.experts = a.experts;
-    p.top = a.top;
     p.dim = a.dim;
-    p.hidden = a.hidden;
     p.renorm = a.renorm;
     p.act = a.act;
     p.scale = a.scale;

@@ -326,6 +326,7 @@ struct MoeArgs {
   float scale;
 };
 // One launch's part (at most 64 tokens), as its kernels get it.
+struct MoeTable;
 struct MoeParams {
   const uint8_t *q1, *d1, *q3, *d3, *q2, *d2;
   const float* logits;
@@ -333,6 +334,7 @@ struct MoeParams {
   void* out;
   uint16_t* h;        // halves of act(gate) * up, tokens * top rows of `hidden`, `parts` times
   float2* h_factor;   // of each 32 of a row: what products with them are multiplied by, what is taken off then
+  MoeTable* table;    // the routing, for moe_down
   int32_t* ids;
   float* shares;
   long long logits_stride;
@@ -341,13 +343,13 @@ struct MoeParams {
   int tokens, experts, top, dim, hidden;
   int renorm, act, out_bf16, w2_q4;
   float scale;
-  int unit;              // tokens of a unit at most
+  int unit, down_unit;   // tokens of a unit at most, moe_up's and moe_down's
   int tiles_item;        // tiles of 32 rows of an item (moe_up)
   int ks;                // warps that share a tile's columns (moe_up)
   int cached;            // chunks of the warps' columns that shared memory keeps (moe_up)
   int ring;              // stages of a warp's ring, 2 to 4
   int max_units;
-  int off_units, off_share, off_zero, off_red, off_cols, off_ring;  // places in shared memory
+  int off_units, off_zero, off_red, off_cols, off_ring;  // places in shared memory
 };
 constexpr int64_t kMoeMaxDim = 1 << 24;
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16);

@@ -78,82 +78,56 @@ __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// The experts of the tokens that this warp routes, two tokens at a time (each step waits for the one before it).  EACH: experts a lane
-// has.  share, where it is wanted, gets the tokens' shares.
-template <int W, int EACH>
+// The experts of the tokens that this warp routes, and their shares.  (Small rather than unrolled: code that runs once a launch costs what
+// it takes to fetch.)
+template <int W>
 __device__ __forceinline__ void choose(Routing& r, const MoeParams& p, float* share) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  for (int tok0 = wid; tok0 < p.tokens; tok0 += 2 * W) {
-    uint32_t key[2][EACH];
-    bool bad[2];
-    float sum[2], most[2];
-    uint32_t mine[2] = {0u, 0u};  // lane k: the k-th's key
+  constexpr int kEach = kExperts / 32;
+#pragma unroll 1
+  for (int tok = wid; tok < p.tokens; tok += W) {
+    uint32_t key[kEach], best = 0;
+    bool bad = false;
+    const float* logits = p.logits + tok * p.logits_stride + lane;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int tok = tok0 + s * W;
-      bool odd = false;
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < EACH; ++i) {
-        const int e = lane + 32 * i;
-        float l = -INFINITY;
-        if (tok < p.tokens && e < p.experts) l = __ldg(p.logits + tok * p.logits_stride + e);
-        odd |= !(l < INFINITY);
-        key[s][i] = l > -INFINITY ? ordered(l) : 0u;
-        best = max(best, key[s][i]);
-      }
-      bad[s] = __any_sync(0xffffffffu, odd);
-      sum[s] = most[s] = 0.f;
-      if (share != nullptr) {
-        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-        most[s] = high != 0 ? unordered(high) : 0.f;
-        if (!p.renorm) {
-#pragma unroll
-          for (int i = 0; i < EACH; ++i) sum[s] += key[s][i] != 0 ? expf(unordered(key[s][i]) - most[s]) : 0.f;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < EACH; ++i) key[s][i] = bad[s] ? 0u : key[s][i];
+    for (int i = 0; i < kEach; ++i) {
+      float l = -INFINITY;
+      if (lane + 32 * i < p.experts) l = __ldg(logits + 32 * i);
+      bad |= !(l < INFINITY);
+      key[i] = l > -INFINITY ? ordered(l) : 0u;
+      best = max(best, key[i]);
     }
+    bad = __any_sync(0xffffffffu, bad);
+    const uint32_t high0 = __reduce_max_sync(0xffffffffu, best);
+    const float most = high0 != 0 ? unordered(high0) : 0.f;
+    float sum = 0.f;
+    if (!p.renorm)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sum += key[i] != 0 ? expf(unordered(key[i]) - most) : 0.f;
+    uint32_t mine = 0u;  // lane k: the k-th's key
+#pragma unroll 1
     for (int k = 0; k < p.top; ++k) {
       // the lane's best: the larger key, then the lower expert
-      uint32_t best[2], high[2];
-      int at[2], e[2];
+      int at = lane;
+      best = key[0];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        best[s] = key[s][0];
-        at[s] = lane;
-#pragma unroll
-        for (int i = 1; i < EACH; ++i) {
-          at[s] = key[s][i] > best[s] ? lane + 32 * i : at[s];
-          best[s] = max(best[s], key[s][i]);
-        }
+      for (int i = 1; i < kEach; ++i) {
+        at = key[i] > best ? lane + 32 * i : at;
+        best = max(best, key[i]);
       }
+      const uint32_t high = bad ? 0u : __reduce_max_sync(0xffffffffu, best);
+      const int e = (int)__reduce_min_sync(0xffffffffu, best == high && high != 0 ? (unsigned)at : 0xffffu);
+      mine = lane == k ? high : mine;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) high[s] = __reduce_max_sync(0xffffffffu, best[s]);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) e[s] = (int)__reduce_min_sync(0xffffffffu, best[s] == high[s] && high[s] != 0 ? (unsigned)at[s] : 0xffffu);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        mine[s] = lane == k ? high[s] : mine[s];
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) key[s][i] = e[s] == lane + 32 * i ? 0u : key[s][i];
-        if (lane == s && tok0 + s * W < p.tokens) r.sel[(tok0 + s * W) * p.top + k] = (uint16_t)e[s];
-      }
+      for (int i = 0; i < kEach; ++i) key[i] = e == lane + 32 * i ? 0u : key[i];
+      if (lane == 0) r.sel[tok * p.top + k] = (uint16_t)e;
     }
+    if (bad && lane == 0) atomicOr(&r.bad[tok >> 5], 1u << (tok & 31));
+    const float w = mine != 0 ? expf(unordered(mine) - most) : 0.f;
+    float total = p.renorm ? w : sum;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int tok = tok0 + s * W;
-      if (tok >= p.tokens) continue;
-      if (bad[s] && lane == 0) atomicOr(&r.bad[tok >> 5], 1u << (tok & 31));
-      if (share != nullptr) {
-        const float w = mine[s] != 0 ? expf(unordered(mine[s]) - most[s]) : 0.f;
-        float total = p.renorm ? w : sum[s];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane < p.top) share[tok * p.top + lane] = bad[s] ? NAN : w == 0.f ? 0.f : __fdiv_rn(w, total);
-      }
-    }
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane < p.top) share[tok * p.top + lane] = bad ? NAN : w == 0.f ? 0.f : __fdiv_rn(w, total);
   }
 }
 
@@ -163,10 +137,7 @@ __device__ __forceinline__ void route(Routing& r, const MoeParams& p, float* sha
   for (int e = threadIdx.x; e < 2 * kExperts; e += 32 * W) r.mask[0][e] = 0u;
   if (threadIdx.x < 2) r.bad[threadIdx.x] = 0u;
   __syncthreads();
-  if (p.experts <= 128)
-    choose<W, 4>(r, p, share);
-  else
-    choose<W, kExperts / 32>(r, p, share);
+  choose<W>(r, p, share);
   __syncthreads();
   for (int i = threadIdx.x; i < p.tokens * p.top; i += 32 * W) {
     const int x = r.sel[i], tok = i / p.top;
@@ -190,7 +161,7 @@ __device__ __forceinline__ void form_units(Routing& r, const Units& units, const
   if (lane == 31) r.part[wid] = upto;
   __syncthreads();
   int all = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < W; ++w) {
     const int n = r.part[w];
     upto += w < wid ? n : 0;
@@ -504,7 +475,7 @@ __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, co
   const int lane = threadIdx.x & 31;
   constexpr int kPieces = S::kChunk / 8;  // of a token
   float2* factors = reinterpret_cast<float2*>(to + max_vectors * S::kVector);
-#pragma unroll 2
+#pragma unroll 1
   for (int i = 0; i < u.cols * kPieces; i += 32) {
     const int k = (i + lane) / kPieces, piece = (i + lane) % kPieces;
     const int tok = __shfl_sync(0xffffffffu, u.tok, k & 31);
@@ -559,26 +530,27 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   griddep_launch_dependents();
   if (threadIdx.x < 32) reinterpret_cast<uint32_t*>(smem + p.off_zero)[threadIdx.x] = 0u;
   const Units units(smem + p.off_units, p.max_units);
-  // the last CTA (whose run of items is none of the longer ones) leaves the routing for moe_down, in units of its own size, and the call's
-  // ids and shares.  (The rings' room is free as yet.)
-  const bool leaves = blockIdx.x == gridDim.x - 1;
-  float* share = leaves ? reinterpret_cast<float*>(smem + p.off_ring) : nullptr;
+  // The CTAs leave the routing for moe_down, in units of its own size, and the call's ids and shares: each a part (one CTA by itself would
+  // hold all others up, for code that it alone fetches).  The rings' room is free as yet.
+  float* share = reinterpret_cast<float*>(smem + p.off_ring);
   route<kUpWarps>(r, p, share);
-  for (int rounds = leaves && p.down_unit != p.unit ? 2 : 1; rounds > 0; --rounds) {
+#pragma unroll 1
+  for (int rounds = p.down_unit != p.unit ? 2 : 1, first = 1; rounds > 0; --rounds, first = 0) {
     form_units<kUpWarps>(r, units, p, rounds == 2 ? p.down_unit : p.unit);
-    if (share != nullptr) {
-      uint8_t* at = reinterpret_cast<uint8_t*>(p.table);
-      if (threadIdx.x == 0) *p.table = MoeTable{r.units, {r.bad[0], r.bad[1]}, 0};
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + p.off_units);
-      uint32_t* to = reinterpret_cast<uint32_t*>(at + sizeof(MoeTable));
-      for (int i = threadIdx.x; i < Units::bytes(p.max_units) / 4; i += kUpThreads) to[i] = from[i];
-      float* shares = reinterpret_cast<float*>(at + sizeof(MoeTable) + Units::bytes(p.max_units));
-      for (int i = threadIdx.x; i < p.tokens * p.top; i += kUpThreads) {
-        shares[i] = share[i];
-        if (p.ids != nullptr) p.ids[i] = r.sel[i] == 0xffff ? -1 : (int)r.sel[i];
-        if (p.shares != nullptr) p.shares[i] = share[i];
+    if (first != 0) {
+      const int places = p.tokens * p.top, words = Units::bytes(p.max_units) / 4, step = gridDim.x * kUpThreads;
+      uint32_t* to = reinterpret_cast<uint32_t*>(p.table + 1);
+      for (int i = blockIdx.x * kUpThreads + threadIdx.x; i < words + places; i += step) {
+        if (i < words) {
+          to[i] = reinterpret_cast<const uint32_t*>(smem + p.off_units)[i];
+        } else {
+          const int k = i - words;
+          to[i] = __float_as_uint(share[k]);
+          if (p.ids != nullptr) p.ids[k] = r.sel[k] == 0xffff ? -1 : (int)r.sel[k];
+          if (p.shares != nullptr) p.shares[k] = share[k];
+        }
       }
-      share = nullptr;
+      if (threadIdx.x == 0) *p.table = MoeTable{r.units, {r.bad[0], r.bad[1]}, 0};  // (the same from every CTA)
       __syncthreads();
     }
   }
@@ -622,6 +594,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     }
     copies_commit();
   };
+#pragma unroll 1
   for (int i = 0; i < p.ring - 1; ++i) issue();
 
   int cs = 0, held = -1;  // held: the unit that u is, and whose columns the cache has
@@ -651,14 +624,25 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
           c.b += c.b == zeros ? 0 : j * cache_bytes;
           c.xs += c.xs == zeros ? 0 : j * cache_bytes;
         }
-#pragma unroll
+        // rows 0 .. 15, then 16 .. 31: the sums change places between them, so that both are one piece of code
+#pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           __syncwarp();  // every lane is done with the slot that is filled next
           issue();
           wait_ring(p.ring);
           __syncwarp();
-          consume_any<WT, F16>(ring + cs * S::kBytes, c, sets, acc[m]);
+          consume_any<WT, F16>(ring + cs * S::kBytes, c, sets, acc[0]);
           cs = cs + 1 == p.ring ? 0 : cs + 1;
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float keep = acc[0][w][v][h];
+                acc[0][w][v][h] = acc[1][w][v][h];
+                acc[1][w][v][h] = keep;
+              }
         }
       }
     }
@@ -805,6 +789,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
       if (ps < s1) next_unit();
     }
   };
+#pragma unroll 1
   for (int i = 0; i < p.ring - 1; ++i) {
     if (ps < s1) {
       weights(slot_p);

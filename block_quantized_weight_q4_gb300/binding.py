@@ -766,37 +766,47 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, 
     Returns ids, int64 (rows,): what embed() and logprobs() take."""
     import torch
     f32 = torch.float32
-    for t in (logits, noise):
-        if t.dim() != 2 or t.dtype is not f32 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError("logits and noise must be float32 (rows, vocab) tensors with contiguous rows")
-    rows, vocab = logits.shape
-    if noise.shape != logits.shape:
+    shape = logits.shape
+    if len(shape) != 2 or logits.dtype is not f32 or noise.dtype is not f32:
+        raise ValueError("logits and noise must be float32 (rows, vocab) tensors with contiguous rows")
+    rows, vocab = shape
+    if noise.shape != shape:
         raise ValueError("noise must have the logits' shape")
-    for t, dtype in ((temperature, f32), (top_k, torch.int32), (top_p, f32), (min_p, f32)):
-        if t is not None and (t.dtype is not dtype or t.shape != (rows,) or not t.is_contiguous()):
-            raise ValueError("temperature, top_p and min_p must be contiguous float32 (rows,) tensors, top_k int32")
+    ls, ns = logits.stride(), noise.stride()
+    if vocab > 1 and (ls[1] != 1 or ns[1] != 1):
+        raise ValueError("logits and noise must be float32 (rows, vocab) tensors with contiguous rows")
     if ids is None:
         ids = torch.empty((rows,), dtype=torch.int64, device=logits.device)
     elif ids.dtype is not torch.int64 or ids.shape != (rows,) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int64 (rows,) tensor")
-    st = load_library().qmv_sample(rows, vocab, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, noise.data_ptr(),
-                                   noise.stride(0) if rows > 1 else vocab,
-                                   None if temperature is None else temperature.data_ptr(),
-                                   None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
-                                   None if min_p is None else min_p.data_ptr(), ids.data_ptr(),
-                                   _raw_stream(stream, logits.get_device(), noise.get_device(), ids.get_device(),
-                                               *[t.get_device() for t in (temperature, top_k, top_p, min_p) if t is not None]))
+    on, at = [noise.get_device(), ids.get_device()], []
+    for t, dtype in ((temperature, f32), (top_k, torch.int32), (top_p, f32), (min_p, f32)):
+        if t is None:
+            at.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != (rows,) or not t.is_contiguous():
+            raise ValueError("temperature, top_p and min_p must be contiguous float32 (rows,) tensors, top_k int32")
+        at.append(t.data_ptr())
+        on.append(t.get_device())
+    st = load_library().qmv_sample(rows, vocab, logits.data_ptr(), ls[0] if rows > 1 else vocab, noise.data_ptr(),
+                                   ns[0] if rows > 1 else vocab, *at, ids.data_ptr(), _raw_stream(stream, logits.get_device(), *on))
     _check(st, "qmv_sample")
     return ids
 
 
-def _out_type(out, what="out"):
-    import torch
-    if out == "f32":
-        return X_F32, torch.float32
-    if out == "bf16":
-        return X_BF16, torch.bfloat16
-    raise ValueError(f"{what} must be 'bf16' or 'f32'")
+_OUT_TYPES = None
+
+
+def _out_type(out):
+    """The code and torch type of "f32" or "bf16"."""
+    global _OUT_TYPES
+    if _OUT_TYPES is None:
+        import torch
+        _OUT_TYPES = {"f32": (X_F32, torch.float32), "bf16": (X_BF16, torch.bfloat16)}
+    found = _OUT_TYPES.get(out)
+    if found is None:
+        raise ValueError("out must be 'bf16' or 'f32'")
+    return found
 
 
 def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: float = 1.0, out="f32", y=None, stream=None):
@@ -807,11 +817,13 @@ def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: fl
     code, dtype = _out_type(out)
     if ids.dtype is not torch.int64 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int64 tensor")
-    if W.dtype is not torch.uint8 or not W.is_contiguous() or W.numel() < weight_bytes(wtype, scale_dtype, vocab, cols):
+    n = vocab * cols
+    need = ((n if wtype == Q8_0 else n // 2) + 63) // 64 * 64 + n // 32 * (2 if scale_dtype == SCALE_F16 else 4)  # the image's bytes
+    if W.dtype is not torch.uint8 or W.numel() < need or not W.is_contiguous():
         raise ValueError("W must be a contiguous uint8 tensor of the matrix image's bytes")
     shape = ids.shape + (cols,)
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=W.device)
+        y = torch.empty(shape, dtype=dtype, device=ids.device)
     elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
         raise ValueError("y must be a contiguous tensor of ids' shape and cols, of the output's type")
     st = load_library().qmv_embed(wtype, scale_dtype, vocab, cols, W.data_ptr(), ids.data_ptr(), ids.numel(), scale, code,
@@ -823,10 +835,14 @@ def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: fl
 ROPE_PAIRS = {"neighbours": 0, "halves": 1}
 
 
-def _rope_rows(t, heads, dim, rows, what):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.shape[0] != rows:
-        raise ValueError(f"{what} must be a ({rows}, {heads}, {dim}) tensor")
-    return _head_rows(t, heads, dim, rows, what)
+def _stride_of_rows(t, shape, what):
+    """The row stride of a tensor of that shape, (rows, heads, dim), whose rows are contiguous."""
+    if t.shape == shape:
+        rows, heads, dim = shape
+        row, head, value = t.stride()
+        if (value == 1 and (head == dim or heads == 1)) or rows == 0:
+            return row if rows > 1 else heads * dim
+    raise ValueError(f"{what} must be a {tuple(shape)} tensor with contiguous rows")
 
 
 def qk_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps: float = 1e-6, pairs="halves", factor: float = 1.0, out=None,
@@ -838,48 +854,61 @@ def qk_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps: float = 1e-6, pa
     (2i and 2i + 1).  out: "f32" or "bf16" (q's own type by default).  q_out, k_out: where to write (q and k themselves
     for an update in place).  Returns q_out, k_out."""
     import torch
-    if q.dim() != 3:
+    shape, xt, f32 = q.shape, q.dtype, torch.float32
+    if len(shape) != 3:
         raise ValueError("q must be a (rows, heads, head_dim) tensor")
-    rows, heads, dim = q.shape
+    rows, heads, dim = shape
     x = _x_dtype(q)
-    qs, kvh, ks = _rope_rows(q, heads, dim, rows, "q"), 0, 0
-    if k is not None:
-        if k.dim() != 3 or k.dtype is not q.dtype:
+    if pairs not in ROPE_PAIRS:
+        raise ValueError("pairs must be 'halves' or 'neighbours'")
+    code, dtype = (x, xt) if out is None else _out_type(out)
+    qs = _stride_of_rows(q, shape, "q")
+    if q_out is None:
+        q_out, qos = torch.empty(shape, dtype=dtype, device=q.device), heads * dim
+    else:
+        qos = _stride_of_rows(q_out, shape, "q_out")
+    on = [q_out.get_device()]
+    if k is None:
+        if k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight need k")
+        kvh = ks = kos = 0
+        kp = kop = None
+    else:
+        kshape = k.shape
+        if len(kshape) != 3 or k.dtype is not xt:
             raise ValueError("k must be a (rows, kv_heads, head_dim) tensor of q's type")
-        kvh = k.shape[1]
-        ks = _rope_rows(k, kvh, dim, rows, "k")
-    f32 = torch.float32
-    if (pos is None) != (freq is None):
-        raise ValueError("pos and freq go together")
-    rot = 0
-    if freq is not None:
+        kvh = kshape[1]
+        ks = _stride_of_rows(k, (rows, kvh, dim), "k")
+        if k_out is None:
+            k_out, kos = torch.empty(kshape, dtype=dtype, device=q.device), kvh * dim
+        else:
+            kos = _stride_of_rows(k_out, (rows, kvh, dim), "k_out")
+            if k_out.dtype is not dtype:
+                raise ValueError("q_out and k_out must be of the output's type")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        on += (k.get_device(), k_out.get_device())
+    if q_out.dtype is not dtype:
+        raise ValueError("q_out and k_out must be of the output's type")
+    if freq is None or pos is None:
+        if freq is not pos:
+            raise ValueError("pos and freq go together")
+        rot, pp, fp = 0, None, None
+    else:
         if freq.dtype is not f32 or freq.dim() != 1 or not freq.is_contiguous():
             raise ValueError("freq must be a contiguous float32 (rot_dim / 2,) tensor")
         if pos.dtype is not torch.int32 or pos.shape != (rows,) or not pos.is_contiguous():
             raise ValueError("pos must be a contiguous int32 (rows,) tensor")
-        rot = 2 * freq.shape[0]
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not f32 or w.shape != (dim,) or not w.is_contiguous()):
-            raise ValueError("q_weight and k_weight must be contiguous float32 (head_dim,) tensors")
-    if pairs not in ROPE_PAIRS:
-        raise ValueError("pairs must be 'halves' or 'neighbours'")
-    code, dtype = (x, q.dtype) if out is None else _out_type(out)
-    if q_out is None:
-        q_out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device)
-    if k is None:
-        if k_out is not None or k_weight is not None:
-            raise ValueError("k_out and k_weight need k")
-    elif k_out is None:
-        k_out = torch.empty((rows, kvh, dim), dtype=dtype, device=k.device)
-    if q_out.dtype is not dtype or (k_out is not None and k_out.dtype is not dtype):
-        raise ValueError("q_out and k_out must be of the output's type")
-    qos = _rope_rows(q_out, heads, dim, rows, "q_out")
-    kos = 0 if k is None else _rope_rows(k_out, kvh, dim, rows, "k_out")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    st = load_library().qmv_qk_rope(x, rows, heads, kvh, dim, q.data_ptr(), qs, ptr(k), ks, ptr(q_weight), ptr(k_weight), eps,
-                                    ptr(pos), ptr(freq), rot, ROPE_PAIRS[pairs], factor, code, q_out.data_ptr(), qos, ptr(k_out), kos,
-                                    _raw_stream(stream, q.get_device(), *[t.get_device() for t in
-                                                (k, pos, freq, q_weight, k_weight, q_out, k_out) if t is not None]))
+        rot, pp, fp = 2 * freq.numel(), pos.data_ptr(), freq.data_ptr()
+        on += (pos.get_device(), freq.get_device())
+    wp = [None, None]
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is not None:
+            if w.dtype is not f32 or w.shape != (dim,) or not w.is_contiguous():
+                raise ValueError("q_weight and k_weight must be contiguous float32 (head_dim,) tensors")
+            wp[i] = w.data_ptr()
+            on.append(w.get_device())
+    st = load_library().qmv_qk_rope(x, rows, heads, kvh, dim, q.data_ptr(), qs, kp, ks, wp[0], wp[1], eps, pp, fp, rot, ROPE_PAIRS[pairs],
+                                    factor, code, q_out.data_ptr(), qos, kop, kos, _raw_stream(stream, q.get_device(), *on))
     _check(st, "qmv_qk_rope")
     return q_out, k_out
 
@@ -902,6 +931,7 @@ class Moe:
             if W.dtype is not torch.uint8 or not W.is_contiguous() or need == 0 or W.numel() < need:
                 raise ValueError("W1, W3 and W2 must be contiguous uint8 tensors of the matrix images' bytes")
         self.experts, self.dim, self.hidden = experts, dim, hidden
+        self._scratch = {}  # bytes of scratch memory, by the call's numbers
         self.W1, self.W3, self.W2 = W1, W3, W2
         self._c = _MoeC(wtype13, wtype2, scale_dtype, experts, dim, hidden, W1.data_ptr(), W3.data_ptr(), W2.data_ptr())
         self._p = ctypes.addressof(self._c)
@@ -916,32 +946,36 @@ def moe(layer: Moe, x, logits, top: int, renorm: bool = True, scale: float = 1.0
     torch's allocator for this call (with a stream other than the current one, give it, and keep it until that stream is done)."""
     import torch
     code, dtype = _out_type(out)
-    if act not in ACT_CODES:
+    act_code = ACT_CODES.get(act)
+    if act_code is None:
         raise ValueError("act must be 'silu' or 'gelu'")
-    if x.dim() != 2 or x.shape[1] != layer.dim or not x.is_contiguous():
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != layer.dim or not x.is_contiguous():
         raise ValueError("x must be a contiguous (tokens, dim) tensor")
-    n = x.shape[0]
-    if logits.dtype is not torch.float32 or logits.shape != (n, layer.experts) or (layer.experts > 1 and logits.stride(1) != 1):
+    n, experts = shape[0], layer.experts
+    if logits.dtype is not torch.float32 or logits.shape != (n, experts) or (experts > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a float32 (tokens, experts) tensor with contiguous rows")
+    dev = x.device
     if y is None:
-        y = torch.empty((n, layer.dim), dtype=dtype, device=x.device)
-    elif y.dtype is not dtype or y.shape != (n, layer.dim) or not y.is_contiguous():
+        y = torch.empty(shape, dtype=dtype, device=dev)
+    elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
         raise ValueError("y must be a contiguous (tokens, dim) tensor of the output's type")
-    need = moe_scratch_bytes(n, top, layer.hidden, out)
+    need = layer._scratch.get((n, top, code))
+    if need is None:
+        need = layer._scratch[n, top, code] = moe_scratch_bytes(n, top, layer.hidden, out)
     if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         if stream is not None:
             scratch.record_stream(stream)
     elif scratch.dtype is not torch.uint8 or scratch.numel() < need or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous uint8 tensor of moe_scratch_bytes()")
-    ids = shares = None
+    ids = shares = ip = sp = None
     if routing:
-        ids = torch.empty((n, top), dtype=torch.int32, device=x.device)
-        shares = torch.empty((n, top), dtype=torch.float32, device=x.device)
-    st = load_library().qmv_moe(layer._p, n, logits.data_ptr(), logits.stride(0) if n > 1 else layer.experts, top, 1 if renorm else 0,
-                                scale, ACT_CODES[act], _x_dtype(x), x.data_ptr(), code, y.data_ptr(),
-                                None if ids is None else ids.data_ptr(), None if shares is None else shares.data_ptr(),
-                                scratch.data_ptr(),
+        ids = torch.empty((n, max(top, 0)), dtype=torch.int32, device=dev)
+        shares = torch.empty((n, max(top, 0)), dtype=torch.float32, device=dev)
+        ip, sp = ids.data_ptr(), shares.data_ptr()
+    st = load_library().qmv_moe(layer._p, n, logits.data_ptr(), logits.stride(0) if n > 1 else experts, top, 1 if renorm else 0, scale,
+                                act_code, _x_dtype(x), x.data_ptr(), code, y.data_ptr(), ip, sp, scratch.data_ptr(),
                                 _raw_stream(stream, x.get_device(), logits.get_device(), y.get_device(), scratch.get_device(), layer._index))
     _check(st, "qmv_moe")
     return (y, ids, shares) if routing else y

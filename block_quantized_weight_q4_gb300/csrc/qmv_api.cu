@@ -843,6 +843,8 @@ int qmv_qk_rope(int x_dtype, int64_t rows, int heads, int kv_heads, int head_dim
   if (st != QMV_OK) return st;
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || (rot_dim > 0 && (!aligned(pos, 4) || !aligned(freq, 4))))
     return QMV_E_ALIGN;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return QMV_E_CUDA;
   RopeArgs a;
   a.q = q;
   a.k = k;
@@ -861,7 +863,7 @@ int qmv_qk_rope(int x_dtype, int64_t rows, int heads, int kv_heads, int head_dim
   a.rot = rot_dim;
   a.eps = eps;
   a.factor = factor;
-  return launch_rope(a, head_dim, x_dtype == QMV_X_BF16, out_dtype == QMV_X_BF16, pairs == QMV_ROPE_HALVES, rows, stream) ==
+  return launch_rope(a, head_dim, x_dtype == QMV_X_BF16, out_dtype == QMV_X_BF16, pairs == QMV_ROPE_HALVES, rows, dev, stream) ==
                  cudaSuccess
              ? QMV_OK
              : QMV_E_CUDA;

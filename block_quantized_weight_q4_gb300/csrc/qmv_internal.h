@@ -309,7 +309,8 @@ struct RopeArgs {
   int rot;
   float eps, factor;
 };
-cudaError_t launch_rope(const RopeArgs& a, int head_dim, bool x_bf16, bool out_bf16, bool halves, int64_t rows, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& a, int head_dim, bool x_bf16, bool out_bf16, bool halves, int64_t rows, const DeviceInfo& dev,
+                        cudaStream_t stream);
 
 struct MoeArgs {
   MatrixRef w1, w3, w2;

@@ -4,9 +4,14 @@
 //   (a, b) -> (a cos t - b sin t, a sin t + b cos t) factor,   t = pos freq_i,
 // for the pairs (s_2i, s_2i+1) or (s_i, s_i+rot/2) of a head's first `rot` values; the others pass.
 //
-// Angles: t is formed in 64 bits in turns, and what is left of whole turns goes to cospi / sinpi in float32, so a far
-// position costs no accuracy.  That is rot / 2 angles a row, once for all its heads, in shared memory: the 64-bit work is
-// 10 operations an angle, shared by all heads.
+// Angles: a frequency in turns as an integer of 64 bits, once a CTA; times the position, whose whole turns fall off the integer's top, it is
+// the angle to 2^-33 turns at any position (64 x 32-bit integer products in place of the 64-bit floating point that a GB300 has little
+// of).  sinpi / cospi of that in float32, once for all heads of a row, in shared memory.
+//
+// Bound by the rows' bytes in and out; below that by a chain of loads, angles, one barrier and stores, so a CTA takes several rows where
+// there are many: their angles together, their values two rows ahead.
+#include <type_traits>
+
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
 
@@ -14,125 +19,144 @@ namespace qmv {
 
 namespace {
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 
-// pos * freq radians, less its whole turns, in units of pi: the product (31 + 24 bits) and its product with 1 / 2 pi (106 bits,
-// in two parts) keep what 64 bits round away, so the error is the float32 rounding of the result alone.
-__device__ __forceinline__ float angle(double pos, double freq) {
-  const double kTurn = 0.15915494309189535, kTurnLow = -9.8393383375912e-18;  // 1 / 2 pi
-  const double a = pos * freq, a_low = fma(pos, freq, -a);
-  const double t = a * kTurn;
-  const double low = fma(a, kTurn, -t) + fma(a, kTurnLow, a_low * kTurn);
-  return (float)(2.0 * ((t - rint(t)) + low));
+// freq radians in turns, the fraction of one in units of 2^-64: freq / 2 pi in two parts of 53 bits, so that what is rounded is
+// below a unit or two.
+__device__ __forceinline__ unsigned long long turns_of(double freq) {
+  const double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;  // 1 / 2 pi
+  const double t = freq * kTurn, low = fma(freq, kTurn, -t) + freq * kTurnLow;
+  const double part = t - floor(t);  // (exact)
+  return (unsigned long long)(part * 0x1p64) + (unsigned long long)(long long)(low * 0x1p64);
 }
 
-// A CTA takes one row: a group of D / 8 lanes holds a head, 8 values a lane.
+// A CTA takes `block` rows: a group of D / 8 lanes holds a head of a row, 8 values a lane: eight in a row, or (HALVES) four of the lower half
+// and the four that turn with them, so that no value changes lanes.
 template <int D, bool XB, bool OB, bool HALVES>
-__global__ void __launch_bounds__(kMaxThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 2) rope_kernel(const __grid_constant__ RopeArgs a, long long rows, int block) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int L = D / 8;
-  __shared__ float2 turn[D / 2];
-  const long long row = blockIdx.x;
+  extern __shared__ float2 turn[];  // block x rot / 2
+  const long long row0 = (long long)blockIdx.x * block;
+  const int n = (int)min((long long)block, rows - row0);
   const int heads = a.heads + a.kv_heads;
   const int gl = threadIdx.x % L;
   const int slots = blockDim.x / L;
-  float v[8];
-  auto load = [&](int head) {
+  // the lane's two fours: values lo .. lo + 3 and hi .. hi + 3 of the head; four angles where it turns
+  const bool turns_here = 8 * gl < a.rot;
+  const int lo = HALVES && turns_here ? 4 * gl : 8 * gl, hi = HALVES && turns_here ? a.rot / 2 + 4 * gl : 8 * gl + 4;
+  using Raw = typename std::conditional<XB, uint2, float4>::type;
+  alignas(16) Raw raw[2][2];  // two rows' values are on their way
+  const int mine = threadIdx.x / L;
+  auto load = [&](Raw (&to)[2], int head, int r) {
+    if (head >= heads || r >= n) return;
     const bool is_k = head >= a.heads;
-    const void* x = is_k ? a.k : a.q;
-    const long long at = is_k ? row * a.k_stride + (long long)(head - a.heads) * D : row * a.q_stride + (long long)head * D;
+    const long long at = is_k ? (row0 + r) * a.k_stride + (long long)(head - a.heads) * D : (row0 + r) * a.q_stride + (long long)head * D;
     // (plain loads: the outputs may be the inputs' own places)
-    if (XB) {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at + 8 * gl);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    constexpr int kSize = XB ? 2 : 4;
+    const uint8_t* x = static_cast<const uint8_t*>(is_k ? a.k : a.q) + at * kSize;
+    if (XB && !HALVES) {
+      const uint4 u = *reinterpret_cast<const uint4*>(x + lo * kSize);
+      reinterpret_cast<uint4&>(to) = u;
     } else {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 8 * gl);
-      const float4 f0 = f[0], f1 = f[1];
-      v[0] = f0.x, v[1] = f0.y, v[2] = f0.z, v[3] = f0.w;
-      v[4] = f1.x, v[5] = f1.y, v[6] = f1.z, v[7] = f1.w;
+      to[0] = *reinterpret_cast<const Raw*>(x + lo * kSize);
+      to[1] = *reinterpret_cast<const Raw*>(x + hi * kSize);
     }
   };
-  int head = threadIdx.x / L;
-  if (head < heads) load(head);  // on its way while the angles are formed
+  load(raw[0], mine, 0);  // while the angles are formed
+  load(raw[1], mine, 1);
   const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    const float half_turns = angle((double)__ldg(a.pos + row), (double)__ldg(a.freq + i));
+  unsigned long long turns = 0;
+  for (int i = threadIdx.x, held = -1; i < half * n; i += blockDim.x) {
+    const int r = i / half, f = i - r * half;
+    if (f != held) turns = turns_of((double)__ldg(a.freq + f)), held = f;
+    const unsigned long long t = turns * (unsigned long long)(long long)__ldg(a.pos + row0 + r);
+    // the upper half as a signed number of half turns
     float c, s;
-    sincospif(half_turns, &s, &c);
-    turn[i] = make_float2(c * a.factor, s * a.factor);
+    sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+    // the first pairs of the lanes' four angles, then the second: 16-byte loads of neighbours lie in different banks
+    turn[r * half + ((f & 2) / 2 * (half / 4) + f / 4) * 2 + (f & 1)] = make_float2(c * a.factor, s * a.factor);
   }
   __syncthreads();
   // every lane of a warp goes round as often: the shuffles need them all
-  for (int first = 0; first < heads; first += slots, head += slots) {
-    const bool live = head < heads;
-    if (!live) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    } else if (first > 0) {
-      load(head);
-    }
-    const bool is_k = head >= a.heads;
+  for (int first = 0; first < heads; first += slots) {
+    const int head = first + mine;
+    const bool live = head < heads, is_k = head >= a.heads;
     const float* w = is_k ? a.k_weight : a.q_weight;
-    if (a.q_weight != nullptr || a.k_weight != nullptr) {
-      float sum = 0.f;
+    float ww[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (w != nullptr && live) {
-        const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), a.eps));
-        const float4* wf = reinterpret_cast<const float4*>(w + 8 * gl);
-        const float4 w0 = __ldg(wf), w1 = __ldg(wf + 1);
-        const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], r), ww[e]);
-      }
+    for (int e = 0; e < 8; ++e) ww[e] = w != nullptr ? __ldg(w + (e < 4 ? lo + e : hi + e - 4)) : 0.f;
+    if (first > 0) {
+      load(raw[0], head, 0);
+      load(raw[1], head, 1);
     }
-    if (HALVES) {
-      const int hl = a.rot / 16;  // lanes of a half
-      const bool lower = gl < hl, in = gl < 2 * hl;
-      const int lane = threadIdx.x & 31;
-      const int from = !in ? lane : lower ? lane + hl : lane - hl;
+    auto one = [&](Raw (&from)[2], int r) {
+      float v[8];
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(from);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = __shfl_sync(0xffffffffu, v[e], from);
-        if (in) {
-          const float2 t = turn[8 * (lower ? gl : gl - hl) + e];
-          v[e] = lower ? fmaf(v[e], t.x, -__fmul_rn(u, t.y)) : fmaf(u, t.y, __fmul_rn(v[e], t.x));
+      for (int e = 0; e < 8; ++e) v[e] = !live ? 0.f : XB ? __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16) : __uint_as_float(u[e]);
+      load(from, head, r + 2);
+      if (a.q_weight != nullptr || a.k_weight != nullptr) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (w != nullptr && live) {
+          const float s = __frsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), a.eps));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], s), ww[e]);
         }
       }
-    } else if (8 * gl < a.rot) {
+      if (turns_here) {
+        const float4* table = reinterpret_cast<const float4*>(turn + r * half);
+        const float4 t0 = table[gl], t1 = table[half / 4 + gl];
+        const float c[4] = {t0.x, t0.z, t1.x, t1.z}, s[4] = {t0.y, t0.w, t1.y, t1.w};
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 t = turn[4 * gl + e / 2];
-        const float x0 = v[e], x1 = v[e + 1];
-        v[e] = fmaf(x0, t.x, -__fmul_rn(x1, t.y));
-        v[e + 1] = fmaf(x0, t.y, __fmul_rn(x1, t.x));
+        for (int i = 0; i < 4; ++i) {
+          float &x = v[HALVES ? i : 2 * i], &y = v[HALVES ? i + 4 : 2 * i + 1];
+          const float u = x;
+          x = fmaf(u, c[i], -__fmul_rn(y, s[i]));
+          y = fmaf(u, s[i], __fmul_rn(y, c[i]));
+        }
       }
-    }
-    if (live) {
-      void* out = is_k ? a.k_out : a.q_out;
-      const long long at = (is_k ? row * a.k_out_stride + (long long)(head - a.heads) * D : row * a.q_out_stride + (long long)head * D) + 8 * gl;
-      if (OB) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
-            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        f[0] = make_float4(v[0], v[1], v[2], v[3]);
-        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+      if (live) {
+        constexpr int kSize = OB ? 2 : 4;
+        const long long at = is_k ? (row0 + r) * a.k_out_stride + (long long)(head - a.heads) * D : (row0 + r) * a.q_out_stride + (long long)head * D;
+        uint8_t* out = static_cast<uint8_t*>(is_k ? a.k_out : a.q_out) + at * kSize;
+        if (OB) {
+          const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          if (HALVES) {
+            *reinterpret_cast<uint2*>(out + lo * 2) = make_uint2(w.x, w.y);
+            *reinterpret_cast<uint2*>(out + hi * 2) = make_uint2(w.z, w.w);
+          } else {
+            *reinterpret_cast<uint4*>(out + lo * 2) = w;
+          }
+        } else {
+          *reinterpret_cast<float4*>(out + lo * 4) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(out + hi * 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
       }
+    };
+    for (int r = 0; r < n; r += 2) {
+      one(raw[0], r);
+      if (r + 1 < n) one(raw[1], r + 1);
     }
   }
 }
 
 template <int D>
-cudaError_t launch_dim(const RopeArgs& a, bool x_bf16, bool out_bf16, bool halves, int64_t rows, cudaStream_t stream) {
-  const int lanes = (a.heads + a.kv_heads) * (D / 8);
-  const int threads = lanes >= kMaxThreads ? kMaxThreads : (lanes + 31) / 32 * 32;
-  auto go = [&](auto kern) { return launch_dependent(kern, dim3((unsigned)rows), threads, 0, stream, a); };
+cudaError_t launch_dim(const RopeArgs& a, bool x_bf16, bool out_bf16, bool halves, int64_t rows, const DeviceInfo& dev, cudaStream_t stream) {
+  // the heads in as few even shares as the threads take
+  const int heads = a.heads + a.kv_heads, most = kMaxThreads / (D / 8), shares = (heads + most - 1) / most;
+  const int threads = ((heads + shares - 1) / shares * (D / 8) + 31) / 32 * 32;
+  // rows of a CTA: up to 8, so that every SM still gets as many CTAs as it holds twice over
+  int block = 1;
+  while (block < 8 && rows / (2 * block) >= 2LL * dev.sm_count * (2048 / threads)) block *= 2;
+  auto go = [&](auto kern) {
+    return launch_dependent(kern, dim3((unsigned)((rows + block - 1) / block)), threads, (size_t)block * a.rot / 2 * sizeof(float2), stream, a, rows, block);
+  };
   if (x_bf16) {
     if (out_bf16) return halves ? go(rope_kernel<D, true, true, true>) : go(rope_kernel<D, true, true, false>);
     return halves ? go(rope_kernel<D, true, false, true>) : go(rope_kernel<D, true, false, false>);
@@ -143,10 +167,11 @@ cudaError_t launch_dim(const RopeArgs& a, bool x_bf16, bool out_bf16, bool halve
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, int head_dim, bool x_bf16, bool out_bf16, bool halves, int64_t rows, cudaStream_t stream) {
-  if (head_dim == 64) return launch_dim<64>(a, x_bf16, out_bf16, halves, rows, stream);
-  if (head_dim == 128) return launch_dim<128>(a, x_bf16, out_bf16, halves, rows, stream);
-  return launch_dim<256>(a, x_bf16, out_bf16, halves, rows, stream);
+cudaError_t launch_rope(const RopeArgs& a, int head_dim, bool x_bf16, bool out_bf16, bool halves, int64_t rows, const DeviceInfo& dev,
+                        cudaStream_t stream) {
+  if (head_dim == 64) return launch_dim<64>(a, x_bf16, out_bf16, halves, rows, dev, stream);
+  if (head_dim == 128) return launch_dim<128>(a, x_bf16, out_bf16, halves, rows, dev, stream);
+  return launch_dim<256>(a, x_bf16, out_bf16, halves, rows, dev, stream);
 }
 
 }  // namespace qmv

@@ -73,9 +73,9 @@ struct Row {
 
 // A logit's distance below the maximum in powers of two, its bucket and its weight.
 __device__ __forceinline__ float below(const Row& r, float x) { return (r.max - x) * r.scale; }
-__device__ __forceinline__ int bucket_of(float t) {  // (NaN, of 0 * inf, gives 0)
-  return min((int)(t * 32.f), kBuckets - 1);
-}
+// (The nearest 32nd, by an addition that leaves it in the lowest bits: conversions have a quarter of the rate.)
+__device__ __forceinline__ int bucket_of(float t) { return __float_as_int(fminf(t * 32.f, (float)(kBuckets - 1)) + 8388608.f) & (kBuckets - 1); }
+static_assert((kBuckets & (kBuckets - 1)) == 0, "a mask");
 __device__ __forceinline__ float exp2_of(float t) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
@@ -138,6 +138,11 @@ __device__ __forceinline__ float log2_of_normal(float e) {  // (-infinity for su
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(e));
   return y;
 }
+// x's score in powers of two below the maximum's, with the random number e.
+__device__ __forceinline__ float score_of(const Row& r, float x, float e) {
+  const float t = e >= 0x1p-126f ? log2_of_normal(e) : e > 0.f ? log2_of(e) : INFINITY;
+  return fmaf(x - r.max, r.scale, -t);
+}
 
 struct Shared {
   uint32_t count[kBuckets], low[kBuckets], high[kBuckets];
@@ -169,13 +174,15 @@ struct Shared {
 static_assert(sizeof(float) * (kChunks + 1) <= 3 * sizeof(uint32_t) * kBuckets, "the buckets' room holds the chunks' best scores");
 
 __device__ __forceinline__ float block_max(Shared& sh, float v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5] = v;
+  if (lane == 0) sh.part[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = sh.part[0];
-  for (int w = 1; w < kWarps; ++w) v = fmaxf(v, sh.part[w]);
+  v = sh.part[lane % kWarps];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -193,16 +200,21 @@ __device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, Key& m, uint
   __syncthreads();
   if (lane == 31) sh.scan_count[wid] = c, sh.scan_mass[wid] = m;
   __syncthreads();
-  uint32_t bc = 0;
-  Key bm = 0;
-  all_c = 0, all_m = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == wid) bc = all_c, bm = all_m;
-    all_c += sh.scan_count[w];
-    all_m += sh.scan_mass[w];
+  // the warps' totals, scanned by every warp for itself
+  uint32_t wc = sh.scan_count[lane % kWarps];
+  Key wm = sh.scan_mass[lane % kWarps];
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const uint32_t uc = __shfl_up_sync(0xffffffffu, wc, o, kWarps);
+    const Key um = __shfl_up_sync(0xffffffffu, wm, o, kWarps);
+    if (lane % kWarps >= o) wc += uc, wm += um;
   }
-  c += bc - c0;
-  m += bm - m0;
+  all_c = __shfl_sync(0xffffffffu, wc, kWarps - 1);
+  all_m = __shfl_sync(0xffffffffu, wm, kWarps - 1);
+  const uint32_t bc = __shfl_sync(0xffffffffu, wc, (wid + 31) & 31);
+  const Key bm = __shfl_sync(0xffffffffu, wm, (wid + 31) & 31);
+  c += (wid > 0 ? bc : 0u) - c0;
+  m += (wid > 0 ? bm : 0ull) - m0;
 }
 
 __device__ __forceinline__ void add(Shared& sh, int b, uint32_t mass) {
@@ -216,10 +228,10 @@ __device__ __forceinline__ void clear(Shared& sh) {
 }
 
 // A thread's two buckets over all ranks.
-__device__ __forceinline__ void gather(cg::cluster_group& cl, Shared& sh, int ranks, uint32_t (&c)[2], Key (&m)[2]) {
+__device__ void gather(cg::cluster_group& cl, Shared& sh, int ranks, uint32_t (&c)[2], Key (&m)[2]) {
   c[0] = c[1] = 0;
   m[0] = m[1] = 0;
-#pragma unroll 2
+#pragma unroll 4
   for (int r = 0; r < ranks; ++r) {
     const Shared* o = ranks == 1 ? &sh : cl.map_shared_rank(&sh, r);
     const uint2 n = reinterpret_cast<const uint2*>(o->count)[threadIdx.x], l = reinterpret_cast<const uint2*>(o->low)[threadIdx.x],
@@ -257,21 +269,42 @@ __device__ bool find_border(Shared& sh, const uint32_t (&c)[2], const Key (&m)[2
   return found;
 }
 
-// The smallest mapped logit whose bucket is at most b (buckets fall as logits rise).
-__device__ __forceinline__ uint32_t edge_of(const Row& r, int b) {
-  uint32_t lo = ordered(-INFINITY) + 1, hi = ordered(r.max);  // the maximum is in bucket 0
+// The smallest mapped logit whose bucket is at most b, or (min_p > 0) whose weight is min_p at least; both rise with the logit, and the
+// maximum's do.
+// (32 values at a time, one a lane; whole warps.)
+__device__ __forceinline__ uint32_t edge_of(const Row& r, int b, float min_p) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = kMasked + 1, hi = ordered(r.max);
+#pragma unroll 1
   while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (bucket_of(below(r, unordered(mid))) <= b)
-      hi = mid;
-    else
-      lo = mid + 1;
+    const uint32_t step = max((hi - lo) / 32, 1u), far = min(lane * step, hi - lo);
+    const float t = below(r, unordered(lo + far));
+    const uint32_t holds = __ballot_sync(0xffffffffu, min_p > 0.f ? weight_of(t) >= min_p : bucket_of(t) <= b);
+    const uint32_t first = holds != 0 ? __ffs(holds) - 1 : 32;  // the first lane whose value holds
+    if (first == 0) return lo;
+    const uint32_t from = lo;
+    lo = from + min((first - 1) * step, hi - from) + 1;
+    if (first < 32) hi = from + min(first * step, hi - from);
   }
   return lo;
 }
 
 // The collected keys in descending order.
 __device__ void sort_list(Shared& sh, int n) {
+  if (n <= kThreads) {
+    // a key's place is how many are larger (no two are equal): a few hundred comparisons, and two barriers
+    const bool in = (int)threadIdx.x < n;
+    const Key mine = in ? sh.list[threadIdx.x] : 0;
+    int place = 0;
+    if ((int)(threadIdx.x & ~31u) < n) {
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) place += sh.list[i] > mine;
+    }
+    __syncthreads();
+    if (in) sh.list[place] = mine;
+    __syncthreads();
+    return;
+  }
   int size = 32;
   while (size < n) size <<= 1;
   for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
@@ -350,23 +383,17 @@ __device__ uint32_t collect(cg::cluster_group& cl, const Row& r, Shared& sh, Sha
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const float4* xv = reinterpret_cast<const float4*>(r.x + r.head);
   const int subs = (r.q1 - r.q0 + 31) / 32;
-  for (int s = wid; s < subs; s += 4 * kWarps) {
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int sub = s + i * kWarps, q = r.q0 + 32 * sub + lane;
-      v[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (q < r.q1 && sh.chunk[sub >> r.shift] >= least) v[i] = __ldg(xv + q);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int id = r.head + 4 * (r.q0 + 32 * (s + i * kWarps) + lane);
-      const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      list_keys<4>(home, x, id, [&](float y, int j) {
-        const Key k = key_of(y, (uint32_t)j);
-        return y > -INFINITY && k >= lo && k <= hi;
-      });
-    }
+#pragma unroll 1
+  for (int sub = wid; sub < subs; sub += kWarps) {
+    if (sh.chunk[sub >> r.shift] < least) continue;  // (most of them)
+    const int q = r.q0 + 32 * sub + lane, id = r.head + 4 * q;
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (q < r.q1) v = __ldg(xv + q);
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    list_keys<4>(home, x, id, [&](float y, int j) {
+      const Key k = key_of(y, (uint32_t)j);
+      return y > -INFINITY && k >= lo && k <= hi;
+    });
   }
   if (r.ends && wid == 0) {
     const int tail = r.n - r.head - 4 * r.quads;
@@ -406,14 +433,14 @@ __device__ Border resolve(cg::cluster_group& cl, const Row& r, Shared& sh, Share
   Key above_mass = sh.above_mass;
   Key lo, hi;
   const bool whole = above + inside <= kList;
-  lo = (Key)edge_of(r, sh.bucket) << 32;
+  lo = (Key)edge_of(r, sh.bucket, 0.f) << 32;
   if (lo < floor) lo = floor;  // (the histograms count none below it)
   if (whole) {
     hi = ~(Key)0;
     above = 0;
     above_mass = 0;
   } else {
-    hi = sh.bucket == 0 ? ~(Key)0 : ((Key)edge_of(r, sh.bucket - 1) << 32) - 1;
+    hi = sh.bucket == 0 ? ~(Key)0 : ((Key)edge_of(r, sh.bucket - 1, 0.f) << 32) - 1;
   }
   // cut again by the keys' bits: no two keys are equal, so at most 6 rounds of 10 bits leave fewer than the list holds
   for (int round = 0; !whole && inside > kList && round < 8; ++round) {
@@ -768,11 +795,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     __syncthreads();
     if (lane == 0) sh.scan_count[wid] = v;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) v = max(v, sh.scan_count[w]);
+    v = __reduce_max_sync(0xffffffffu, sh.scan_count[lane % kWarps]);
     if (ranks > 1) {
       if (threadIdx.x == 0) sh.rank_max = v;
       cl.sync();
-      for (int i = 0; i < ranks; ++i) v = max(v, cl.map_shared_rank(&sh, i)->rank_max);
+      v = __reduce_max_sync(0xffffffffu, cl.map_shared_rank(&sh, lane % ranks)->rank_max);  // (a lane a rank)
     }
     return v;
   };
@@ -863,11 +890,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     id = __reduce_min_sync(0xffffffffu, id);
     if (lane == 0) sh.scan_count[wid] = (uint32_t)id;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) id = min(id, (int)sh.scan_count[w]);
+    id = __reduce_min_sync(0xffffffffu, (int)sh.scan_count[lane % kWarps]);
     if (ranks > 1) {
       if (threadIdx.x == 0) sh.rank_id = id;
       cl.sync();
-      for (int i = 0; i < ranks; ++i) id = min(id, cl.map_shared_rank(&sh, i)->rank_id);
+      id = __reduce_min_sync(0xffffffffu, cl.map_shared_rank(&sh, lane % ranks)->rank_id);
     }
     if (rank == 0 && threadIdx.x == 0) p.ids[row] = id == INT32_MAX ? -1 : id;
   };
@@ -915,16 +942,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   // scores in powers of two below the maximum's
-  auto kept_by_m = [&](float x) { return !by_m || x == r.max || weight_of(below(r, x)) >= min_p; };
-  auto score = [&](float x, float e) { return e > 0.f ? (x - r.max) * r.scale - log2_of(e) : -INFINITY; };
+  const float least_m = by_m ? unordered(edge_of(r, 0, fminf(min_p, 1.f))) : -INFINITY;  // the least logit of min-p's weight
+  auto kept_by_m = [&](float x) { return x >= least_m; };
+  auto score = [&](float x, float e) { return score_of(r, x, e); };
 
-  // a value that all logits of min-p's weight reach (a little low: what is kept is asked of each)
-  float reach_m = -INFINITY;
-  if (by_m) {
-    const float edge = -log2_of(fminf(min_p, 1.f)) / r.scale;
-    reach_m = r.max - edge * (1.f + 0x1p-18f) - 0x1p-20f * fabsf(r.max);
-  }
-  const uint32_t least = reach_m > -INFINITY ? ordered(reach_m) : kMasked + 1;
+  const float reach_m = least_m;
+  const uint32_t least = by_m ? ordered(least_m) : kMasked + 1;
 
   // ---- the borders of top-k and top-p
   Border border{0, 0, 0};
@@ -1067,10 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (bucket >= 0) {
     const uint32_t above_count = sh.above_count;
     const Key above_mass = sh.above_mass;
-    auto kind = [&](float x, int) {
-      const int b = bucket_of(below(r, x));
-      return b < bucket ? (int)kept_by_m(x) : b == bucket ? 2 : 0;
-    };
+    const float from = unordered(edge_of(r, bucket, 0.f)), above = bucket > 0 ? unordered(edge_of(r, bucket - 1, 0.f)) : INFINITY;
+    auto kind = [&](float x, int) { return x >= above ? (int)kept_by_m(x) : x >= from ? 2 : 0; };
     most = draw_pass(r, sh, home, kMasked + 1, true, kind, score);  // (the bucket is collected whole, whatever min-p keeps)
     cl.sync();
     const uint32_t n = home->listed;

@@ -4,7 +4,7 @@
 //   h_e  = act(W1_e x_t) * (W3_e x_t),   out_t = scale * sum_{e in E(t)} p_e W2_e h_e.
 //
 // Two launches.  Every CTA of the first works out the routing itself from the logits (a maximum over a warp's lanes `top` times
-// a token: a launch of its own would cost more), and one of them leaves it for the second.  A unit is an expert with up to 4 of its tokens (2
+// a token: a launch of its own would cost more), and they leave it for the second together.  A unit is an expert with up to 4 of its tokens (2
 // where they are float32: a value is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after
 // the first.
 //   moe_up:   items of (unit, 32 rows of W1 and of W3), each CTA a run of them; a CTA's warps share an item's columns and meet in
@@ -19,10 +19,14 @@
 // rows, scaled by the weights' and the activations' scales in float32: a quarter of the loads and scalings that
 // one block an MMA would take, and 2 vectors fill the 8 columns.
 //
-// Levels: a Q4_0 nibble n in the lowest bits of a half is the subnormal number n 2^-24, in the next four bits n 2^-20: masks make
-// MMA operands of a word of 8 nibbles, without arithmetic.  Values 16 .. 31 of a block's activations are kept as a 16th, and the level's
-// -8 is taken from the block's sum: sum (n - 8) x = sum n x - 8 sum x (the two are at most twice what the sum's terms weigh, so
-// no accuracy goes).  Q8_0 quants become exact halves by a magic number.
+// Levels, bfloat16 outputs: a Q4_0 nibble n in the lowest bits of a half is the subnormal number n 2^-24, in the next four bits n 2^-20:
+// masks make MMA operands of a word of 8 nibbles, without arithmetic.  Values 16 .. 31 of a block's activations are kept as a 16th, and the
+// level's -8 is taken from the block's sum: sum (n - 8) x = sum n x - 8 sum x.  The tensor core cuts a product's bits at a distance from the
+// largest operands' exponents, and a subnormal operand's exponent is that of 2^-14: products lose 6 to 10 bits there, about 2^-18 of a
+// result (2e-6 of the output's norm where it was left in float32, against 1.5e-7 with whole levels) and nothing beside a bfloat16's 2^-9.
+// Float32 outputs and activations (WHOLE): levels as whole halves, a subtraction or an fma for two.  Those everywhere would be slower where
+// the weights' bytes count: 1 token over two experts of 11008 x 4096 54.3 against 44.4 us, 32 over 128 of 768 x 2048 111 against 95 us
+// (1 of 512 x 1024 13.7 us either way).  Q8_0 quants become exact halves by a magic number.
 // An activation is a half after the power of two that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16
 // down to 2^-27 of the largest; float32 values (and h for float32 outputs) are two halves, 22 bits; h for bfloat16 outputs one, 2^-11
 // relative.
@@ -298,10 +302,10 @@ struct Rows {
 
 // Eight values of a block of 32 (elements 8 piece ..) that four neighbouring lanes hold, as halves at the power of two that brings the block's
 // largest into [2^14, 2^15): hi, and with LO what hi leaves (11 more bits).  For Q4_0 in the order in which masks take a word's nibbles (0, 2,
-// 1, 3 of each four), the block's second half as a 16th.  mul, off: what the products' sum is multiplied by and what is taken off
-// then (hi's, then lo's).
-template <int WT, bool LO>
-__device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32_t (&hi)[4], uint32_t (&lo)[4], float (&mul)[2], float (&off)[2]) {
+// 1, 3 of each four), the block's second half as a 16th (!WHOLE).  mul, off: what the products' sum is multiplied by and what is taken off
+// then.
+template <int WT, bool LO, bool WHOLE>
+__device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32_t (&hi)[4], uint32_t (&lo)[4], float& mul, float& off) {
   float amax = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
@@ -309,8 +313,10 @@ __device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32
   for (int o = 1; o <= 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   float up, down;
   half_stage_scale(amax, up, down);
-  const float part = WT == QMV_Q4_0 && piece >= 2 ? 0.0625f : 1.f, back = WT == QMV_Q4_0 && piece >= 2 ? 16.f : 1.f;
-  float sum = 0.f, sum_lo = 0.f;
+  static_assert(WHOLE || !LO, "two halves are for whole levels");
+  constexpr bool kBits = WT == QMV_Q4_0 && !WHOLE;
+  const float part = kBits && piece >= 2 ? 0.0625f : 1.f, back = kBits && piece >= 2 ? 16.f : 1.f;
+  float sum = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int i = WT == QMV_Q4_0 ? (e & 2) * 2 + (e & 1) : 2 * e, j = WT == QMV_Q4_0 ? i + 2 : i + 1;
@@ -319,29 +325,36 @@ __device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32
     const float ha = __half2float(__ushort_as_half((unsigned short)(hi[e] & 0xffffu)));
     const float hb = __half2float(__ushort_as_half((unsigned short)(hi[e] >> 16)));
     sum += ha + hb;
-    if (LO) {
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(b - hb), "f"(a - ha));
-      sum_lo += __half2float(__ushort_as_half((unsigned short)(lo[e] & 0xffffu))) + __half2float(__ushort_as_half((unsigned short)(lo[e] >> 16)));
-    }
+    if (LO) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[e]) : "f"(b - hb), "f"(a - ha));
   }
-  mul[0] = mul[1] = down;
-  off[0] = off[1] = 0.f;
-  if (WT == QMV_Q4_0) {
-    sum *= back, sum_lo *= back;
+  mul = down;
+  off = 0.f;
+  if (kBits) {
+    sum *= back;
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (LO) sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
-    }
-    mul[0] = mul[1] = down * 0x1p24f;
-    off[0] = 8.f * sum * down, off[1] = 8.f * sum_lo * down;
+    for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    mul = down * 0x1p24f;
+    off = 8.f * sum * down;
   }
+}
+
+// The nibbles of a word's bytes 0 and 2 as two halves: the low ones and the high ones; WHOLE: levels, else bits (see above).
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t low_levels(uint32_t w) {
+  const uint32_t n = w & 0x000F000Fu;
+  return WHOLE ? f16x2_sub(n | 0x64006400u, 0x64086408u) : n;  // (1024 + n) - 1032
+}
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t high_levels(uint32_t w) {
+  const uint32_t n = w & 0x00F000F0u;
+  if (!WHOLE) return n;
+  return f16x2_fma(n | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 n) / 16 - 72
 }
 
 // One stage's products: acc[m][set] += what row tile m (rows g and g + 8 of it) gives for this lane's two blocks and vector.
 // b: this lane's column (its vector and block of the first four blocks), moving by `step` from set to set and by `group` from four blocks to
 // the next (both 0 at zeros, for lanes without a column); xs: the vector's factors of the lane's two blocks.
-template <int WT, bool F16, int SETS>
+template <int WT, bool F16, bool WHOLE, int SETS>
 __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t step, uint32_t group, uint32_t xs, uint32_t xs_step,
                                         float (&acc)[2][2][2]) {
   using S = Stage<WT, F16>;
@@ -387,12 +400,13 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
           const uint32_t wg = q[m][0][2 * j + k], wh = q[m][1][2 * j + k];
           if (WT == QMV_Q4_0) {
             // nibbles of bytes 0 and 2, then of bytes 1 and 3
-            constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
             const uint32_t sg = wg >> 8, sh = wh >> 8;
+            const uint32_t lo[4] = {low_levels<WHOLE>(wg), low_levels<WHOLE>(wh), low_levels<WHOLE>(sg), low_levels<WHOLE>(sh)};
+            const uint32_t hi[4] = {high_levels<WHOLE>(wg), high_levels<WHOLE>(wh), high_levels<WHOLE>(sg), high_levels<WHOLE>(sh)};
 #pragma unroll
             for (int v = 0; v < SETS; ++v) {
-              mma_f16_16816(c[m][v], wg & kLow, wh & kLow, sg & kLow, sh & kLow, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
-              mma_f16_16816(c[m][v], wg & kHigh, wh & kHigh, sg & kHigh, sh & kHigh, x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
+              mma_f16_16816(c[m][v], lo[0], lo[1], lo[2], lo[3], x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
+              mma_f16_16816(c[m][v], hi[0], hi[1], hi[2], hi[3], x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
             }
           } else {
             uint32_t g01, g23, h01, h23;
@@ -423,8 +437,8 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
         }
 #pragma unroll
         for (int v = 0; v < SETS; ++v) {
-          const float s0 = WT == QMV_Q4_0 ? fmaf(c[m][v][2 * h], f[v][0], -f[v][1]) : c[m][v][2 * h] * f[v][0];
-          const float s1 = WT == QMV_Q4_0 ? fmaf(c[m][v][2 * h + 1], f[v][2], -f[v][3]) : c[m][v][2 * h + 1] * f[v][2];
+          const float s0 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h], f[v][0], -f[v][1]) : c[m][v][2 * h] * f[v][0];
+          const float s1 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h + 1], f[v][2], -f[v][3]) : c[m][v][2 * h + 1] * f[v][2];
           acc[m][v][h] = fmaf(d.x, s0, fmaf(d.y, s1, acc[m][v][h]));
         }
       }
@@ -460,17 +474,17 @@ __device__ __forceinline__ Columns columns_of(uint32_t columns, uint32_t zeros, 
 }
 
 // A unit of one or two vectors, or of three or four.
-template <int WT, bool F16>
+template <int WT, bool F16, bool WHOLE>
 __device__ __forceinline__ void consume_any(uint32_t stage, const Columns& c, int sets, float (&acc)[2][2][2]) {
   if (sets == 1)
-    consume<WT, F16, 1>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
+    consume<WT, F16, WHOLE, 1>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
   else
-    consume<WT, F16, 2>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
+    consume<WT, F16, WHOLE, 2>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
 }
 
 // ------------------------------------------------------------------------------------------ gate and up
 // A warp's columns of chunk c, converted: `vectors` halves of up to kVectors vectors, then their scales, at `to`.
-template <typename S, int WT, bool XF32>
+template <typename S, int WT, bool XF32, bool WHOLE>
 __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, const void* x, const Unit& u, int c, int cols) {
   const int lane = threadIdx.x & 31;
   constexpr int kPieces = S::kChunk / 8;  // of a token
@@ -497,16 +511,16 @@ __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, co
       }
     }
     uint32_t hi[4], lo[4];
-    float mul[2], off[2];
-    to_halves<WT, XF32>(v, piece & 3, hi, lo, mul, off);
+    float mul, off;
+    to_halves<WT, XF32, WHOLE>(v, piece & 3, hi, lo, mul, off);
     if (in) {
       const int vec = XF32 ? 2 * k : k;
       uint8_t* at16 = to + vec * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16;
       *reinterpret_cast<uint4*>(at16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if (XF32) *reinterpret_cast<uint4*>(at16 + S::kVector) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       if ((piece & 3) == 0) {
-        factors[vec * S::kBlocks + (piece >> 2)] = make_float2(mul[0], off[0]);
-        if (XF32) factors[(vec + 1) * S::kBlocks + (piece >> 2)] = make_float2(mul[1], off[1]);
+        factors[vec * S::kBlocks + (piece >> 2)] = make_float2(mul, off);
+        if (XF32) factors[(vec + 1) * S::kBlocks + (piece >> 2)] = make_float2(mul, off);
       }
     }
   }
@@ -514,7 +528,7 @@ __device__ __forceinline__ void convert_columns(uint8_t* to, int max_vectors, co
 
 constexpr int kUpWarps = 16, kUpThreads = kUpWarps * 32;
 
-template <int WT, bool F16, bool XF32>
+template <int WT, bool F16, bool XF32, bool WHOLE>
 __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_constant__ MoeParams p) {
   using S = Stage<WT, F16>;
   constexpr int kUnit = XF32 ? kVectors / 2 : kVectors;  // tokens of a unit at most
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       u = unit_of(units, unit);
       if (works && n <= p.cached) {
         __syncwarp();
-        for (int j = 0; j < n; ++j) convert_columns<S, WT, XF32>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
+        for (int j = 0; j < n; ++j) convert_columns<S, WT, XF32, WHOLE>(cache + j * cache_bytes, max_vectors, p.x, u, c0 + j, p.dim);
         __syncwarp();
       }
       held = unit;
@@ -619,7 +633,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         Columns c = col0;
         if (n > p.cached) {
           __syncwarp();
-          convert_columns<S, WT, XF32>(cache, max_vectors, p.x, u, c0 + j, p.dim);
+          convert_columns<S, WT, XF32, WHOLE>(cache, max_vectors, p.x, u, c0 + j, p.dim);
         } else {
           c.b += c.b == zeros ? 0 : j * cache_bytes;
           c.xs += c.xs == zeros ? 0 : j * cache_bytes;
@@ -631,7 +645,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
           issue();
           wait_ring(p.ring);
           __syncwarp();
-          consume_any<WT, F16>(ring + cs * S::kBytes, c, sets, acc[0]);
+          consume_any<WT, F16, WHOLE>(ring + cs * S::kBytes, c, sets, acc[0]);
           cs = cs + 1 == p.ring ? 0 : cs + 1;
 #pragma unroll
           for (int w = 0; w < 2; ++w)
@@ -684,25 +698,22 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         float to, down;
         half_stage_scale(amax, to, down);
         // as to_halves() leaves activations, for W2's type
-        const bool split = p.w2_q4 && lane >= 16;
+        const bool bits = p.w2_q4 && p.parts == 1, split = bits && lane >= 16;
         const float v = h * to * (split ? 0.0625f : 1.f);
         const __half hi = __float2half_rn(v), lo = __float2half_rn(isfinite(v) ? v - __half2float(hi) : 0.f);
         const int place = p.w2_q4 ? (lane & ~3) | (lane & 1) << 1 | (lane >> 1 & 1) : lane;
         __half* out = reinterpret_cast<__half*>(p.h) + (long long)slot * p.hidden + 32 * ht + place;
         out[0] = hi;
         if (p.parts > 1) out[p.h_plane] = lo;
-        float sum = 0.f, sum_lo = 0.f;
-        if (p.w2_q4) {
-          sum = __half2float(hi) * (split ? 16.f : 1.f), sum_lo = __half2float(lo) * (split ? 16.f : 1.f);
+        float sum = 0.f;
+        if (bits) {
+          sum = __half2float(hi) * (split ? 16.f : 1.f);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
-          }
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         if (lane < p.parts)
           p.h_factor[((long long)lane * p.tokens * p.top + slot) * (p.hidden / 32) + ht] =
-              make_float2(p.w2_q4 ? down * 0x1p24f : down, 8.f * (lane == 0 ? sum : sum_lo) * down);
+              make_float2(bits ? down * 0x1p24f : down, 8.f * sum * down);
       }
     }
     if ((first += p.tiles_item) >= tiles) first = 0, ++unit;
@@ -836,7 +847,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     Columns c = col0;
     c.b += c.b == zeros ? 0 : cs * stage_bytes;
     c.xs += c.xs == zeros ? 0 : cs * stage_bytes;
-    consume_any<WT, F16>(ring + cs * stage_bytes, c, (u.cols * PARTS + 1) / 2, acc);
+    consume_any<WT, F16, PARTS == 2>(ring + cs * stage_bytes, c, (u.cols * PARTS + 1) / 2, acc);
     cs = cs + 1 == p.ring ? 0 : cs + 1;
     if (++cc == chunks) {
       flush();
@@ -938,9 +949,12 @@ cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStrea
   const int tiles = p.hidden / 32;
   for (p.tiles_item = kUpWarps / p.ks; p.tiles_item > 1 && units * ((tiles + p.tiles_item - 1) / p.tiles_item) < dev.sm_count;) p.tiles_item /= 2;
   const long long items = units * ((tiles + p.tiles_item - 1) / p.tiles_item);
-  auto kern = x_f32 ? moe_up_kernel<WT, F16, true> : moe_up_kernel<WT, F16, false>;
-  static bool done[2][64] = {};
-  const cudaError_t err = allow_smem(kern, dev, done[x_f32]);
+  const int which = x_f32 ? 2 : WT == QMV_Q4_0 && p.parts == 2;
+  auto kern = which == 2   ? moe_up_kernel<WT, F16, true, true>
+              : which == 1 ? moe_up_kernel<WT, F16, false, WT == QMV_Q4_0>
+                           : moe_up_kernel<WT, F16, false, false>;
+  static bool done[3][64] = {};
+  const cudaError_t err = allow_smem(kern, dev, done[which]);
   if (err != cudaSuccess) return err;
   return launch_dependent(kern, dim3((unsigned)(items < dev.sm_count ? items : dev.sm_count)), kUpThreads, smem, stream, p);
 }

@@ -171,3 +171,20 @@ def test_nothing_to_do_and_refusals(qmv):
             qmv.moe(layer.dev, x, logits, top)
     with pytest.raises(ValueError):
         qmv.Moe(2, 2, 1, 4, 64, 128, layer.dev.W1, layer.dev.W3, layer.dev.W2)
+
+
+@pytest.mark.parametrize("sf", [0, 1])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("wt", [0, 1])
+def test_float32_outputs_are_float32(qmv, wt, sf, bf16):
+    """Float32 outputs hold the accuracy of float32 sums, for either type of x: about 16 roundings of 2^-24 (8 steps of a block on the tensor
+    core, the warps' and blocks' sums) of values up to twice the result, each of gate, up and down: sqrt(3) sqrt(16) 2 2^-24 = 2^-20.2 of
+    the output's norm, where the errors' signs are by chance."""
+    wt = (qmv.Q4_0, qmv.Q8_0)[wt]
+    layer = Layer(qmv, wt, wt, sf, 8, 1024, 512, seed=91)
+    rng = np.random.default_rng(92)
+    x, xd = _x(rng, 5, 1024, bf16)
+    logits = rng.standard_normal((5, 8)).astype(F)
+    y = qmv.moe(layer.dev, xd, dev_x(logits), 3).cpu().numpy().astype(np.float64)
+    want, _, _, _, _ = step_ref.moe(layer.w1, layer.w3, layer.w2, x, logits, 3, True, 1.0, "silu", 2)
+    assert np.linalg.norm(y - want) <= 2.0 ** -20 * np.linalg.norm(want)

@@ -776,7 +776,7 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, 
     if vocab > 1 and (ls[1] != 1 or ns[1] != 1):
         raise ValueError("logits and noise must be float32 (rows, vocab) tensors with contiguous rows")
     if ids is None:
-        ids = torch.empty((rows,), dtype=torch.int64, device=logits.device)
+        ids = logits.new_empty((rows,), dtype=torch.int64)
     elif ids.dtype is not torch.int64 or ids.shape != (rows,) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int64 (rows,) tensor")
     on, at = [noise.get_device(), ids.get_device()], []
@@ -823,7 +823,7 @@ def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: fl
         raise ValueError("W must be a contiguous uint8 tensor of the matrix image's bytes")
     shape = ids.shape + (cols,)
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=ids.device)
+        y = ids.new_empty(shape, dtype=dtype)
     elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
         raise ValueError("y must be a contiguous tensor of ids' shape and cols, of the output's type")
     st = load_library().qmv_embed(wtype, scale_dtype, vocab, cols, W.data_ptr(), ids.data_ptr(), ids.numel(), scale, code,
@@ -835,10 +835,18 @@ def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: fl
 ROPE_PAIRS = {"neighbours": 0, "halves": 1}
 
 
+def _new_like(t, dtype):
+    """A contiguous tensor of t's shape (empty_like() takes half the host's time of empty(), new_empty() two thirds)."""
+    import torch
+    return torch.empty_like(t) if t.dtype is dtype and t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
+
+
 def _stride_of_rows(t, shape, what):
     """The row stride of a tensor of that shape, (rows, heads, dim), whose rows are contiguous."""
     if t.shape == shape:
         rows, heads, dim = shape
+        if t.is_contiguous():
+            return heads * dim
         row, head, value = t.stride()
         if (value == 1 and (head == dim or heads == 1)) or rows == 0:
             return row if rows > 1 else heads * dim
@@ -864,7 +872,7 @@ def qk_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps: float = 1e-6, pa
     code, dtype = (x, xt) if out is None else _out_type(out)
     qs = _stride_of_rows(q, shape, "q")
     if q_out is None:
-        q_out, qos = torch.empty(shape, dtype=dtype, device=q.device), heads * dim
+        q_out, qos = _new_like(q, dtype), heads * dim
     else:
         qos = _stride_of_rows(q_out, shape, "q_out")
     on = [q_out.get_device()]
@@ -880,7 +888,7 @@ def qk_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps: float = 1e-6, pa
         kvh = kshape[1]
         ks = _stride_of_rows(k, (rows, kvh, dim), "k")
         if k_out is None:
-            k_out, kos = torch.empty(kshape, dtype=dtype, device=q.device), kvh * dim
+            k_out, kos = _new_like(k, dtype), kvh * dim
         else:
             kos = _stride_of_rows(k_out, (rows, kvh, dim), "k_out")
             if k_out.dtype is not dtype:
@@ -955,24 +963,23 @@ def moe(layer: Moe, x, logits, top: int, renorm: bool = True, scale: float = 1.0
     n, experts = shape[0], layer.experts
     if logits.dtype is not torch.float32 or logits.shape != (n, experts) or (experts > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a float32 (tokens, experts) tensor with contiguous rows")
-    dev = x.device
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=dev)
+        y = _new_like(x, dtype)
     elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
         raise ValueError("y must be a contiguous (tokens, dim) tensor of the output's type")
     need = layer._scratch.get((n, top, code))
     if need is None:
         need = layer._scratch[n, top, code] = moe_scratch_bytes(n, top, layer.hidden, out)
     if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        scratch = x.new_empty((max(need, 16),), dtype=torch.uint8)
         if stream is not None:
             scratch.record_stream(stream)
     elif scratch.dtype is not torch.uint8 or scratch.numel() < need or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous uint8 tensor of moe_scratch_bytes()")
     ids = shares = ip = sp = None
     if routing:
-        ids = torch.empty((n, max(top, 0)), dtype=torch.int32, device=dev)
-        shares = torch.empty((n, max(top, 0)), dtype=torch.float32, device=dev)
+        ids = x.new_empty((n, max(top, 0)), dtype=torch.int32)
+        shares = logits.new_empty((n, max(top, 0)))
         ip, sp = ids.data_ptr(), shares.data_ptr()
     st = load_library().qmv_moe(layer._p, n, logits.data_ptr(), logits.stride(0) if n > 1 else experts, top, 1 if renorm else 0, scale,
                                 act_code, _x_dtype(x), x.data_ptr(), code, y.data_ptr(), ip, sp, scratch.data_ptr(),

@@ -684,9 +684,9 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
  * that leaves none, and with a temperature of 2^-100 or less (0, negative or NaN), top_k 1 or top_p 0, the id is that of
  * the largest logit.  A logit of -infinity is a masked id.  A row that holds NaN, or in which every logit is
  * -infinity, gives -1; one that holds +infinity the lowest id of those.
- * (A temperature above 2^100 counts as that.)  The sums that place the top_p border are float32 sums of a few terms
- * each, then exact: a border may be off by 2^-20 of the mass.  Scores near the largest are compared in 64 bits.  Results
- * do not depend on timing or on the other rows of the call.
+ * (A temperature above 2^100 counts as that.)  The top_p border is placed by sums of w as integers in units of
+ * 2^-31: it may be off by 2^-20 of the kept mass, and by vocab 2^-32 of the largest w where that is more.  Scores near the
+ * largest are compared in 64 bits.  Results do not depend on timing or on the other rows of the call.
  * Allocates nothing and uses no workspace.
  * Returns QMV_OK, QMV_E_ARG (rows < 0, null logits, noise or ids), QMV_E_SHAPE (vocab not within 1..
  * QMV_SAMPLE_MAX_VOCAB - 1, strides below vocab, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */
@@ -760,7 +760,8 @@ size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dt
  *   logits : device, float32, token t at element t * logits_stride (at least experts), 4-byte aligned.
  *   x      : device, tokens x dim, x_dtype QMV_X_F32 or QMV_X_BF16, contiguous, 16-byte aligned.
  *   act    : QMV_ACT_SILU or QMV_ACT_GELU_TANH.
- *   out    : device, tokens x dim of out_dtype (QMV_X_F32 or QMV_X_BF16), contiguous, 16-byte aligned, fully written.
+ *   out    : device, tokens x dim of out_dtype (QMV_X_F32 or QMV_X_BF16), contiguous, 16-byte aligned, fully written; no
+ *            output overlaps anything else of the call.
  *   ids, shares : device, tokens x top int32 / float32: the experts and their p in descending order; each may be NULL.
  *   scratch : device, qmv_moe_scratch_bytes(), 16-byte aligned: h between the call's launches.  Calls that may overlap in
  *            time need scratch memory of their own, captured graphs too.

@@ -9,7 +9,12 @@
 // of).  sinpi / cospi of that in float32, once for all heads of a row, in shared memory.
 //
 // Bound by the rows' bytes in and out; below that by a chain of loads, angles, one barrier and stores, so a CTA takes several rows where
-// there are many: their angles together, their values two rows ahead.
+// there are many: their angles together, their values two rows ahead.  The rows are cut so that the CTAs fill whole rounds of what the SMs
+// hold at once, up to 8 each (powers of two of them: 8192 rows 37.6, 3000 rows 24.6, 1024 rows 9.6 us; as it is 35.0, 15.1, 7.1 us; up
+// to 4: 37.6, 17.0, 7.1; up to 16: 34.2, 15.1, 7.1 and float32 rows 56.5 against 54.7 us).
+// GB300, 32 + 8 heads of 128: 8192 bfloat16 rows with norms, half of each head turned, 35.0 us (4.8 TB/s; all of it 38.4, without norms 32.0),
+// float32 ones 54.7 us (6.1 TB/s); 256 float32 rows 4.7, one bfloat16 row 2.7 us.  The bfloat16 rows' instructions, about 12 a value, take
+// two thirds of the issue slots.
 #include <type_traits>
 
 #include "qmv_common.cuh"
@@ -47,25 +52,42 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rope_kernel(const __grid_const
   const bool turns_here = 8 * gl < a.rot;
   const int lo = HALVES && turns_here ? 4 * gl : 8 * gl, hi = HALVES && turns_here ? a.rot / 2 + 4 * gl : 8 * gl + 4;
   using Raw = typename std::conditional<XB, uint2, float4>::type;
-  alignas(16) Raw raw[2][2];  // two rows' values are on their way
+  alignas(16) Raw raw[2][2] = {};  // two rows' values are on their way
   const int mine = threadIdx.x / L;
-  auto load = [&](Raw (&to)[2], int head, int r) {
-    if (head >= heads || r >= n) return;
+  // where the lane reads and writes, a row further each time
+  constexpr int kIn = XB ? 2 : 4, kOut = OB ? 2 : 4;
+  const uint8_t* in = nullptr;
+  uint8_t* out = nullptr;
+  long long in_step = 0, out_step = 0;
+  bool live = false;
+  const float* w = nullptr;
+  auto place = [&](int head) {
+    live = head < heads;
     const bool is_k = head >= a.heads;
-    const long long at = is_k ? (row0 + r) * a.k_stride + (long long)(head - a.heads) * D : (row0 + r) * a.q_stride + (long long)head * D;
-    // (plain loads: the outputs may be the inputs' own places)
-    constexpr int kSize = XB ? 2 : 4;
-    const uint8_t* x = static_cast<const uint8_t*>(is_k ? a.k : a.q) + at * kSize;
-    if (XB && !HALVES) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + lo * kSize);
-      reinterpret_cast<uint4&>(to) = u;
-    } else {
-      to[0] = *reinterpret_cast<const Raw*>(x + lo * kSize);
-      to[1] = *reinterpret_cast<const Raw*>(x + hi * kSize);
-    }
+    const int of = is_k ? head - a.heads : head;
+    in_step = (is_k ? a.k_stride : a.q_stride) * kIn;
+    out_step = (is_k ? a.k_out_stride : a.q_out_stride) * kOut;
+    in = static_cast<const uint8_t*>(is_k ? a.k : a.q) + row0 * in_step + (of * D + lo) * kIn;
+    out = static_cast<uint8_t*>(is_k ? a.k_out : a.q_out) + row0 * out_step + (of * D + lo) * kOut;
+    w = is_k ? a.k_weight : a.q_weight;
   };
-  load(raw[0], mine, 0);  // while the angles are formed
-  load(raw[1], mine, 1);
+  const int in_far = (hi - lo) * kIn, out_far = (hi - lo) * kOut;
+  auto load = [&](Raw (&to)[2], int r) {
+    if (live && r < n) {
+      // (plain loads: the outputs may be the inputs' own places)
+      if (XB && !HALVES) {
+        const uint4 u = *reinterpret_cast<const uint4*>(in);
+        reinterpret_cast<uint4&>(to) = u;
+      } else {
+        to[0] = *reinterpret_cast<const Raw*>(in);
+        to[1] = *reinterpret_cast<const Raw*>(in + in_far);
+      }
+    }
+    in += in_step;
+  };
+  place(mine);
+  load(raw[0], 0);  // while the angles are formed
+  load(raw[1], 1);
   const int half = a.rot / 2;
   unsigned long long turns = 0;
   for (int i = threadIdx.x, held = -1; i < half * n; i += blockDim.x) {
@@ -81,30 +103,28 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rope_kernel(const __grid_const
   __syncthreads();
   // every lane of a warp goes round as often: the shuffles need them all
   for (int first = 0; first < heads; first += slots) {
-    const int head = first + mine;
-    const bool live = head < heads, is_k = head >= a.heads;
-    const float* w = is_k ? a.k_weight : a.q_weight;
+    if (first > 0) {
+      place(first + mine);
+      load(raw[0], 0);
+      load(raw[1], 1);
+    }
     float ww[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) ww[e] = w != nullptr ? __ldg(w + (e < 4 ? lo + e : hi + e - 4)) : 0.f;
-    if (first > 0) {
-      load(raw[0], head, 0);
-      load(raw[1], head, 1);
-    }
     auto one = [&](Raw (&from)[2], int r) {
       float v[8];
       const uint32_t* u = reinterpret_cast<const uint32_t*>(from);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = !live ? 0.f : XB ? __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16) : __uint_as_float(u[e]);
-      load(from, head, r + 2);
+      for (int e = 0; e < 8; ++e) v[e] = XB ? __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16) : __uint_as_float(u[e]);
+      load(from, r + 2);
       if (a.q_weight != nullptr || a.k_weight != nullptr) {
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (w != nullptr && live) {
-          const float s = __frsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), a.eps));
+        if (w != nullptr) {
+          const float s = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], s), ww[e]);
         }
@@ -122,22 +142,20 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rope_kernel(const __grid_const
         }
       }
       if (live) {
-        constexpr int kSize = OB ? 2 : 4;
-        const long long at = is_k ? (row0 + r) * a.k_out_stride + (long long)(head - a.heads) * D : (row0 + r) * a.q_out_stride + (long long)head * D;
-        uint8_t* out = static_cast<uint8_t*>(is_k ? a.k_out : a.q_out) + at * kSize;
         if (OB) {
-          const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          const uint4 u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
           if (HALVES) {
-            *reinterpret_cast<uint2*>(out + lo * 2) = make_uint2(w.x, w.y);
-            *reinterpret_cast<uint2*>(out + hi * 2) = make_uint2(w.z, w.w);
+            *reinterpret_cast<uint2*>(out) = make_uint2(u.x, u.y);
+            *reinterpret_cast<uint2*>(out + out_far) = make_uint2(u.z, u.w);
           } else {
-            *reinterpret_cast<uint4*>(out + lo * 2) = w;
+            *reinterpret_cast<uint4*>(out) = u;
           }
         } else {
-          *reinterpret_cast<float4*>(out + lo * 4) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(out + hi * 4) = make_float4(v[4], v[5], v[6], v[7]);
+          *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(out + out_far) = make_float4(v[4], v[5], v[6], v[7]);
         }
       }
+      out += out_step;
     };
     for (int r = 0; r < n; r += 2) {
       one(raw[0], r);
@@ -151,9 +169,10 @@ cudaError_t launch_dim(const RopeArgs& a, bool x_bf16, bool out_bf16, bool halve
   // the heads in as few even shares as the threads take
   const int heads = a.heads + a.kv_heads, most = kMaxThreads / (D / 8), shares = (heads + most - 1) / most;
   const int threads = ((heads + shares - 1) / shares * (D / 8) + 31) / 32 * 32;
-  // rows of a CTA: up to 8, so that every SM still gets as many CTAs as it holds twice over
-  int block = 1;
-  while (block < 8 && rows / (2 * block) >= 2LL * dev.sm_count * (2048 / threads)) block *= 2;
+  // rows of a CTA: up to kMaxBlock, such that the CTAs fill whole rounds of what the SMs hold (64 registers a thread)
+  constexpr int kMaxBlock = 8;
+  const int64_t held = (int64_t)dev.sm_count * (1024 / threads), rounds = (rows + held * kMaxBlock - 1) / (held * kMaxBlock);
+  const int block = (int)((rows + held * rounds - 1) / (held * rounds));
   auto go = [&](auto kern) {
     return launch_dependent(kern, dim3((unsigned)((rows + block - 1) / block)), threads, (size_t)block * a.rot / 2 * sizeof(float2), stream, a, rows, block);
   };

@@ -776,7 +776,7 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, 
     if vocab > 1 and (ls[1] != 1 or ns[1] != 1):
         raise ValueError("logits and noise must be float32 (rows, vocab) tensors with contiguous rows")
     if ids is None:
-        ids = logits.new_empty((rows,), dtype=torch.int64)
+        ids = torch.empty((rows,), dtype=torch.int64, device=logits.device)
     elif ids.dtype is not torch.int64 or ids.shape != (rows,) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int64 (rows,) tensor")
     on, at = [noise.get_device(), ids.get_device()], []
@@ -823,7 +823,7 @@ def embed(wtype: int, scale_dtype: int, vocab: int, cols: int, W, ids, scale: fl
         raise ValueError("W must be a contiguous uint8 tensor of the matrix image's bytes")
     shape = ids.shape + (cols,)
     if y is None:
-        y = ids.new_empty(shape, dtype=dtype)
+        y = torch.empty(shape, dtype=dtype, device=ids.device)
     elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
         raise ValueError("y must be a contiguous tensor of ids' shape and cols, of the output's type")
     st = load_library().qmv_embed(wtype, scale_dtype, vocab, cols, W.data_ptr(), ids.data_ptr(), ids.numel(), scale, code,
@@ -836,9 +836,9 @@ ROPE_PAIRS = {"neighbours": 0, "halves": 1}
 
 
 def _new_like(t, dtype):
-    """A contiguous tensor of t's shape (empty_like() takes half the host's time of empty(), new_empty() two thirds)."""
+    """A contiguous tensor of t's shape (empty_like() takes the least of the host's time, new_empty() twice that of empty())."""
     import torch
-    return torch.empty_like(t) if t.dtype is dtype and t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
+    return torch.empty_like(t) if t.dtype is dtype and t.is_contiguous() else torch.empty(t.shape, dtype=dtype, device=t.device)
 
 
 def _stride_of_rows(t, shape, what):
@@ -971,15 +971,15 @@ def moe(layer: Moe, x, logits, top: int, renorm: bool = True, scale: float = 1.0
     if need is None:
         need = layer._scratch[n, top, code] = moe_scratch_bytes(n, top, layer.hidden, out)
     if scratch is None:
-        scratch = x.new_empty((max(need, 16),), dtype=torch.uint8)
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
         if stream is not None:
             scratch.record_stream(stream)
     elif scratch.dtype is not torch.uint8 or scratch.numel() < need or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous uint8 tensor of moe_scratch_bytes()")
     ids = shares = ip = sp = None
     if routing:
-        ids = x.new_empty((n, max(top, 0)), dtype=torch.int32)
-        shares = logits.new_empty((n, max(top, 0)))
+        ids = torch.empty((n, max(top, 0)), dtype=torch.int32, device=x.device)
+        shares = torch.empty((n, max(top, 0)), dtype=torch.float32, device=x.device)
         ip, sp = ids.data_ptr(), shares.data_ptr()
     st = load_library().qmv_moe(layer._p, n, logits.data_ptr(), logits.stride(0) if n > 1 else experts, top, 1 if renorm else 0, scale,
                                 act_code, _x_dtype(x), x.data_ptr(), code, y.data_ptr(), ip, sp, scratch.data_ptr(),

@@ -16,6 +16,12 @@
 //
 // Scores are float32; those close to the best are formed again in 64 bits, so equal draws are told apart as the definition does.
 // A row is one cluster's: 1, 2, 4 or 8 CTAs, which join in distributed shared memory; no workspace.
+//
+// Bound by the logits' bytes for many unfiltered rows (and the noise's, which only they read whole); else by a chain of passes, joins and a
+// sort for few rows, and by instructions and shared-memory atomics for flat rows under top-p.  GB300, rows of 151936: one row with all cuts
+// 17.1 us; 64 rows greedy 13, unfiltered 18, min-p 35, top-k 50, top-p 84, mixed 70 us; 512 rows unfiltered 104 us (6.0 TB/s), greedy
+// 58, all cuts 137, top-p 350 us.  (With conversions for the buckets, branches for what a draw takes and a binary search of borders: one
+// row 18, 64 mixed rows 81 us.)
 #include <cooperative_groups.h>
 
 #include <mutex>

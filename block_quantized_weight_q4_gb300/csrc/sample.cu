@@ -1045,44 +1045,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     // the buckets of all logits (min-p alone: the pass below)
     if (by_k || by_p) {
-    const bool both = by_k && by_p;
-    cl.sync();
-    clear(sh);
-    __syncthreads();
-    if (by_k) bucket_pass<false>(r, sh);
-    if (by_p) bucket_pass<true>(r, sh);
-    cl.sync();
-    uint32_t c[2], all_c;
-    Key m[2], all_m;
-    gather(cl, sh, ranks, c, m);
-    uint32_t pc = c[0] + c[1];
-    Key pm = m[0] + m[1];
-    block_scan(sh, pc, pm, all_c, all_m);
-    __syncthreads();
-    const bool cut_k = by_k && (uint32_t)k < all_c;  // (a row may hold fewer finite logits)
-    want = (double)top_p * (double)all_m;
-    if (cut_k && both) {
-      // the k-th logit itself, then the buckets of those above it
-      find_border(sh, c, m, 0, 0, (uint32_t)k, 0.0);
-      border = resolve(cl, r, sh, home, rank, ranks, 0, (uint32_t)k, 0.0, top_p);
-      if (border.listed == 0) {
-        cl.sync();
-        clear(sh);
-        __syncthreads();
-        for_each(r, sh.chunk, (uint32_t)(border.key >> 32), [&](float x, int id, int) {
-          if (key_of(x, (uint32_t)id) >= border.key) add(sh, bucket_of(below(r, x)), mass_of(below(r, x)));
-        });
-        cl.sync();
-        gather(cl, sh, ranks, c, m);
-        find_border(sh, c, m, 0, 0, 0, (double)top_p * (double)border.mass);
-        const Border bp = resolve(cl, r, sh, home, rank, ranks, border.key, 0, (double)top_p * (double)border.mass, 1.f);
-        border.key = bp.key > border.key ? bp.key : border.key;
+      const bool both = by_k && by_p;
+      cl.sync();
+      clear(sh);
+      __syncthreads();
+      if (by_k) bucket_pass<false>(r, sh);
+      if (by_p) bucket_pass<true>(r, sh);
+      cl.sync();
+      uint32_t c[2], all_c;
+      Key m[2], all_m;
+      gather(cl, sh, ranks, c, m);
+      uint32_t pc = c[0] + c[1];
+      Key pm = m[0] + m[1];
+      block_scan(sh, pc, pm, all_c, all_m);
+      __syncthreads();
+      const bool cut_k = by_k && (uint32_t)k < all_c;  // (a row may hold fewer finite logits)
+      want = (double)top_p * (double)all_m;
+      if (cut_k && both) {
+        // the k-th logit itself, then the buckets of those above it
+        find_border(sh, c, m, 0, 0, (uint32_t)k, 0.0);
+        border = resolve(cl, r, sh, home, rank, ranks, 0, (uint32_t)k, 0.0, top_p);
+        if (border.listed == 0) {
+          cl.sync();
+          clear(sh);
+          __syncthreads();
+          for_each(r, sh.chunk, (uint32_t)(border.key >> 32), [&](float x, int id, int) {
+            if (key_of(x, (uint32_t)id) >= border.key) add(sh, bucket_of(below(r, x)), mass_of(below(r, x)));
+          });
+          cl.sync();
+          gather(cl, sh, ranks, c, m);
+          find_border(sh, c, m, 0, 0, 0, (double)top_p * (double)border.mass);
+          const Border bp = resolve(cl, r, sh, home, rank, ranks, border.key, 0, (double)top_p * (double)border.mass, 1.f);
+          border.key = bp.key > border.key ? bp.key : border.key;
+        }
+      } else if (cut_k || by_p) {
+        first = cut_k ? (uint32_t)k : 0u;
+        find_border(sh, c, m, 0, 0, first, want);
+        bucket = sh.bucket;
       }
-    } else if (cut_k || by_p) {
-      first = cut_k ? (uint32_t)k : 0u;
-      find_border(sh, c, m, 0, 0, first, want);
-      bucket = sh.bucket;
-    }
     }
   }
 

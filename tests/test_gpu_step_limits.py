@@ -200,3 +200,45 @@ def test_embed_more_than_2_31_values(qmv):
     table = torch.cat([table, torch.zeros_like(table[:1])])
     for at in (0, 299, 2 ** 19 - 1, n - 40):
         assert torch.equal(y[at:at + 40], table[ids[at:at + 40]])
+
+
+def test_embed_more_than_2_31_pieces(qmv):
+    """An output of more than 2^31 pieces of 16 bytes: launches over parts of the rows."""
+    import torch
+    m = inputs.make_matrix(1, 0, 50, 32, seed=5)
+    W = torch.from_numpy(m.W).cuda()
+    n = 2 ** 29 + 1000
+    ids = torch.arange(n, device="cuda").remainder_(51)
+    y = qmv.embed(1, 0, 50, 32, W, ids, out="bf16")
+    table = torch.from_numpy(oracle.dequant(m.W, 1, 0, 50, 32)).cuda().bfloat16()
+    table = torch.cat([table, torch.zeros_like(table[:1])])
+    for at in (0, 2 ** 28 - 50, 2 ** 29 - 400, 2 ** 29 - 200, n - 100):
+        assert torch.equal(y[at:at + 100], table[ids[at:at + 100]])
+    del y, ids
+    torch.cuda.empty_cache()
+
+
+def test_sample_2_30_ids(qmv):
+    """A row of more than 2^30 ids: a few stand out, at its ends and at the borders of whole pieces."""
+    import torch
+    n = 2 ** 30 + 5
+    x = torch.full((1, n), -20.0, device="cuda")
+    e = torch.ones((1, n), device="cuda")
+    at = torch.tensor([n - 1, 0, 2 ** 30 - 1, 2 ** 30, 77777777], device="cuda")
+    x[0, at] = torch.tensor([1.0, 0.5, 0.75, 0.25, 0.0], device="cuda")
+
+    def one(**how):
+        types = {"top_k": torch.int32}
+        return qmv.sample(x, e, **{k: torch.tensor([v], dtype=types.get(k, torch.float32), device="cuda") for k, v in how.items()}).item()
+
+    assert one(temperature=0.0) == n - 1 and one() == n - 1
+    e[0, 2 ** 30] = 1e-3  # 0.25 + 6.9: ahead of the others, where it is kept
+    assert one() == 2 ** 30 and one(top_k=4) == 2 ** 30 and one(top_k=3) == n - 1 and one(min_p=0.4) == 2 ** 30 and one(min_p=0.5) == n - 1
+    e[0, n - 3] = 1e-15  # -20 + 34.5: ahead of all, where nothing is cut off
+    assert one() == n - 3 and one(temperature=2.0) == n - 3
+    assert one(top_k=1000) == 2 ** 30  # of equal logits the lowest ids are kept
+    assert one(min_p=0.1) == 2 ** 30 and one(top_k=5, min_p=0.4) == 2 ** 30
+    x[0, 12345] = float("nan")
+    assert one() == -1 and one(top_k=5) == -1
+    del x, e
+    torch.cuda.empty_cache()

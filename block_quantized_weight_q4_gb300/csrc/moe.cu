@@ -5,7 +5,7 @@
 //
 // Two launches.  Every CTA of the first works out the routing itself from the logits (a maximum over a warp's lanes `top` times
 // a token: a launch of its own would cost more), and they leave it for the second together.  A unit is an expert with up to 4 of its tokens (2
-// where they are float32: a value is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after
+// where they are float32, and always for h: a value is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after
 // the first.
 //   moe_up:   items of (unit, 32 rows of W1 and of W3), each CTA a run of them; a CTA's warps share an item's columns and meet in
 //             shared memory, where gate and up become h.
@@ -16,9 +16,9 @@
 // Bound by the weights' bytes; below that by what comes before them: the routing, code that is fetched once, the fill of two pipelines
 // (about 12 us of a call; so what runs once is small and no CTA runs code that the others do not: one CTA that alone left the routing
 // cost 7 us).  TMA boxes in place of cp.async measured 53.9 against 52.7 us (1 token, two of 8 experts of 11008 x 4096) and 112 against
-// 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 44.4 us (152 MB) and 95 us
+// 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 45.6 us (152 MB) and 114 us
 // (297 MB), in their long stretches 4.5 to 5.7 TB/s; 7 tokens over 16 Q8_0 experts of 1408 x 2048 41.8 us; 1 token, 4 of 32 of 512 x 1024
-// 13.8 us.
+// 12.5 us.
 //
 // Products: m16n8k16 with IEEE halves.  Lane t of a row's four lanes takes a whole block of 32 weights (one or two 16-byte loads), so an
 // MMA's k slots hold four different blocks; the columns are 2 vectors x those 4 blocks, and a lane's B values are
@@ -33,10 +33,11 @@
 // result (2e-6 of the output's norm where it was left in float32, against 1.5e-7 with whole levels) and nothing beside a bfloat16's 2^-9.
 // Float32 outputs and activations (WHOLE): levels as whole halves, a subtraction or an fma for two.  Those everywhere would be slower where
 // the weights' bytes count: 1 token over two experts of 11008 x 4096 54.3 against 44.4 us, 32 over 128 of 768 x 2048 111 against 95 us
-// (1 of 512 x 1024 13.7 us either way).  Q8_0 quants become exact halves by a magic number.
+// (1 of 512 x 1024: no difference).  Q8_0 quants become exact halves by a magic number.
 // An activation is a half after the power of two that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16
-// down to 2^-27 of the largest; float32 values (and h for float32 outputs) are two halves, 22 bits; h for bfloat16 outputs one, 2^-11
-// relative.
+// down to 2^-27 of the largest; float32 values and h are two halves, 22 bits.  (One half of h for bfloat16 outputs put 2e-4 of the output's
+// norm beside the 1.6e-3 of the outputs' own rounding, and one output in ten on another bfloat16 than the formula's.  It left units of 4
+// tokens to moe_down: 44.4 and 95 us; units of 4 with two halves, 8 vectors in two rounds, measured 47.9 and 114 us.)
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -62,6 +63,7 @@ constexpr int kTokens = 64;    // of a launch
 constexpr int kExperts = QMV_MOE_MAX_EXPERTS;
 constexpr int kTop = QMV_MOE_MAX_TOP;
 constexpr int kVectors = 4;    // of a unit: two to an MMA
+constexpr int kParts = 2;      // vectors of a row of h, its halves: hi and lo
 constexpr int kRowsStage = 32;
 
 // ------------------------------------------------------------------------------------------ routing
@@ -705,20 +707,25 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         float to, down;
         half_stage_scale(amax, to, down);
         // as to_halves() leaves activations, for W2's type
-        const bool bits = p.w2_q4 && p.parts == 1, split = bits && lane >= 16;
+        const bool bits = p.w2_q4 && p.out_bf16, split = bits && lane >= 16;
         const float v = h * to * (split ? 0.0625f : 1.f);
         const __half hi = __float2half_rn(v), lo = __float2half_rn(isfinite(v) ? v - __half2float(hi) : 0.f);
         const int place = p.w2_q4 ? (lane & ~3) | (lane & 1) << 1 | (lane >> 1 & 1) : lane;
         __half* out = reinterpret_cast<__half*>(p.h) + (long long)slot * p.hidden + 32 * ht + place;
         out[0] = hi;
-        if (p.parts > 1) out[p.h_plane] = lo;
-        float sum = 0.f;
+        out[p.h_plane] = lo;
+        float sum = 0.f;  // lane 0: of the block's hi, lane 1: of its lo
         if (bits) {
-          sum = __half2float(hi) * (split ? 16.f : 1.f);
+          const float back = split ? 16.f : 1.f;
+          float high = __half2float(hi) * back, low = __half2float(lo) * back;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          for (int o = 16; o > 0; o >>= 1) {
+            high += __shfl_xor_sync(0xffffffffu, high, o);
+            low += __shfl_xor_sync(0xffffffffu, low, o);
+          }
+          sum = lane == 0 ? high : low;
         }
-        if (lane < p.parts)
+        if (lane < kParts)
           p.h_factor[((long long)lane * p.tokens * p.top + slot) * (p.hidden / 32) + ht] =
               make_float2(bits ? down * 0x1p24f : down, 8.f * sum * down);
       }
@@ -730,14 +737,14 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
 // ------------------------------------------------------------------------------------------ down
 constexpr int kDownWarps = 8, kDownThreads = kDownWarps * 32;
 
-template <int WT, bool F16, int PARTS>
+template <int WT, bool F16, bool WHOLE>
 __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_constant__ MoeParams p, int ranks) {
   using S = Stage<WT, F16>;
-  constexpr int kUnit = kVectors / PARTS;  // tokens of a unit
+  constexpr int kUnit = kVectors / kParts;  // tokens of a unit
   extern __shared__ __align__(1024) uint8_t smem[];
   float* tiles = reinterpret_cast<float*>(smem + p.off_red);  // a warp's tokens x 32 rows
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int max_vectors = min(p.tokens, kUnit) * PARTS;
+  const int max_vectors = min(p.tokens, kUnit) * kParts;
   const int stage_bytes = S::kBytes + S::columns(max_vectors);
   const uint32_t ring = smem_u32(smem + p.off_ring) + wid * p.ring * stage_bytes;
   const uint32_t zeros = smem_u32(smem + p.off_zero);
@@ -772,8 +779,8 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     pu = unit_of(units, ps_u);
     const long long row = (long long)pu.expert * p.dim + row0;
     rows.set(p.q2, p.d2, p.q2, p.d2, row, row + 16, p.hidden);
-    const int slot = __shfl_sync(0xffffffffu, pu.slot, lane / PARTS);
-    h_at = (uint32_t)((lane % PARTS * p.h_plane + (long long)slot * p.hidden) / 64);
+    const int slot = __shfl_sync(0xffffffffu, pu.slot, lane / kParts);
+    h_at = (uint32_t)((lane % kParts * p.h_plane + (long long)slot * p.hidden) / 64);
   };
   if (s0 < s1) next_unit();
   // the vectors' halves and scales: a piece of 16 bytes a lane and vector
@@ -781,7 +788,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     const uint32_t to = ring + at * stage_bytes + S::kBytes;
     constexpr int kPieces = S::kChunk / 8;       // of a vector
     constexpr int kTogether = 32 / kPieces;      // vectors of one instruction
-    const int vectors = pu.cols * PARTS, piece = lane % kPieces;
+    const int vectors = pu.cols * kParts, piece = lane % kPieces;
     const int first = ps_c * S::kChunk + piece * 8;
     const bool live = first < p.hidden;
 #pragma unroll
@@ -789,12 +796,12 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
       if (i >= vectors) break;
       const int v = i + lane / kPieces;
       const uint32_t row = __shfl_sync(0xffffffffu, h_at, v);
-      const int slot = __shfl_sync(0xffffffffu, pu.slot, v / PARTS);
+      const int slot = __shfl_sync(0xffffffffu, pu.slot, v / kParts);
       if (v >= vectors) continue;
       copy_async<16>(to + v * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16, p.h + (long long)row * 64 + (live ? first : 0), live);
       if ((piece & 3) == 0)
         copy_async<8>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 8,
-                      p.h_factor + ((long long)(v % PARTS) * p.tokens * p.top + slot) * (p.hidden / 32) + (live ? first / 32 : 0), live);
+                      p.h_factor + ((long long)(v % kParts) * p.tokens * p.top + slot) * (p.hidden / 32) + (live ? first / 32 : 0), live);
     }
   };
   auto weights = [&](int at) { rows.load(ring + at * stage_bytes, ps_c, 0, p.hidden); };
@@ -825,17 +832,16 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   auto flush = [&]() {
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const int col = PARTS == 2 ? v : 2 * v + (t >> 1);
-      const int tok = __shfl_sync(0xffffffffu, u.tok, col);
-      const float part = share[__shfl_sync(0xffffffffu, u.slot, col)];  // (lanes without a token: of the first, unused)
+      const int tok = __shfl_sync(0xffffffffu, u.tok, v);
+      const float part = share[__shfl_sync(0xffffffffu, u.slot, v)];  // (lanes without a token: of the first, unused)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float a = acc[m][v][h];
           a += __shfl_xor_sync(0xffffffffu, a, 1);
-          if (PARTS == 2) a += __shfl_xor_sync(0xffffffffu, a, 2);
-          if (col < u.cols && (PARTS == 2 ? t == 0 : (t & 1) == 0)) my[tok * kRowsStage + 16 * m + 8 * h + g] += part * a;
+          a += __shfl_xor_sync(0xffffffffu, a, 2);
+          if (v < u.cols && t == 0) my[tok * kRowsStage + 16 * m + 8 * h + g] += part * a;
           acc[m][v][h] = 0.f;
         }
     }
@@ -854,7 +860,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     Columns c = col0;
     c.b += c.b == zeros ? 0 : cs * stage_bytes;
     c.xs += c.xs == zeros ? 0 : cs * stage_bytes;
-    consume_any<WT, F16, PARTS == 2>(ring + cs * stage_bytes, c, (u.cols * PARTS + 1) / 2, acc);
+    consume_any<WT, F16, WHOLE>(ring + cs * stage_bytes, c, u.cols, acc);
     cs = cs + 1 == p.ring ? 0 : cs + 1;
     if (++cc == chunks) {
       flush();
@@ -934,7 +940,7 @@ cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStrea
   // the warps' columns are kept where they leave room for the rings; units of fewer tokens where they do not (Q4_0 with float32 scales)
   size_t smem = 0;
   bool fits = false;
-  for (p.unit = most; p.unit >= 1 && !fits; p.unit -= fits ? 0 : 1) {
+  for (p.unit = p.tokens < most ? p.tokens : most; p.unit >= 1 && !fits; p.unit -= fits ? 0 : 1) {
     const int tokens = p.tokens < p.unit ? p.tokens : p.unit, columns = S::columns(x_f32 ? 2 * tokens : tokens);
     p.max_units = max_units(p.tokens, p.top, p.experts, p.unit < p.down_unit ? p.unit : p.down_unit);
     p.off_zero = (int)round_up(p.off_units + Units::bytes(p.max_units), 128);
@@ -956,7 +962,7 @@ cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStrea
   const int tiles = p.hidden / 32;
   for (p.tiles_item = kUpWarps / p.ks; p.tiles_item > 1 && units * ((tiles + p.tiles_item - 1) / p.tiles_item) < dev.sm_count;) p.tiles_item /= 2;
   const long long items = units * ((tiles + p.tiles_item - 1) / p.tiles_item);
-  const int which = x_f32 ? 2 : WT == QMV_Q4_0 && p.parts == 2;
+  const int which = x_f32 ? 2 : WT == QMV_Q4_0 && !p.out_bf16;
   auto kern = which == 2   ? moe_up_kernel<WT, F16, true, true>
               : which == 1 ? moe_up_kernel<WT, F16, false, WT == QMV_Q4_0>
                            : moe_up_kernel<WT, F16, false, false>;
@@ -969,7 +975,7 @@ cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStrea
 template <int WT, bool F16>
 cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream) {
   using S = Stage<WT, F16>;
-  const int vectors = (p.tokens < p.down_unit ? p.tokens : p.down_unit) * p.parts;
+  const int vectors = (p.tokens < p.down_unit ? p.tokens : p.down_unit) * kParts;
   const int stage = S::kBytes + S::columns(vectors);
   p.off_zero = (int)round_up(sizeof(MoeTable) + Units::bytes(p.max_units) + (size_t)p.tokens * p.top * 4, 128);
   p.off_red = p.off_zero + 128;
@@ -989,9 +995,10 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
   const long long stages = (long long)(p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) * chunks;
   int ranks = 1;
   while (ranks < 8 && tiles * ranks * 2 <= per_sm * dev.sm_count && stages >= 2 * ranks * kDownWarps) ranks *= 2;
-  auto kern = p.parts == 2 ? moe_down_kernel<WT, F16, 2> : moe_down_kernel<WT, F16, 1>;
+  const int which = WT == QMV_Q4_0 && !p.out_bf16;
+  auto kern = which == 1 ? moe_down_kernel<WT, F16, WT == QMV_Q4_0> : moe_down_kernel<WT, F16, false>;
   static bool done[2][64] = {};
-  const cudaError_t err = allow_smem(kern, dev, done[p.parts - 1]);
+  const cudaError_t err = allow_smem(kern, dev, done[which]);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * ranks));
@@ -1012,10 +1019,10 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
 
 }  // namespace
 
-size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16) {
+size_t moe_scratch_bytes(int64_t tokens, int top, int hidden) {
   const size_t t = tokens < kTokens ? tokens : kTokens;
   const int pairs = (int)t * top;
-  return (size_t)pairs * (hidden * 2 + hidden / 32 * 8) * (out_bf16 ? 1 : 2) + sizeof(MoeTable) + Units::bytes(pairs) + (size_t)pairs * 4;
+  return (size_t)pairs * (hidden * 2 + hidden / 32 * 8) * kParts + sizeof(MoeTable) + Units::bytes(pairs) + (size_t)pairs * 4;
 }
 
 cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -1032,10 +1039,9 @@ cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t str
     p.top = a.top;
     p.h = static_cast<uint16_t*>(a.scratch);
     p.h_plane = (long long)p.tokens * a.top * a.hidden;
-    p.parts = a.out_bf16 ? 1 : 2;
-    p.h_factor = reinterpret_cast<float2*>(p.h + p.parts * p.h_plane);
-    p.table = reinterpret_cast<MoeTable*>(p.h_factor + (size_t)p.parts * p.tokens * p.top * (p.hidden / 32));
-    p.down_unit = kVectors / p.parts;
+    p.h_factor = reinterpret_cast<float2*>(p.h + kParts * p.h_plane);
+    p.table = reinterpret_cast<MoeTable*>(p.h_factor + (size_t)kParts * p.tokens * p.top * (p.hidden / 32));
+    p.down_unit = p.tokens < kVectors / kParts ? p.tokens : kVectors / kParts;  // (one or two tokens: one set of units for both kernels)
     p.w2_q4 = a.w2.wtype == QMV_Q4_0;
     p.ids = a.ids == nullptr ? nullptr : a.ids + t0 * a.top;
     p.shares = a.shares == nullptr ? nullptr : a.shares + t0 * a.top;

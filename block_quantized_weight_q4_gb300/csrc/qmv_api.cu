@@ -872,7 +872,7 @@ int qmv_qk_rope(int x_dtype, int64_t rows, int heads, int kv_heads, int head_dim
 size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dtype) {
   if (tokens < 0 || top < 1 || top > QMV_MOE_MAX_TOP || hidden <= 0 || hidden % 64 != 0 || hidden >= kMoeMaxDim) return 0;
   if (out_dtype != QMV_X_F32 && out_dtype != QMV_X_BF16) return 0;
-  return moe_scratch_bytes(tokens, top, (int)hidden, out_dtype == QMV_X_BF16);
+  return moe_scratch_bytes(tokens, top, (int)hidden);
 }
 
 int qmv_moe(const qmv_moe_layer* layer, int64_t tokens, const float* logits, int64_t logits_stride, int top, int renorm, float scale,

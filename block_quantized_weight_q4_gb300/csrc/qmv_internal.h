@@ -333,14 +333,13 @@ struct MoeParams {
   const float* logits;
   const void* x;
   void* out;
-  uint16_t* h;        // halves of act(gate) * up, tokens * top rows of `hidden`, `parts` times
+  uint16_t* h;        // halves of act(gate) * up, tokens * top rows of `hidden`: hi, then (from h_plane on) lo
   float2* h_factor;   // of each 32 of a row: what products with them are multiplied by, what is taken off then
   MoeTable* table;    // the routing, for moe_down
   int32_t* ids;
   float* shares;
   long long logits_stride;
   long long h_plane;  // elements between h's parts
-  int parts;
   int tokens, experts, top, dim, hidden;
   int renorm, act, out_bf16, w2_q4;
   float scale;
@@ -353,7 +352,7 @@ struct MoeParams {
   int off_units, off_zero, off_red, off_cols, off_ring;  // places in shared memory
 };
 constexpr int64_t kMoeMaxDim = 1 << 24;
-size_t moe_scratch_bytes(int64_t tokens, int top, int hidden, bool out_bf16);
+size_t moe_scratch_bytes(int64_t tokens, int top, int hidden);
 cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace qmv

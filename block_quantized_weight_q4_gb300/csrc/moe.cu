@@ -16,9 +16,9 @@
 // Bound by the weights' bytes; below that by what comes before them: the routing, code that is fetched once, the fill of two pipelines
 // (about 12 us of a call; so what runs once is small and no CTA runs code that the others do not: one CTA that alone left the routing
 // cost 7 us).  TMA boxes in place of cp.async measured 53.9 against 52.7 us (1 token, two of 8 experts of 11008 x 4096) and 112 against
-// 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 45.6 us (152 MB) and 114 us
+// 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 46 us (152 MB) and 116 us
 // (297 MB), in their long stretches 4.5 to 5.7 TB/s; 7 tokens over 16 Q8_0 experts of 1408 x 2048 41.8 us; 1 token, 4 of 32 of 512 x 1024
-// 12.5 us.
+// 12.6 us.
 //
 // Products: m16n8k16 with IEEE halves.  Lane t of a row's four lanes takes a whole block of 32 weights (one or two 16-byte loads), so an
 // MMA's k slots hold four different blocks; the columns are 2 vectors x those 4 blocks, and a lane's B values are
@@ -243,7 +243,7 @@ struct Stage {
   static constexpr int kScaleRow = kBlocks * (F16 ? 2 : 4);
   static constexpr int kBytes = kQ + kRowsStage * kScaleRow;
   // a vector's chunk: its blocks' halves, 64 of 80 bytes a block, so that the lanes that read four blocks lie in different banks.
-  // Then for each block what a sum of products is multiplied by and what is taken off it then.
+  // Then for each block what a sum of products is multiplied by at the end, and what is taken off it first.
   static constexpr int kBlock = 80;
   static constexpr int kVector = kBlocks * kBlock;
   static __host__ __device__ constexpr int columns(int vectors) { return vectors * (kVector + kBlocks * 8); }
@@ -309,10 +309,19 @@ struct Rows {
   }
 };
 
+// The power of two that brings a block's largest magnitude into [2^14, 2^15), and its inverse; at most 2^126 (a block below 2^-112 stays below
+// 2^14 then, its values multiples of 2^-23), so that both are normal.  1 for zeros, infinity and NaN.
+__device__ __forceinline__ void block_scale(float amax, float& up, float& down) {
+  const int e = (int)(__float_as_uint(amax) >> 23);
+  const int scale = amax == 0.f || e == 255 ? 127 : min(268 - e, 253);
+  up = __uint_as_float((uint32_t)scale << 23);
+  down = __uint_as_float((uint32_t)(254 - scale) << 23);
+}
+
 // Eight values of a block of 32 (elements 8 piece ..) that four neighbouring lanes hold, as halves at the power of two that brings the block's
 // largest into [2^14, 2^15): hi, and with LO what hi leaves (11 more bits).  For Q4_0 in the order in which masks take a word's nibbles (0, 2,
-// 1, 3 of each four), the block's second half as a 16th (!WHOLE).  mul, off: what the products' sum is multiplied by and what is taken off
-// then.
+// 1, 3 of each four), the block's second half as a 16th (!WHOLE).  off: what is taken off the products'
+// sum; mul: what it is multiplied by, after the weights' scale (before it, or with the levels' 2^24, it would pass float32's range).
 template <int WT, bool LO, bool WHOLE>
 __device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32_t (&hi)[4], uint32_t (&lo)[4], float& mul, float& off) {
   float amax = 0.f;
@@ -321,7 +330,7 @@ __device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   float up, down;
-  half_stage_scale(amax, up, down);
+  block_scale(amax, up, down);
   static_assert(WHOLE || !LO, "two halves are for whole levels");
   constexpr bool kBits = WT == QMV_Q4_0 && !WHOLE;
   const float part = kBits && piece >= 2 ? 0.0625f : 1.f, back = kBits && piece >= 2 ? 16.f : 1.f;
@@ -342,8 +351,7 @@ __device__ __forceinline__ void to_halves(const float (&v)[8], int piece, uint32
     sum *= back;
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    mul = down * 0x1p24f;
-    off = 8.f * sum * down;
+    off = 8.f * sum;
   }
 }
 
@@ -427,7 +435,7 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
         }
     }
     // columns 2 t and 2 t + 1: vector t / 2 of the set, blocks 2 (t & 1) and the next
-    float f[SETS][4];  // multiplied by, taken off; of both blocks
+    float f[SETS][4];  // multiplied by, taken off before; of both blocks
 #pragma unroll
     for (int v = 0; v < SETS; ++v) lds_f32x4(xs + v * xs_step + i * 32, f[v]);
 #pragma unroll
@@ -446,9 +454,9 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
         }
 #pragma unroll
         for (int v = 0; v < SETS; ++v) {
-          const float s0 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h], f[v][0], -f[v][1]) : c[m][v][2 * h] * f[v][0];
-          const float s1 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h + 1], f[v][2], -f[v][3]) : c[m][v][2 * h + 1] * f[v][2];
-          acc[m][v][h] = fmaf(d.x, s0, fmaf(d.y, s1, acc[m][v][h]));
+          const float s0 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h], 0x1p24f, -f[v][1]) : c[m][v][2 * h];
+          const float s1 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h + 1], 0x1p24f, -f[v][3]) : c[m][v][2 * h + 1];
+          acc[m][v][h] = fmaf(s0 * d.x, f[v][0], fmaf(s1 * d.y, f[v][2], acc[m][v][h]));
         }
       }
   }
@@ -705,7 +713,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         const float h = glu(p.act, gate, up);
         const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(isnan(h) ? 0.f : fabsf(h))));
         float to, down;
-        half_stage_scale(amax, to, down);
+        block_scale(amax, to, down);
         // as to_halves() leaves activations, for W2's type
         const bool bits = p.w2_q4 && p.out_bf16, split = bits && lane >= 16;
         const float v = h * to * (split ? 0.0625f : 1.f);
@@ -727,7 +735,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         }
         if (lane < kParts)
           p.h_factor[((long long)lane * p.tokens * p.top + slot) * (p.hidden / 32) + ht] =
-              make_float2(bits ? down * 0x1p24f : down, 8.f * sum * down);
+              make_float2(down, 8.f * sum);
       }
     }
     if ((first += p.tiles_item) >= tiles) first = 0, ++unit;

@@ -334,7 +334,7 @@ struct MoeParams {
   const void* x;
   void* out;
   uint16_t* h;        // halves of act(gate) * up, tokens * top rows of `hidden`: hi, then (from h_plane on) lo
-  float2* h_factor;   // of each 32 of a row: what products with them are multiplied by, what is taken off then
+  float2* h_factor;   // of each 32 of a row: what products with them are multiplied by, what is taken off before
   MoeTable* table;    // the routing, for moe_down
   int32_t* ids;
   float* shares;

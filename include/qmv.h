@@ -772,7 +772,8 @@ size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dt
  * timing, the last bits of a token may depend on the other tokens of its block of 64.  Levels enter the tensor core as exact
  * halves, an activation as a half after the power of two that brings the largest of its 32 columns into [2^14, 2^15) (bfloat16 values are
  * exact down to 2^-27 of that largest; float32 ones two halves, 22 bits), act(gate) * up likewise as two halves (22 bits); values below
- * 2^-24 of their block's largest are multiples of 2^-34 of it.
+ * 2^-24 of their block's largest are multiples of 2^-34 of it (of 2^-149, where that largest is below 2^-112).  Activations may be any finite
+ * float32, with weights' scales below 2^100; infinity or NaN among them makes the token's results NaN or infinite.
  * Tokens go in blocks of 64, each of two launches that read every used expert's weights: for prompts of many tokens
  * the weights' bytes are read once a block.
  * tokens 0 launches nothing.  Returns QMV_OK, QMV_E_FORMAT (types, act), QMV_E_ARG (null pointer, tokens < 0, scale not finite), QMV_E_SHAPE

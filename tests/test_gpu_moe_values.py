@@ -43,3 +43,66 @@ def test_bfloat16_outputs_are_rounded_once(qmv, wt, sf, bf16):
     gap = 2.0 ** (np.floor(np.log2(np.abs(want))) - 7)
     most = np.minimum(1, 0.8 * e / gap).sum()
     assert (y != near).sum() <= most + 6 * np.sqrt(most) + 3
+
+
+def _scaled(qmv, wt, experts, dim, hidden, seed, *by):
+    """A layer of float32 scales whose W1, W3 and W2 are those of make_matrix times 2^by."""
+    import torch
+    layer = Layer(qmv, wt, wt, 0, experts, dim, hidden, seed=seed)
+    images = []
+    for name, W, b, rows, cols in (("w1", layer.dev.W1, by[0], hidden, dim), ("w3", layer.dev.W3, by[1], hidden, dim), ("w2", layer.dev.W2, by[2], dim, hidden)):
+        off = qmv.scale_offset(wt, 0, experts * rows, cols)
+        W = W.clone()
+        d = W[off:off + experts * rows * cols // 8].view(torch.float32) * 2.0 ** b
+        assert d.isfinite().all() and ((d == 0) | (d.abs() >= 2.0 ** -126)).all()  # (else they would be rounded)
+        W[off:off + experts * rows * cols // 8] = d.view(torch.uint8)
+        images.append(W)
+        setattr(layer, name, getattr(layer, name).astype(np.float64) * 2.0 ** b)
+    layer.dev = qmv.Moe(wt, wt, 0, experts, dim, hidden, *images)
+    return layer
+
+
+@pytest.mark.parametrize("wt", [1, 2])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("amp,by,act", [
+    (119, (-112, -113, 0), "silu"),   # x at the top of the range
+    (124, (-114, -115, -8), "gelu"),
+    (60, (0, 0, -114), "silu"),       # act(gate) * up there: 2^123 at most for Q4_0, but 2^131, past the range, for Q8_0
+    (56, (0, 0, -112), "silu"),
+    (-120, (96, 96, 47), "gelu"),     # x at the bottom
+    (-130, (94, 92, 76), "silu"),     # (subnormal numbers)
+    (-58, (0, 0, 99), "silu"),        # act(gate) * up there
+])
+def test_ends_of_the_range(qmv, wt, bf16, out, amp, by, act):
+    """Finite results stay what the formula says where activations or act(gate) * up come near float32's ends.  Float32 outputs: 2^-20 of
+    their norm, as sums of 16 roundings of gate, up and down by chance of sign.  bfloat16 ones: 2^-8 of each for its rounding, and 2^-17 of the norm before it."""
+    tokens, dim, hidden = 5, 512, 256
+    layer = _scaled(qmv, wt, 4, dim, hidden, 71, *by)
+    rng = np.random.default_rng(72)
+    x, xd = _x(rng, tokens, dim, bf16, 2.0 ** amp)
+    logits = rng.standard_normal((tokens, 4)).astype(F)
+    y = qmv.moe(layer.dev, xd, dev_x(logits), 2, act=act, out=out).double().cpu().numpy()
+    want = step_ref.moe(layer.w1, layer.w3, layer.w2, x, logits, 2, True, 1.0, act, 2)[0]
+    norm = np.linalg.norm(want)
+    if amp == 60 and wt == 1:
+        assert not np.isfinite(y).all()
+        return
+    assert np.isfinite(norm) and norm > 1e-30 and np.isfinite(y).all()
+    assert np.linalg.norm(y - want) <= (2.0 ** -20 if out == "f32" else 2.0 ** -8 + 2.0 ** -17) * norm
+
+
+def test_blocks_of_both_ends(qmv):
+    """One token's blocks of 32 from 2^-140 to 2^120: each at a power of two of its own."""
+    layer = _scaled(qmv, 2, 1, 512, 64, 73, -100, -100, 60)
+    rng = np.random.default_rng(74)
+    amps = np.repeat(2.0 ** np.linspace(-140, 120, 16), 32)
+    for only in (None, 15):  # all blocks, the largest alone
+        x = (rng.standard_normal((2, 512)) * amps).astype(F)
+        if only is not None:
+            x[:, :32 * only] = 0
+        for out in ("f32", "bf16"):
+            y = qmv.moe(layer.dev, dev_x(x), dev_x(np.zeros((2, 1), F)), 1, out=out).double().cpu().numpy()
+            want = step_ref.moe(layer.w1, layer.w3, layer.w2, x, np.zeros((2, 1), F), 1, True, 1.0, "silu", 2)[0]
+            assert np.isfinite(want).all()
+            assert np.linalg.norm(y - want) <= (2.0 ** -20 if out == "f32" else 2.0 ** -8 + 2.0 ** -17) * np.linalg.norm(want)

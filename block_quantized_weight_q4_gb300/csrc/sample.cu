@@ -708,7 +708,8 @@ __device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* hom
   return most;
 }
 
-// The pass of a draw from the whole row: each chunk's best score (in powers of two, nothing subtracted), and whether the row holds NaN.
+// The pass of a draw from the whole row: each chunk's best score (in powers of two, nothing subtracted), and whether the row holds NaN or
+// +infinity (whose score is NaN, and lost, where the random number is infinite, negative or NaN).
 // A random number that is not above 0, subnormal ones among them, makes a score that is infinite or NaN: the caller looks again.
 __device__ __forceinline__ bool free_pass(const Row& r, Shared& sh, float& most) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -716,10 +717,10 @@ __device__ __forceinline__ bool free_pass(const Row& r, Shared& sh, float& most)
   const float4* ev = reinterpret_cast<const float4*>(r.e + r.head);
   const int subs = (r.q1 - r.q0 + 31) / 32;
   int* best = reinterpret_cast<int*>(sh.best());
-  float nan = 0.f;
+  float high = 0.f;
   most = -INFINITY;
   auto score = [&](float x, float e) {
-    nan = max_nan(nan, x);
+    high = max_nan(high, x);
     return fmaf(x, r.scale, -log2_of_normal(e));
   };
   for (int s = wid; s < subs; s += 4 * kWarps) {
@@ -755,7 +756,7 @@ __device__ __forceinline__ bool free_pass(const Row& r, Shared& sh, float& most)
     most = max_nan(most, o);
     if (lane == 0) best[r.chunks] = mapped(o);
   }
-  return nan != nan;
+  return !(high < INFINITY);
 }
 
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p, int ranks) {
@@ -914,9 +915,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const bool wide = ((reinterpret_cast<uintptr_t>(r.e + r.head)) & 15) == 0;
     if (wide) {
       float most;
-      const bool nan = free_pass(r, sh, most);
-      // NaN, infinite scores and those so large that float32 leaves them coarse are left to the passes by the maximum
-      const float m = unordered(over_ranks(nan || !(most < INFINITY) ? 0xffffffffu : ordered(most)));
+      const bool special = free_pass(r, sh, most);
+      // NaN, infinities, infinite scores and those so large that float32 leaves them coarse are left to the passes by the maximum
+      const float m = unordered(over_ranks(special || !(most < INFINITY) ? 0xffffffffu : ordered(most)));
       if (fabsf(m) < 2048.f) {
         auto score = [&](float x, float e) { return fmaf(x, r.scale, -log2_of_normal(e)); };
         // |x scale| is at most that of the score and |log2 e| together

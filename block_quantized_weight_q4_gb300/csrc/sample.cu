@@ -144,10 +144,11 @@ __device__ __forceinline__ float log2_of_normal(float e) {  // (-infinity for su
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(e));
   return y;
 }
-// x's score in powers of two below the maximum's, with the random number e.
+// x's score in powers of two below the maximum's, with the random number e; -infinity where e is not one (not above 0, infinite, NaN).
+// Any other score stays finite, however far x lies below at a low temperature: those at the floor are told apart in 64 bits.
 __device__ __forceinline__ float score_of(const Row& r, float x, float e) {
   const float t = e >= 0x1p-126f ? log2_of_normal(e) : e > 0.f ? log2_of(e) : INFINITY;
-  return fmaf(x - r.max, r.scale, -t);
+  return t < INFINITY ? fmaxf(fmaf(x - r.max, r.scale, -t), -1e38f) : -INFINITY;
 }
 
 struct Shared {

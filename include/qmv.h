@@ -680,7 +680,7 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
  *   min_p : of those the ids with w_j >= min_p (0 or less, or NaN: all; above 1 as 1),
  * and its id is the kept one with the largest (logit_j - max) / temperature - ln noise_j, equal ones by the lower id:
  * a draw from the kept w, each of them chosen with w_j over their sum.  The noise of ids that are cut off does not
- * matter (and is not read where the cuts leave few).  An id whose noise is not above 0 (or NaN) is not chosen; where
+ * matter (and is not read where the cuts leave few).  An id whose noise is not above 0, infinite or NaN is not chosen; where
  * that leaves none, and with a temperature of 2^-100 or less (0, negative or NaN), top_k 1 or top_p 0, the id is that of
  * the largest logit.  A logit of -infinity is a masked id.  A row that holds NaN, or in which every logit is
  * -infinity, gives -1; one that holds +infinity the lowest id of those.

@@ -2,6 +2,8 @@
 import numpy as np
 import pytest
 
+from test_gpu_sample import _logits
+
 pytestmark = pytest.mark.gpu
 F = np.float32
 
@@ -63,3 +65,99 @@ def test_scores_past_float32(qmv, vocab):
     e[:] = rng.choice(np.array([0.0, -2.0, np.nan, np.inf], F), e.shape)  # none that can be chosen: the largest
     for cut in (None, up(k)):
         assert qmv.sample(up(x), up(e), up(t), cut).tolist() == x.argmax(axis=1).tolist()
+
+
+def _kept(x, t, k, p, m):
+    """The row's ids in descending order, and how many of the first are kept: lo at least, hi at most, by the documentation's slack.
+    Top-p's: each weight off by (1 + ln 1/w) 2^-21 of itself and 2^-32 of the largest, so as far off the mass above an id and the
+    kept mass; a row's sum by float32 additions of vocab / 4096 terms in a thread and 5 + 8 steps of joining.  Min-p's: 64 bits'."""
+    x64 = x.astype(np.float64) + 0.0
+    order = np.lexsort((np.arange(x.size), -x64))
+    n = int(np.isfinite(x).sum())
+    z = (x64[order[:n]] - x64[order[0]]) / np.float64(F(t))
+    if 0 < k < n:
+        n = k
+    z = z[:n]
+    w = np.exp(z)
+    lo = hi = n
+    if p < 1:
+        eps = (1 - z) * 2.0 ** -21 * w + 2.0 ** -32
+        before, off = np.cumsum(w) - w, np.cumsum(eps) - eps
+        total, far = w.sum(), eps.sum() + w.sum() * (x.size / 4096 + 13) * 2.0 ** -24
+        lo = max(1, int((before + off < np.float64(F(p)) * (total - far)).sum()))
+        hi = max(1, int((before - off < np.float64(F(p)) * (total + far)).sum()))
+    if m > 0:
+        m = min(np.float64(F(m)), 1.0)
+        off = 2.0 ** -45 if m < 1 else 0.0
+        lo, hi = min(lo, int((w >= m * (1 + off)).sum())), min(hi, int((w >= m * (1 - off)).sum()))
+    return order, np.exp(z), max(lo, 1), max(hi, 1)
+
+
+# logits, their count, and the settings: what places the border is on the right
+ROUTES = [
+    ("flat", 5000, 0.9, 60, 0.8, 0.0),        # the list holds everything kept
+    ("sharp", 30011, 0.8, 0, 0.95, 0.0),
+    ("sharp", 30011, 0.8, 50, 0.9, 0.05),
+    ("flat", 30011, 0.9, 0, 0.5, 0.0),        # top-p: a bucket is collected
+    ("flat", 30011, 1.1, 0, 0.9, 0.0),
+    ("flat", 30011, 0.7, 0, 0.999, 0.0),
+    ("flat", 151936, 0.9, 0, 0.95, 0.0),
+    ("flat", 30011, 1.0, 2049, 1.0, 0.0),     # top-k past the list: a bucket
+    ("flat", 30011, 0.8, 20000, 1.0, 0.0),
+    ("flat", 3000, 1.0, 2500, 1.0, 0.0),
+    ("flat", 30011, 1.0, 2500, 0.7, 0.0),     # both: the k-th logit, then the mass above it
+    ("flat", 30011, 1.3, 20000, 0.9, 0.0),
+    ("flat", 30011, 0.6, 5000, 0.999, 0.0),
+    ("steps", 30011, 1.0, 0, 0.7, 0.0),       # equal logits: the bucket is cut again by the keys' bits
+    ("steps", 30011, 0.9, 9000, 1.0, 0.0),
+    ("steps", 30011, 0.9, 9000, 0.8, 0.0),
+    ("equal", 3000, 1.0, 0, 0.5, 0.0),
+    ("equal", 30011, 0.8, 0, 0.9, 0.0),
+    ("equal", 30011, 0.8, 2500, 1.0, 0.0),
+    ("equal", 30011, 1.3, 20000, 0.7, 0.0),
+    ("near", 3000, 1.3, 2900, 0.7, 0.0),
+    ("near", 30011, 1.0, 0, 0.5, 0.0),
+    ("near", 30011, 1.0, 20000, 1.0, 0.0),
+    ("near", 30011, 1.0, 20000, 0.3, 0.0),
+    ("flat", 30011, 0.9, 0, 0.9, 0.02),       # min-p after them
+    ("flat", 30011, 1.1, 0, 0.99, 0.001),
+    ("flat", 30011, 1.0, 5000, 1.0, 0.01),
+    ("flat", 30011, 1.0, 20000, 0.95, 0.003),
+    ("near", 30011, 1.0, 20000, 1.0, 1.0),
+    ("sharp", 30011, 1.0, 0, 1.0, 0.1),       # min-p alone
+    ("flat", 30011, 1.0, 0, 1.0, 0.05),
+    ("flat", 30011, 1.2, 0, 1.0, 1e-4),
+    ("flat", 151936, 0.9, 0, 1.0, 1e-6),
+    ("flat", 30011, 0.6, 0, 1.0, 1e-8),
+    ("equal", 30011, 1.0, 0, 1.0, 1.0),
+    ("flat", 300001, 1.0, 0, 0.9, 0.0),       # rows of more chunks than there are places for
+    ("flat", 300001, 1.0, 100000, 0.9, 0.0),
+    ("sharp", 300001, 0.9, 0, 0.9, 1e-5),
+    ("near", 300001, 1.0, 0, 0.7, 0.0),
+    ("steps", 300001, 1.0, 100000, 1.0, 0.0),
+    ("flat", 1000003, 1.0, 0, 0.9, 0.0),
+]
+
+
+@pytest.mark.parametrize("kind,vocab,t,k,p,m", ROUTES)
+def test_borders(qmv, kind, vocab, t, k, p, m):
+    """Of ids around the border one at a time gets noise that puts it ahead of all others: it comes out where it is kept, else the
+    largest logit does.  In one call for all of them, and for some in a call of their own (more CTAs a row)."""
+    import torch
+    rng = np.random.default_rng([vocab, len(kind), k, int(1000 * p)])
+    x = _logits(rng, 1, vocab, kind)[0]
+    order, w, lo, hi = _kept(x, t, k, p, m)
+    finite = int(np.isfinite(x).sum())
+    assert hi - lo <= 2 + 2.0 ** -7 * hi  # (what the slack leaves open)
+    at = sorted({i for i in (0, 1, lo // 2, lo - 3, lo - 2, lo - 1) if 0 <= i < lo} | {i for i in (hi, hi + 1, hi + 2, hi + 100, finite - 1) if hi <= i < finite})
+    assert w[[i for i in at if i < lo]].min() > 1e-25  # (the noise outweighs that)
+    rows = len(at)
+    e = torch.ones((rows, vocab), device="cuda")
+    e[torch.arange(rows), torch.from_numpy(order[at]).cuda()] = 1e-30
+    logits = torch.from_numpy(x).cuda().repeat(rows, 1)
+    how = dict(temperature=torch.full((rows,), t, device="cuda"), top_k=torch.full((rows,), k, dtype=torch.int32, device="cuda"),
+               top_p=torch.full((rows,), p, device="cuda"), min_p=torch.full((rows,), m, device="cuda"))
+    want = [int(order[i]) if i < lo else int(order[0]) for i in at]
+    assert qmv.sample(logits, e, **how).tolist() == want
+    for r in range(max(0, sum(i < lo for i in at) - 2), min(rows, sum(i < lo for i in at) + 2)):
+        assert qmv.sample(logits[r:r + 1], e[r:r + 1], **{n: v[r:r + 1] for n, v in how.items()}).item() == want[r]

@@ -87,7 +87,6 @@ __device__ __forceinline__ float exp2_of(float t) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
   return y;
 }
-__device__ __forceinline__ float weight_of(float t) { return t > 0.f ? exp2_of(-t) : 1.f; }
 // The weight as an integer in units of 2^-31: sums of them are exact, so no order of adding matters.  An id counts
 // to 2^-32 of the largest.
 __device__ __forceinline__ uint32_t mass_of(float t) { return t > 0.f ? __float2uint_rn(exp2_of(-t) * 0x1p31f) : 0x80000000u; }
@@ -124,6 +123,9 @@ __device__ __forceinline__ void for_each(const Row& r, const uint32_t* chunk_max
     f(__ldg(r.x + id), id, r.chunks);
   }
 }
+
+// (one piece of code, which two places fetch)
+__device__ __noinline__ double log_of(double v) { return log(v); }
 
 struct Draw {  // a candidate's score in 64 bits; the larger wins, then the lower id
   double s;
@@ -165,6 +167,7 @@ struct Shared {
   int rank_id;
   // what rank 0 or every rank found
   uint32_t reaching;  // rank 0's: chunks whose maxima reach min-p's value
+  uint32_t edge_m;    // the least mapped logit that min-p keeps
   float reach;  // what the chunks' maxima tell: every kept logit reaches it (NaN: they do not tell)
   int bucket;
   uint32_t above_count, in_count;
@@ -276,24 +279,36 @@ __device__ bool find_border(Shared& sh, const uint32_t (&c)[2], const Key (&m)[2
   return found;
 }
 
-// The smallest mapped logit whose bucket is at most b, or (min_p > 0) whose weight is min_p at least; both rise with the logit, and the
-// maximum's do.
-// (32 values at a time, one a lane; whole warps.)
-__device__ __forceinline__ uint32_t edge_of(const Row& r, int b, float min_p) {
+// The smallest mapped logit of lo .. hi that `holds`, which hi does and every logit above one that does.  (32 values at a time, one a
+// lane; whole warps.)
+template <typename F>
+__device__ __forceinline__ uint32_t least_of(uint32_t lo, uint32_t hi, F holds) {
   const uint32_t lane = threadIdx.x & 31;
-  uint32_t lo = kMasked + 1, hi = ordered(r.max);
 #pragma unroll 1
   while (lo < hi) {
     const uint32_t step = max((hi - lo) / 32, 1u), far = min(lane * step, hi - lo);
-    const float t = below(r, unordered(lo + far));
-    const uint32_t holds = __ballot_sync(0xffffffffu, min_p > 0.f ? weight_of(t) >= min_p : bucket_of(t) <= b);
-    const uint32_t first = holds != 0 ? __ffs(holds) - 1 : 32;  // the first lane whose value holds
+    const uint32_t which = __ballot_sync(0xffffffffu, holds(unordered(lo + far)));
+    const uint32_t first = which != 0 ? __ffs(which) - 1 : 32;  // the first lane whose value holds
     if (first == 0) return lo;
     const uint32_t from = lo;
     lo = from + min((first - 1) * step, hi - from) + 1;
     if (first < 32) hi = from + min(first * step, hi - from);
   }
   return lo;
+}
+// ... whose bucket is at most b.
+__device__ __forceinline__ uint32_t edge_of(const Row& r, int b) {
+  return least_of(kMasked + 1, ordered(r.max), [&](float x) { return bucket_of(below(r, x)) <= b; });
+}
+
+// ... whose weight is min_p at least: x - max >= T ln min_p in 64 bits, so that how small min_p is costs no accuracy; looked for as far around
+// float32's answer as that may be off.
+__device__ __forceinline__ uint32_t edge_of_weight(const Row& r, float T, float min_p) {
+  const double least = (double)T * log_of(min_p);
+  const float z = T * logf(min_p), about = r.max + z, off = 0x1p-20f * fabsf(z) + 0x1p-21f * fabsf(r.max) + 0x1p-149f;
+  const uint32_t top = ordered(r.max);
+  return least_of(max(ordered(about - off), kMasked + 1), min(ordered(about + off), top),
+                  [&](float x) { return (double)x - (double)r.max >= least; });
 }
 
 // The collected keys in descending order.
@@ -440,14 +455,14 @@ __device__ Border resolve(cg::cluster_group& cl, const Row& r, Shared& sh, Share
   Key above_mass = sh.above_mass;
   Key lo, hi;
   const bool whole = above + inside <= kList;
-  lo = (Key)edge_of(r, sh.bucket, 0.f) << 32;
+  lo = (Key)edge_of(r, sh.bucket) << 32;
   if (lo < floor) lo = floor;  // (the histograms count none below it)
   if (whole) {
     hi = ~(Key)0;
     above = 0;
     above_mass = 0;
   } else {
-    hi = sh.bucket == 0 ? ~(Key)0 : ((Key)edge_of(r, sh.bucket - 1, 0.f) << 32) - 1;
+    hi = sh.bucket == 0 ? ~(Key)0 : ((Key)edge_of(r, sh.bucket - 1) << 32) - 1;
   }
   // cut again by the keys' bits: no two keys are equal, so at most 6 rounds of 10 bits leave fewer than the list holds
   for (int round = 0; !whole && inside > kList && round < 8; ++round) {
@@ -835,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (rank == 0 && threadIdx.x == 0) p.ids[row] = sh.close_id[0];
       return;
     }
-    auto exact = [&](float x, float e, int id) { return Draw{((double)x - (double)r.max) / (double)T - log((double)e), id}; };
+    auto exact = [&](float x, float e, int id) { return Draw{((double)x - (double)r.max) / (double)T - log_of((double)e), id}; };
     Draw d{0.0, -1};
     if (n > (uint32_t)kClose) {
       visit(least, [&](float x, float e, int id) {
@@ -950,7 +965,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   // scores in powers of two below the maximum's
-  const float least_m = by_m ? unordered(edge_of(r, 0, fminf(min_p, 1.f))) : -INFINITY;  // the least logit of min-p's weight
+  float least_m = -INFINITY;  // the least logit of min-p's weight
+  if (by_m) {
+    if (wid == 0) {  // (64-bit units are few)
+      const uint32_t edge = edge_of_weight(r, T, fminf(min_p, 1.f));
+      if (lane == 0) sh.edge_m = edge;
+    }
+    __syncthreads();
+    least_m = unordered(sh.edge_m);
+  }
   auto kept_by_m = [&](float x) { return x >= least_m; };
   auto score = [&](float x, float e) { return score_of(r, x, e); };
 
@@ -1098,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (bucket >= 0) {
     const uint32_t above_count = sh.above_count;
     const Key above_mass = sh.above_mass;
-    const float from = unordered(edge_of(r, bucket, 0.f)), above = bucket > 0 ? unordered(edge_of(r, bucket - 1, 0.f)) : INFINITY;
+    const float from = unordered(edge_of(r, bucket)), above = bucket > 0 ? unordered(edge_of(r, bucket - 1)) : INFINITY;
     auto kind = [&](float x, int) { return x >= above ? (int)kept_by_m(x) : x >= from ? 2 : 0; };
     most = draw_pass(r, sh, home, kMasked + 1, true, kind, score);  // (the bucket is collected whole, whatever min-p keeps)
     cl.sync();

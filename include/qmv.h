@@ -685,9 +685,9 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
  * the largest logit.  A logit of -infinity is a masked id.  A row that holds NaN, or in which every logit is
  * -infinity, gives -1; one that holds +infinity the lowest id of those.
  * (A temperature above 2^100 counts as that.)  The top_p border is placed by sums of w as integers in units of
- * 2^-31 (where nothing else cuts first, the sum of the row by float32 sums of vocab / 4096 terms at most): it may be off by
- * 2^-20 of the kept mass in rows of up to 2^20 ids, and by vocab 2^-32 of the largest w where that is more; the min_p border
- * by 2^-20 of min_p.  Scores near the largest are compared in 64 bits.  Results do not depend on timing or on the other rows of the call.
+ * 2^-31 of the largest (where top_k does not cut first, the sum of the row by float32 sums of vocab / 4096 terms at most, 2^-24
+ * of it for each), of weights that are off by (1 + ln 1/w) 2^-21 of themselves and 2^-32 of the largest at most.  The min_p border and
+ * scores near the largest are those of 64 bits.  Results do not depend on timing or on the other rows of the call.
  * Allocates nothing and uses no workspace.
  * Returns QMV_OK, QMV_E_ARG (rows < 0, null logits, noise or ids), QMV_E_SHAPE (vocab not within 1..
  * QMV_SAMPLE_MAX_VOCAB - 1, strides below vocab, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */

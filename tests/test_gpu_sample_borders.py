@@ -161,3 +161,26 @@ def test_borders(qmv, kind, vocab, t, k, p, m):
     assert qmv.sample(logits, e, **how).tolist() == want
     for r in range(max(0, sum(i < lo for i in at) - 2), min(rows, sum(i < lo for i in at) + 2)):
         assert qmv.sample(logits[r:r + 1], e[r:r + 1], **{n: v[r:r + 1] for n, v in how.items()}).item() == want[r]
+
+
+def test_min_p_to_the_last_bit(qmv):
+    """The smallest float32 logit of min-p's weight is kept, the one below it is not, whatever min-p, temperature and maximum."""
+    import torch
+    rng = np.random.default_rng(21)
+    n = 400
+    t, m = rng.uniform(0.3, 2.0, n).astype(F), (10.0 ** rng.uniform(-12, -0.05, n)).astype(F)
+    top = (rng.standard_normal(n) * 10.0 ** rng.uniform(-3, 2, n)).astype(F)
+    t[:4], m[:4] = [2.0 ** 100, 2.0 ** -60, 1.0, 1.0], [1e-3, 0.9, 1e-45, 1.0]
+    least = top.astype(np.float64) + t.astype(np.float64) * np.log(m.astype(np.float64))
+    kept = least.astype(F)
+    kept = np.where(kept < least, np.nextafter(kept, F(np.inf)), kept)
+    kept[3] = top[3]
+    for off in (0, 1):
+        x = np.full((n, 9), F(-3e38))
+        x[:, 7], x[:, 5 - off] = top, kept if off == 0 else np.nextafter(kept, F(-np.inf))
+        e = np.ones((n, 9), F)
+        e[:, 5 - off] = 1e-38
+        clear = (x[:, 5 - off] > x[:, 0]) & (x[:, 5 - off] < top) & (t * 80 > top - x[:, 5 - off])  # (the noise outweighs the distance)
+        assert clear.sum() > n - 10
+        got = qmv.sample(*(torch.from_numpy(a).cuda() for a in (x, e, t)), min_p=torch.from_numpy(m).cuda()).cpu().numpy()
+        assert np.array_equal(got[clear], np.full(n, 5 if off == 0 else 7)[clear])

@@ -4,9 +4,10 @@
 //   (a, b) -> (a cos t - b sin t, a sin t + b cos t) factor,   t = pos freq_i,
 // for the pairs (s_2i, s_2i+1) or (s_i, s_i+rot/2) of a head's first `rot` values; the others pass.
 //
-// Angles: a frequency in turns as an integer of 64 bits, once a CTA; times the position, whose whole turns fall off the integer's top, it is
-// the angle to 2^-33 turns at any position (64 x 32-bit integer products in place of the 64-bit floating point that a GB300 has little
-// of).  sinpi / cospi of that in float32, once for all heads of a row, in shared memory.
+// Angles: a frequency in turns as an integer of 64 bits, off by 2 units at most, once a CTA; times the position, whose whole turns fall off
+// the integer's top, it is the angle to 2^-32 turns at the farthest position (64 x 32-bit integer products in place of the 64-bit floating
+// point that a GB300 has little of).  sinpi / cospi of its first 24 bits in float32, turned by what those leave, once for all heads of a
+// row, in shared memory.
 //
 // Bound by the rows' bytes in and out; below that by a chain of loads, angles, one barrier and stores, so a CTA takes several rows where
 // there are many: their angles together, their values two rows ahead.  The rows are cut so that the CTAs fill whole rounds of what the SMs
@@ -26,13 +27,25 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 
-// freq radians in turns, the fraction of one in units of 2^-64: freq / 2 pi in two parts of 53 bits, so that what is rounded is
-// below a unit or two.
+// freq radians in turns, the fraction of one in units of 2^-64: |freq| / 2 pi in two parts of 53 bits, so that what is rounded is
+// below two units.
 __device__ __forceinline__ unsigned long long turns_of(double freq) {
   const double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;  // 1 / 2 pi
-  const double t = freq * kTurn, low = fma(freq, kTurn, -t) + freq * kTurnLow;
-  const double part = t - floor(t);  // (exact)
-  return (unsigned long long)(part * 0x1p64) + (unsigned long long)(long long)(low * 0x1p64);
+  const double f = fabs(freq), t = f * kTurn, low = fma(f, kTurn, -t) + f * kTurnLow;
+  const double part = t - floor(t);  // (exact, as t is not negative)
+  const unsigned long long turns = (unsigned long long)(part * 0x1p64) + (unsigned long long)(long long)(low * 0x1p64);
+  return freq < 0.0 ? 0ull - turns : turns;
+}
+
+// sin and cos of t units of 2^-64 turns: of its first 24 bits, as a signed number of half turns, then turned by the rest, whose square is
+// below 2^-42.
+__device__ __forceinline__ void sincos_of(unsigned long long t, float& s, float& c) {
+  const int first = (int)(uint32_t)(t >> 32) & ~0xff;
+  const float rest = (float)(uint32_t)(t >> 16 & 0xffffffu) * (3.14159265f * 0x1p-47f);
+  float s0, c0;
+  sincospif((float)first * 0x1p-31f, &s0, &c0);
+  s = fmaf(c0, rest, s0);
+  c = fmaf(-s0, rest, c0);
 }
 
 // A CTA takes `block` rows: a group of D / 8 lanes holds a head of a row, 8 values a lane: eight in a row, or (HALVES) four of the lower half
@@ -94,9 +107,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rope_kernel(const __grid_const
     const int r = i / half, f = i - r * half;
     if (f != held) turns = turns_of((double)__ldg(a.freq + f)), held = f;
     const unsigned long long t = turns * (unsigned long long)(long long)__ldg(a.pos + row0 + r);
-    // the upper half as a signed number of half turns
     float c, s;
-    sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+    sincos_of(t, s, c);
     // the first pairs of the lanes' four angles, then the second: 16-byte loads of neighbours lie in different banks
     turn[r * half + ((f & 2) / 2 * (half / 4) + f / 4) * 2 + (f & 1)] = make_float2(c * a.factor, s * a.factor);
   }

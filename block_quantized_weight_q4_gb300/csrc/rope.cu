@@ -103,14 +103,19 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rope_kernel(const __grid_const
   load(raw[1], 1);
   const int half = a.rot / 2;
   unsigned long long turns = 0;
+  float none = 0.f;  // NaN where the frequency is past what two parts of 1 / 2 pi reduce, or not finite
   for (int i = threadIdx.x, held = -1; i < half * n; i += blockDim.x) {
     const int r = i / half, f = i - r * half;
-    if (f != held) turns = turns_of((double)__ldg(a.freq + f)), held = f;
+    if (f != held) {
+      const float freq = __ldg(a.freq + f);
+      none = fabsf(freq) < 0x1p40f ? 0.f : NAN;
+      turns = turns_of((double)freq), held = f;
+    }
     const unsigned long long t = turns * (unsigned long long)(long long)__ldg(a.pos + row0 + r);
     float c, s;
     sincos_of(t, s, c);
     // the first pairs of the lanes' four angles, then the second: 16-byte loads of neighbours lie in different banks
-    turn[r * half + ((f & 2) / 2 * (half / 4) + f / 4) * 2 + (f & 1)] = make_float2(c * a.factor, s * a.factor);
+    turn[r * half + ((f & 2) / 2 * (half / 4) + f / 4) * 2 + (f & 1)] = make_float2(fmaf(c, a.factor, none), fmaf(s, a.factor, none));
   }
   __syncthreads();
   // every lane of a warp goes round as often: the shuffles need them all

@@ -715,7 +715,8 @@ int qmv_embed(int wtype, int scale_dtype, int64_t vocab, int64_t cols, const voi
  *   s = x * weight / sqrt(mean(x^2) + eps)     (float32; s = x where the weight is NULL)
  *   for pair i of the first rot_dim values, with t = pos[row] * freq[i]:
  *   (a, b) -> (a cos t - b sin t, a sin t + b cos t) * factor;  the values past rot_dim are s.
- * t is formed in 64 bits, so a far position costs no accuracy.
+ * t is formed in 64 bits, so a far position costs no accuracy (2^-32 turns at the farthest).  A frequency of 2^40 or more, or one that
+ * is not finite, makes its pair NaN.  The sum of squares is float32, added in a fixed order.
  *   q : device, row r of head h at element r * q_stride + h * head_dim, x_dtype QMV_X_F32 or QMV_X_BF16; k likewise with
  *       kv_heads heads.  kv_heads 0: no keys (k and k_out are not looked at).  q_out, k_out likewise with their
  *       strides, out_dtype QMV_X_F32 or QMV_X_BF16; each row 16-byte aligned.  An output may be its input (the same

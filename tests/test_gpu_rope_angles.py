@@ -45,3 +45,27 @@ def test_angles(qmv, far, sign):
         assert (size < 2.0 ** -10).sum() > 100
         bound = 2.0 ** -29 * max(far / 2 ** 31, 2.0 ** -10) + 2.0 ** -43 + 5.0 * 2.0 ** -24 * size
         assert np.all(err <= bound), float(np.max(err / bound))
+
+
+@pytest.mark.parametrize("halves", [True, False])
+def test_frequencies_without_an_angle(qmv, halves):
+    """Frequencies that are not finite, or 2^40 and more, give NaN in their pairs and change nothing else; those below are exact."""
+    import torch
+    bad = np.array([np.nan, np.inf, -np.inf, 2.0 ** 40, -3e38], F)
+    fine = np.array([np.nextafter(F(2.0 ** 40), F(0)), -1e9, 12345.678, 0.0, -0.0, 1e-45, 0.25, 1.5, 7.0, 3e11, -1e12], F)
+    freq = np.concatenate([fine[:5], bad, fine[5:]])
+    pos = np.array([0, 1, -1, 77, 2 ** 31 - 1, -2 ** 31], np.int32)
+    half = freq.size
+    x = torch.zeros((pos.size, 2, 64), device="cuda")
+    x[:, 1], x[:, 0, 2 * half:] = 3.0, 5.0
+    a = slice(0, half) if halves else slice(0, 2 * half, 2)
+    b = slice(half, 2 * half) if halves else slice(1, 2 * half, 2)
+    x[:, 0, a] = 1.0
+    y = qmv.qk_rope(x, None, torch.from_numpy(pos).cuda(), torch.from_numpy(freq).cuda(), pairs="halves" if halves else "neighbours")[0].cpu().numpy()
+    none = np.isin(np.arange(half), np.arange(5, 10))
+    for part in (a, b):
+        assert np.isnan(y[:, :, part][..., none]).all() and np.isfinite(y[:, :, part][..., ~none]).all()
+    assert np.all(y[:, 0, 2 * half:] == 5.0) and np.all(y[:, 1, 2 * half:] == 3.0)
+    t = pos.astype(np.longdouble)[:, None] * freq[~none].astype(np.longdouble)  # (55 bits: exact)
+    assert np.all(np.abs(y[:, 0, a][:, ~none] - np.cos(t)) <= 2.0 ** -28 + 5.0 * 2.0 ** -24)
+    assert np.all(np.abs(y[:, 0, b][:, ~none] - np.sin(t)) <= 2.0 ** -28 + 5.0 * 2.0 ** -24)

@@ -760,7 +760,7 @@ def logprobs(logits, given=None, top: int = 0, entropy: bool = True, stream=None
 
 
 def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, stream=None):
-    """The next id of each row of logits (qmv_sample): logits and noise (rows, vocab) float32, rows may be strided;
+    """The next id of each row of logits (qmv_sample): logits and noise (rows, vocab) float32, rows may be strided or one (expand);
     noise: exponential random numbers (torch.empty_like(logits).exponential_()).  temperature, top_p, min_p: float32
     (rows,), top_k int32 (rows,) CUDA tensors, whose contents are read when the call runs on the device, or None.
     Returns ids, int64 (rows,): what embed() and logprobs() take."""

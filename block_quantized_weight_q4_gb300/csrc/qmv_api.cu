@@ -780,7 +780,9 @@ int qmv_sample(int64_t rows, int64_t vocab, const float* logits, int64_t stride,
                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int64_t* ids,
                cudaStream_t stream) {
   if (rows < 0) return QMV_E_ARG;
-  if (vocab <= 0 || vocab >= QMV_SAMPLE_MAX_VOCAB || stride < vocab || noise_stride < vocab) return QMV_E_SHAPE;
+  if (vocab <= 0 || vocab >= QMV_SAMPLE_MAX_VOCAB) return QMV_E_SHAPE;
+  // (nothing is written to either: rows may be one)
+  if ((stride != 0 && stride < vocab) || (noise_stride != 0 && noise_stride < vocab)) return QMV_E_SHAPE;
   if (rows > INT32_MAX / 8 || (rows > 0 && (stride > INT64_MAX / 4 / rows || noise_stride > INT64_MAX / 4 / rows)))
     return QMV_E_SHAPE;
   if (rows == 0) return QMV_OK;

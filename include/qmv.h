@@ -667,8 +667,9 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
 #define QMV_SAMPLE_MAX_VOCAB 2147479552 /* 2^31 - 4096 */
 
 /* The next id of each row of logits (float32, as the products leave them), from given random numbers.
- *   logits : device, row r at element r * stride (stride >= vocab), 4-byte aligned (16-byte aligned rows are read faster).
- *   noise  : device, row r at element r * noise_stride: exponential random numbers (mean 1), one for each id.
+ *   logits : device, row r at element r * stride (stride >= vocab, or 0: all rows are one, as for many rollouts of one prompt), 4-byte
+ *            aligned (16-byte aligned rows are read faster).
+ *   noise  : device, row r at element r * noise_stride (likewise): exponential random numbers (mean 1), one for each id.
  *   temperature, top_k, top_p, min_p : device, one value a row (float32, int32, float32, float32), or NULL for
  *            1, 0, 1, 0: nothing changed or cut off.  They are read when the call runs on the device.
  *   ids    : device, rows int64, 8-byte aligned.
@@ -690,7 +691,7 @@ int qmv_logprobs(int64_t rows, int64_t vocab, const float *logits, int64_t strid
  * scores near the largest are those of 64 bits.  Results do not depend on timing or on the other rows of the call.
  * Allocates nothing and uses no workspace.
  * Returns QMV_OK, QMV_E_ARG (rows < 0, null logits, noise or ids), QMV_E_SHAPE (vocab not within 1..
- * QMV_SAMPLE_MAX_VOCAB - 1, strides below vocab, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */
+ * QMV_SAMPLE_MAX_VOCAB - 1, strides below vocab but 0, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */
 int qmv_sample(int64_t rows, int64_t vocab, const float *logits, int64_t stride, const float *noise,
                int64_t noise_stride, const float *temperature, const int32_t *top_k, const float *top_p,
                const float *min_p, int64_t *ids, cudaStream_t stream);

@@ -184,3 +184,17 @@ def test_min_p_to_the_last_bit(qmv):
         assert clear.sum() > n - 10
         got = qmv.sample(*(torch.from_numpy(a).cuda() for a in (x, e, t)), min_p=torch.from_numpy(m).cuda()).cpu().numpy()
         assert np.array_equal(got[clear], np.full(n, 5 if off == 0 else 7)[clear])
+
+
+@pytest.mark.parametrize("vocab", [5, 3001, 32000])
+def test_rows_that_are_one(qmv, vocab):
+    """Logits, noise or both expanded to rows: as if they had been copied into each."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    rows = 37
+    x, e = torch.randn((1, vocab), device="cuda", generator=g), torch.empty((rows, vocab), device="cuda").exponential_(generator=g)
+    t, p = torch.rand(rows, device="cuda", generator=g) + 0.5, torch.rand(rows, device="cuda", generator=g)
+    for how in ({}, dict(temperature=t, top_p=p)):
+        assert torch.equal(qmv.sample(x.expand(rows, -1), e, **how), qmv.sample(x.repeat(rows, 1), e, **how))
+        assert torch.equal(qmv.sample(x.repeat(rows, 1), e[:1].expand(rows, -1), **how), qmv.sample(x.repeat(rows, 1), e[:1].repeat(rows, 1), **how))
+        assert torch.equal(qmv.sample(x.expand(rows, -1), e[:1].expand(rows, -1), **how), qmv.sample(x.repeat(rows, 1), e[:1].repeat(rows, 1), **how))

@@ -939,7 +939,7 @@ class Moe:
             if W.dtype is not torch.uint8 or not W.is_contiguous() or need == 0 or W.numel() < need:
                 raise ValueError("W1, W3 and W2 must be contiguous uint8 tensors of the matrix images' bytes")
         self.experts, self.dim, self.hidden = experts, dim, hidden
-        self._scratch = {}  # bytes of scratch memory, by the call's numbers
+        self._scratch = (None, 0)  # the last call's numbers, and its bytes of scratch memory
         self.W1, self.W3, self.W2 = W1, W3, W2
         self._c = _MoeC(wtype13, wtype2, scale_dtype, experts, dim, hidden, W1.data_ptr(), W3.data_ptr(), W2.data_ptr())
         self._p = ctypes.addressof(self._c)
@@ -967,9 +967,10 @@ def moe(layer: Moe, x, logits, top: int, renorm: bool = True, scale: float = 1.0
         y = _new_like(x, dtype)
     elif y.dtype is not dtype or y.shape != shape or not y.is_contiguous():
         raise ValueError("y must be a contiguous (tokens, dim) tensor of the output's type")
-    need = layer._scratch.get((n, top, code))
-    if need is None:
-        need = layer._scratch[n, top, code] = moe_scratch_bytes(n, top, layer.hidden, out)
+    numbers, need = layer._scratch
+    if numbers != (n, top, code):
+        need = moe_scratch_bytes(n, top, layer.hidden, out)
+        layer._scratch = (n, top, code), need
     if scratch is None:
         scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
         if stream is not None:

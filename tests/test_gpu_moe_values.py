@@ -106,3 +106,22 @@ def test_blocks_of_both_ends(qmv):
             want = step_ref.moe(layer.w1, layer.w3, layer.w2, x, np.zeros((2, 1), F), 1, True, 1.0, "silu", 2)[0]
             assert np.isfinite(want).all()
             assert np.linalg.norm(y - want) <= (2.0 ** -20 if out == "f32" else 2.0 ** -8 + 2.0 ** -17) * np.linalg.norm(want)
+
+
+def test_a_layer_does_not_grow(qmv):
+    """Calls of many counts of tokens leave nothing behind in the layer."""
+    import torch
+    layer = Layer(qmv, 2, 2, 1, 4, 64, 64, seed=81).dev
+
+    def held():
+        return sum(len(v) for v in vars(layer).values() if isinstance(v, (dict, list, tuple, set)))
+
+    def call(n, top, out):
+        return qmv.moe(layer, torch.ones((n, 64), device="cuda"), torch.zeros((n, 4), device="cuda"), top, out=out)
+
+    call(1, 1, "f32")
+    before = held()
+    for n in range(1, 70):
+        call(n, 1 + n % 4, "bf16" if n % 3 else "f32")
+    assert held() == before
+    assert torch.equal(call(66, 2, "f32"), call(66, 2, "f32"))

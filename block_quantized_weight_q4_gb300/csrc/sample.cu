@@ -24,7 +24,6 @@
 // row 18, 64 mixed rows 81 us.)
 #include <cooperative_groups.h>
 
-#include <mutex>
 
 #include "qmv_common.cuh"
 #include "qmv_internal.h"

@@ -5,7 +5,7 @@
 //
 // Two launches.  Every CTA of the first works out the routing itself from the logits (a maximum over a warp's lanes `top` times
 // a token: a launch of its own would cost more), and they leave it for the second together.  A unit is an expert with up to 4 of its tokens (2
-// where they are float32, and always for h: a value is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after
+// where they are float32: a value is two vectors then); an expert that more tokens chose has more units, whose weights come from L2 after
 // the first.
 //   moe_up:   items of (unit, 32 rows of W1 and of W3), each CTA a run of them; a CTA's warps share an item's columns and meet in
 //             shared memory, where gate and up become h.
@@ -16,7 +16,7 @@
 // Bound by the weights' bytes; below that by what comes before them: the routing, code that is fetched once, the fill of two pipelines
 // (about 12 us of a call; so what runs once is small and no CTA runs code that the others do not: one CTA that alone left the routing
 // cost 7 us).  TMA boxes in place of cp.async measured 53.9 against 52.7 us (1 token, two of 8 experts of 11008 x 4096) and 112 against
-// 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 46 us (152 MB) and 116 us
+// 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 46 us (152 MB) and 106 us
 // (297 MB), in their long stretches 4.5 to 5.7 TB/s; 7 tokens over 16 Q8_0 experts of 1408 x 2048 41.8 us; 1 token, 4 of 32 of 512 x 1024
 // 12.6 us.
 //
@@ -36,8 +36,9 @@
 // (1 of 512 x 1024: no difference).  Q8_0 quants become exact halves by a magic number.
 // An activation is a half after the power of two that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16
 // down to 2^-27 of the largest; float32 values and h are two halves, 22 bits.  (One half of h for bfloat16 outputs put 2e-4 of the output's
-// norm beside the 1.6e-3 of the outputs' own rounding, and one output in ten on another bfloat16 than the formula's.  It left units of 4
-// tokens to moe_down: 44.4 and 95 us; units of 4 with two halves, 8 vectors in two rounds, measured 47.9 and 114 us.)
+// norm beside the 1.6e-3 of the outputs' own rounding, and one output in ten on another bfloat16 than the formula's.  Its products
+// were half as many: 44.4 and 95 us.)  A value's hi and lo have one factor, so their products meet in one MMA's sums; as vectors of their own
+// they took 46.3 and 116 us.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -60,6 +61,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxWarps = 16;
 constexpr int kTokens = 64;    // of a launch
+constexpr int kTokensWide = 48;  // for which moe_down's tiles leave room beside stages of units of 4
 constexpr int kExperts = QMV_MOE_MAX_EXPERTS;
 constexpr int kTop = QMV_MOE_MAX_TOP;
 constexpr int kVectors = 4;    // of a unit: two to an MMA
@@ -246,7 +248,7 @@ struct Stage {
   // Then for each block what a sum of products is multiplied by at the end, and what is taken off it first.
   static constexpr int kBlock = 80;
   static constexpr int kVector = kBlocks * kBlock;
-  static __host__ __device__ constexpr int columns(int vectors) { return vectors * (kVector + kBlocks * 8); }
+  static __host__ __device__ constexpr int columns(int vectors, int factors) { return vectors * kVector + factors * kBlocks * 8; }
 };
 
 // Where a lane reads a stage's rows: 16 rows of one matrix image and 16 of another (or of the same, at another place).  Moving to
@@ -368,27 +370,35 @@ __device__ __forceinline__ uint32_t high_levels(uint32_t w) {
   return f16x2_fma(n | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 n) / 16 - 72
 }
 
-// One stage's products: acc[m][set] += what row tile m (rows g and g + 8 of it) gives for this lane's two blocks and vector.
-// b: this lane's column (its vector and block of the first four blocks), moving by `step` from set to set and by `group` from four blocks to
-// the next (both 0 at zeros, for lanes without a column); xs: the vector's factors of the lane's two blocks.
-template <int WT, bool F16, bool WHOLE, int SETS>
-__device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t step, uint32_t group, uint32_t xs, uint32_t xs_step,
-                                        float (&acc)[2][2][2]) {
+// Where a lane reads B from: b its column (its vector and block of the first four blocks), moving by `step` from set to set, by `group` from
+// four blocks to the next and by `part` from a vector's hi to its lo (all 0 at zeros, for lanes without a column); xs the vector's factors
+// of the lane's two blocks, moving by xs_step from set to set.
+struct Columns {
+  uint32_t b, step, group, part, xs, xs_step;
+};
+
+// One stage's products: acc[m][set] += what row tile m (rows g and g + 8 of it) gives for this lane's two blocks and vector.  PARTS 2: of a
+// vector's hi and lo, which have one factor; in a sum each (each MMA cuts what it adds to: with both in one, float32 outputs were off by
+// 3.4e-7 of their norm in place of 1.7e-7) but for levels as bits.
+template <int WT, bool F16, bool WHOLE, int SETS, int PARTS>
+__device__ __forceinline__ void consume(uint32_t stage, const Columns& at, float (&acc)[2][2][2]) {
   using S = Stage<WT, F16>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   constexpr int kGroups = S::kBlocks / 4;
   constexpr int kPieces = WT == QMV_Q4_0 ? 1 : 2;  // of 16 bytes, of a block
+  constexpr bool kBits = WT == QMV_Q4_0 && !WHOLE;
+  constexpr int kSums = kBits ? 1 : PARTS;
   // this lane's piece of row g: the other four pieces (Q4_0), or the other one of two (Q8_0), lie where the exchange puts them
   const uint32_t near = ((t * kPieces) ^ ((g & 1) * S::kTurn)) << 4;
   const uint32_t q0 = stage + g * 128 + near, q1 = stage + g * 128 + (near ^ (WT == QMV_Q4_0 ? 64 : 16));
   const uint32_t d0 = stage + S::kQ + g * S::kScaleRow + 2 * (t & 1) * (F16 ? 2 : 4);
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    float c[2][SETS][4];
+    float c[2][SETS * kSums][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int v = 0; v < SETS; ++v) c[m][v][0] = c[m][v][1] = c[m][v][2] = c[m][v][3] = 0.f;
+      for (int v = 0; v < SETS * kSums; ++v) c[m][v][0] = c[m][v][1] = c[m][v][2] = c[m][v][3] = 0.f;
     uint32_t q[2][2][4 * kPieces];  // [tile][row g, g + 8][word]
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -404,11 +414,12 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
     // eight elements of a block at a time: one load of B (two for Q4_0, whose words hold elements 16 apart)
 #pragma unroll
     for (int j = 0; j < 2 * kPieces; ++j) {
-      uint32_t x[SETS][2][4];  // [set][first, elements 16 further][halves]
+      uint32_t x[SETS * PARTS][2][4];  // [set, hi and lo][first, elements 16 further][halves]
 #pragma unroll
-      for (int v = 0; v < SETS; ++v) {
-        lds_u32x4(b + v * step + i * group + j * 16, x[v][0]);
-        if (WT == QMV_Q4_0) lds_u32x4(b + v * step + i * group + 32 + j * 16, x[v][1]);
+      for (int v = 0; v < SETS * PARTS; ++v) {
+        const uint32_t from = at.b + v / PARTS * at.step + v % PARTS * at.part + i * at.group + j * 16;
+        lds_u32x4(from, x[v][0]);
+        if (WT == QMV_Q4_0) lds_u32x4(from + 32, x[v][1]);
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -421,41 +432,46 @@ __device__ __forceinline__ void consume(uint32_t stage, uint32_t b, uint32_t ste
             const uint32_t lo[4] = {low_levels<WHOLE>(wg), low_levels<WHOLE>(wh), low_levels<WHOLE>(sg), low_levels<WHOLE>(sh)};
             const uint32_t hi[4] = {high_levels<WHOLE>(wg), high_levels<WHOLE>(wh), high_levels<WHOLE>(sg), high_levels<WHOLE>(sh)};
 #pragma unroll
-            for (int v = 0; v < SETS; ++v) {
-              mma_f16_16816(c[m][v], lo[0], lo[1], lo[2], lo[3], x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
-              mma_f16_16816(c[m][v], hi[0], hi[1], hi[2], hi[3], x[v][1][2 * k], x[v][1][2 * k + 1], c[m][v]);
+            for (int v = 0; v < SETS * PARTS; ++v) {
+              float(&sum)[4] = c[m][v * kSums / PARTS];
+              mma_f16_16816(sum, lo[0], lo[1], lo[2], lo[3], x[v][0][2 * k], x[v][0][2 * k + 1], sum);
+              mma_f16_16816(sum, hi[0], hi[1], hi[2], hi[3], x[v][1][2 * k], x[v][1][2 * k + 1], sum);
             }
           } else {
             uint32_t g01, g23, h01, h23;
             q8_word_to_f16_levels(wg, g01, g23);
             q8_word_to_f16_levels(wh, h01, h23);
 #pragma unroll
-            for (int v = 0; v < SETS; ++v) mma_f16_16816(c[m][v], g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], c[m][v]);
+            for (int v = 0; v < SETS * PARTS; ++v) {
+              float(&sum)[4] = c[m][v * kSums / PARTS];
+              mma_f16_16816(sum, g01, h01, g23, h23, x[v][0][2 * k], x[v][0][2 * k + 1], sum);
+            }
           }
         }
     }
     // columns 2 t and 2 t + 1: vector t / 2 of the set, blocks 2 (t & 1) and the next
     float f[SETS][4];  // multiplied by, taken off before; of both blocks
 #pragma unroll
-    for (int v = 0; v < SETS; ++v) lds_f32x4(xs + v * xs_step + i * 32, f[v]);
+    for (int v = 0; v < SETS; ++v) lds_f32x4(at.xs + v * at.xs_step + i * 32, f[v]);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t at = d0 + (16 * m + 8 * h) * S::kScaleRow + 4 * i * (F16 ? 2 : 4);
+        const uint32_t from = d0 + (16 * m + 8 * h) * S::kScaleRow + 4 * i * (F16 ? 2 : 4);
         float2 d;
         if (F16) {
-          const uint32_t u = lds_u32(at);
+          const uint32_t u = lds_u32(from);
           d = __half22float2(*reinterpret_cast<const __half2*>(&u));
         } else {
           uint32_t u0, u1;
-          lds_u32x2(at, u0, u1);
+          lds_u32x2(from, u0, u1);
           d = make_float2(__uint_as_float(u0), __uint_as_float(u1));
         }
 #pragma unroll
         for (int v = 0; v < SETS; ++v) {
-          const float s0 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h], 0x1p24f, -f[v][1]) : c[m][v][2 * h];
-          const float s1 = WT == QMV_Q4_0 && !WHOLE ? fmaf(c[m][v][2 * h + 1], 0x1p24f, -f[v][3]) : c[m][v][2 * h + 1];
+          float s0 = c[m][v * kSums][2 * h], s1 = c[m][v * kSums][2 * h + 1];
+          if (kSums == 2) s0 += c[m][v * kSums + kSums - 1][2 * h], s1 += c[m][v * kSums + kSums - 1][2 * h + 1];
+          if (kBits) s0 = fmaf(s0, 0x1p24f, -f[v][1]), s1 = fmaf(s1, 0x1p24f, -f[v][3]);
           acc[m][v][h] = fmaf(s0 * d.x, f[v][0], fmaf(s1 * d.y, f[v][2], acc[m][v][h]));
         }
       }
@@ -471,32 +487,21 @@ __device__ __forceinline__ void wait_ring(int ring) {  // all but the newest rin
     copies_wait<3>();
 }
 
-// Where a lane reads B from: `columns` holds the unit's vectors (then their blocks' scales), `zeros` 128 bytes of zeros.
-struct Columns {
-  uint32_t b, step, group, xs, xs_step;
-};
-template <typename S>
-__device__ __forceinline__ Columns columns_of(uint32_t columns, uint32_t zeros, int max_vectors) {
+// A unit's columns at `columns`: PARTS halves of each of up to `most` vectors, then the vectors' factors; `zeros`: 128 bytes of zeros.
+template <typename S, int PARTS>
+__device__ __forceinline__ Columns columns_of(uint32_t columns, uint32_t zeros, int most) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int v = g >> 2;
-  const bool mine = (g & 3) == t && v < max_vectors;
+  const bool mine = (g & 3) == t && v < most;
   Columns c;
-  c.b = mine ? columns + v * S::kVector + t * S::kBlock : zeros;
-  c.step = mine && 2 + v < max_vectors ? 2 * S::kVector : 0;
+  c.b = mine ? columns + v * PARTS * S::kVector + t * S::kBlock : zeros;
+  c.step = mine && 2 + v < most ? 2 * PARTS * S::kVector : 0;
   c.group = mine ? 4 * S::kBlock : 0;
+  c.part = mine ? S::kVector : 0;
   const int sv = t >> 1;
-  c.xs = sv < max_vectors ? columns + max_vectors * S::kVector + sv * S::kBlocks * 8 + 2 * (t & 1) * 8 : zeros;
-  c.xs_step = 2 + sv < max_vectors ? 2 * S::kBlocks * 8 : 0;  // (what is read for a vector that is not there goes nowhere)
+  c.xs = sv < most ? columns + most * PARTS * S::kVector + sv * S::kBlocks * 8 + 2 * (t & 1) * 8 : zeros;
+  c.xs_step = 2 + sv < most ? 2 * S::kBlocks * 8 : 0;  // (what is read for a vector that is not there goes nowhere)
   return c;
-}
-
-// A unit of one or two vectors, or of three or four.
-template <int WT, bool F16, bool WHOLE>
-__device__ __forceinline__ void consume_any(uint32_t stage, const Columns& c, int sets, float (&acc)[2][2][2]) {
-  if (sets == 1)
-    consume<WT, F16, WHOLE, 1>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
-  else
-    consume<WT, F16, WHOLE, 2>(stage, c.b, c.step, c.group, c.xs, c.xs_step, acc);
 }
 
 // ------------------------------------------------------------------------------------------ gate and up
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int max_vectors = min(p.tokens, p.unit) * (XF32 ? 2 : 1);
   const uint32_t ring = smem_u32(smem + p.off_ring) + wid * p.ring * S::kBytes;
-  const int cache_bytes = S::columns(max_vectors);
+  const int cache_bytes = S::columns(max_vectors, max_vectors);
   uint8_t* cache = smem + p.off_cols + wid * p.cached * cache_bytes;  // the warp's columns, of p.cached chunks
   griddep_wait();
   griddep_launch_dependents();
@@ -631,7 +636,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   int cs = 0, held = -1;  // held: the unit that u is, and whose columns the cache has
   int unit = item0 / items_unit, first = item0 % items_unit * p.tiles_item;
   Unit u{};
-  const Columns col0 = columns_of<S>(smem_u32(cache), zeros, max_vectors);
+  const Columns col0 = columns_of<S, 1>(smem_u32(cache), zeros, max_vectors);
   for (int item = item0; item < item1; ++item) {
     const int tile = first + tile_local;
     if (held != unit) {
@@ -662,7 +667,11 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
           issue();
           wait_ring(p.ring);
           __syncwarp();
-          consume_any<WT, F16, WHOLE>(ring + cs * S::kBytes, c, sets, acc[0]);
+          // one or two vectors, or three or four
+          if (sets == 1)
+            consume<WT, F16, WHOLE, 1, 1>(ring + cs * S::kBytes, c, acc[0]);
+          else
+            consume<WT, F16, WHOLE, 2, 1>(ring + cs * S::kBytes, c, acc[0]);
           cs = cs + 1 == p.ring ? 0 : cs + 1;
 #pragma unroll
           for (int w = 0; w < 2; ++w)
@@ -722,20 +731,13 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         __half* out = reinterpret_cast<__half*>(p.h) + (long long)slot * p.hidden + 32 * ht + place;
         out[0] = hi;
         out[p.h_plane] = lo;
-        float sum = 0.f;  // lane 0: of the block's hi, lane 1: of its lo
+        float sum = 0.f;
         if (bits) {
-          const float back = split ? 16.f : 1.f;
-          float high = __half2float(hi) * back, low = __half2float(lo) * back;
+          sum = (__half2float(hi) + __half2float(lo)) * (split ? 16.f : 1.f);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            high += __shfl_xor_sync(0xffffffffu, high, o);
-            low += __shfl_xor_sync(0xffffffffu, low, o);
-          }
-          sum = lane == 0 ? high : low;
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        if (lane < kParts)
-          p.h_factor[((long long)lane * p.tokens * p.top + slot) * (p.hidden / 32) + ht] =
-              make_float2(down, 8.f * sum);
+        if (lane == 0) p.h_factor[(long long)slot * (p.hidden / 32) + ht] = make_float2(down, 8.f * sum);
       }
     }
     if ((first += p.tiles_item) >= tiles) first = 0, ++unit;
@@ -745,15 +747,15 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
 // ------------------------------------------------------------------------------------------ down
 constexpr int kDownWarps = 8, kDownThreads = kDownWarps * 32;
 
-template <int WT, bool F16, bool WHOLE>
-__global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_constant__ MoeParams p, int ranks) {
+// UNIT: tokens of a unit at most.
+template <int WT, bool F16, bool WHOLE, int UNIT>
+__global__ void __launch_bounds__(kDownThreads, UNIT > 2 ? 1 : 2) moe_down_kernel(const __grid_constant__ MoeParams p, int ranks) {
   using S = Stage<WT, F16>;
-  constexpr int kUnit = kVectors / kParts;  // tokens of a unit
   extern __shared__ __align__(1024) uint8_t smem[];
   float* tiles = reinterpret_cast<float*>(smem + p.off_red);  // a warp's tokens x 32 rows
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int max_vectors = min(p.tokens, kUnit) * kParts;
-  const int stage_bytes = S::kBytes + S::columns(max_vectors);
+  const int most = min(p.tokens, UNIT);
+  const int stage_bytes = S::kBytes + S::columns(most * kParts, most);
   const uint32_t ring = smem_u32(smem + p.off_ring) + wid * p.ring * stage_bytes;
   const uint32_t zeros = smem_u32(smem + p.off_zero);
   cg::cluster_group cl = cg::this_cluster();
@@ -800,16 +802,16 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     const int first = ps_c * S::kChunk + piece * 8;
     const bool live = first < p.hidden;
 #pragma unroll
-    for (int i = 0; i < kVectors; i += kTogether) {
+    for (int i = 0; i < UNIT * kParts; i += kTogether) {
       if (i >= vectors) break;
       const int v = i + lane / kPieces;
       const uint32_t row = __shfl_sync(0xffffffffu, h_at, v);
       const int slot = __shfl_sync(0xffffffffu, pu.slot, v / kParts);
       if (v >= vectors) continue;
       copy_async<16>(to + v * S::kVector + (piece >> 2) * S::kBlock + (piece & 3) * 16, p.h + (long long)row * 64 + (live ? first : 0), live);
-      if ((piece & 3) == 0)
-        copy_async<8>(to + max_vectors * S::kVector + (v * S::kBlocks + (piece >> 2)) * 8,
-                      p.h_factor + ((long long)(v % kParts) * p.tokens * p.top + slot) * (p.hidden / 32) + (live ? first / 32 : 0), live);
+      if ((piece & 3) == 0 && v % kParts == 0)
+        copy_async<8>(to + most * kParts * S::kVector + (v / kParts * S::kBlocks + (piece >> 2)) * 8,
+                      p.h_factor + (long long)slot * (p.hidden / 32) + (live ? first / 32 : 0), live);
     }
   };
   auto weights = [&](int at) { rows.load(ring + at * stage_bytes, ps_c, 0, p.hidden); };
@@ -832,7 +834,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     copies_commit();
   }
 
-  const Columns col0 = columns_of<S>(ring + S::kBytes, zeros, max_vectors);
+  const Columns col0 = columns_of<S, kParts>(ring + S::kBytes, zeros, most);
   float acc[2][2][2] = {};  // [tile][set][row g, g + 8]
   int cs = 0, cc = s0 % chunks, cu = s0 / chunks;
   Unit u{};
@@ -840,16 +842,17 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
   auto flush = [&]() {
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const int tok = __shfl_sync(0xffffffffu, u.tok, v);
-      const float part = share[__shfl_sync(0xffffffffu, u.slot, v)];  // (lanes without a token: of the first, unused)
+      if (2 * v >= UNIT) break;
+      const int col = 2 * v + (t >> 1);
+      const int tok = __shfl_sync(0xffffffffu, u.tok, col);
+      const float part = share[__shfl_sync(0xffffffffu, u.slot, col)];  // (lanes without a token: of the first, unused)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float a = acc[m][v][h];
           a += __shfl_xor_sync(0xffffffffu, a, 1);
-          a += __shfl_xor_sync(0xffffffffu, a, 2);
-          if (v < u.cols && t == 0) my[tok * kRowsStage + 16 * m + 8 * h + g] += part * a;
+          if (col < u.cols && (t & 1) == 0) my[tok * kRowsStage + 16 * m + 8 * h + g] += part * a;
           acc[m][v][h] = 0.f;
         }
     }
@@ -868,7 +871,10 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_down_kernel(const __grid_
     Columns c = col0;
     c.b += c.b == zeros ? 0 : cs * stage_bytes;
     c.xs += c.xs == zeros ? 0 : cs * stage_bytes;
-    consume_any<WT, F16, WHOLE>(ring + cs * stage_bytes, c, u.cols, acc);
+    if (UNIT <= 2 || u.cols <= 2)
+      consume<WT, F16, WHOLE, 1, kParts>(ring + cs * stage_bytes, c, acc);
+    else
+      consume<WT, F16, WHOLE, 2, kParts>(ring + cs * stage_bytes, c, acc);
     cs = cs + 1 == p.ring ? 0 : cs + 1;
     if (++cc == chunks) {
       flush();
@@ -949,7 +955,7 @@ cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStrea
   size_t smem = 0;
   bool fits = false;
   for (p.unit = p.tokens < most ? p.tokens : most; p.unit >= 1 && !fits; p.unit -= fits ? 0 : 1) {
-    const int tokens = p.tokens < p.unit ? p.tokens : p.unit, columns = S::columns(x_f32 ? 2 * tokens : tokens);
+    const int tokens = p.tokens < p.unit ? p.tokens : p.unit, vectors = x_f32 ? 2 * tokens : tokens, columns = S::columns(vectors, vectors);
     p.max_units = max_units(p.tokens, p.top, p.experts, p.unit < p.down_unit ? p.unit : p.down_unit);
     p.off_zero = (int)round_up(p.off_units + Units::bytes(p.max_units), 128);
     p.off_red = p.off_zero + 128;
@@ -983,14 +989,14 @@ cudaError_t launch_up(MoeParams& p, bool x_f32, const DeviceInfo& dev, cudaStrea
 template <int WT, bool F16>
 cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream) {
   using S = Stage<WT, F16>;
-  const int vectors = (p.tokens < p.down_unit ? p.tokens : p.down_unit) * kParts;
-  const int stage = S::kBytes + S::columns(vectors);
+  const int most = p.tokens < p.down_unit ? p.tokens : p.down_unit;
+  const int stage = S::kBytes + S::columns(most * kParts, most);
   p.off_zero = (int)round_up(sizeof(MoeTable) + Units::bytes(p.max_units) + (size_t)p.tokens * p.top * 4, 128);
   p.off_red = p.off_zero + 128;
   p.off_ring = (int)round_up(p.off_red + (size_t)kDownWarps * kRowsStage * p.tokens * 4, 128);
   size_t smem = 0;
-  int per_sm = 2;
-  for (; per_sm >= 1; --per_sm) {
+  int per_sm;
+  for (per_sm = p.down_unit > 2 ? 1 : 2; per_sm >= 1; --per_sm) {
     for (p.ring = per_sm == 2 ? 2 : 4; p.ring >= 2; --p.ring) {
       smem = p.off_ring + (size_t)kDownWarps * p.ring * stage;
       if (smem <= room(dev, per_sm)) break;
@@ -1003,9 +1009,12 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
   const long long stages = (long long)(p.experts < p.tokens * p.top ? p.experts : p.tokens * p.top) * chunks;
   int ranks = 1;
   while (ranks < 8 && tiles * ranks * 2 <= per_sm * dev.sm_count && stages >= 2 * ranks * kDownWarps) ranks *= 2;
-  const int which = WT == QMV_Q4_0 && !p.out_bf16;
-  auto kern = which == 1 ? moe_down_kernel<WT, F16, WT == QMV_Q4_0> : moe_down_kernel<WT, F16, false>;
-  static bool done[2][64] = {};
+  const bool whole = WT == QMV_Q4_0 && !p.out_bf16, wide = p.down_unit > 2;
+  constexpr bool kQ4 = WT == QMV_Q4_0;
+  auto kern = whole ? (wide ? moe_down_kernel<WT, F16, kQ4, 4> : moe_down_kernel<WT, F16, kQ4, 2>)
+                    : (wide ? moe_down_kernel<WT, F16, false, 4> : moe_down_kernel<WT, F16, false, 2>);
+  const int which = 2 * whole + wide;
+  static bool done[4][64] = {};
   const cudaError_t err = allow_smem(kern, dev, done[which]);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
@@ -1030,13 +1039,17 @@ cudaError_t launch_down(MoeParams p, const DeviceInfo& dev, cudaStream_t stream)
 size_t moe_scratch_bytes(int64_t tokens, int top, int hidden) {
   const size_t t = tokens < kTokens ? tokens : kTokens;
   const int pairs = (int)t * top;
-  return (size_t)pairs * (hidden * 2 + hidden / 32 * 8) * kParts + sizeof(MoeTable) + Units::bytes(pairs) + (size_t)pairs * 4;
+  return (size_t)pairs * (hidden * 2 * kParts + hidden / 32 * 8) + sizeof(MoeTable) + Units::bytes(pairs) + (size_t)pairs * 4;
 }
 
 cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  for (int64_t t0 = 0; t0 < a.tokens; t0 += kTokens) {
+  // blocks of 48 tokens, the last of up to 64 (256 over 128 experts of 768 x 2048: 717 us against 762 for blocks of 64; but 64 at once 184 against
+  // 212 for 48 and 16)
+  int64_t block;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += block) {
+    block = a.tokens - t0 <= kTokens ? a.tokens - t0 : kTokensWide;
     MoeParams p{};
-    p.tokens = (int)(a.tokens - t0 < kTokens ? a.tokens - t0 : kTokens);
+    p.tokens = (int)block;
     p.q1 = a.w1.q, p.d1 = a.w1.d, p.q3 = a.w3.q, p.d3 = a.w3.d, p.q2 = a.w2.q, p.d2 = a.w2.d;
     p.logits = a.logits + t0 * a.logits_stride;
     p.logits_stride = a.logits_stride;
@@ -1045,15 +1058,20 @@ cudaError_t launch_moe(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t str
     p.out_bf16 = a.out_bf16;
     p.hidden = a.hidden;
     p.top = a.top;
+    p.experts = a.experts;
     p.h = static_cast<uint16_t*>(a.scratch);
     p.h_plane = (long long)p.tokens * a.top * a.hidden;
     p.h_factor = reinterpret_cast<float2*>(p.h + kParts * p.h_plane);
-    p.table = reinterpret_cast<MoeTable*>(p.h_factor + (size_t)kParts * p.tokens * p.top * (p.hidden / 32));
-    p.down_unit = p.tokens < kVectors / kParts ? p.tokens : kVectors / kParts;  // (one or two tokens: one set of units for both kernels)
+    p.table = reinterpret_cast<MoeTable*>(p.h_factor + (size_t)p.tokens * p.top * (p.hidden / 32));
+    // Units of 4 tokens for moe_down from 2 tokens an expert on: one CTA of 128 to 248 registers a thread an SM, two units' weights once.  32 tokens
+    // over 128 experts (2 each) 105 against 113 us, 48 (3) 128 against 148, 48 over 8 large ones (12) 591 against 670; but 1 token over two
+    // large ones 49.7 against 46.5 us, 7 over 16 Q8_0 ones (1.3) 43.5 against 41.4, and none far off either way between.
+    // (One or two tokens: one set of units for both kernels.)
+    p.down_unit = p.tokens <= kTokensWide && p.tokens * a.top >= 2 * a.experts ? 4 : 2;
+    if (p.tokens < p.down_unit) p.down_unit = p.tokens;
     p.w2_q4 = a.w2.wtype == QMV_Q4_0;
     p.ids = a.ids == nullptr ? nullptr : a.ids + t0 * a.top;
     p.shares = a.shares == nullptr ? nullptr : a.shares + t0 * a.top;
-    p.experts = a.experts;
     p.dim = a.dim;
     p.renorm = a.renorm;
     p.act = a.act;

@@ -771,13 +771,13 @@ size_t qmv_moe_scratch_bytes(int64_t tokens, int top, int64_t hidden, int out_dt
  * An expert of logit -infinity is not used (where that leaves fewer than top, ids of -1 with p 0; a token without
  * experts gives zeros).  A token whose logits hold NaN or +infinity gives NaN, and ids of -1.
  * The sums are float32 in an order that follows from the sizes and the routing alone: results do not depend on
- * timing, the last bits of a token may depend on the other tokens of its block of 64.  Levels enter the tensor core as exact
+ * timing, the last bits of a token may depend on the other tokens of its block (below).  Levels enter the tensor core as exact
  * halves, an activation as a half after the power of two that brings the largest of its 32 columns into [2^14, 2^15) (bfloat16 values are
  * exact down to 2^-27 of that largest; float32 ones two halves, 22 bits), act(gate) * up likewise as two halves (22 bits); values below
  * 2^-24 of their block's largest are multiples of 2^-34 of it (of 2^-149, where that largest is below 2^-112).  Activations may be any finite
  * float32, with weights' scales below 2^100; infinity or NaN among them makes the token's results NaN or infinite.
- * Tokens go in blocks of 64, each of two launches that read every used expert's weights: for prompts of many tokens
- * the weights' bytes are read once a block.
+ * Tokens go in blocks of 48, the last of up to 64, each of two launches that read every used expert's weights: for prompts of many
+ * tokens the weights' bytes are read once a block.
  * tokens 0 launches nothing.  Returns QMV_OK, QMV_E_FORMAT (types, act), QMV_E_ARG (null pointer, tokens < 0, scale not finite), QMV_E_SHAPE
  * (the layer's numbers, top not 1..min(experts, QMV_MOE_MAX_TOP), logits_stride, sizes that overflow), QMV_E_ALIGN or QMV_E_CUDA. */
 int qmv_moe(const qmv_moe_layer *layer, int64_t tokens, const float *logits, int64_t logits_stride, int top, int renorm,

@@ -4,7 +4,7 @@ import pytest
 
 import step_ref
 from helpers import dev_x
-from test_gpu_moe import Layer, _x
+from test_gpu_moe import Layer, _check, _x
 
 pytestmark = pytest.mark.gpu
 F = np.float32
@@ -125,3 +125,17 @@ def test_a_layer_does_not_grow(qmv):
         call(n, 1 + n % 4, "bf16" if n % 3 else "f32")
     assert held() == before
     assert torch.equal(call(66, 2, "f32"), call(66, 2, "f32"))
+
+
+@pytest.mark.parametrize("wt,sf", [(1, 0), (1, 1), (2, 0), (2, 1)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens,experts,top,dim,hidden", [
+    (48, 256, 16, 64, 64), (49, 256, 16, 64, 64), (48, 3, 3, 128, 320), (47, 12, 2, 192, 64), (3, 2, 2, 320, 128), (112, 4, 2, 64, 128), (113, 2, 1, 64, 64),
+    (31, 16, 1, 64, 64), (33, 16, 1, 64, 64), (48, 5, 3, 2112, 64), (40, 4, 2, 64, 2112)])
+def test_units_and_blocks(qmv, wt, sf, out, tokens, experts, top, dim, hidden):
+    """Units of 2 and of 4 tokens on both sides of what chooses them, with the most tokens and places that they take, and blocks of both sizes."""
+    rng = np.random.default_rng([tokens, experts, dim])
+    layer = Layer(qmv, wt, wt, sf, experts, dim, hidden, seed=83)
+    x, xd = _x(rng, tokens, dim, out == "bf16")
+    logits = rng.standard_normal((tokens, experts)).astype(F)
+    _check(layer, qmv.moe(layer.dev, xd, dev_x(logits), top, out=out, routing=True), x, logits, top, True, 1.0, "silu", out == "bf16")

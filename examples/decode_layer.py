@@ -37,7 +37,7 @@ class Model:
         import block_quantized_weight_q4_gb300 as qmv
         self.qmv, self.torch = qmv, torch
         self.dim, self.heads, self.kv_heads, self.hidden, self.vocab = dim, heads, kv_heads, hidden, vocab
-        self.head_dim, self.experts, self.top = dim // heads, experts, top
+        self.head_dim, self.experts, self.top = dim // heads, experts, min(top, max(experts, 1))
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
 
@@ -142,7 +142,7 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--tokens", type=int, default=12)
-    ap.add_argument("--experts", type=int, default=0, help="experts a layer, two for each token (0: one FFN)")
+    ap.add_argument("--experts", type=int, default=0, help="experts a layer, two for each token, or the one there is (0: one FFN)")
     ap.add_argument("--temperature", type=float, default=0.0)
     ap.add_argument("--top-k", type=int, default=0)
     ap.add_argument("--top-p", type=float, default=1.0)

@@ -6,7 +6,8 @@
 // store).  A piece is 16 bytes of the output, 8 bfloat16 or 4 float32 values, so that a warp's store is whole lines; a thread has kEach
 // pieces' loads on their way at once (2, 3, 4, 6 of them: 10.6, 9.9, 10.0, 14.6 us for 4096 rows of 4096 bfloat16 values, 15.8, 14.6, 14.3,
 // 16.3 us for float32 ones).  Pieces of 32 bytes a thread, half of each line at a time: 10.0 and 19.9 us.
-// GB300: 4096 rows of 4096 from Q4_0, bfloat16 10.0 us (4.2 TB/s of 42 MB), float32 14.3 us (5.3 TB/s of 76 MB); 1 row of 1024 1.4 us.
+// GB300: 4096 rows of 4096 from Q4_0, bfloat16 10.0 us (4.2 TB/s of 42 MB; 14.6 instructions a value, 77% of the issue slots, as the code
+// is: each byte is loaded and masked by two threads, one for each nibble), float32 14.3 us (5.3 TB/s of 76 MB); 1 row of 1024 1.5 us.
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
 

@@ -17,8 +17,8 @@
 // (about 12 us of a call; so what runs once is small and no CTA runs code that the others do not: one CTA that alone left the routing
 // cost 7 us).  TMA boxes in place of cp.async measured 53.9 against 52.7 us (1 token, two of 8 experts of 11008 x 4096) and 112 against
 // 102 us (32 tokens, 8 of 128 experts of 768 x 2048).  GB300, Q4_0 with half scales, bfloat16 in and out: those two 46 us (152 MB) and 106 us
-// (297 MB), in their long stretches 4.5 to 5.7 TB/s; 7 tokens over 16 Q8_0 experts of 1408 x 2048 41.8 us; 1 token, 4 of 32 of 512 x 1024
-// 12.6 us.
+// (297 MB), in their long stretches 4.5 to 5.7 TB/s; 7 tokens over 16 Q8_0 experts of 1408 x 2048 41.5 us; 1 token, 4 of 32 of 512 x 1024
+// 12.4 us.
 //
 // Products: m16n8k16 with IEEE halves.  Lane t of a row's four lanes takes a whole block of 32 weights (one or two 16-byte loads), so an
 // MMA's k slots hold four different blocks; the columns are 2 vectors x those 4 blocks, and a lane's B values are

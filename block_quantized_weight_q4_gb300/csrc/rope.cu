@@ -13,9 +13,9 @@
 // there are many: their angles together, their values two rows ahead.  The rows are cut so that the CTAs fill whole rounds of what the SMs
 // hold at once, up to 8 each (powers of two of them: 8192 rows 37.6, 3000 rows 24.6, 1024 rows 9.6 us; as it is 35.0, 15.1, 7.1 us; up
 // to 4: 37.6, 17.0, 7.1; up to 16: 34.2, 15.1, 7.1 and float32 rows 56.5 against 54.7 us).
-// GB300, 32 + 8 heads of 128: 8192 bfloat16 rows with norms, half of each head turned, 35.0 us (4.8 TB/s; all of it 38.4, without norms 32.0),
-// float32 ones 54.7 us (6.1 TB/s); 256 float32 rows 4.7, one bfloat16 row 2.7 us.  The bfloat16 rows' instructions, about 12 a value, take
-// two thirds of the issue slots.
+// GB300, 32 + 8 heads of 128: 8192 bfloat16 rows with norms, half of each head turned, 35.4 us (4.7 TB/s; all of it 35.8, without norms 32.3),
+// float32 ones 55.9 us (6.0 TB/s); 256 float32 rows 4.8, one bfloat16 row 2.8 us.  The bfloat16 rows take 17 instructions a value and 60% of
+// the issue slots, as the code is: a float at a time, with selects and shuffles where a call has no norm, too.
 #include <type_traits>
 
 #include "qmv_common.cuh"

@@ -19,11 +19,12 @@
 //
 // Bound by the logits' bytes for many unfiltered rows (and the noise's, which only they read whole); else by a chain of passes, joins and a
 // sort for few rows, and by instructions and shared-memory atomics for flat rows under top-p.  GB300, rows of 151936: one row with all cuts
-// 17.1 us; 64 rows greedy 13, unfiltered 18, min-p 35, top-k 50, top-p 84, mixed 70 us; 512 rows unfiltered 104 us (6.0 TB/s), greedy
-// 58, all cuts 137, top-p 350 us.  (With conversions for the buckets, branches for what a draw takes and a binary search of borders: one
+// 18.0 us (17.1 without min-p's logarithm in 64 bits); 64 rows greedy 13, unfiltered 18, min-p 36, top-k 51, top-p 84, mixed 71 us; 512
+// rows unfiltered 105 us (5.9 TB/s), greedy 59, all cuts 139, top-p 353 us.  (With conversions for the buckets, branches for what a draw takes and a binary search of borders: one
 // row 18, 64 mixed rows 81 us.)
 #include <cooperative_groups.h>
 
+#include <cfloat>
 
 #include "qmv_common.cuh"
 #include "qmv_internal.h"
@@ -73,7 +74,7 @@ struct Row {
   int head, quads, q0, q1;
   int shift, chunks;  // the CTA's chunks, without the ends
   bool ends;
-  float max, scale;   // scale: log2 e / T
+  float max, scale, floor;  // scale: log2 e / T; floor: the distance from the maximum at which a score is -1e38, or the type's lowest
 };
 
 // A logit's distance below the maximum in powers of two, its bucket and its weight.
@@ -123,9 +124,6 @@ __device__ __forceinline__ void for_each(const Row& r, const uint32_t* chunk_max
   }
 }
 
-// (one piece of code, which two places fetch)
-__device__ __noinline__ double log_of(double v) { return log(v); }
-
 struct Draw {  // a candidate's score in 64 bits; the larger wins, then the lower id
   double s;
   int id;
@@ -146,10 +144,10 @@ __device__ __forceinline__ float log2_of_normal(float e) {  // (-infinity for su
   return y;
 }
 // x's score in powers of two below the maximum's, with the random number e; -infinity where e is not one (not above 0, infinite, NaN).
-// Any other score stays finite, however far x lies below at a low temperature: those at the floor are told apart in 64 bits.
+// Any other score stays finite, however far x lies below at a low temperature: those at the floor (-1e38) are told apart in 64 bits.
 __device__ __forceinline__ float score_of(const Row& r, float x, float e) {
   const float t = e >= 0x1p-126f ? log2_of_normal(e) : e > 0.f ? log2_of(e) : INFINITY;
-  return t < INFINITY ? fmaxf(fmaf(x - r.max, r.scale, -t), -1e38f) : -INFINITY;
+  return fmaf(fmaxf(x - r.max, r.floor), r.scale, -t);
 }
 
 struct Shared {
@@ -303,7 +301,7 @@ __device__ __forceinline__ uint32_t edge_of(const Row& r, int b) {
 // ... whose weight is min_p at least: x - max >= T ln min_p in 64 bits, so that how small min_p is costs no accuracy; looked for as far around
 // float32's answer as that may be off.
 __device__ __forceinline__ uint32_t edge_of_weight(const Row& r, float T, float min_p) {
-  const double least = (double)T * log_of(min_p);
+  const double least = (double)T * log((double)min_p);
   const float z = T * logf(min_p), about = r.max + z, off = 0x1p-20f * fabsf(z) + 0x1p-21f * fabsf(r.max) + 0x1p-149f;
   const uint32_t top = ordered(r.max);
   return least_of(max(ordered(about - off), kMasked + 1), min(ordered(about + off), top),
@@ -806,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const bool whole_row = !greedy && !by_k && !by_p && !by_m;
   const float inv_t = __fdiv_rn(1.f, T);
   r.scale = __fmul_rn(1.4426950408889634f, inv_t);
+  r.floor = fmaxf(__fdiv_rn(-1e38f, r.scale), -FLT_MAX);
   r.max = 0.f;
   // a score is float32: its logarithm is off by 2^-21 of |log2 e| (< 150) at most, the difference, product and sum by a few 2^-24
   // of their own size; candidates as close to the best as that are looked at again
@@ -849,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (rank == 0 && threadIdx.x == 0) p.ids[row] = sh.close_id[0];
       return;
     }
-    auto exact = [&](float x, float e, int id) { return Draw{((double)x - (double)r.max) / (double)T - log_of((double)e), id}; };
+    auto exact = [&](float x, float e, int id) { return Draw{((double)x - (double)r.max) / (double)T - log((double)e), id}; };
     Draw d{0.0, -1};
     if (n > (uint32_t)kClose) {
       visit(least, [&](float x, float e, int id) {

@@ -77,6 +77,9 @@ struct Row {
   float max, scale, floor;  // scale: log2 e / T; floor: the distance from the maximum at which a score is -1e38, or the type's lowest
 };
 
+// The id of a quad's first logit.  (Unsigned: lanes past a row's end form them, too, and in rows of nearly 2^31 ids those wrap.)
+__device__ __forceinline__ int id_at(const Row& r, int q) { return (int)((uint32_t)r.head + 4u * (uint32_t)q); }
+
 // A logit's distance below the maximum in powers of two, its bucket and its weight.
 __device__ __forceinline__ float below(const Row& r, float x) { return (r.max - x) * r.scale; }
 // (The nearest 32nd, by an addition that leaves it in the lowest bits: conversions have a quarter of the rate.)
@@ -672,7 +675,7 @@ __device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* hom
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-      const int id = r.head + 4 * (r.q0 + 32 * (s + i * kWarps) + lane);
+      const int id = id_at(r, r.q0 + 32 * (s + i * kWarps) + lane);
       part[i] = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -680,7 +683,7 @@ __device__ __forceinline__ float draw_pass(const Row& r, Shared& sh, Shared* hom
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-      const int sub = s + i * kWarps, id = r.head + 4 * (r.q0 + 32 * sub + lane);
+      const int sub = s + i * kWarps, id = id_at(r, r.q0 + 32 * sub + lane);
       float t = -INFINITY;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

@@ -198,3 +198,25 @@ def test_rows_that_are_one(qmv, vocab):
         assert torch.equal(qmv.sample(x.expand(rows, -1), e, **how), qmv.sample(x.repeat(rows, 1), e, **how))
         assert torch.equal(qmv.sample(x.repeat(rows, 1), e[:1].expand(rows, -1), **how), qmv.sample(x.repeat(rows, 1), e[:1].repeat(rows, 1), **how))
         assert torch.equal(qmv.sample(x.expand(rows, -1), e[:1].expand(rows, -1), **how), qmv.sample(x.repeat(rows, 1), e[:1].repeat(rows, 1), **how))
+
+
+def test_the_longest_row(qmv):
+    """2^31 - 4097 ids, the most that there may be: a few stand out, at the row's ends."""
+    import torch
+    n = 2 ** 31 - 4097
+    x = torch.full((1, n), -30.0, device="cuda")
+    e = torch.ones((1, n), device="cuda")
+    x[0, [n - 1, n - 2, 0, 2 ** 30 + 3]] = torch.tensor([0.5, 1.0, 0.75, 0.25], device="cuda")
+
+    def one(**how):
+        return qmv.sample(x, e, **{k: torch.tensor([v], dtype=torch.int32 if k == "top_k" else torch.float32, device="cuda") for k, v in how.items()}).item()
+
+    assert one() == one(temperature=0.0) == one(top_k=4) == one(top_p=0.9) == n - 2
+    e[0, n - 1] = 1e-3
+    assert one() == one(top_k=3) == one(top_k=5000) == one(min_p=0.5) == one(top_p=0.9999) == n - 1
+    assert one(top_k=2) == one(min_p=0.7) == one(top_p=0.5) == n - 2  # (1 of 2.86 of the weight, 1.78 with the next)
+    e[0, n - 3] = 1e-25  # -30 + 57.6: ahead of all where nothing is cut off
+    assert one() == n - 3 and one(top_k=5000) == n - 1
+    assert one(top_k=n - 1) == n - 1 and one(top_k=n) == n - 3  # (the highest id of the lowest logit is the last in order)
+    del x, e
+    torch.cuda.empty_cache()

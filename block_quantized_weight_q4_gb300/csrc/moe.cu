@@ -32,7 +32,7 @@
 // largest operands' exponents, and a subnormal operand's exponent is that of 2^-14: products lose 6 to 10 bits there, about 2^-18 of a
 // result (2e-6 of the output's norm where it was left in float32, against 1.5e-7 with whole levels) and nothing beside a bfloat16's 2^-9.
 // Float32 outputs and activations (WHOLE): levels as whole halves, a subtraction or an fma for two.  Those everywhere would be slower where
-// the weights' bytes count: 1 token over two experts of 11008 x 4096 54.3 against 44.4 us, 32 over 128 of 768 x 2048 111 against 95 us
+// the weights' bytes count: 1 token over two experts of 11008 x 4096 54.6 against 46.3 us, 32 over 128 of 768 x 2048 119 against 105 us
 // (1 of 512 x 1024: no difference).  Q8_0 quants become exact halves by a magic number.
 // An activation is a half after the power of two that brings its block's (32 values') largest into [2^14, 2^15): exact for bfloat16
 // down to 2^-27 of the largest; float32 values and h are two halves, 22 bits.  (One half of h for bfloat16 outputs put 2e-4 of the output's
